@@ -389,4 +389,88 @@ q8_status q8_gemm_ex(const int8_t *q, const uint16_t *s, int64_t N, int64_t K, c
                           reinterpret_cast<cudaStream_t>(stream));
 }
 
+// ---- decode step ---------------------------------------------------------------
+static q8_status check_cache(const q8_kv_cache *c) {
+    if (!c) return Q8_ERR_ARG;
+    const int32_t ps = c->page_size;
+    if (ps < 16 || ps > 1024 || (ps & (ps - 1)) != 0) return Q8_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return Q8_ERR_SHAPE;
+    if (c->kv_heads < 1 || c->kv_heads > 1024 || c->pages < 1) return Q8_ERR_SHAPE;
+    if (!c->kq || !c->ks || !c->vq || !c->vs) return Q8_ERR_ARG;
+    if (!aligned(c->kq, 16) || !aligned(c->ks, 16) || !aligned(c->vq, 16) || !aligned(c->vs, 16)) return Q8_ERR_ALIGN;
+    return Q8_OK;
+}
+
+static q8_status check_kv_rows(const q8_kv_cache *c, const void *k, const void *v, int64_t ldk, int64_t ldv,
+                               int32_t dtype, const int64_t *slots, int64_t T, const uint32_t *dev_status) {
+    q8_status st = check_cache(c);
+    if (st != Q8_OK) return st;
+    if (dtype != Q8_DTYPE_F32 && dtype != Q8_DTYPE_BF16) return Q8_ERR_ARG;
+    const int64_t row = static_cast<int64_t>(c->kv_heads) * c->head_dim;
+    if (T < 0 || T > INT32_MAX || ldk < row || ldv < row || ldk > INT32_MAX || ldv > INT32_MAX) return Q8_ERR_SHAPE;
+    if (T == 0) return Q8_OK;
+    if (!k || !v || !slots) return Q8_ERR_ARG;
+    const int64_t mult = dtype == Q8_DTYPE_F32 ? 4 : 8;
+    if (!aligned(k, 16) || !aligned(v, 16) || ldk % mult != 0 || ldv % mult != 0 || !aligned(slots, 8)) return Q8_ERR_ALIGN;
+    if (dev_status && !aligned(dev_status, 4)) return Q8_ERR_ALIGN;
+    return Q8_OK;
+}
+
+q8_status q8_kv_append(const q8_kv_cache *cache, const void *k, const void *v, int64_t ldk, int64_t ldv, int32_t dtype,
+                       const int64_t *slots, int64_t T, uint32_t *dev_status, q8_stream_t stream) {
+    q8_status st = check_kv_rows(cache, k, v, ldk, ldv, dtype, slots, T, dev_status);
+    if (st != Q8_OK || T == 0) return st;
+    const DeviceInfo *di;
+    st = check_arch(&di);
+    if (st != Q8_OK) return st;
+    return launch_kv_append(*cache, k, v, ldk, ldv, dtype, slots, T, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q8_status q8_kv_read(const q8_kv_cache *cache, const int64_t *slots, int64_t T, void *k, void *v, int64_t ldk,
+                     int64_t ldv, int32_t dtype, uint32_t *dev_status, q8_stream_t stream) {
+    q8_status st = check_kv_rows(cache, k, v, ldk, ldv, dtype, slots, T, dev_status);
+    if (st != Q8_OK || T == 0) return st;
+    const DeviceInfo *di;
+    st = check_arch(&di);
+    if (st != Q8_OK) return st;
+    return launch_kv_read(*cache, slots, T, k, v, ldk, ldv, dtype, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static q8_status check_heads(int32_t batch, int32_t q_heads, int32_t kv_heads) {
+    if (batch < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || q_heads > 65536) return Q8_ERR_SHAPE;
+    return Q8_OK;
+}
+
+size_t q8_attn_decode_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+    if (check_heads(batch, q_heads, kv_heads) != Q8_OK || batch == 0) return 0;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+    return attn_workspace(q_heads, kv_heads, head_dim);
+}
+
+q8_status q8_attn_decode(const q8_kv_cache *cache, const uint16_t *q, int64_t ldq, int32_t q_heads,
+                         const int32_t *table, int32_t table_width, const int32_t *lens, int32_t batch, float scale,
+                         float softcap, int32_t window, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
+                         uint32_t *dev_status, q8_stream_t stream) {
+    q8_status st = check_cache(cache);
+    if (st != Q8_OK) return st;
+    st = check_heads(batch, q_heads, cache->kv_heads);
+    if (st != Q8_OK) return st;
+    if (table_width < 0 || static_cast<int64_t>(table_width) * cache->page_size > INT32_MAX - 4096) return Q8_ERR_SHAPE;
+    if (window < 0 || !(softcap >= 0.0f) || !(scale - scale == 0.0f) || softcap - softcap != 0.0f) return Q8_ERR_ARG;
+    if (ldq < static_cast<int64_t>(q_heads) * cache->head_dim) return Q8_ERR_SHAPE;
+    if (batch == 0) return Q8_OK;
+    if (!q || !lens || !out || (table_width > 0 && !table)) return Q8_ERR_ARG;
+    if (!aligned(q, 16) || ldq % 8 != 0 || !aligned(out, 16) || !aligned(lens, 4) || !aligned(table, 4) ||
+        !aligned(lse, 4) || !aligned(dev_status, 4))
+        return Q8_ERR_ALIGN;
+    const size_t need = attn_workspace(q_heads, cache->kv_heads, cache->head_dim);
+    if (!ws || ws_bytes < need) return Q8_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return Q8_ERR_ALIGN;
+    const DeviceInfo *di;
+    st = check_arch(&di);
+    if (st != Q8_OK) return st;
+    AttnArgs a = {q, table, lens, out, lse, ldq, q_heads, table_width, batch, window, scale, softcap};
+    return launch_attn(*cache, a, ws, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -1,0 +1,695 @@
+// q8_attn.cu -- attention of one new token per sequence over a paged Q8_0
+// key-value cache, split over the cache's length and joined in one launch.
+//
+// Mathematics.  With s_t = scale * q . k_t and any m, out = (sum_t 2^(s'_t - m)
+// v_t) / (sum_t 2^(s'_t - m)), s' = s log2(e).  A warp walks tokens keeping
+// (m, l, O) = (reference maximum, sum, weighted sum); two such triples join
+// into (max m, l1 2^(m1 - m) + l2 2^(m2 - m), ...), which is how the warps of
+// a CTA and the CTAs of a sequence are put together, in a fixed order.  The
+// reference is moved only when a score passes it by 4 (a vote, no shuffles
+// otherwise): any m gives the same quotient, and weights stay below 2^4.
+//
+// Scores: keys' codes are exact in binary16, and each query head is scaled by
+// a power of two so that its largest value lies in [2^14, 2^15): the bf16
+// query is then exact in binary16 down to 2^-31 of that value.  A warp MMA
+// (m16n8k16) multiplies 16 tokens x 32 codes by 8 query heads; the block's
+// scale multiplies its fp32 result, as in the matmuls.
+// Weighted sum: O^T = V^T P, 32 dimensions x 16 tokens by 8 heads.  The
+// weight is rounded to binary16, the value s * code too (2^-11 each at most,
+// against 2^-8 of the bf16 result), sums are fp32.  Value scales above 512 could
+// overflow s * code: such a tile takes s 2^-9 and p 2^9.
+//
+// Bound: bytes of the cache, 2.125 per dimension and token, each read once
+// for up to 16 query heads.
+//
+// Split: every warp is its own pipeline over 16-token tiles (a tile lies in
+// one page, so its codes and scales are four contiguous runs), filled by
+// 16-byte asynchronous copies; a warp waits for nobody until its item ends.
+// Work is cut into units of kWarps tiles (the sequences' lengths are read on
+// the device); CTA c takes units [c * per, (c + 1) * per) of the list of all
+// (sequence, key head, group of query heads) items, so CTAs carry the same
+// load whatever the lengths.  An item within one CTA is finished there; the
+// others leave (m, l, O) in the workspace and the last CTA to arrive joins
+// them in CTA order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "q8_dev.cuh"
+#include "q8_internal.h"
+
+namespace q8 {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnitTokens = kWarps * 16;
+constexpr int kMaxGrid = 1024;    // CTAs a launch may have (sizes the workspace)
+constexpr int kMinUnits = 4;      // units a CTA takes at least
+constexpr float kGrow = 4.0f;     // log2 growth of a score that moves the reference
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttnParams {
+    const int8_t *kq, *vq;
+    const uint16_t *ks, *vs;
+    const uint16_t *q;
+    const int32_t *table, *lens;
+    uint16_t *out;
+    float *lse;
+    uint32_t *tickets;  // [kMaxGrid]
+    float *parts;       // [2 * kMaxGrid][HG * (D + 2)]
+    uint32_t *status;
+    int64_t ldq;
+    int32_t batch, q_heads, kv_heads, group, splits;  // splits: runs of HG heads in a group
+    int32_t table_width, pages, page_shift, window;
+    float scale, softcap;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The token (0 .. 7) that MMA row f stands for; rows f + 8 stand for token
+// + 8.  Chunks of 16 bytes are stored at chunk ^ (128-byte line & 7); these
+// orders make both access patterns hit all banks once: keys (rows f = 0..3
+// and 4..7, two chunks each) and values (rows 0, 2, 4, 6 and 1, 3, 5, 7).
+template <int D>
+__device__ __forceinline__ int token_of(int f) {
+    constexpr uint32_t order = D == 64 ? 0x37265140u : (D == 128 ? 0x57136420u : 0x67453210u);
+    return (order >> (4 * f)) & 7;
+}
+// Byte offset of 16-byte chunk c of a tile's token r.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    const uint32_t m = r * (D / 16) + c;
+    return (m ^ ((m >> 3) & 7)) * 16;
+}
+
+// Where a CTA is in the list of items: the sequence, its head (key head *
+// splits + run of heads), the unit within the item.
+struct Walk {
+    int b, hh, unit, units;  // units of this sequence's items
+    int len, first;          // tokens, and the first one seen
+    int base;                // first token of unit 0 (a multiple of 16)
+};
+
+__device__ __forceinline__ int seq_len(const AttnParams &p, int b, bool flag) {
+    const int n = p.lens[b], top = p.table_width << p.page_shift;
+    const int c = min(max(n, 0), top);
+    if (flag && c != n && p.status) atomicOr(p.status, Q8_DEV_BAD_INDEX);
+    return c;
+}
+__device__ __forceinline__ int seq_first(const AttnParams &p, int len) {
+    return p.window > 0 ? max(0, len - p.window) : 0;
+}
+__device__ __forceinline__ int seq_units(const AttnParams &p, int len) {
+    const int base = seq_first(p, len) & ~15;
+    return (len - base + kUnitTokens - 1) / kUnitTokens;
+}
+__device__ __forceinline__ void enter(const AttnParams &p, Walk &w) {
+    w.len = seq_len(p, w.b, false);
+    w.first = seq_first(p, w.len);
+    w.base = w.first & ~15;
+    w.units = seq_units(p, w.len);
+}
+// The next unit of the list (the caller knows that there is one).
+__device__ __forceinline__ void advance(const AttnParams &p, Walk &w) {
+    if (++w.unit < w.units) return;
+    w.unit = 0;
+    if (++w.hh < p.kv_heads * p.splits) return;
+    w.hh = 0;
+    do {
+        ++w.b;
+        enter(p, w);
+    } while (w.units == 0 && w.b + 1 < p.batch);
+}
+
+template <int D, int NT>
+struct Cfg {
+    static constexpr int HG = 8 * NT;              // query heads of an item
+    static constexpr int kCodes = 16 * D;          // bytes of a tile's key (or value) codes
+    static constexpr int kScales = D;              // bytes of its scales: 16 * (D / 32) * 2
+    static constexpr int kStage = 2 * (kCodes + kScales);
+    static constexpr int kStages = D == 256 ? 3 : (D == 128 ? 4 : 6);
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kOPitch = D + 8;
+    static constexpr int kJoin = (HG * kOPitch + 2 * kWarps * HG + 2 * HG) * 4;
+    static constexpr int kSmem = kRing + kJoin;
+    static constexpr int kPart = HG * (D + 2);     // floats of one partial result
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ AttnParams p) {
+    using C = Cfg<D, NT>;
+    constexpr int NB = D / 32;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long s_scan[kWarps];
+    __shared__ uint32_t s_last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    float *const s_o = reinterpret_cast<float *>(smem + C::kRing);
+    float *const s_m = s_o + C::HG * C::kOPitch;  // [kWarps][HG]
+    float *const s_l = s_m + kWarps * C::HG;
+    float *const s_mm = s_l + kWarps * C::HG;     // [HG] joined
+    float *const s_ll = s_mm + C::HG;
+
+    // ---- the list: how long it is, and where this CTA begins --------------------
+    const int heads = p.kv_heads * p.splits;
+    long long total = 0;
+    for (int b = tid; b < p.batch; b += kThreads) total += seq_units(p, seq_len(p, b, blockIdx.x == 0));
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) s_scan[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kWarps; ++w) total += s_scan[w];
+    total *= heads;
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinUnits));
+    const long long u0 = per * blockIdx.x, u1 = min(u0 + per, total);
+
+    // sequences of no tokens have no units: write their answer
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+        if (seq_len(p, b, false) > 0) continue;
+        for (int i = tid; i < p.q_heads * D / 8; i += kThreads)
+            reinterpret_cast<uint4 *>(p.out)[static_cast<int64_t>(b) * p.q_heads * (D / 8) + i] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+            for (int i = tid; i < p.q_heads; i += kThreads) p.lse[static_cast<int64_t>(b) * p.q_heads + i] = -INFINITY;
+    }
+    if (u0 >= u1) return;
+
+    // the sequence that holds unit u0: each warp scans for itself, 32 at a time
+    Walk wk;
+    {
+        long long before = 0;
+        int b0 = 0;
+        while (true) {
+            const int b = b0 + lane;
+            long long n = b < p.batch ? static_cast<long long>(seq_units(p, seq_len(p, b, false))) * heads : 0;
+            long long run = n;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += v;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, before + run > u0);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                before += __shfl_sync(0xffffffffu, run - n, src);
+                wk.b = b0 + src;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, run, 31);
+            b0 += 32;
+        }
+        enter(p, wk);
+        const long long in = u0 - before;
+        wk.hh = static_cast<int>(in / wk.units);
+        wk.unit = static_cast<int>(in - static_cast<long long>(wk.hh) * wk.units);
+    }
+
+    // ---- this warp's pipeline ------------------------------------------------------
+    const uint32_t ring = smem_addr(smem) + warp * C::kStages * C::kStage;
+    Walk ld = wk;              // the next unit to load
+    long long ld_left = u1 - u0;
+    int ld_slot = 0;
+    int ld_page = -1;          // page of the tile to load next, read one step ahead
+    uint32_t held = 0;         // bit i: slot i holds a tile
+    auto tile_of = [&](const Walk &w) { return w.base + w.unit * kUnitTokens + warp * 16; };
+    auto fetch_page = [&]() {
+        ld_page = -1;
+        if (ld_left > 0) {
+            const int tok = tile_of(ld);
+            if (tok < ld.len) ld_page = p.table[static_cast<int64_t>(ld.b) * p.table_width + (tok >> p.page_shift)];
+        }
+    };
+    auto load = [&]() {
+        if (ld_left > 0) {
+            const int tok = tile_of(ld);
+            const bool ok = tok < ld.len && static_cast<uint32_t>(ld_page) < static_cast<uint32_t>(p.pages);
+            held = (held & ~(1u << ld_slot)) | (static_cast<uint32_t>(ok) << ld_slot);
+            // a page outside the cache: its tokens are left out
+            if (!ok && tok < ld.len && lane == 0 && p.status) atomicOr(p.status, Q8_DEV_BAD_INDEX);
+            if (ok) {
+                const int kvh = ld.hh / p.splits;
+                const int64_t row = ((static_cast<int64_t>(ld_page) * p.kv_heads + kvh) << p.page_shift) +
+                                    (tok & ((1 << p.page_shift) - 1));
+                const uint32_t st = ring + ld_slot * C::kStage;
+                const int8_t *kc = p.kq + row * D, *vc = p.vq + row * D;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int m = i * 32 + lane;
+                    const uint32_t at = (m ^ ((m >> 3) & 7)) * 16;
+                    cp_async16(st + at, kc + m * 16);
+                    cp_async16(st + C::kCodes + at, vc + m * 16);
+                }
+                if (lane < D / 8) {
+                    const bool is_v = lane >= D / 16;
+                    const int c = is_v ? lane - D / 16 : lane;
+                    const uint8_t *src = reinterpret_cast<const uint8_t *>((is_v ? p.vs : p.ks) + row * NB) + c * 16;
+                    cp_async16(st + 2 * C::kCodes + lane * 16, src);
+                }
+            }
+            --ld_left;
+            if (ld_left > 0) advance(p, ld);
+            fetch_page();
+        }
+        ld_slot = ld_slot + 1 == C::kStages ? 0 : ld_slot + 1;
+        cp_async_commit();
+    };
+    fetch_page();
+    for (int i = 0; i < C::kStages - 1; ++i) load();
+
+    // ---- items ---------------------------------------------------------------------
+    long long left = u1 - u0;
+    long long item0 = u0 - wk.unit;  // first unit of the current item in the list
+    int slot = 0;
+    while (left > 0) {
+        const int seg_first = wk.unit;
+        const int seg = static_cast<int>(min(left, static_cast<long long>(wk.units - wk.unit)));
+        const int kvh = wk.hh / p.splits, run = wk.hh - kvh * p.splits;
+        const int head0 = kvh * p.group + run * C::HG;          // first query head of the item
+        const int nheads = min(C::HG, p.group - run * C::HG);
+        // this lane's query fragments: head g (+ 8 per n-tile), 8 dimensions of each block
+        uint32_t qf[NT][NB][4];
+        float fac[NT][2];  // scores of head 2t, 2t + 1: MMA result -> log2 units (or softcap's argument)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int h = n * 8 + g;
+            uint4 raw[NB];
+            float amax = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                raw[b] = h < nheads ? *reinterpret_cast<const uint4 *>(p.q + wk.b * p.ldq + static_cast<int64_t>(head0 + h) * D +
+                                                                       32 * b + 8 * t)
+                                    : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16lo_f32(w[i])), fabsf(bf16hi_f32(w[i]))));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^e with amax * 2^e in [2^14, 2^15); exponents kept where 2^e and 2^-e are normal
+            int ex = static_cast<int>(__float_as_uint(amax) >> 23);
+            ex = min(max(ex, 30), 240);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - ex) << 23);
+            const float down = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qf[n][b][i] = f32x2_to_f16x2(bf16lo_f32(w[i]) * up, bf16hi_f32(w[i]) * up);
+            }
+            float f = p.scale * down;
+            f = p.softcap > 0.f ? f / p.softcap : f * kLog2e;
+            fac[n][0] = __shfl_sync(0xffffffffu, f, (2 * t) * 4);
+            fac[n][1] = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
+        }
+        float m[NT][2], l[NT][2], o[NT][D / 16][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+        }
+
+        for (int s = 0; s < seg; ++s) {
+            const int tok = wk.base + (seg_first + s) * kUnitTokens + warp * 16;
+            cp_async_wait<C::kStages - 2>();
+            __syncwarp();
+            const bool live = (held >> slot) & 1;
+            load();  // into the slot that the step before this one read
+            const uint32_t st = ring + slot * C::kStage;
+            if (live) {
+                const int r0 = token_of<D>(g);
+                // ---- scores: 16 tokens x 8 NT heads
+                float acc[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+                const uint32_t sk = st + 2 * C::kCodes;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint32_t in = (t & 1) * 8;
+                    const uint2 w0 = lds64(st + chunk_at<D>(r0, 2 * b + (t >> 1)) + in);
+                    const uint2 w1 = lds64(st + chunk_at<D>(r0 + 8, 2 * b + (t >> 1)) + in);
+                    uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+                    codes4_to_f16x2(w0.x, a0, a2);
+                    codes4_to_f16x2(w1.x, a1, a3);
+                    codes4_to_f16x2(w0.y, b0, b2);
+                    codes4_to_f16x2(w1.y, b1, b3);
+                    const uint32_t sc = lds32(sk + (r0 * NB + b) * 2 & ~3u), sd = lds32(sk + ((r0 + 8) * NB + b) * 2 & ~3u);
+                    const float s0 = f16_bits_to_f32((b & 1) ? sc >> 16 : sc & 0xFFFFu);
+                    const float s1 = f16_bits_to_f32((b & 1) ? sd >> 16 : sd & 0xFFFFu);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
+                        mma_f16_16816(d0, d1, d2, d3, a0, a1, a2, a3, qf[n][b][0], qf[n][b][1]);
+                        mma_f16_16816(d0, d1, d2, d3, b0, b1, b2, b3, qf[n][b][2], qf[n][b][3]);
+                        acc[n][0] = fmaf(s0, d0, acc[n][0]);
+                        acc[n][1] = fmaf(s0, d1, acc[n][1]);
+                        acc[n][2] = fmaf(s1, d2, acc[n][2]);
+                        acc[n][3] = fmaf(s1, d3, acc[n][3]);
+                    }
+                }
+                // ---- weights
+                const bool whole = tok >= wk.first && tok + 16 <= wk.len;
+                const bool in0 = whole || (tok + r0 >= wk.first && tok + r0 < wk.len);
+                const bool in1 = whole || (tok + r0 + 8 >= wk.first && tok + r0 + 8 < wk.len);
+                bool grows = false;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x = acc[n][i] * fac[n][i & 1];
+                        if (p.softcap > 0.f) x = p.softcap * kLog2e * tanhf(x);
+                        x = (i < 2 ? in0 : in1) ? x : -INFINITY;
+                        acc[n][i] = x;
+                        grows = grows || x > m[n][i & 1] + kGrow;
+                    }
+                if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float x = fmaxf(acc[n][j], acc[n][2 + j]);
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                            x = fmaxf(x, m[n][j]);
+                            const float f = m[n][j] == -INFINITY ? 0.f : ex2(m[n][j] - x);
+                            m[n][j] = x;
+                            l[n][j] *= f;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) o[n][i][j] *= f, o[n][i][2 + j] *= f;
+                        }
+                }
+                uint32_t pf[NT][2];
+                const uint32_t sv = sk + C::kScales;
+                const int ra = token_of<D>(2 * t), rb = token_of<D>(2 * t + 1);
+                // value scales of tokens (ra, rb) and (ra + 8, rb + 8), as pairs
+                uint32_t s01[NB], s89[NB];
+                uint32_t top = 0;
+                {
+                    uint32_t x[4][NB / 2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = ((i & 1) ? rb : ra) + ((i & 2) ? 8 : 0);
+                        const bool in = whole || (tok + r >= wk.first && tok + r < wk.len);
+#pragma unroll
+                        for (int b = 0; b < NB / 2; ++b) {
+                            x[i][b] = in ? lds32(sv + r * NB * 2 + b * 4) : 0u;
+                            const uint32_t lo = x[i][b] & 0x7FFFu, hi = (x[i][b] >> 16) & 0x7FFFu;
+                            top = max(top, max(lo, hi));
+                        }
+                    }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        s01[b] = __byte_perm(x[0][b / 2], x[1][b / 2], (b & 1) ? 0x7632 : 0x5410);
+                        s89[b] = __byte_perm(x[2][b / 2], x[3][b / 2], (b & 1) ? 0x7632 : 0x5410);
+                    }
+                }
+                const bool big = __any_sync(0xffffffffu, top > 0x6000u);  // a scale above 512
+                if (big) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        s01[b] = hmul2(s01[b], 0x18001800u);  // 2^-9
+                        s89[b] = hmul2(s89[b], 0x18001800u);
+                    }
+                }
+                const float up = big ? 512.f : 1.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float ref = m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1];
+                        w[i] = ex2(acc[n][i] - ref);
+                    }
+                    l[n][0] += w[0] + w[2];
+                    l[n][1] += w[1] + w[3];
+                    pf[n][0] = movmatrix(f32x2_to_f16x2(w[0] * up, w[1] * up));
+                    pf[n][1] = movmatrix(f32x2_to_f16x2(w[2] * up, w[3] * up));
+                }
+                // ---- weighted values
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint32_t vb = st + C::kCodes + (g & 3) * 4;
+                    const int c = 2 * b + (g >> 2);
+                    const uint32_t wa = lds32(vb + chunk_at<D>(ra, c)) ^ 0x80808080u;
+                    const uint32_t wb = lds32(vb + chunk_at<D>(rb, c)) ^ 0x80808080u;
+                    const uint32_t wc = lds32(vb + chunk_at<D>(ra + 8, c)) ^ 0x80808080u;
+                    const uint32_t wd = lds32(vb + chunk_at<D>(rb + 8, c)) ^ 0x80808080u;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {  // dimensions 32 b + 4 g + 2 i, + 1
+                        const uint32_t x = __byte_perm(wa, wb, i ? 0x7362 : 0x5140);
+                        const uint32_t y = __byte_perm(wc, wd, i ? 0x7362 : 0x5140);
+                        const uint32_t k1152 = 0x64806480u;
+                        const uint32_t a0 = hmul2(hsub2(__byte_perm(x, 0x64646464u, 0x4140), k1152), s01[b]);
+                        const uint32_t a1 = hmul2(hsub2(__byte_perm(x, 0x64646464u, 0x4342), k1152), s01[b]);
+                        const uint32_t a2 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4140), k1152), s89[b]);
+                        const uint32_t a3 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4342), k1152), s89[b]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16_16816(o[n][2 * b + i][0], o[n][2 * b + i][1], o[n][2 * b + i][2], o[n][2 * b + i][3],
+                                          a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                    }
+                }
+            }
+            slot = slot + 1 == C::kStages ? 0 : slot + 1;
+        }
+
+        // ---- join the warps -------------------------------------------------------------
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x = l[n][j];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                l[n][j] = x;
+                if (g == 0) {
+                    s_m[warp * C::HG + n * 8 + 2 * t + j] = m[n][j];
+                    s_l[warp * C::HG + n * 8 + 2 * t + j] = x;
+                }
+            }
+        __syncthreads();
+        if (tid < C::HG) {
+            float mm = -INFINITY, ll = 0.f;
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * C::HG + tid]);
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = s_m[w * C::HG + tid];
+                ll += mw == -INFINITY ? s_l[w * C::HG + tid] : s_l[w * C::HG + tid] * ex2(mw - mm);
+            }
+            s_mm[tid] = mm;
+            s_ll[tid] = ll;
+        }
+        for (int w = 0; w < kWarps; ++w) {
+            __syncthreads();
+            if (warp != w) continue;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int h = n * 8 + 2 * t + j;
+                    const float f = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - s_mm[h]);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        float2 *at = reinterpret_cast<float2 *>(s_o + h * C::kOPitch + 32 * (i >> 1) + 4 * g + 2 * (i & 1));
+                        float2 v = make_float2(o[n][i][j] * f, o[n][i][2 + j] * f);
+                        if (w > 0) {
+                            const float2 old = *at;
+                            v.x += old.x;
+                            v.y += old.y;
+                        }
+                        *at = v;
+                    }
+                }
+        }
+        __syncthreads();
+
+        // ---- give the item's answer, or leave a part of it --------------------------------
+        auto answer = [&]() {
+            for (int i = tid; i < nheads * (D / 4); i += kThreads) {
+                const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+                const float ll = s_ll[h], r = ll == 0.f ? 0.f : 1.f / ll;
+                const float *src = s_o + h * C::kOPitch + d;
+                const __nv_bfloat162 x = __floats2bfloat162_rn(src[0] * r, src[1] * r);
+                const __nv_bfloat162 y = __floats2bfloat162_rn(src[2] * r, src[3] * r);
+                uint2 v;
+                v.x = *reinterpret_cast<const uint32_t *>(&x);
+                v.y = *reinterpret_cast<const uint32_t *>(&y);
+                *reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(wk.b) * p.q_heads + head0 + h) * D + d) = v;
+            }
+            if (p.lse && tid < nheads) {
+                const float mm = s_mm[tid], ll = s_ll[tid];
+                p.lse[static_cast<int64_t>(wk.b) * p.q_heads + head0 + tid] =
+                    ll == 0.f ? -INFINITY : fmaf(mm, 0.69314718055994531f, logf(ll));
+            }
+        };
+        if (seg == wk.units) {
+            answer();
+        } else {
+            const int c0 = static_cast<int>(item0 / per), c1 = static_cast<int>((item0 + wk.units - 1) / per);
+            float *const mine = p.parts + static_cast<int64_t>(2 * blockIdx.x + (seg_first == 0 ? 1 : 0)) * C::kPart;
+            for (int i = tid; i < C::HG * (D / 4); i += kThreads) {
+                const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+                *reinterpret_cast<float4 *>(mine + h * D + d) = *reinterpret_cast<const float4 *>(s_o + h * C::kOPitch + d);
+            }
+            if (tid < C::HG) {
+                mine[C::HG * D + tid] = s_mm[tid];
+                mine[C::HG * D + C::HG + tid] = s_ll[tid];
+            }
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const uint32_t n = atomicAdd(p.tickets + c0, 1u);
+                s_last = n == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
+                if (s_last) p.tickets[c0] = 0u;
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                auto part = [&](int c) { return p.parts + static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * C::kPart; };
+                if (tid < C::HG) {
+                    float mm = -INFINITY, ll = 0.f;
+                    for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(part(c) + C::HG * D + tid));
+                    for (int c = c0; c <= c1; ++c) {
+                        const float mc = __ldcg(part(c) + C::HG * D + tid), lc = __ldcg(part(c) + C::HG * D + C::HG + tid);
+                        ll += mc == -INFINITY ? lc : lc * ex2(mc - mm);
+                    }
+                    s_mm[tid] = mm;
+                    s_ll[tid] = ll;
+                }
+                __syncthreads();
+                for (int i = tid; i < nheads * (D / 4); i += kThreads) {
+                    const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+                    const float mm = s_mm[h];
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int c = c0; c <= c1; ++c) {
+                        const float *q = part(c);
+                        const float mc = __ldcg(q + C::HG * D + h);
+                        const float f = mc == -INFINITY ? 1.f : ex2(mc - mm);
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(q + h * D + d));
+                        sum.x = fmaf(v.x, f, sum.x), sum.y = fmaf(v.y, f, sum.y);
+                        sum.z = fmaf(v.z, f, sum.z), sum.w = fmaf(v.w, f, sum.w);
+                    }
+                    *reinterpret_cast<float4 *>(s_o + h * C::kOPitch + d) = sum;
+                }
+                __syncthreads();
+                answer();
+            }
+        }
+        __syncthreads();
+
+        left -= seg;
+        item0 += wk.units;
+        if (left > 0) {
+            wk.unit = wk.units - 1;
+            advance(p, wk);
+        }
+    }
+    cp_async_wait<0>();
+}
+
+int ilog2(int64_t v) {
+    int s = 0;
+    while ((int64_t(1) << s) < v) ++s;
+    return s;
+}
+
+// Query heads that share one pass over the keys: 16 where a group has more
+// than 8 (the keys and values are then read once for all of them), else 8;
+// at 256 dimensions 16 heads' sums would not fit the registers.
+int tiles_of(int group, int head_dim) { return head_dim <= 128 && group > 8 ? 2 : 1; }
+
+template <int D, int NT>
+q8_status launch(const AttnParams &p, int64_t most_units, const DeviceInfo *di, cudaStream_t stream) {
+    using C = Cfg<D, NT>;
+    static std::atomic<int> per_sm[64];
+    int n = di->device < 64 ? per_sm[di->device].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        if (cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<D, NT>, kThreads, C::kSmem) != cudaSuccess)
+            return Q8_ERR_CUDA;
+        if (n < 1) return Q8_ERR_UNSUPPORTED;
+        if (di->device < 64) per_sm[di->device].store(n, std::memory_order_relaxed);
+    }
+    int64_t grid = static_cast<int64_t>(n) * di->sm_count;
+    if (grid > kMaxGrid) grid = kMaxGrid;
+    const int64_t need = (most_units + kMinUnits - 1) / kMinUnits;
+    if (grid > need) grid = need;
+    if (grid < 1) grid = 1;
+    attn_kernel<D, NT><<<static_cast<unsigned>(grid), kThreads, C::kSmem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? Q8_OK : Q8_ERR_CUDA;
+}
+
+}  // namespace
+
+// Counters, then two partial results per CTA.
+size_t attn_workspace(int q_heads, int kv_heads, int head_dim) {
+    const int hg = 8 * tiles_of(q_heads / kv_heads, head_dim);
+    return static_cast<size_t>(kMaxGrid) * 4 + static_cast<size_t>(2) * kMaxGrid * hg * (head_dim + 2) * 4;
+}
+
+q8_status launch_attn(const q8_kv_cache &c, const AttnArgs &a, void *ws, uint32_t *dev_status, cudaStream_t stream) {
+    const DeviceInfo *di = device_info();
+    if (!di) return Q8_ERR_CUDA;
+    AttnParams p = {};
+    p.kq = c.kq, p.vq = c.vq, p.ks = c.ks, p.vs = c.vs;
+    p.q = a.q, p.table = a.table, p.lens = a.lens, p.out = a.out, p.lse = a.lse;
+    p.tickets = static_cast<uint32_t *>(ws);
+    p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kMaxGrid * 4);
+    p.status = dev_status;
+    p.ldq = a.ldq;
+    p.batch = a.batch, p.q_heads = a.q_heads, p.kv_heads = c.kv_heads;
+    p.group = a.q_heads / c.kv_heads;
+    const int nt = tiles_of(p.group, c.head_dim);
+    p.splits = (p.group + 8 * nt - 1) / (8 * nt);
+    p.table_width = a.table_width, p.pages = c.pages, p.page_shift = ilog2(c.page_size);
+    p.window = a.window, p.scale = a.scale, p.softcap = a.softcap;
+    int64_t span = static_cast<int64_t>(a.table_width) * c.page_size;
+    if (a.window > 0 && span > a.window + 15) span = a.window + 15;
+    const int64_t most = (span + kUnitTokens - 1) / kUnitTokens * a.batch * p.kv_heads * p.splits;
+    if (c.head_dim == 64) return nt == 1 ? launch<64, 1>(p, most, di, stream) : launch<64, 2>(p, most, di, stream);
+    if (c.head_dim == 128) return nt == 1 ? launch<128, 1>(p, most, di, stream) : launch<128, 2>(p, most, di, stream);
+    return launch<256, 1>(p, most, di, stream);
+}
+
+}  // namespace q8

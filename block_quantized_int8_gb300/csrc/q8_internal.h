@@ -161,4 +161,22 @@ q8_status launch_gemm_tc(const int8_t *q, const uint16_t *s, int64_t N, int64_t 
                          const uint16_t *x, int64_t ldx, int32_t M, uint16_t *y, int64_t ldy, int32_t tile,
                          int32_t splits, uint32_t *dev_status, cudaStream_t stream);
 
+// ---- decode step: key-value cache and attention ---------------------------------
+q8_status launch_kv_append(const q8_kv_cache &c, const void *k, const void *v, int64_t ldk, int64_t ldv, int32_t dtype,
+                           const int64_t *slots, int64_t T, uint32_t *dev_status, cudaStream_t stream);
+q8_status launch_kv_read(const q8_kv_cache &c, const int64_t *slots, int64_t T, void *k, void *v, int64_t ldk,
+                         int64_t ldv, int32_t dtype, uint32_t *dev_status, cudaStream_t stream);
+
+struct AttnArgs {
+    const uint16_t *q;
+    const int32_t *table, *lens;
+    uint16_t *out;
+    float *lse;
+    int64_t ldq;
+    int32_t q_heads, table_width, batch, window;
+    float scale, softcap;
+};
+size_t attn_workspace(int q_heads, int kv_heads, int head_dim);
+q8_status launch_attn(const q8_kv_cache &c, const AttnArgs &a, void *ws, uint32_t *dev_status, cudaStream_t stream);
+
 }  // namespace q8

@@ -28,20 +28,9 @@
 
 #include "q8_dev.cuh"
 #include "q8_internal.h"
+#include "q8_quant.cuh"
 
 namespace q8 {
-
-__device__ __forceinline__ int32_t code_of(float v, float sf, float rcp) {
-    const float a = fabsf(v);
-    float k = fminf(floorf(__fadd_rn(__fmul_rn(a, rcp), 0.5f)), 128.0f);
-    if (__fmul_rn(__fadd_rn(k, 0.5f), sf) <= a) {
-        k = __fadd_rn(k, 1.0f);
-    } else if (k > 0.0f && __fmul_rn(__fsub_rn(k, 0.5f), sf) > a) {
-        k = __fsub_rn(k, 1.0f);
-    }
-    const int32_t ki = static_cast<int32_t>(fminf(k, 127.0f));
-    return v < 0.0f ? -ki : ki;
-}
 
 __device__ __forceinline__ int32_t code_fl32(float v, float d) {
     const float t = __fdiv_rn(v, d);

@@ -27,6 +27,8 @@ Q8_ERR_ARG, Q8_ERR_ALIGN, Q8_ERR_SHAPE, Q8_ERR_WORKSPACE, Q8_ERR_ARCH, Q8_ERR_CU
 Q8_DEV_NONFINITE = 0x1
 Q8_DEV_SCALE_OVF = 0x2
 Q8_DEV_TIMEOUT = 0x4
+Q8_DEV_BAD_INDEX = 0x8
+Q8_DTYPE_F32, Q8_DTYPE_BF16 = 0, 1
 Q8_SKINNY_MAX_M = 32
 Q8_MAX_BATCH = 64
 Q8_VARIANT_AUTO, Q8_VARIANT_SIMT, Q8_VARIANT_MMA, Q8_VARIANT_BATCH_INVARIANT, Q8_VARIANT_W8A8 = 0, 1, 2, 3, 4
@@ -39,7 +41,8 @@ EXPORTS = ("q8_quantize_rows", "q8_gemv", "q8_gemm_skinny", "q8_linear_batch", "
            "q8_abi_version", "q8_gemm_skinny_noalloc", "q8_gemm_ex", "q8_gguf_to_planar",
            "q8_planar_to_gguf", "q8_quantize_rows_ex", "q8_selftest_wait_timeout",
            "q8_stream_read", "q8_stream_read_out_words", "q8_linear_chain", "q8_linear_chain_workspace_size",
-           "q8_gemm_w8a8", "q8_gemm_w8a8_workspace_size")
+           "q8_gemm_w8a8", "q8_gemm_w8a8_workspace_size", "q8_kv_append", "q8_kv_read", "q8_attn_decode",
+           "q8_attn_decode_workspace_size")
 Q8_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -60,6 +63,12 @@ class ChainStep(ctypes.Structure):
                 ("y", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("next", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class _CKvCache(ctypes.Structure):
+    _fields_ = [("kq", ctypes.c_void_p), ("ks", ctypes.c_void_p), ("vq", ctypes.c_void_p), ("vs", ctypes.c_void_p),
+                ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
 
 
 # how the next step of a chain takes its x from this step's y
@@ -108,12 +117,18 @@ def lib():
         L.q8_stream_read.argtypes = [P, SZ, P, P]
         L.q8_stream_read.restype = ctypes.c_int
         L.q8_stream_read_out_words.restype = SZ
+        L.q8_kv_append.argtypes = [P, P, P, I64, I64, I32, P, I64, P, P]
+        L.q8_kv_read.argtypes = [P, P, I64, P, P, I64, I64, I32, P, P]
+        L.q8_attn_decode.argtypes = [P, P, I64, I32, P, I32, P, I32, ctypes.c_float, ctypes.c_float, I32, P, P, P, SZ, P, P]
+        L.q8_attn_decode_workspace_size.argtypes = [I32, I32, I32, I32]
+        L.q8_attn_decode_workspace_size.restype = SZ
         L.q8_status_str.argtypes = [ctypes.c_int]
         L.q8_status_str.restype = ctypes.c_char_p
         L.q8_abi_version.restype = I32
         for name in ("q8_quantize_rows", "q8_quantize_rows_ex", "q8_gemv", "q8_gemm_skinny", "q8_linear_batch",
                      "q8_linear_batch_ex", "q8_linear_batch_chained", "q8_gguf_to_planar",
-                     "q8_planar_to_gguf", "q8_gemm", "q8_gemm_ex", "q8_gemm_skinny_noalloc", "q8_linear_chain", "q8_gemm_w8a8"):
+                     "q8_planar_to_gguf", "q8_gemm", "q8_gemm_ex", "q8_gemm_skinny_noalloc", "q8_linear_chain", "q8_gemm_w8a8",
+                     "q8_kv_append", "q8_kv_read", "q8_attn_decode"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -368,3 +383,127 @@ def q8_gemm(q, s, x, y=None, dev_status=None, stream=None, tile=0, splits=0):
                           _p(dev_status), _stream(stream))
     _check(st, "q8_gemm")
     return y
+
+
+# ---------------------------------------------------------------------------
+# the rest of a decode step
+# ---------------------------------------------------------------------------
+class KvCache:
+    """A paged key-value cache in Q8_0 blocks (q8_kv_cache): codes int8
+    [pages, kv_heads, page_size, head_dim], scales 16-bit [..., head_dim / 32].
+    Holds the tensors; make it once per cache."""
+
+    def __init__(self, kq, ks, vq, vs):
+        for n, t in (("kq", kq), ("vq", vq)):
+            _cuda(t, n, (torch.int8,), 4)
+        for n, t in (("ks", ks), ("vs", vs)):
+            _cuda(t, n, _B16, 4)
+        shape = tuple(kq.shape)
+        scales = shape[:3] + (shape[3] // 32,)
+        if tuple(vq.shape) != shape or tuple(ks.shape) != scales or tuple(vs.shape) != scales:
+            raise ValueError("keys and values share the shape [pages, kv_heads, page_size, head_dim], scales [..., head_dim / 32]")
+        if not all(t.is_contiguous() for t in (kq, ks, vq, vs)):
+            raise ValueError("the cache's tensors must be contiguous")
+        if len({t.device for t in (kq, ks, vq, vs)}) != 1:
+            raise ValueError("the cache's tensors must be on one device")
+        self.kq, self.ks, self.vq, self.vs = kq, ks, vq, vs
+        self.pages, self.kv_heads, self.page_size, self.head_dim = shape
+        self.device = kq.device
+        self._c = _CKvCache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1], shape[3])
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
+        """An uninitialised cache of that shape."""
+        a = (pages, kv_heads, page_size, head_dim)
+        b = (pages, kv_heads, page_size, head_dim // 32)
+        return cls(torch.empty(a, dtype=torch.int8, device=device), torch.empty(b, dtype=torch.float16, device=device),
+                   torch.empty(a, dtype=torch.int8, device=device), torch.empty(b, dtype=torch.float16, device=device))
+
+
+_ROW_DTYPES = {torch.float32: Q8_DTYPE_F32, torch.bfloat16: Q8_DTYPE_BF16}
+
+
+def _kv_rows(cache, t, name, n, dtype=None):
+    """The row stride of [n, kv_heads * head_dim] or [n, kv_heads, head_dim] rows (heads contiguous)."""
+    if not t.is_cuda or t.dtype not in _ROW_DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be a float32 or bfloat16 CUDA tensor, keys and values alike")
+    row = cache.kv_heads * cache.head_dim
+    sh, sd = tuple(t.shape), t.stride()
+    if sh == (n, cache.kv_heads, cache.head_dim):
+        ok = sd[2] == 1 and (sd[1] == cache.head_dim or cache.kv_heads == 1)
+    else:
+        ok = sh == (n, row) and sd[1] == 1
+    if not ok and n > 0:
+        raise ValueError(f"{name} must hold {n} rows of {cache.kv_heads} x {cache.head_dim} values, each row contiguous")
+    return sd[0] if n > 1 else row
+
+
+def q8_kv_append(cache, k, v, slots, dev_status=None, stream=None):
+    """Quantize the rows k, v ([T, kv_heads, head_dim] or [T, kv_heads * head_dim], fp32 or
+    bf16) into the cache's slots (int64 [T]; negative: skipped)."""
+    _cuda(slots, "slots", (torch.int64,), 1)
+    n = slots.shape[0]
+    if n > 1 and slots.stride(0) != 1:
+        raise ValueError("slots must be contiguous")
+    ldk, ldv = _kv_rows(cache, k, "k", n), _kv_rows(cache, v, "v", n, k.dtype)
+    st = lib().q8_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[k.dtype], slots.data_ptr(), n,
+                            _p(dev_status), _stream(stream))
+    _check(st, "q8_kv_append")
+
+
+def q8_kv_read(cache, slots, k=None, v=None, dtype=torch.float32, dev_status=None, stream=None):
+    """The values of the cache's slots: (k, v), each [T, kv_heads, head_dim] in `dtype`
+    (or in the given rows' own type); a negative slot gives zeros."""
+    _cuda(slots, "slots", (torch.int64,), 1)
+    n = slots.shape[0]
+    if n > 1 and slots.stride(0) != 1:
+        raise ValueError("slots must be contiguous")
+    shape = (n, cache.kv_heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=cache.device)
+    ldk, ldv = _kv_rows(cache, k, "k", n), _kv_rows(cache, v, "v", n, k.dtype)
+    st = lib().q8_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[k.dtype],
+                          _p(dev_status), _stream(stream))
+    _check(st, "q8_kv_read")
+    return k, v
+
+
+def q8_attn_decode_workspace_size(batch: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().q8_attn_decode_workspace_size(batch, q_heads, kv_heads, head_dim))
+
+
+def q8_attn_decode(q, cache, table, lens, scale=None, softcap=0.0, window=0, out=None, lse=None, ws=None, dev_status=None,
+                   stream=None):
+    """Attention of one new token per sequence over the cache: q bf16 [B, q_heads, head_dim],
+    table int32 [B, pages of a sequence], lens int32 [B] (the new token included).
+    Returns (out bf16 [B, q_heads, head_dim], lse fp32 [B, q_heads]).  scale defaults to
+    1 / sqrt(head_dim); softcap 0: none; window 0: all tokens."""
+    _cuda(q, "q", (torch.bfloat16,), 3)
+    _cuda(table, "table", (torch.int32,), 2)
+    _cuda(lens, "lens", (torch.int32,), 1)
+    B, H, D = q.shape
+    if D != cache.head_dim or table.shape[0] != B or lens.shape[0] != B:
+        raise ValueError("q is [B, q_heads, head_dim] with the cache's head_dim, table [B, pages], lens [B]")
+    sq = q.stride()
+    if (sq[2] != 1 or (H > 1 and sq[1] != D)) and B > 0:
+        raise ValueError("each row of q must be contiguous")
+    if not table.is_contiguous() or not lens.is_contiguous():
+        raise ValueError("table and lens must be contiguous")
+    if out is None:
+        out = torch.empty((B, H, D), dtype=torch.bfloat16, device=q.device)
+    elif _cuda(out, "out", (torch.bfloat16,), 3).shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape")
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    elif tuple(_cuda(lse, "lse", (torch.float32,), 2).shape) != (B, H) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous, [B, q_heads]")
+    if ws is None:
+        ws = workspace(q8_attn_decode_workspace_size(B, H, cache.kv_heads, D), q.device)
+    st = lib().q8_attn_decode(cache._ref, q.data_ptr(), sq[0] if B > 1 else H * D, H, table.data_ptr(), table.shape[1],
+                              lens.data_ptr(), B, D ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
+                              lse.data_ptr(), _p(ws), 0 if ws is None else ws.numel(), _p(dev_status), _stream(stream))
+    _check(st, "q8_attn_decode")
+    return out, lse

@@ -61,6 +61,7 @@ typedef enum q8_status {
 #define Q8_DEV_NONFINITE 0x1u /* quantizer: a block held NaN/Inf; stored as zero codes, zero scale */
 #define Q8_DEV_SCALE_OVF 0x2u /* quantizer: amax/127 overflowed binary16; block stored as zeros */
 #define Q8_DEV_TIMEOUT   0x4u /* a bounded wait gave up; outputs of that call are not valid */
+#define Q8_DEV_BAD_INDEX 0x8u /* a slot, page number or length outside the cache; what it named was left out */
 
 #define Q8_BLOCK 32          /* weights per block along K */
 #define Q8_SKINNY_MAX_M 32   /* largest M for q8_gemv / q8_gemm_skinny / q8_linear_batch */
@@ -443,6 +444,92 @@ q8_status q8_gemm_skinny_noalloc(const int8_t *q, const uint16_t *s, int64_t N, 
                                  const uint16_t *x, int64_t ldx, int32_t M,
                                  float *y, int64_t ldy,
                                  uint32_t *dev_status, q8_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The rest of a decode step: a Q8_0 key-value cache and its attention, a
+ * mixture of Q8_0 experts, and the draw of the next token.  The source pages
+ * put these around the matmul ("Frigg" README: the model card, the int8 KV
+ * cache flag, the sampler; "aubier" README: split-K attention over 256 to
+ * 262,144 keys, expert stores) and give no code for them.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of rows the calls below take or return. */
+#define Q8_DTYPE_F32 0
+#define Q8_DTYPE_BF16 1
+
+/*
+ * A paged key-value cache in Q8_0 blocks (along the head dimension).  A page
+ * holds page_size consecutive tokens of one sequence for every key head:
+ *   codes   int8     [pages][kv_heads][page_size][head_dim]
+ *   scales  binary16 [pages][kv_heads][page_size][head_dim / 32]
+ * for keys (kq, ks) and values (vq, vs); 16-byte aligned device memory of
+ * the caller.  page_size: a power of two, 16 .. 1024; head_dim: 64, 128 or
+ * 256; kv_heads >= 1; pages >= 1.  Slot i of the cache is token
+ * i % page_size of page i / page_size.
+ */
+typedef struct q8_kv_cache {
+    int8_t *kq;
+    uint16_t *ks;
+    int8_t *vq;
+    uint16_t *vs;
+    int32_t pages, page_size, kv_heads, head_dim;
+} q8_kv_cache;
+
+/*
+ * q8_kv_append -- quantize T tokens' keys and values into their slots.
+ *   k, v  : [T][ldk], [T][ldv] rows of kv_heads * head_dim values of `dtype`
+ *           (Q8_DTYPE_F32 or Q8_DTYPE_BF16), 16-byte aligned; ldk, ldv in
+ *           elements, >= kv_heads * head_dim, a multiple of 4 (fp32) or 8
+ *           (bf16), so a row may be a part of a wider matmul's output.
+ *   slots : int64 [T] (8-byte aligned).  A negative slot skips its token
+ *           (padding); one past the cache is skipped and sets
+ *           Q8_DEV_BAD_INDEX.  Slots that occur twice get one of the rows,
+ *           undefined which.
+ * Codes and scales are those of q8_quantize_rows (Q8_QUANT_EXACT) on the
+ * values, bit for bit, with the same flags.  T == 0 is a no-op.
+ */
+q8_status q8_kv_append(const q8_kv_cache *cache, const void *k, const void *v, int64_t ldk, int64_t ldv,
+                       int32_t dtype, const int64_t *slots, int64_t T, uint32_t *dev_status, q8_stream_t stream);
+
+/*
+ * q8_kv_read -- the values s * q of T slots, as fp32 (exact) or bf16 (one
+ * round to nearest even), in rows as q8_kv_append takes them.  A negative
+ * slot, or one past the cache (Q8_DEV_BAD_INDEX), gives a row of zeros.
+ */
+q8_status q8_kv_read(const q8_kv_cache *cache, const int64_t *slots, int64_t T, void *k, void *v, int64_t ldk,
+                     int64_t ldv, int32_t dtype, uint32_t *dev_status, q8_stream_t stream);
+
+/*
+ * q8_attn_decode -- attention of one new token per sequence over its cache:
+ *   s_t = scale * q . k_t             (softcap > 0: softcap * tanh(s_t / softcap))
+ *   out = sum_t softmax(s)_t v_t      over t in [max(0, len - window), len)
+ * (window 0: all len tokens).  Query head i reads key head
+ * i / (q_heads / kv_heads).
+ *   q     : bf16 [batch][ldq], q_heads * head_dim values a row, 16-byte
+ *           aligned, ldq a multiple of 8
+ *   table : int32 [batch][table_width]: the page of each page_size tokens of
+ *           a sequence; entries past its length are not read.  A page number
+ *           outside the cache leaves its tokens out and sets Q8_DEV_BAD_INDEX.
+ *   lens  : int32 [batch] tokens in the cache (the new one included); outside
+ *           0 .. table_width * page_size it is clamped and sets
+ *           Q8_DEV_BAD_INDEX.  Nothing past a length enters the result,
+ *           whatever the cache holds there.
+ *   out   : bf16 [batch][q_heads][head_dim], 16-byte aligned
+ *   lse   : float [batch][q_heads], log(sum_t exp(s_t)); may be NULL
+ * A sequence of no tokens gives out = 0 and lse = -inf.  Sums, the running
+ * maximum and lse are fp32; key codes enter exactly, weights and dequantised
+ * values are rounded to binary16 (2^-11 relative at most) before their product.
+ *   ws    : q8_attn_decode_workspace_size() bytes, 256-byte aligned, zeroed
+ *           once; the kernel leaves its counters zero.  Not for two calls
+ *           that may run at the same time.
+ * The work is split over the sequences' lengths as the device reads them, so
+ * a captured graph may be replayed with other lengths.
+ */
+q8_status q8_attn_decode(const q8_kv_cache *cache, const uint16_t *q, int64_t ldq, int32_t q_heads,
+                         const int32_t *table, int32_t table_width, const int32_t *lens, int32_t batch, float scale,
+                         float softcap, int32_t window, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
+                         uint32_t *dev_status, q8_stream_t stream);
+size_t q8_attn_decode_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim);
 
 /* Human-readable name of a status code (static string). */
 const char *q8_status_str(q8_status st);
