@@ -179,4 +179,19 @@ struct AttnArgs {
 size_t attn_workspace(int q_heads, int kv_heads, int head_dim);
 q8_status launch_attn(const q8_kv_cache &c, const AttnArgs &a, void *ws, uint32_t *dev_status, cudaStream_t stream);
 
+// ---- decode step: mixture of experts ---------------------------------------------
+struct MoeArgs {
+    const uint16_t *x;
+    const float *logits;
+    const int8_t *q13, *q2;
+    const uint16_t *s13, *s2;
+    float *y;
+    int32_t *ids;
+    float *weights;
+    int64_t ldx, ldl, ldy;
+    int32_t T, E, H, F, top_k, renorm;
+};
+size_t moe_workspace(int T, int F, int top_k);
+q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStream_t stream);
+
 }  // namespace q8

@@ -42,7 +42,7 @@ EXPORTS = ("q8_quantize_rows", "q8_gemv", "q8_gemm_skinny", "q8_linear_batch", "
            "q8_planar_to_gguf", "q8_quantize_rows_ex", "q8_selftest_wait_timeout",
            "q8_stream_read", "q8_stream_read_out_words", "q8_linear_chain", "q8_linear_chain_workspace_size",
            "q8_gemm_w8a8", "q8_gemm_w8a8_workspace_size", "q8_kv_append", "q8_kv_read", "q8_attn_decode",
-           "q8_attn_decode_workspace_size")
+           "q8_attn_decode_workspace_size", "q8_moe", "q8_moe_workspace_size")
 Q8_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -122,13 +122,16 @@ def lib():
         L.q8_attn_decode.argtypes = [P, P, I64, I32, P, I32, P, I32, ctypes.c_float, ctypes.c_float, I32, P, P, P, SZ, P, P]
         L.q8_attn_decode_workspace_size.argtypes = [I32, I32, I32, I32]
         L.q8_attn_decode_workspace_size.restype = SZ
+        L.q8_moe.argtypes = [P, I64, P, I64, I32, I32, I32, I32, P, P, P, P, I64, I64, P, I64, P, P, P, SZ, P, P]
+        L.q8_moe_workspace_size.argtypes = [I32, I32, I64, I64, I32]
+        L.q8_moe_workspace_size.restype = SZ
         L.q8_status_str.argtypes = [ctypes.c_int]
         L.q8_status_str.restype = ctypes.c_char_p
         L.q8_abi_version.restype = I32
         for name in ("q8_quantize_rows", "q8_quantize_rows_ex", "q8_gemv", "q8_gemm_skinny", "q8_linear_batch",
                      "q8_linear_batch_ex", "q8_linear_batch_chained", "q8_gguf_to_planar",
                      "q8_planar_to_gguf", "q8_gemm", "q8_gemm_ex", "q8_gemm_skinny_noalloc", "q8_linear_chain", "q8_gemm_w8a8",
-                     "q8_kv_append", "q8_kv_read", "q8_attn_decode"):
+                     "q8_kv_append", "q8_kv_read", "q8_attn_decode", "q8_moe"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -507,3 +510,51 @@ def q8_attn_decode(q, cache, table, lens, scale=None, softcap=0.0, window=0, out
                               lse.data_ptr(), _p(ws), 0 if ws is None else ws.numel(), _p(dev_status), _stream(stream))
     _check(st, "q8_attn_decode")
     return out, lse
+
+
+def q8_moe_workspace_size(T: int, E: int, H: int, F: int, top_k: int) -> int:
+    return int(lib().q8_moe_workspace_size(T, E, H, F, top_k))
+
+
+def q8_moe(x, logits, q13, s13, q2, s2, top_k, renorm=True, y=None, ids=None, weights=None, ws=None, dev_status=None,
+           stream=None):
+    """A mixture-of-experts layer for T <= 32 tokens: x bf16 [T, H], router logits fp32 [T, E],
+    experts' gate and up rows (q13 int8 [E, 2 F, H], s13) and down rows (q2 int8 [E, H, F], s2).
+    Returns (y fp32 [T, H], ids int32 [T, top_k], weights fp32 [T, top_k])."""
+    _cuda(x, "x", (torch.bfloat16,), 2)
+    _cuda(logits, "logits", (torch.float32,), 2)
+    _cuda(q13, "q13", (torch.int8,), 3)
+    _cuda(q2, "q2", (torch.int8,), 3)
+    _cuda(s13, "s13", _B16, 3)
+    _cuda(s2, "s2", _B16, 3)
+    T, H = x.shape
+    E, F = logits.shape[1], q2.shape[2]
+    if tuple(q13.shape) != (E, 2 * F, H) or tuple(q2.shape) != (E, H, F) or logits.shape[0] != T:
+        raise ValueError("x is [T, H], logits [T, E], q13 [E, 2 F, H] and q2 [E, H, F]")
+    if tuple(s13.shape) != (E, 2 * F, H // 32) or tuple(s2.shape) != (E, H, F // 32):
+        raise ValueError("s13 and s2 hold a scale per 32 codes")
+    if not (q13.is_contiguous() and s13.is_contiguous() and q2.is_contiguous() and s2.is_contiguous()):
+        raise ValueError("the experts' tensors must be contiguous")
+    if T > 0 and (x.stride(1) != 1 or logits.stride(1) != 1):
+        raise ValueError("x and logits must have unit inner stride")
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.float32, device=x.device)
+    elif tuple(_cuda(y, "y", (torch.float32,), 2).shape) != (T, H) or y.stride(1) != 1:
+        raise ValueError("y must be [T, H] with unit inner stride")
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+    elif tuple(_cuda(ids, "ids", (torch.int32,), 2).shape) != (T, top_k) or not ids.is_contiguous():
+        raise ValueError("ids must be contiguous, [T, top_k]")
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+    elif tuple(_cuda(weights, "weights", (torch.float32,), 2).shape) != (T, top_k) or not weights.is_contiguous():
+        raise ValueError("weights must be contiguous, [T, top_k]")
+    if ws is None:
+        ws = workspace(q8_moe_workspace_size(T, E, H, F, top_k), x.device)
+    one = T <= 1
+    st = lib().q8_moe(x.data_ptr(), H if one else x.stride(0), logits.data_ptr(), E if one else logits.stride(0), T, E, top_k,
+                      int(renorm), q13.data_ptr(), s13.data_ptr(), q2.data_ptr(), s2.data_ptr(), H, F, y.data_ptr(),
+                      H if one else y.stride(0), ids.data_ptr(), weights.data_ptr(), _p(ws), 0 if ws is None else ws.numel(),
+                      _p(dev_status), _stream(stream))
+    _check(st, "q8_moe")
+    return y, ids, weights

@@ -531,6 +531,39 @@ q8_status q8_attn_decode(const q8_kv_cache *cache, const uint16_t *q, int64_t ld
                          uint32_t *dev_status, q8_stream_t stream);
 size_t q8_attn_decode_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim);
 
+/*
+ * q8_moe -- a mixture-of-experts layer with Q8_0 experts for T <= 32 tokens:
+ *   each token takes the top_k experts of largest logit (ties: the lower
+ *   index); w_j = exp(l_j - l_max) / z, z summed over the chosen experts
+ *   (renorm != 0) or over all (renorm == 0);
+ *   y_t = sum_j w_j * W2_e (silu(W1_e x_t) * (W3_e x_t)),  silu(a) = a / (1 + e^-a)
+ * with the experts' weights read once for all tokens that chose them.
+ *   x       : bf16 [T][ldx], ldx >= H and a multiple of 8, 16-byte aligned
+ *   logits  : float [T][ldl], ldl >= E (the router's product, for instance
+ *             q8_gemm_skinny's y).  An expert with logit -inf is never
+ *             chosen, nor one with NaN (which sets Q8_DEV_NONFINITE); a token
+ *             with fewer than top_k others takes those, and one with none
+ *             gets y = 0.
+ *   q13,s13 : Q8_0 [E][2 F][H]: an expert's F gate rows (W1), then its F up
+ *             rows (W3);  q2, s2: Q8_0 [E][H][F] (W2); 16-byte aligned
+ *   y       : float [T][ldy], ldy >= H
+ *   ids     : int32 [T][top_k] the chosen experts, -1 for none; may be NULL
+ *   weights : float [T][top_k] their w_j; may be NULL
+ *   ws      : q8_moe_workspace_size() bytes, 256-byte aligned, zeroed once;
+ *             not for two calls that may run at the same time
+ * H and F multiples of 32; 1 <= E <= 512; 1 <= top_k <= min(16, E).
+ * Products are exact and summed in fp32; hidden units are kept to 22 bits.
+ * The second kernel is a programmatic dependent of the first; work before
+ * the call in the stream is complete before either reads anything.
+ */
+#define Q8_MOE_MAX_EXPERTS 512
+#define Q8_MOE_MAX_TOP_K 16
+q8_status q8_moe(const uint16_t *x, int64_t ldx, const float *logits, int64_t ldl, int32_t T, int32_t E, int32_t top_k,
+                 int32_t renorm, const int8_t *q13, const uint16_t *s13, const int8_t *q2, const uint16_t *s2, int64_t H,
+                 int64_t F, float *y, int64_t ldy, int32_t *ids, float *weights, void *ws, size_t ws_bytes,
+                 uint32_t *dev_status, q8_stream_t stream);
+size_t q8_moe_workspace_size(int32_t T, int32_t E, int64_t H, int64_t F, int32_t top_k);
+
 /* Human-readable name of a status code (static string). */
 const char *q8_status_str(q8_status st);
 

@@ -24,3 +24,43 @@ def attention(q, k, v, scale, softcap=0.0, window=0):
     e = np.exp(s - m)
     p = e / e.sum()
     return p @ v, m + np.log(e.sum()), p @ np.abs(v), float((np.abs(k) @ np.abs(q)).max() * abs(scale))
+
+
+def route(logits, top_k, renorm):
+    """One token's experts: (ids [top_k] with -1 for none, weights [top_k])."""
+    l = np.where(np.isnan(logits), -np.inf, logits.astype(np.float64))
+    order = np.argsort(-l, kind="stable")[:top_k]
+    ids = np.where(l[order] > -np.inf, order, -1)
+    if ids[0] < 0:
+        return ids, np.zeros(top_k)
+    with np.errstate(invalid="ignore"):
+        e = np.where(l == l.max(), 1.0, np.exp(l - l.max()))
+    w = np.where(ids >= 0, e[order], 0.0)
+    return ids, w / (w.sum() if renorm else e.sum())
+
+
+def moe(x, logits, w13, w2, top_k, renorm):
+    """Returns (y[T, H], bound[T, H], ids, weights).  The bound is what fp32 sums of K / 32
+    blocks may be off (each block's product exact up to its own 32-term sum), carried
+    through SwiGLU (silu's slope is below 1.1) and the down product, with 2^-20 of each
+    hidden unit (exponential, division, product) and 2^-22 of its block's largest (how it is kept)."""
+    T, H = x.shape
+    F = w2.shape[2]
+    y, tol = np.zeros((T, H)), np.zeros((T, H))
+    ids, ws = np.zeros((T, top_k), dtype=int), np.zeros((T, top_k))
+    c1, c2 = (H / 32 + 40) * 2.0 ** -24, (F / 32 + 40) * 2.0 ** -24
+    for t in range(T):
+        ids[t], ws[t] = route(logits[t], top_k, renorm)
+        for e, w in zip(ids[t], ws[t]):
+            if e < 0:
+                continue
+            z, b = w13[e] @ x[t], np.abs(w13[e]) @ np.abs(x[t])
+            a, u = z[:F], z[F:]
+            with np.errstate(over="ignore"):
+                s = a / (1 + np.exp(-a))
+            act = s * u
+            top = np.repeat(np.abs(act).reshape(-1, 32).max(1), 32)
+            da = 1.1 * c1 * b[:F] * np.abs(u) + np.abs(s) * c1 * b[F:] + 2.0 ** -20 * np.abs(act) + 2.0 ** -22 * top
+            y[t] += w * (w2[e] @ act)
+            tol[t] += w * (np.abs(w2[e]) @ (da + c2 * np.abs(act)) + 2.0 ** -20 * np.abs(w2[e] @ act))
+    return y, tol, ids, ws

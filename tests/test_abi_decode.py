@@ -90,3 +90,30 @@ def test_attn_validation(L):
     assert L.q8_attn_decode_workspace_size(3, 7, 2, 128) == 0
     assert L.q8_attn_decode_workspace_size(3, 8, 2, 96) == 0
     assert L.q8_attn_decode_workspace_size(0, 8, 2, 128) == 0
+
+
+def moe(L, x=A, ldx=64, logits=A, ldl=8, T=3, E=8, k=2, q13=A, s13=A, q2=A, s2=A, H=64, F=96, y=A, ldy=64, ids=A, w=A, ws=A,
+        wsb=1 << 40, status=None):
+    return L.q8_moe(x, ldx, logits, ldl, T, E, k, 1, q13, s13, q2, s2, H, F, y, ldy, ids, w, ws, wsb, status, None)
+
+
+def test_moe_validation(L):
+    from block_quantized_int8_gb300 import q8
+    for kw in (dict(T=-1), dict(T=33), dict(E=0), dict(E=513), dict(H=48), dict(F=0), dict(H=0), dict(F=33), dict(ldx=63),
+               dict(ldl=7), dict(ldy=63), dict(H=1 << 21)):
+        assert moe(L, **kw) == q8.Q8_ERR_SHAPE, kw
+    for kw in (dict(k=0), dict(k=9), dict(k=17, E=32, ldl=32)):
+        assert moe(L, **kw) == q8.Q8_ERR_ARG, kw
+    for a in ("x", "logits", "q13", "s13", "q2", "s2", "y"):
+        assert moe(L, **{a: None}) == q8.Q8_ERR_ARG, a
+    for a, off in (("x", 8), ("logits", 2), ("q13", 8), ("s13", 2), ("q2", 4), ("s2", 8), ("y", 2), ("ids", 1), ("w", 2),
+                   ("ws", 16), ("status", 1)):
+        assert moe(L, **{a: A + off}) == q8.Q8_ERR_ALIGN, a
+    assert moe(L, ldx=68) == q8.Q8_ERR_ALIGN
+    need = L.q8_moe_workspace_size(3, 8, 64, 96, 2)
+    assert need > 0
+    assert moe(L, ws=None) == q8.Q8_ERR_WORKSPACE
+    assert moe(L, wsb=need - 1) == q8.Q8_ERR_WORKSPACE
+    assert moe(L, T=0) == q8.Q8_OK
+    assert L.q8_moe_workspace_size(33, 8, 64, 96, 2) == 0
+    assert L.q8_moe_workspace_size(3, 8, 64, 96, 9) == 0
