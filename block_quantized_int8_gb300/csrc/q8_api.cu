@@ -508,4 +508,23 @@ q8_status q8_moe(const uint16_t *x, int64_t ldx, const float *logits, int64_t ld
     return launch_moe(a, ws, dev_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
+q8_status q8_sample(const void *logits, int32_t dtype, int64_t ld, int32_t rows, int64_t V, const float *temperature,
+                    const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
+                    float *logprob, int32_t *kept, uint32_t *dev_status, q8_stream_t stream) {
+    if (dtype != Q8_DTYPE_F32 && dtype != Q8_DTYPE_BF16) return Q8_ERR_ARG;
+    if (rows < 0 || rows > (1 << 24) || V < 1 || V > Q8_SAMPLE_MAX_V || ld < V) return Q8_ERR_SHAPE;
+    if (rows == 0) return Q8_OK;
+    if (!logits || !u || !token) return Q8_ERR_ARG;
+    if (!aligned(logits, dtype == Q8_DTYPE_F32 ? 4 : 2) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+        !aligned(min_p, 4) || !aligned(u, 4) || !aligned(token, 4) || !aligned(logprob, 4) || !aligned(kept, 4) ||
+        !aligned(dev_status, 4))
+        return Q8_ERR_ALIGN;
+    const DeviceInfo *di;
+    const q8_status st = check_arch(&di);
+    if (st != Q8_OK) return st;
+    SampleArgs a = {logits, temperature, top_p, min_p, u, top_k, token, kept, logprob, ld, rows, static_cast<int32_t>(V),
+                    dtype == Q8_DTYPE_BF16 ? 1 : 0};
+    return launch_sample(a, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

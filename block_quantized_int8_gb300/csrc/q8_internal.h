@@ -194,4 +194,16 @@ struct MoeArgs {
 size_t moe_workspace(int T, int F, int top_k);
 q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStream_t stream);
 
+// ---- decode step: the next token ---------------------------------------------------
+struct SampleArgs {
+    const void *logits;
+    const float *temperature, *top_p, *min_p, *u;
+    const int32_t *top_k;
+    int32_t *token, *kept;
+    float *logprob;
+    int64_t ld;
+    int32_t rows, V, bf16;
+};
+q8_status launch_sample(const SampleArgs &a, uint32_t *dev_status, cudaStream_t stream);
+
 }  // namespace q8

@@ -42,7 +42,8 @@ EXPORTS = ("q8_quantize_rows", "q8_gemv", "q8_gemm_skinny", "q8_linear_batch", "
            "q8_planar_to_gguf", "q8_quantize_rows_ex", "q8_selftest_wait_timeout",
            "q8_stream_read", "q8_stream_read_out_words", "q8_linear_chain", "q8_linear_chain_workspace_size",
            "q8_gemm_w8a8", "q8_gemm_w8a8_workspace_size", "q8_kv_append", "q8_kv_read", "q8_attn_decode",
-           "q8_attn_decode_workspace_size", "q8_moe", "q8_moe_workspace_size")
+           "q8_attn_decode_workspace_size", "q8_moe", "q8_moe_workspace_size",
+           "q8_sample")
 Q8_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -125,13 +126,15 @@ def lib():
         L.q8_moe.argtypes = [P, I64, P, I64, I32, I32, I32, I32, P, P, P, P, I64, I64, P, I64, P, P, P, SZ, P, P]
         L.q8_moe_workspace_size.argtypes = [I32, I32, I64, I64, I32]
         L.q8_moe_workspace_size.restype = SZ
+        L.q8_sample.argtypes = [P, I32, I64, I32, I64, P, P, P, P, P, P, P, P, P, P]
         L.q8_status_str.argtypes = [ctypes.c_int]
         L.q8_status_str.restype = ctypes.c_char_p
         L.q8_abi_version.restype = I32
         for name in ("q8_quantize_rows", "q8_quantize_rows_ex", "q8_gemv", "q8_gemm_skinny", "q8_linear_batch",
                      "q8_linear_batch_ex", "q8_linear_batch_chained", "q8_gguf_to_planar",
                      "q8_planar_to_gguf", "q8_gemm", "q8_gemm_ex", "q8_gemm_skinny_noalloc", "q8_linear_chain", "q8_gemm_w8a8",
-                     "q8_kv_append", "q8_kv_read", "q8_attn_decode", "q8_moe"):
+                     "q8_kv_append", "q8_kv_read", "q8_attn_decode", "q8_moe",
+                     "q8_sample"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -558,3 +561,39 @@ def q8_moe(x, logits, q13, s13, q2, s2, top_k, renorm=True, y=None, ids=None, we
                       _p(dev_status), _stream(stream))
     _check(st, "q8_moe")
     return y, ids, weights
+
+
+def _per_row(t, name, n, dtype):
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must hold one value per row, contiguous")
+    return t.data_ptr()
+
+
+def q8_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, token=None, logprob=None, kept=None,
+              dev_status=None, stream=None):
+    """Draw one word per row of logits [rows, V] (fp32 or bf16) from uniform numbers u fp32
+    [rows] in [0, 1).  temperature, top_p, min_p fp32 [rows] and top_k int32 [rows] may be
+    None.  Returns (token int32, logprob fp32, kept int32), each [rows]."""
+    if not logits.is_cuda or logits.dtype not in _ROW_DTYPES:
+        raise TypeError("logits must be a float32 or bfloat16 CUDA tensor")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [rows, V] with unit inner stride")
+    n, V = logits.shape
+    args = [_per_row(temperature, "temperature", n, torch.float32), _per_row(top_k, "top_k", n, torch.int32),
+            _per_row(top_p, "top_p", n, torch.float32), _per_row(min_p, "min_p", n, torch.float32),
+            _per_row(u, "u", n, torch.float32)]
+    if token is None:
+        token = torch.empty(n, dtype=torch.int32, device=logits.device)
+    if logprob is None:
+        logprob = torch.empty(n, dtype=torch.float32, device=logits.device)
+    if kept is None:
+        kept = torch.empty(n, dtype=torch.int32, device=logits.device)
+    st = lib().q8_sample(logits.data_ptr(), _ROW_DTYPES[logits.dtype], logits.stride(0) if n > 1 else V, n, V, *args,
+                         _per_row(token, "token", n, torch.int32), _per_row(logprob, "logprob", n, torch.float32),
+                         _per_row(kept, "kept", n, torch.int32), _p(dev_status), _stream(stream))
+    _check(st, "q8_sample")
+    return token, logprob, kept

@@ -564,6 +564,34 @@ q8_status q8_moe(const uint16_t *x, int64_t ldx, const float *logits, int64_t ld
                  uint32_t *dev_status, q8_stream_t stream);
 size_t q8_moe_workspace_size(int32_t T, int32_t E, int64_t H, int64_t F, int32_t top_k);
 
+/*
+ * q8_sample -- draw one word per row of logits from a given uniform number.
+ *   With m a row's largest logit: e_i = exp((l_i - m) / temperature) (1 where
+ *   l_i = m) and the mass w_i = floor(e_i * 2^40), a whole number, so that
+ *   every sum is exact and the answer depends on no order of adding.  Words
+ *   are ranked by logit, descending; equal logits by index, ascending.
+ *     top-k  keeps the first top_k (<= 0 or > V: all);
+ *     top-p  keeps, of those, the words before which less than
+ *            ceil(top_p * their sum) lies (top_p >= 1: all; always at least one);
+ *     min-p  keeps, of those, the words with e_i >= min_p;
+ *   with W the sum of what is left and r = floor(u * W) (binary64, u binary32),
+ *   the token is the first word in index order whose running sum passes r.
+ *   temperature <= 0 takes the first of the largest logits.
+ *   logits : `dtype` [rows][ld], ld >= V (fp32 4-byte, bf16 2-byte aligned);
+ *            -inf forbids a word; NaN too, and sets Q8_DEV_NONFINITE
+ *   temperature, top_k, top_p, min_p : one value per row; each may be NULL
+ *            (1, all, 1, 0)
+ *   u      : float [rows] in [0, 1)
+ *   token  : int32 [rows]; -1 where no word is left
+ *   logprob: float [rows], log(w_token / W), -inf where there is none; may be NULL
+ *   kept   : int32 [rows], how many words of mass > 0 were left; may be NULL
+ * 1 <= V <= 2^20.  No workspace.
+ */
+#define Q8_SAMPLE_MAX_V (1 << 20)
+q8_status q8_sample(const void *logits, int32_t dtype, int64_t ld, int32_t rows, int64_t V, const float *temperature,
+                    const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
+                    float *logprob, int32_t *kept, uint32_t *dev_status, q8_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char *q8_status_str(q8_status st);
 

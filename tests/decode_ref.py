@@ -64,3 +64,45 @@ def moe(x, logits, w13, w2, top_k, renorm):
             y[t] += w * (w2[e] @ act)
             tol[t] += w * (np.abs(w2[e]) @ (da + c2 * np.abs(act)) + 2.0 ** -20 * np.abs(w2[e] @ act))
     return y, tol, ids, ws
+
+
+def sample(logits, T, k, p, min_p, u):
+    """One row, in binary64.  Returns (kept range, probability by word, total slack): the
+    words kept are certain up to places where binary32 exponentials (2^-21 relative) could
+    decide otherwise; the slack is the probability that hangs on those."""
+    eps = 2.0 ** -20
+    l = np.where(np.isnan(logits), -np.inf, logits.astype(np.float64))
+    V = l.shape[0]
+    if not T > 0:
+        T, k = 1.0, 1
+    if k <= 0 or k > V:
+        k = V
+    m = l.max()
+    if m == -np.inf:
+        return (0, 0), np.zeros(V), 0.0
+    with np.errstate(invalid="ignore"):
+        e = np.where(l == m, 1.0, np.exp(np.where(l == m, 0.0, (l - m) / T)))
+    e[l == -np.inf] = 0.0
+    e = np.where(e >= 2.0 ** -40, e, 0.0)
+    order = np.argsort(-l, kind="stable")
+    r = e[order]
+    r[k:] = 0.0
+    total = r.sum()
+    before = np.cumsum(r) - r
+    sure = r > 2.0 ** -40 * (1 + eps)
+    may = r > 0
+    if p < 1.0:
+        cut = max(p * total, 2.0 ** -40)
+        sure &= before < cut - eps * total
+        may &= before < cut + eps * total
+        sure[0] = may[0]
+    sure &= r >= min_p * (1 + eps)
+    may &= r >= min_p * (1 - eps)
+    if min_p <= 1.0:
+        sure[0] = may[0] = r[0] > 0   # the largest has e = 1 exactly
+    prob = np.zeros(V)
+    both = np.where(may, r, 0.0)
+    if both.sum() > 0:
+        prob[order] = both / both.sum()
+    slack = eps + (np.where(may & ~sure, r, 0.0).sum() / both.sum() if both.sum() > 0 else 0.0)
+    return (int(sure.sum()), int(may.sum())), prob, slack

@@ -117,3 +117,20 @@ def test_moe_validation(L):
     assert moe(L, T=0) == q8.Q8_OK
     assert L.q8_moe_workspace_size(33, 8, 64, 96, 2) == 0
     assert L.q8_moe_workspace_size(3, 8, 64, 96, 9) == 0
+
+
+def sample(L, logits=A, dtype=0, ld=100, rows=2, V=100, T=A, k=A, p=A, m=A, u=A, tok=A, lp=A, kept=A, status=None):
+    return L.q8_sample(logits, dtype, ld, rows, V, T, k, p, m, u, tok, lp, kept, status, None)
+
+
+def test_sample_validation(L):
+    from block_quantized_int8_gb300 import q8
+    assert sample(L, dtype=2) == q8.Q8_ERR_ARG
+    for kw in (dict(V=0), dict(V=(1 << 20) + 1, ld=1 << 21), dict(ld=99), dict(rows=-1)):
+        assert sample(L, **kw) == q8.Q8_ERR_SHAPE, kw
+    for a in ("logits", "u", "tok"):
+        assert sample(L, **{a: None}) == q8.Q8_ERR_ARG, a
+    for a in ("logits", "T", "k", "p", "m", "u", "tok", "lp", "kept", "status"):
+        assert sample(L, **{a: A + 2}) == q8.Q8_ERR_ALIGN, a
+    assert sample(L, logits=A + 1, dtype=1) == q8.Q8_ERR_ALIGN
+    assert sample(L, rows=0) == q8.Q8_OK
