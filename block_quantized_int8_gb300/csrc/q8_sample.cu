@@ -12,22 +12,36 @@
 // sum passes r.  Words with w_i = 0 (below 2^-40 of the likeliest) cannot be
 // drawn and are not counted.
 //
-// No sort: the words kept are a prefix of the ranking, so what is needed is
-// its last word -- the k-th for top-k, the one that reaches the mass for top-p.
-// The 32-bit order key of the logit is searched digit by digit (11, 11, 10
-// bits): a histogram of counts and masses per digit, a scan to the bin that
-// holds the place looked for, then only words of that bin.  Equal logits at
-// the place are kept in index order, counted by division (equal logits have
-// equal masses).
+// The row is not sorted: the words kept are a prefix of the ranking, and what
+// is needed is where it ends.
+//  - top-k up to 128: the row is cut into 256 groups; at least k words are no
+//    smaller than the k-th largest group maximum, and few more are.  The
+//    maxima come with the row's largest logit, so one pass gathers those words
+//    and one CTA sorts them and draws; only they need their exponential.
+//  - larger top-k: a histogram of counts over 2048 equal steps of the distance
+//    from the largest logit (down to exp(-28) or the row's smallest logit) finds
+//    the step that holds the k-th word.
+//  - top-p without a small top-k: every word's e replaces its logit in shared
+//    memory and the masses are summed.  Words below (1 - p) / V of that sum lie
+//    past the end together, so only the others enter a histogram of masses by
+//    e's leading bits (exponent and 5 fraction bits), which finds the bin that
+//    holds the end.
+// If the words up to the end of that step or bin are at most 2048, they are
+// gathered and drawn from by one CTA.  Otherwise the words of that step alone are
+// gathered and sorted to find the last one kept (their logits read again, since
+// different logits may have equal e), and the draw is a pass over the row in
+// index order.  A step that holds more than 2048 words (many equal logits) is
+// searched digit by digit in the logits' 32-bit order keys.  Equal logits at the
+// end of the prefix are kept in index order.
 //
-// A row belongs to a cluster of up to 8 CTAs; each keeps its slice of the row
+// A row belongs to a cluster of up to 16 CTAs; each keeps its slice of the row
 // in shared memory, so the logits are read from memory once.  Bound: by
-// latency for few rows (a handful of passes over shared memory, each with
-// cluster barriers), by the passes' instructions for many.
+// latency for few rows (passes over shared memory with cluster barriers, about
+// 1000 cycles each, between them), by the passes' instructions for many.
 #include <cooperative_groups.h>
-#include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "q8_dev.cuh"
 #include "q8_internal.h"
@@ -38,11 +52,16 @@ namespace q8 {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
-constexpr float kOne = 1099511627776.0f;  // 2^40
+constexpr int kList = 2048;        // words one CTA sorts
+constexpr int kPer = kList / kThreads;
+constexpr int kMaxCluster = 16;
+constexpr int kGroups = 256;       // of a row, for the bound on its k-th logit
+constexpr int kFastK = 128;
+constexpr int kCopies = 4;         // bulk copies of a slice
+constexpr float kUnit = 1.0f / 1099511627776.0f;  // 2^-40
 
 struct SampleParams {
     const void *logits;
@@ -52,24 +71,31 @@ struct SampleParams {
     float *logprob;
     uint32_t *status;
     int64_t ld;
-    int32_t V, slice, bf16, resident;
+    int32_t V, slice;
 };
 
-struct Shared {
-    unsigned long long mass[kBins];
+struct alignas(16) Shared {
+    union {
+        struct {
+            uint32_t mass_lo[kBins], mass_hi[kBins];
+        };
+        unsigned long long list[kList];  // (key, index), in CTA 0; not while a histogram is in use
+    };
     uint32_t count[kBins];
-    unsigned long long sub_mass[kMaxCluster];  // per CTA, written by all of them
+    alignas(16) float groups[kGroups];         // of all CTAs, written by each
+    unsigned long long sub_mass[kMaxCluster];  // per CTA, written by each
     uint32_t sub_count[kMaxCluster];
-    float maxima[kMaxCluster];
+    float minima[kMaxCluster];
     unsigned long long warp_mass[kWarps];
     uint32_t warp_count[kWarps];
-    float warp_max[kWarps];
-    // what a search found, written by the CTA that found it
-    uint32_t digit;
-    uint32_t before_count;
-    unsigned long long before_mass;
-    uint32_t in_count;
-    unsigned long long in_mass;
+    float warp_min[kWarps];
+    float bound;
+    // what a search found, in the CTA that found it
+    uint32_t digit, before_count, in_count;
+    unsigned long long before_mass, in_mass;
+    uint32_t last, ties, ranked;
+    uint32_t listed;  // words in the list of CTA 0
+    uint64_t bars[kCopies];
 };
 
 // Ascending order of this key is descending order of the value (-0 = +0).
@@ -77,289 +103,782 @@ __device__ __forceinline__ uint32_t rank_key(float v) {
     const uint32_t b = __float_as_uint(v + 0.0f);
     return (b & 0x80000000u) ? b : ~(b | 0x80000000u);
 }
+__device__ __forceinline__ float unkey(uint32_t key) { return __uint_as_float((key & 0x80000000u) ? key : ~key & 0x7FFFFFFFu); }
 
 struct Row {
     float top, temp;
-    __device__ __forceinline__ float weight(float l) const { return l == top ? 1.0f : expf(__fdiv_rn(l - top, temp)); }
-    // e below 2^-40 has no mass: nothing to compute below exp(-28)
-    __device__ __forceinline__ unsigned long long mass(float l, float &e) const {
-        e = 0.f;
-        if (l == -INFINITY || l - top < -28.0f * temp) return 0ull;
-        e = weight(l);
-        return static_cast<unsigned long long>(e * kOne);
+    __device__ __forceinline__ float weight(float l) const {
+        // a division by 1 is left out: the quotient is the same
+        const float d = l - top, q = temp == 1.0f ? d : __fdiv_rn(d, temp);
+        return l == top ? 1.0f : (l == -INFINITY ? 0.0f : expf(q));
     }
 };
-
-__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// floor(e 2^40) for 0 <= e <= 1 from e's own bits: 64-bit conversions are slow here (the pass
+// over 16384 words took 20,000 cycles with two of them a word)
+__device__ __forceinline__ unsigned long long mass_of(float e) {
+    const uint32_t b = __float_as_uint(e), m = (b & 0x7FFFFFu) | 0x800000u;
+    const int shift = static_cast<int>(b >> 23) - 110;  // e = m 2^(exponent - 150)
+    if (shift >= 0) return static_cast<unsigned long long>(m) << shift;
+    return m >> min(-shift, 31);
 }
-__device__ __forceinline__ uint32_t warp_sum(uint32_t v) { return __reduce_add_sync(0xffffffffu, v); }
 
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ SampleParams p) {
-    extern __shared__ __align__(16) uint8_t smem[];
+// Ascending sort of n words (a power of two, 128 .. kList): four neighbours a
+// thread, exchanged in registers, by shuffles within a warp and through shared
+// memory across warps.
+__device__ void sort_list(unsigned long long *v, int n) {
+    const int tid = threadIdx.x;
+    const bool mine = tid * kPer < n;
+    unsigned long long x[kPer];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) x[j] = mine ? v[tid * kPer + j] : 0ull;
+    for (int size = 2; size <= n; size <<= 1) {
+        for (int step = size >> 1; step > 0; step >>= 1) {
+            if (step >= 32 * kPer) {
+                __syncthreads();
+                if (mine)
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) v[tid * kPer + j] = x[j];
+                __syncthreads();
+            }
+            if (mine) {
+                unsigned long long y[kPer];
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    if (step >= 32 * kPer)
+                        y[j] = v[(tid * kPer + j) ^ step];
+                    else if (step >= kPer)
+                        y[j] = __shfl_xor_sync(0xffffffffu, x[j], step / kPer);
+                    else
+                        y[j] = step == 1 ? x[j ^ 1] : x[j ^ 2];
+                }
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int i = tid * kPer + j;
+                    const bool small = ((i & step) == 0) == ((i & size) == 0);  // this place takes the smaller
+                    x[j] = (small == (x[j] < y[j])) ? x[j] : y[j];
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (mine)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[tid * kPer + j] = x[j];
+    __syncthreads();
+}
+
+// Exclusive running sums of m and c over the threads of the CTA, and the totals.
+__device__ void scan_cta(Shared &s, unsigned long long m, uint32_t c, unsigned long long &m_before, uint32_t &c_before,
+                         unsigned long long &m_all, uint32_t &c_all) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned long long mr = m;
+    uint32_t cr = c;
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long mv = __shfl_up_sync(0xffffffffu, mr, o);
+        const uint32_t cv = __shfl_up_sync(0xffffffffu, cr, o);
+        if (lane >= o) mr += mv, cr += cv;
+    }
+    __syncthreads();
+    if (lane == 31) s.warp_mass[warp] = mr, s.warp_count[warp] = cr;
+    __syncthreads();
+    m_all = 0, c_all = 0;
+    unsigned long long mb = 0;
+    uint32_t cb = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == warp) mb = m_all, cb = c_all;
+        m_all += s.warp_mass[w];
+        c_all += s.warp_count[w];
+    }
+    m_before = mr - m + mb, c_before = cr - c + cb;
+}
+
+// log(w / all): through 1 - (all - w) / all where the word has most of the mass
+__device__ __forceinline__ float log_share(unsigned long long w, unsigned long long all) {
+    return 2 * w > all ? log1pf(-__fdiv_rn(static_cast<float>(all - w), static_cast<float>(all)))
+                       : logf(__fdiv_rn(static_cast<float>(w), static_cast<float>(all)));
+}
+// The mass that is passed by the token drawn with u.
+__device__ __forceinline__ unsigned long long place_of(float u, unsigned long long all) {
+    const double x = floor(static_cast<double>(u) * static_cast<double>(all));
+    const unsigned long long r = x > 0.0 ? static_cast<unsigned long long>(x) : 0ull;
+    return r > all - 1 ? all - 1 : r;
+}
+// The mass that top-p asks for.
+__device__ __forceinline__ unsigned long long mass_wanted(float top_p, unsigned long long total) {
+    const double cut = ceil(static_cast<double>(top_p) * static_cast<double>(total));
+    return cut < 1.0 ? 1ull : static_cast<unsigned long long>(cut);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
-    float *const vals = reinterpret_cast<float *>(smem + sizeof(Shared));
+    float *const buf = reinterpret_cast<float *>(smem + sizeof(Shared));
+    using Elem = typename std::conditional<BF16, uint16_t, float>::type;
+    constexpr int kVec = 16 / sizeof(Elem);
     cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_arrive();  // before any CTA writes into another's shared memory, both run
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int row = blockIdx.x / ranks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int first = min(rank * p.slice, p.V), n = min(p.slice, p.V - first);
-    const int64_t at = row * p.ld + first;
+    const Elem *const logits = static_cast<const Elem *>(p.logits) + row * p.ld;
+    // Slices begin on 16-byte boundaries of the row (rows need not), and words keep
+    // their place within 16 bytes (of the input's type) in shared memory.
+    const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(logits) & 15) / sizeof(Elem));
+    const int first = min(max(rank * p.slice - skew, 0), p.V), n = min((rank + 1) * p.slice - skew, p.V) - first;
+    const int pad = rank == 0 ? skew : 0;
+    const Elem *const mine = logits + first;
+    float *const vals = buf + pad;  // logits, NaN as -inf; later e
 
-    auto global_value = [&](int i) {
-        float v = p.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p.logits)[at + i]) << 16)
-                         : static_cast<const float *>(p.logits)[at + i];
+    auto widen = [](Elem v) -> float {
+        if constexpr (BF16)
+            return __uint_as_float(static_cast<uint32_t>(v) << 16);
+        else
+            return v;
+    };
+    // a word's logit from memory, for the few that need it again
+    auto logit = [&](int i) -> float {
+        const float v = widen(mine[i]);
         return v != v ? -INFINITY : v;
     };
-    auto value = [&](int i) { return p.resident ? vals[i] : global_value(i); };
 
-    // ---- the slice and the row's largest logit ---------------------------------------
-    float top = -INFINITY;
+    // ---- the slice; the row's largest and smallest logits -----------------------------
+    float top = -INFINITY, low = INFINITY;
     bool nan = false;
-    for (int i0 = tid; i0 < n; i0 += kThreads * 8) {
-        float v[8];
+    auto look = [&](float v) -> float {
+        const bool bad = v != v;
+        nan = nan || bad;
+        v = bad ? -INFINITY : v;
+        top = fmaxf(top, v);
+        low = fminf(low, v == -INFINITY ? INFINITY : v);
+        return v;
+    };
+    const int head = min((kVec - pad) % kVec, n), body = (n - head) / kVec;  // words, then runs of 16 bytes
+    if (tid < 2 * kVec) {  // words before and after the whole runs
+        const int i = tid < kVec ? tid : head + body * kVec + tid - kVec;
+        if (tid < kVec ? i < head : i < n) vals[i] = look(widen(mine[i]));
+    }
+    if constexpr (BF16) {
+        const uint4 *const src = reinterpret_cast<const uint4 *>(mine + head);
+        float4 *const dst = reinterpret_cast<float4 *>(vals + head);
+        for (int b0 = tid; b0 < body; b0 += 4 * kThreads) {
+            uint4 q[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = i0 + j * kThreads;
-            v[j] = -INFINITY;
-            if (i < n)
-                v[j] = p.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p.logits)[at + i]) << 16)
-                              : static_cast<const float *>(p.logits)[at + i];
+            for (int j = 0; j < 4; ++j)
+                if (b0 + j * kThreads < body) q[j] = src[b0 + j * kThreads];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int b = b0 + j * kThreads;
+                if (b < body) {
+                    dst[2 * b] = make_float4(look(bf16lo_f32(q[j].x)), look(bf16hi_f32(q[j].x)), look(bf16lo_f32(q[j].y)),
+                                             look(bf16hi_f32(q[j].y)));
+                    dst[2 * b + 1] = make_float4(look(bf16lo_f32(q[j].z)), look(bf16hi_f32(q[j].z)), look(bf16lo_f32(q[j].w)),
+                                                 look(bf16hi_f32(q[j].w)));
+                }
+            }
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = i0 + j * kThreads;
-            if (v[j] != v[j]) v[j] = -INFINITY, nan = true;
-            if (i < n && p.resident) vals[i] = v[j];
-            top = fmaxf(top, v[j]);
+    } else {
+        auto part = [&](int c) { return static_cast<int>(static_cast<int64_t>(body) * c / kCopies); };
+        if (tid == 0) {
+            for (int c = 0; c < kCopies; ++c) mbar_init(&s.bars[c], 1);
+            fence_mbar_init();
+            for (int c = 0; c < kCopies; ++c) {
+                const int b0 = part(c), bytes = (part(c + 1) - b0) * 16;
+                mbar_arrive_expect_tx(&s.bars[c], bytes);
+                if (bytes > 0) bulk_g2s(vals + head + b0 * kVec, mine + head + b0 * kVec, bytes, &s.bars[c]);
+            }
+        }
+        __syncthreads();
+        bool late = false;
+        float4 *const run = reinterpret_cast<float4 *>(vals + head);
+        for (int c = 0; c < kCopies; ++c) {
+            late = !mbar_wait_bounded(&s.bars[c], 0) || late;
+            const int b1 = part(c + 1);
+#pragma unroll 4
+            for (int b = part(c) + tid; b < b1; b += kThreads) {
+                const float4 q = run[b];
+                const float4 v = make_float4(look(q.x), look(q.y), look(q.z), look(q.w));
+                if (q.x != q.x || q.y != q.y || q.z != q.z || q.w != q.w) run[b] = v;
+            }
+        }
+        if (late) {
+            if (p.status) atomicOr(p.status, Q8_DEV_TIMEOUT);
+            drain_after_timeout();
         }
     }
     if (nan && p.status) atomicOr(p.status, Q8_DEV_NONFINITE);
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) s.warp_max[warp] = top;
+    // the largest of each of this CTA's kGroups / ranks groups of threads
+    const int group = kThreads * ranks / kGroups;  // threads of a group: a power of two, 2 .. 32
+    for (int o = 1; o < group; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    if (lane == 0) s.warp_min[warp] = low;
+    if (tid == 0) s.listed = 0;
+    cluster.barrier_wait();
+    if (tid % group < ranks) {
+        // a group's threads write its maximum to the CTAs, the lanes in turn
+        for (int c = tid % group; c < ranks; c += group)
+            cluster.map_shared_rank(&s, c)->groups[rank * (kGroups / ranks) + tid / group] = top;
+    }
     __syncthreads();
     if (warp == 0) {
-        top = s.warp_max[lane];
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane < ranks) cluster.map_shared_rank(&s, lane)->maxima[rank] = top;
+        low = s.warp_min[lane % kWarps];
+        for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+        if (lane < ranks) cluster.map_shared_rank(&s, lane)->minima[rank] = low;
     }
     cluster.sync();
-    for (int c = 0; c < ranks; ++c) top = fmaxf(top, s.maxima[c]);
+    top = s.groups[lane], low = s.minima[lane % ranks];
+#pragma unroll
+    for (int i = 32; i < kGroups; i += 32) top = fmaxf(top, s.groups[i + lane]);
+    for (int o = 16; o > 0; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    }
 
     Row r;
     r.top = top;
     r.temp = p.temperature ? p.temperature[row] : 1.0f;
-    int64_t k = p.top_k ? p.top_k[row] : 0;
+    int k = p.top_k ? p.top_k[row] : 0;
     if (!(r.temp > 0.0f)) r.temp = 1.0f, k = 1;
     if (k <= 0 || k > p.V) k = p.V;
     const float top_p = p.top_p ? p.top_p[row] : 1.0f, min_p = p.min_p ? p.min_p[row] : 0.0f;
+    const float u = p.u[row];
 
-    // ---- the place in the ranking where `want_count` words, or `want_mass`, are reached --
-    // Finds the key of the word there, and what lies before that key.
-    struct Found {
-        uint32_t key, before_count, in_count;
-        unsigned long long before_mass, in_mass;  // in_*: of the words with that key
-    };
-    auto search = [&](bool by_mass, unsigned long long want, uint32_t last, Found &f) -> bool {
-        // words with keys above `last` are out; false if fewer than wanted are there
-        uint32_t prefix = 0, before_count = 0;
-        unsigned long long before_mass = 0;
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : kBins;
-            const int above = pass == 0 ? 32 : (pass == 1 ? 21 : 10);
-            for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0, s.mass[i] = 0;
-            __syncthreads();
-            for (int i = tid; i < n; i += kThreads) {
-                const float l = value(i);
-                const uint32_t key = rank_key(l);
-                if (key > last || (pass > 0 && (key >> above) != prefix)) continue;
-                float e;
-                const unsigned long long w = r.mass(l, e);
-                if (w == 0) continue;
-                const uint32_t d = (key >> shift) & (bins - 1);
-                atomicAdd(&s.count[d], 1u);
-                atomicAdd(&s.mass[d], w);
-            }
-            cluster.sync();
-            // CTA `rank` adds up its share of the bins over all CTAs
-            const int share = bins / ranks, b0 = rank * share;
-            uint32_t c_sum = 0;
-            unsigned long long m_sum = 0;
-            uint32_t my_count[2] = {0, 0};
-            unsigned long long my_mass[2] = {0, 0};
-            for (int j = 0; j < 2; ++j) {
-                const int b = tid * 2 + j;  // two neighbouring bins a thread
-                if (b < share)
-                    for (int c = 0; c < ranks; ++c) {
-                        const Shared *o = cluster.map_shared_rank(&s, c);
-                        my_count[j] += o->count[b0 + b];
-                        my_mass[j] += o->mass[b0 + b];
-                    }
-            }
-            // inclusive scan over the CTA's threads
-            c_sum = my_count[0] + my_count[1];
-            m_sum = my_mass[0] + my_mass[1];
-            uint32_t c_run = c_sum;
-            unsigned long long m_run = m_sum;
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t cv = __shfl_up_sync(0xffffffffu, c_run, o);
-                const unsigned long long mv = __shfl_up_sync(0xffffffffu, m_run, o);
-                if (lane >= o) c_run += cv, m_run += mv;
-            }
-            if (lane == 31) s.warp_count[warp] = c_run, s.warp_mass[warp] = m_run;
-            __syncthreads();
-            uint32_t c_all = 0;
-            unsigned long long m_all = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) c_run += c_all, m_run += m_all;
-                c_all += s.warp_count[w];
-                m_all += s.warp_mass[w];
-            }
-            if (tid < ranks) {
-                Shared *o = cluster.map_shared_rank(&s, tid);
-                o->sub_count[rank] = c_all;
-                o->sub_mass[rank] = m_all;
-            }
-            cluster.sync();
-            uint32_t c_before = before_count, c_total = before_count;
-            unsigned long long m_before = before_mass, m_total = before_mass;
-            for (int c = 0; c < ranks; ++c) {
-                if (c == rank) c_before = c_total, m_before = m_total;
-                c_total += s.sub_count[c];
-                m_total += s.sub_mass[c];
-            }
-            if (by_mass ? m_total < want : c_total < want) return false;  // the same for all threads
-            // the bin in which the wanted place lies: before it less than wanted, with it enough
-            uint32_t cb = c_before + c_run - c_sum;
-            unsigned long long mb = m_before + m_run - m_sum;
-            for (int j = 0; j < 2; ++j) {
-                const unsigned long long have = by_mass ? mb : cb;
-                const unsigned long long with = by_mass ? mb + my_mass[j] : static_cast<unsigned long long>(cb) + my_count[j];
-                if (have < want && with >= want) {
-                    for (int c = 0; c < ranks; ++c) {
-                        Shared *o = cluster.map_shared_rank(&s, c);
-                        o->digit = b0 + tid * 2 + j;
-                        o->before_count = cb;
-                        o->before_mass = mb;
-                        o->in_count = my_count[j];
-                        o->in_mass = my_mass[j];
-                    }
-                }
-                cb += my_count[j];
-                mb += my_mass[j];
-            }
-            cluster.sync();
-            prefix = pass == 0 ? s.digit : (pass == 1 ? (prefix << 11) | s.digit : (prefix << 10) | s.digit);
-            before_count = s.before_count;
-            before_mass = s.before_mass;
+    auto nothing = [&]() {
+        if (rank == 0 && tid == 0) {
+            p.token[row] = -1;
+            if (p.logprob) p.logprob[row] = -INFINITY;
+            if (p.kept) p.kept[row] = 0;
         }
-        f.key = prefix;
-        f.before_count = before_count, f.before_mass = before_mass;
-        f.in_count = s.in_count, f.in_mass = s.in_mass;
+    };
+    if (top == -INFINITY) {
+        nothing();
+        return;
+    }
+
+    // CTA 0's list gets every word for which in(i) holds; false, for all threads, if they are too
+    // many.  Leaves a barrier open (all have looked at CTA 0's count): settle() closes it, CTA 0
+    // before it ends.
+    auto gather = [&](auto in, bool from_memory) -> bool {
+        Shared *o = cluster.map_shared_rank(&s, 0);
+        for (int i0 = tid; i0 - tid < n; i0 += 32 * kThreads) {
+            uint32_t hits = 0;  // of this thread's next 32 words
+#pragma unroll 8
+            for (int j = 0; j < 32; ++j) {
+                const int i = i0 + j * kThreads;
+                if (i - tid >= n) break;
+                hits |= i < n && in(i) ? 1u << j : 0u;
+            }
+            if (!__any_sync(0xffffffffu, hits != 0)) continue;
+            uint32_t have = __popc(hits), at = have;
+            for (int q = 1; q < 32; q <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, at, q);
+                if (lane >= q) at += v;
+            }
+            uint32_t base = 0;
+            if (lane == 31) base = atomicAdd(&o->listed, at);
+            at += __shfl_sync(0xffffffffu, base, 31) - have;
+            for (; hits != 0; hits &= hits - 1, ++at)
+                if (at < kList) {
+                    const int i = i0 + (__ffs(hits) - 1) * kThreads;
+                    o->list[at] = static_cast<unsigned long long>(rank_key(from_memory ? logit(i) : vals[i])) << 32 |
+                                  static_cast<uint32_t>(first + i);
+                }
+        }
+        cluster.sync();
+        const bool fits = o->listed <= kList;
+        cluster.barrier_arrive();
+        return fits;
+    };
+    auto settle = [&]() { cluster.barrier_wait(); };
+    // Sorts the list of CTA 0 by (key, index).
+    auto sort = [&](int count) {
+        int m = 128;
+        while (m < count) m <<= 1;
+        if (count <= 128) {  // each word's place is how many come before it
+            unsigned long long x = 0;
+            int at = 0;
+            if (tid < count) x = s.list[tid];
+            if (warp * 32 < count)
+#pragma unroll 8
+                for (int j = 0; j < count; ++j) at += s.list[j] < x ? 1 : 0;
+            __syncthreads();
+            if (tid < count) s.list[at] = x;
+            __syncthreads();
+        } else {
+            for (int i = count + tid; i < m; i += kThreads) s.list[i] = ~0ull;
+            sort_list(s.list, m);
+        }
+    };
+
+    // The whole draw from the list of CTA 0: the row's first words, at least as many as can be
+    // kept.  want = 0: the mass that top-p asks for is that of the first k of them.
+    auto draw_from_list = [&](unsigned long long want) {
+        const int count = static_cast<int>(s.listed);
+        sort(count);
+        const int words_of = count <= 128 ? 1 : kPer;  // words per thread
+        unsigned long long w[kPer], sum = 0;
+        float e[kPer];
+        uint32_t idx[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int i = tid * words_of + j;
+            w[j] = 0, e[j] = 0.f, idx[j] = 0;
+            if (j < words_of && i < count && i < k) {
+                const unsigned long long x = s.list[i];
+                idx[j] = static_cast<uint32_t>(x);
+                e[j] = r.weight(unkey(static_cast<uint32_t>(x >> 32)));
+                w[j] = mass_of(e[j]);
+            }
+            sum += w[j];
+        }
+        unsigned long long before = 0, total;
+        uint32_t c0, c1;
+        if (top_p < 1.0f) {
+            scan_cta(s, sum, 0u, before, c0, total, c1);
+            if (want == 0) want = mass_wanted(top_p, total);
+        }
+        unsigned long long kept = 0;
+        uint32_t words = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const bool in = w[j] != 0 && (!(top_p < 1.0f) || before < want) && e[j] >= min_p;
+            before += w[j];
+            if (!in) w[j] = 0;
+            kept += w[j];
+            words += in ? 1u : 0u;
+        }
+        unsigned long long all;
+        uint32_t all_words;
+        scan_cta(s, kept, words, before, c0, all, all_words);
+        if (all == 0) {
+            nothing();
+            return;
+        }
+        // the words kept, by index: 20 bits of index above 41 of mass
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (w[j] != 0) s.list[c0++] = static_cast<unsigned long long>(idx[j]) << 41 | w[j];
+        __syncthreads();
+        const unsigned long long place = place_of(u, all), low41 = (1ull << 41) - 1;
+        auto give = [&](uint32_t word, unsigned long long mass) {
+            p.token[row] = static_cast<int32_t>(word);
+            if (p.logprob) p.logprob[row] = log_share(mass, all);
+            if (p.kept) p.kept[row] = static_cast<int32_t>(all_words);
+        };
+        if (all_words <= 128) {
+            if (tid < static_cast<int>(all_words)) {
+                const unsigned long long x = s.list[tid];
+                before = 0;
+#pragma unroll 8
+                for (int j = 0; j < static_cast<int>(all_words); ++j) {
+                    const unsigned long long y = s.list[j];
+                    before += y < x ? y & low41 : 0ull;
+                }
+                if (before <= place && place < before + (x & low41)) give(static_cast<uint32_t>(x >> 41), x & low41);
+            }
+            return;
+        }
+        sort(static_cast<int>(all_words));
+        kept = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int i = tid * kPer + j;
+            w[j] = 0;
+            if (i < static_cast<int>(all_words)) {
+                const unsigned long long x = s.list[i];
+                idx[j] = static_cast<uint32_t>(x >> 41);
+                w[j] = x & low41;
+            }
+            kept += w[j];
+        }
+        scan_cta(s, kept, 0u, before, c0, total, c1);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            if (w[j] != 0 && before <= place && place < before + w[j]) give(idx[j], w[j]);
+            before += w[j];
+        }
+    };
+
+    // ---- top-k of few -------------------------------------------------------------------
+    if (k <= kFastK) {
+        // the k-th largest group maximum: the one with fewer than k before it and no more than k - 1 equal ones ahead
+        static_assert(kThreads == 2 * kGroups, "two threads a group");
+        const float x = s.groups[tid >> 1];
+        int at = 0;
+#pragma unroll 8
+        for (int j = (tid & 1) * (kGroups / 2); j < ((tid & 1) + 1) * (kGroups / 2); j += 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(&s.groups[j]);
+            const int me = tid >> 1;
+            at += (y.x > x || (y.x == x && j < me)) + (y.y > x || (y.y == x && j + 1 < me)) +
+                  (y.z > x || (y.z == x && j + 2 < me)) + (y.w > x || (y.w == x && j + 3 < me));
+        }
+        at += __shfl_xor_sync(0xffffffffu, at, 1);
+        if (at == k - 1) s.bound = x;
+        __syncthreads();
+        const float bound = s.bound;
+        if (gather([&](int i) { return vals[i] >= bound && vals[i] > -INFINITY; }, false)) {
+            if (rank == 0) draw_from_list(0ull);
+            settle();
+            return;
+        }
+        settle();
+        if (rank == 0 && tid == 0) s.listed = 0;
+    }
+
+    // ---- searches over the whole row ------------------------------------------------------
+    struct Place {
+        uint32_t bin, before_count, in_count;
+        unsigned long long before_mass, in_mass;
+    };
+    auto clear = [&]() {
+        for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0, s.mass_lo[i] = 0, s.mass_hi[i] = 0;
+        __syncthreads();
+    };
+    // One word a lane into the histogram (bin < 0: none).  A warp of equal bins (equal logits)
+    // adds once.  64-bit sums are kept in two words: whoever carries the low one over adds that
+    // to the high one.
+    auto add_to = [&](int bin, unsigned long long w) {
+        uint32_t one = 1;
+        if (__all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0))) {
+            if (bin < 0) return;
+            for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            one = 32;
+            if (lane != 0) bin = -1;
+        }
+        if (bin >= 0) {
+            atomicAdd(&s.count[bin], one);
+            if (w != 0) {
+                const uint32_t lo = static_cast<uint32_t>(w), old = atomicAdd(&s.mass_lo[bin], lo);
+                const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old ? 1u : 0u);
+                if (hi != 0) atomicAdd(&s.mass_hi[bin], hi);
+            }
+        }
+    };
+    // The bin in which `want` (a count or a mass) is reached, adding to what f says came before;
+    // false, for all threads, if it never is.
+    auto locate = [&](int bins, bool by_mass, unsigned long long want, Place &f) -> bool {
+        cluster.sync();
+        // CTA `rank` adds up its share of the bins over all CTAs, up to four neighbours a thread
+        const int share = bins / ranks, b0 = rank * share, each = (share + kThreads - 1) / kThreads;
+        uint32_t cnt[kBins / kThreads] = {};
+        unsigned long long mas[kBins / kThreads] = {};
+        uint32_t c_sum = 0;
+        unsigned long long m_sum = 0;
+#pragma unroll
+        for (int j = 0; j < kBins / kThreads; ++j) {
+            const int b = tid * each + j;
+            if (j < each && b < share) {
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c)
+                    if (c < ranks) {
+                        const Shared *o = cluster.map_shared_rank(&s, c);
+                        cnt[j] += o->count[b0 + b];
+                        if (by_mass) mas[j] += static_cast<unsigned long long>(o->mass_hi[b0 + b]) << 32 | o->mass_lo[b0 + b];
+                    }
+                c_sum += cnt[j];
+                m_sum += mas[j];
+            }
+        }
+        unsigned long long mb, m_all;
+        uint32_t cb, c_all;
+        scan_cta(s, m_sum, c_sum, mb, cb, m_all, c_all);
+        if (tid < ranks) {
+            Shared *o = cluster.map_shared_rank(&s, tid);
+            o->sub_count[rank] = c_all;
+            o->sub_mass[rank] = m_all;
+        }
+        cluster.sync();
+        uint32_t c_total = f.before_count;
+        unsigned long long m_total = f.before_mass;
+        int owner = -1;
+        for (int c = 0; c < ranks; ++c) {
+            if (c == rank) cb += c_total, mb += m_total;
+            c_total += s.sub_count[c];
+            m_total += s.sub_mass[c];
+            if (owner < 0 && (by_mass ? m_total : c_total) >= want) owner = c;
+        }
+        if (owner < 0) return false;
+        if (rank == owner) {
+#pragma unroll
+            for (int j = 0; j < kBins / kThreads; ++j) {
+                const unsigned long long have = by_mass ? mb : cb;
+                const unsigned long long with = by_mass ? mb + mas[j] : static_cast<unsigned long long>(cb) + cnt[j];
+                if (have < want && with >= want) {
+                    s.digit = b0 + tid * each + j;
+                    s.before_count = cb, s.in_count = cnt[j];
+                    s.before_mass = mb, s.in_mass = mas[j];
+                }
+                cb += cnt[j];
+                mb += mas[j];
+            }
+        }
+        cluster.sync();
+        const Shared *o = cluster.map_shared_rank(&s, owner);
+        f.bin = o->digit;
+        f.before_count = o->before_count, f.in_count = o->in_count;
+        f.before_mass = o->before_mass, f.in_mass = o->in_mass;
         return true;
     };
 
-    uint32_t last = 0xFFFFFFFFu;   // the last key kept
-    uint32_t ties = 0xFFFFFFFFu;   // how many words of that key, in index order
-    bool ranked = false;           // fewer than there are
-    unsigned long long total = 0;  // mass of the words kept so far
-    bool have_total = false;
-    Found f;
-    if (k < p.V && search(false, static_cast<unsigned long long>(k), last, f)) {
-        last = f.key;
-        ties = static_cast<uint32_t>(k) - f.before_count;
-        ranked = ties < f.in_count;
-        total = f.before_mass + f.in_mass / f.in_count * ties;
-        have_total = true;
-    }
-    if (top_p < 1.0f) {
-        if (!have_total) {
-            unsigned long long m = 0;
-            for (int i = tid; i < n; i += kThreads) {
-                float e;
-                m += r.mass(value(i), e);
+    uint32_t last = 0xFFFFFFFFu;  // the last key kept
+    uint32_t ties = 0xFFFFFFFFu;  // how many words of that key, in index order
+    bool ranked = false;          // fewer than there are
+
+    // The last word kept, exactly, when `in` holds for the words of the step in which it lies.
+    // weight(key): a word's share of `want`.
+    auto end_in_step = [&](auto in, bool from_memory, unsigned long long before0, unsigned long long want, auto weight) {
+        gather(in, from_memory);
+        settle();
+        if (rank == 0) {
+            const int count = min(static_cast<int>(s.listed), kList);
+            sort(count);
+            unsigned long long w[kPer], sum = 0, before, total;
+            uint32_t c0, c1;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int i = tid * kPer + j;
+                w[j] = i < count ? weight(static_cast<uint32_t>(s.list[i] >> 32)) : 0ull;
+                sum += w[j];
             }
-            m = warp_sum(m);
-            if (lane == 0) s.warp_mass[warp] = m;
-            __syncthreads();
-            if (warp == 0) {
-                m = warp_sum(s.warp_mass[lane]);
-                if (lane < ranks) cluster.map_shared_rank(&s, lane)->sub_mass[rank] = m;
+            scan_cta(s, sum, 0u, before, c0, total, c1);
+            before += before0;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int i = tid * kPer + j;
+                if (w[j] != 0 && before < want && before + w[j] >= want) {
+                    const uint32_t key = static_cast<uint32_t>(s.list[i] >> 32);
+                    int b = i;
+                    while (b > 0 && static_cast<uint32_t>(s.list[b - 1] >> 32) == key) --b;
+                    s.last = key;
+                    s.ties = static_cast<uint32_t>(i - b + 1);
+                    s.ranked = i + 1 < count && static_cast<uint32_t>(s.list[i + 1] >> 32) == key ? 1u : 0u;
+                }
+                before += w[j];
             }
-            cluster.sync();
-            for (int c = 0; c < ranks; ++c) total += s.sub_mass[c];
-            cluster.sync();
+            if (tid == 0) s.listed = 0;
         }
-        const double cut = ceil(static_cast<double>(top_p) * static_cast<double>(total));
-        const unsigned long long want = cut < 1.0 ? 1ull : static_cast<unsigned long long>(cut);
-        // words before which less than `want` lies: up to the one that reaches it
-        if (search(true, want, last, f)) {
+        cluster.sync();
+        const Shared *o = cluster.map_shared_rank(&s, 0);
+        last = o->last, ties = o->ties, ranked = o->ranked != 0;
+    };
+    // The same by the digits of the order key (11, 11, 10 bits), for any number of equal words.
+    auto end_by_digits = [&](auto in, bool from_memory, bool by_mass, unsigned long long before0, unsigned long long want, auto weight) {
+        uint32_t prefix = 0;
+        Place f = {};
+        f.before_count = by_mass ? 0u : static_cast<uint32_t>(before0);
+        f.before_mass = by_mass ? before0 : 0ull;
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : kBins;
+            const int above = pass == 1 ? 21 : 10;
+            clear();
+            for (int i0 = warp * 32; i0 < n; i0 += kThreads) {
+                const int i = i0 + lane;
+                int d = -1;
+                unsigned long long w = 0;
+                if (i < n && in(i)) {
+                    const uint32_t key = rank_key(from_memory ? logit(i) : vals[i]);
+                    if (pass == 0 || (key >> above) == prefix) {
+                        d = static_cast<int>((key >> shift) & (bins - 1));
+                        w = by_mass ? weight(key) : 0ull;
+                    }
+                }
+                add_to(d, w);
+            }
+            locate(bins, by_mass, want, f);
+            prefix = pass == 0 ? f.bin : (pass == 1 ? (prefix << 11) | f.bin : (prefix << 10) | f.bin);
+        }
+        last = prefix;
+        if (by_mass) {
             const unsigned long long w = f.in_mass / f.in_count;
-            const uint32_t t = static_cast<uint32_t>((want - f.before_mass + w - 1) / w);
-            last = f.key;
-            ties = t;
-            ranked = ties < f.in_count;
+            ties = static_cast<uint32_t>((want - f.before_mass + w - 1) / w);
+        } else {
+            ties = static_cast<uint32_t>(want) - f.before_count;
+        }
+        ranked = ties < f.in_count;
+        cluster.sync();  // everyone has read what was found
+    };
+    // Words with the last key that lie before this thread's first word, i0 .. i1 being its run.
+    const int run = (n + kThreads - 1) / kThreads, i0 = min(tid * run, n), i1 = min(i0 + run, n);
+    auto ties_before = [&](auto key_of) -> uint32_t {
+        uint32_t c = 0, before, all;
+        unsigned long long mb, ma;
+        for (int i = i0; i < i1; ++i) c += key_of(i) == last ? 1u : 0u;
+        scan_cta(s, 0ull, c, mb, before, ma, all);
+        cluster.sync();
+        if (tid < ranks) cluster.map_shared_rank(&s, tid)->sub_count[rank] = all;
+        cluster.sync();
+        for (int b = 0; b < rank; ++b) before += s.sub_count[b];
+        cluster.sync();
+        return before;
+    };
+
+    if (k < p.V) {
+        // steps of the distance from the top: monotone in l, as a difference, a product and a
+        // truncation are, each rounded one way
+        const float far = 28.0f * r.temp, range = fminf(far, top - low);
+        const float per = range > 0.0f && range < INFINITY ? __fdiv_rn(static_cast<float>(kBins - 1), range) : 0.0f;
+        auto step_of = [&](float l) -> int {
+            const float d = top - l;
+            const int b = d <= far && l > -INFINITY ? static_cast<int>(fminf(d * per, static_cast<float>(kBins - 1))) : -1;
+            return l == top ? 0 : b;
+        };
+        clear();
+        for (int w0 = warp * 32; w0 < n; w0 += kThreads * 4) {
+            int b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = w0 + j * kThreads + lane;
+                b[j] = i < n ? step_of(vals[i]) : -1;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) add_to(b[j], 0ull);
+        }
+        Place f = {};
+        const unsigned long long want = static_cast<unsigned long long>(k);
+        if (locate(kBins, false, want, f)) {
+            const int bin = static_cast<int>(f.bin);
+            if (f.before_count + f.in_count <= kList) {
+                gather([&](int i) { const int b = step_of(vals[i]); return b >= 0 && b <= bin; }, false);
+                if (rank == 0) draw_from_list(0ull);
+                settle();
+                return;
+            }
+            auto in = [&](int i) { return step_of(vals[i]) == bin; };
+            if (f.in_count <= kList)
+                end_in_step(in, false, f.before_count, want, [](uint32_t) { return 1ull; });
+            else
+                end_by_digits(in, false, false, f.before_count, want, [](uint32_t) { return 1ull; });
         }
     }
 
-    // ---- the draw: sums in index order, a contiguous run of words per warp ---------------
-    const int run = (n + kWarps - 1) / kWarps, w0 = min(warp * run, n), w1 = min(w0 + run, n);
-    uint32_t eq_before = 0;  // words with the last key before this warp's
-    if (ranked) {
-        uint32_t c = 0;
-        for (int i = w0 + lane; i < w1; i += 32) c += rank_key(value(i)) == last ? 1u : 0u;
-        c = warp_sum(c);
-        if (lane == 0) s.warp_count[warp] = c;
-        __syncthreads();
-        uint32_t all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) eq_before = all;
-            all += s.warp_count[w];
-        }
-        if (tid < ranks) cluster.map_shared_rank(&s, tid)->sub_count[rank] = all;
-        cluster.sync();
-        for (int c2 = 0; c2 < rank; ++c2) eq_before += s.sub_count[c2];
-        cluster.sync();
-    }
-    // mass of word i if it is kept; eq: words with the last key before i
-    auto kept_mass = [&](float l, uint32_t eq) -> unsigned long long {
-        const uint32_t key = rank_key(l);
-        if (key > last || (key == last && eq >= ties)) return 0ull;
-        float e;
-        const unsigned long long w = r.mass(l, e);
-        return e >= min_p ? w : 0ull;
-    };
-    unsigned long long sum = 0;
+    // ---- e in place of the logits, 0 for words that top-k leaves out -------------------------
+    unsigned long long sum = 0;  // of this thread's run
     uint32_t count = 0;
-    {
-        uint32_t eq = eq_before;
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-            const int i = i0 + lane;
-            const float l = i < w1 ? value(i) : -INFINITY;
-            uint32_t mine = eq;
-            if (ranked) {
-                const uint32_t same = __ballot_sync(0xffffffffu, i < w1 && rank_key(l) == last);
-                mine += __popc(same & ((1u << lane) - 1));
-                eq += __popc(same);
+    auto tally = [&](float e) -> unsigned long long {
+        const unsigned long long w = mass_of(e), in = e >= min_p ? w : 0ull;
+        sum += in;
+        count += in != 0 ? 1u : 0u;
+        return w;
+    };
+    // each lane starts elsewhere in its run, so that a warp's reads hit all banks
+    const int turn = run > 0 ? lane % run : 0;
+    unsigned long long total = 0;
+    if (ranked) {
+        uint32_t eq = ties_before([&](int i) { return rank_key(vals[i]); });
+        for (int i = i0; i < i1; ++i) {
+            const uint32_t key = rank_key(vals[i]);
+            const float e = key < last || (key == last && eq < ties) ? r.weight(vals[i]) : 0.f;
+            eq += key == last ? 1u : 0u;
+            vals[i] = e;
+            total += tally(e);
+        }
+        ranked = false;
+    } else {
+        int j = turn;
+        for (int q = 0; q < run; q += 4) {
+            float e[4];
+            int at[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                at[h] = q + h < run ? i0 + j : n;
+                const float l = at[h] < i1 ? vals[at[h]] : -INFINITY;
+                e[h] = rank_key(l) <= last ? r.weight(l) : 0.f;
+                j = j + 1 == run ? 0 : j + 1;
             }
-            const unsigned long long w = i < w1 ? kept_mass(l, ranked ? mine : 0u) : 0ull;
-            sum += w;
-            count += w != 0 ? 1u : 0u;
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (at[h] < i1) {
+                    vals[at[h]] = e[h];
+                    total += tally(e[h]);
+                }
         }
     }
-    sum = warp_sum(sum);
-    count = warp_sum(count);
-    __syncthreads();
-    if (lane == 0) s.warp_mass[warp] = sum, s.warp_count[warp] = count;
-    __syncthreads();
-    unsigned long long cta_mass = 0, before = 0;
-    uint32_t cta_count = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) before = cta_mass;
-        cta_mass += s.warp_mass[w];
-        cta_count += s.warp_count[w];
+
+    // ---- top-p ----------------------------------------------------------------------------
+    uint32_t eq_before = 0;
+    int end_bin = kBins;       // words past this bin are out
+    bool edge = false;         // words of this bin are in up to `last`
+    // bins of e: exponent and 5 fraction bits, the largest first
+    auto bin_of = [](float e) -> int { return e > 0.f ? static_cast<int>(min((0x3F800000u - __float_as_uint(e)) >> 18, kBins - 1u)) : kBins; };
+    if (top_p < 1.0f) {
+        unsigned long long mb, m_all;
+        uint32_t cb, c_all;
+        scan_cta(s, total, 0u, mb, cb, m_all, c_all);
+        cluster.sync();
+        if (tid < ranks) cluster.map_shared_rank(&s, tid)->sub_mass[rank] = m_all;
+        clear();
+        cluster.sync();
+        total = 0;
+        for (int c = 0; c < ranks; ++c) total += s.sub_mass[c];
+        const unsigned long long want = mass_wanted(top_p, total);
+        // words below this e have together less than total - want, or each no mass
+        const float share = __fdiv_rn(static_cast<float>(total - min(want, total)), static_cast<float>(p.V));
+        const float least = fmaxf(share * 0.999f, 1.0f) * kUnit;
+        for (int w0 = warp * 32; w0 < n; w0 += kThreads * 4) {
+            float e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = w0 + j * kThreads + lane;
+                e[j] = i < n ? vals[i] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = e[j] >= least;
+                if (__any_sync(0xffffffffu, in)) add_to(in ? bin_of(e[j]) : -1, in ? mass_of(e[j]) : 0ull);
+            }
+        }
+        Place f = {};
+        if (locate(kBins, true, want, f)) {
+            const int bin = static_cast<int>(f.bin);
+            auto weight = [&](uint32_t key) { return mass_of(r.weight(unkey(key))); };
+            if (f.before_count + f.in_count <= kList) {
+                gather([&](int i) { return vals[i] >= least && bin_of(vals[i]) <= bin; }, true);
+                if (rank == 0) k = p.V, draw_from_list(want);
+                settle();
+                return;
+            }
+            auto in = [&](int i) { return vals[i] >= least && bin_of(vals[i]) == bin; };
+            if (f.in_count <= kList)
+                end_in_step(in, true, f.before_mass, want, weight);
+            else
+                end_by_digits(in, true, true, f.before_mass, want, weight);
+            end_bin = bin, edge = true;
+        }
+        if (edge && ranked) eq_before = ties_before([&](int i) { return bin_of(vals[i]) == end_bin ? rank_key(logit(i)) : 0xFFFFFFFFu; });
     }
+    auto keep = [&](int i, uint32_t eq) -> float {
+        const float e = vals[i];
+        const int b = bin_of(e);
+        if (b < end_bin || !edge) return e;
+        if (b > end_bin) return 0.f;
+        const uint32_t key = rank_key(logit(i));
+        return key < last || (key == last && eq < ties) ? e : 0.f;
+    };
+    if (edge) {
+        sum = 0, count = 0;
+        if (ranked) {
+            uint32_t eq = eq_before;
+            for (int i = i0; i < i1; ++i) {
+                tally(keep(i, eq));
+                if (bin_of(vals[i]) == end_bin) eq += rank_key(logit(i)) == last ? 1u : 0u;
+            }
+        } else {
+            int j = turn;
+#pragma unroll 4
+            for (int q = 0; q < run; ++q) {
+                if (i0 + j < i1) tally(keep(i0 + j, 0u));
+                j = j + 1 == run ? 0 : j + 1;
+            }
+        }
+    }
+
+    // ---- the draw, in index order ------------------------------------------------------------
+    unsigned long long before, cta_mass;
+    uint32_t c_before, cta_count;
+    scan_cta(s, sum, count, before, c_before, cta_mass, cta_count);
+    cluster.sync();
     if (tid < ranks) {
         Shared *o = cluster.map_shared_rank(&s, tid);
         o->sub_mass[rank] = cta_mass;
@@ -374,41 +893,36 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         all_count += s.sub_count[c];
     }
     if (all == 0) {
-        if (rank == 0 && tid == 0) {
-            p.token[row] = -1;
-            if (p.logprob) p.logprob[row] = -INFINITY;
-            if (p.kept) p.kept[row] = 0;
-        }
+        nothing();
         return;
     }
-    const double x = floor(static_cast<double>(p.u[row]) * static_cast<double>(all));
-    unsigned long long rr = x > 0.0 ? static_cast<unsigned long long>(x) : 0ull;
-    if (rr > all - 1) rr = all - 1;
-    if (rr >= before && rr < before + sum) {  // this warp's run holds the token
-        uint32_t eq = eq_before;
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-            const int i = i0 + lane;
-            const float l = i < w1 ? value(i) : -INFINITY;
-            uint32_t mine = eq;
-            if (ranked) {
-                const uint32_t same = __ballot_sync(0xffffffffu, i < w1 && rank_key(l) == last);
-                mine += __popc(same & ((1u << lane) - 1));
+    const unsigned long long place = place_of(u, all);
+    const uint32_t owner = __ballot_sync(0xffffffffu, place >= before && place < before + sum);
+    if (owner) {  // one warp of the row: its lanes walk the owner's run together
+        const int src = __ffs(owner) - 1;
+        before = __shfl_sync(0xffffffffu, before, src);
+        uint32_t eq = __shfl_sync(0xffffffffu, eq_before, src);
+        const int w0 = __shfl_sync(0xffffffffu, i0, src), w1 = __shfl_sync(0xffffffffu, i1, src);
+        for (int b = w0; b < w1; b += 32) {
+            const int i = b + lane;
+            uint32_t my_eq = eq;
+            if (edge && ranked) {
+                const uint32_t same = __ballot_sync(0xffffffffu, i < w1 && bin_of(vals[i]) == end_bin && rank_key(logit(i)) == last);
+                my_eq += __popc(same & ((1u << lane) - 1));
                 eq += __popc(same);
             }
-            const unsigned long long w = i < w1 ? kept_mass(l, ranked ? mine : 0u) : 0ull;
+            const float e = i < w1 ? keep(i, my_eq) : 0.f;
+            const unsigned long long w = e >= min_p ? mass_of(e) : 0ull;
             unsigned long long c = w;
             for (int o = 1; o < 32; o <<= 1) {
                 const unsigned long long v = __shfl_up_sync(0xffffffffu, c, o);
                 if (lane >= o) c += v;
             }
-            const uint32_t hit = __ballot_sync(0xffffffffu, before + c > rr);
+            const uint32_t hit = __ballot_sync(0xffffffffu, before + c > place);
             if (hit) {
                 if (lane == __ffs(hit) - 1) {
                     p.token[row] = first + i;
-                    // log(w / all): through 1 - (all - w) / all where the word has most of the mass
-                    if (p.logprob)
-                        p.logprob[row] = 2 * w > all ? log1pf(-__fdiv_rn(static_cast<float>(all - w), static_cast<float>(all)))
-                                                     : logf(__fdiv_rn(static_cast<float>(w), static_cast<float>(all)));
+                    if (p.logprob) p.logprob[row] = log_share(w, all);
                     if (p.kept) p.kept[row] = static_cast<int32_t>(all_count);
                 }
                 break;
@@ -428,21 +942,25 @@ q8_status launch_sample(const SampleArgs &a, uint32_t *dev_status, cudaStream_t 
     static std::atomic<uint64_t> ready{0};
     const uint64_t bit = 1ull << (di->device & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-            return Q8_ERR_CUDA;
+        for (auto *f : {sample_kernel<false>, sample_kernel<true>})
+            if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+                cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+                return Q8_ERR_CUDA;
         ready.fetch_or(bit);
     }
     SampleParams p = {a.logits, a.temperature, a.top_p, a.min_p, a.u, a.top_k, a.token, a.kept, a.logprob, dev_status,
-                      a.ld, a.V, 0, a.bf16, 0};
-    // CTAs per row: slices of at least 4096 words, at most 8 (a portable cluster)
+                      a.ld, a.V, 0};
+    // CTAs per row: slices of 8192 words for a few rows, where the passes' latency is what counts,
+    // and of 16384 (two CTAs an SM) for many; 16 of them (more than every device promises, but
+    // this one has) for a few rows, and where a slice would not fit otherwise
+    const int least = a.rows <= 8 ? 8192 : 16384;
+    const int most = a.rows <= 8 || a.V > (1 << 18) ? kMaxCluster : kMaxCluster / 2;
     int ranks = 1;
-    while (ranks < kMaxCluster && a.V > 4096 * ranks) ranks *= 2;
-    p.slice = (a.V + ranks - 1) / ranks;
-    const size_t bytes = static_cast<size_t>(p.slice) * 4;
-    p.resident = bytes + sizeof(Shared) <= static_cast<size_t>(kSmem) ? 1 : 0;
+    while (ranks < most && a.V > least * ranks) ranks *= 2;
+    p.slice = ((a.V + 7 + ranks - 1) / ranks + 7) & ~7;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(Shared) + (p.resident ? bytes : 0);
+    cfg.dynamicSmemBytes = sizeof(Shared) + static_cast<size_t>(p.slice) * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -451,7 +969,7 @@ q8_status launch_sample(const SampleArgs &a, uint32_t *dev_status, cudaStream_t 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * ranks);
-    return cudaLaunchKernelEx(&cfg, sample_kernel, p) == cudaSuccess ? Q8_OK : Q8_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, a.bf16 ? sample_kernel<true> : sample_kernel<false>, p) == cudaSuccess ? Q8_OK : Q8_ERR_CUDA;
 }
 
 }  // namespace q8

@@ -149,12 +149,20 @@ def _check(st: int, what: str):
         raise Q8Error(st, what)
 
 
+# The current stream's handle, without making a Stream object (3 us of a call's 15 on the
+# host); through that object where the build lacks the short way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is not None and _get_device is not None:
+            return _raw_stream(_get_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _p(t):
@@ -394,6 +402,14 @@ def q8_gemm(q, s, x, y=None, dev_status=None, stream=None, tile=0, splits=0):
 # ---------------------------------------------------------------------------
 # the rest of a decode step
 # ---------------------------------------------------------------------------
+def _new(stream, make):
+    """make() with its allocations (and zeroing) ordered on the call's stream."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+        return make()
+
+
 class KvCache:
     """A paged key-value cache in Q8_0 blocks (q8_kv_cache): codes int8
     [pages, kv_heads, page_size, head_dim], scales 16-bit [..., head_dim / 32].
@@ -467,9 +483,9 @@ def q8_kv_read(cache, slots, k=None, v=None, dtype=torch.float32, dev_status=Non
         raise ValueError("slots must be contiguous")
     shape = (n, cache.kv_heads, cache.head_dim)
     if k is None:
-        k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=cache.device)
+        k = _new(stream, lambda: torch.empty(shape, dtype=dtype if v is None else v.dtype, device=cache.device))
     if v is None:
-        v = torch.empty(shape, dtype=k.dtype, device=cache.device)
+        v = _new(stream, lambda: torch.empty(shape, dtype=k.dtype, device=cache.device))
     ldk, ldv = _kv_rows(cache, k, "k", n), _kv_rows(cache, v, "v", n, k.dtype)
     st = lib().q8_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[k.dtype],
                           _p(dev_status), _stream(stream))
@@ -499,15 +515,15 @@ def q8_attn_decode(q, cache, table, lens, scale=None, softcap=0.0, window=0, out
     if not table.is_contiguous() or not lens.is_contiguous():
         raise ValueError("table and lens must be contiguous")
     if out is None:
-        out = torch.empty((B, H, D), dtype=torch.bfloat16, device=q.device)
+        out = _new(stream, lambda: torch.empty((B, H, D), dtype=torch.bfloat16, device=q.device))
     elif _cuda(out, "out", (torch.bfloat16,), 3).shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape")
     if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        lse = _new(stream, lambda: torch.empty((B, H), dtype=torch.float32, device=q.device))
     elif tuple(_cuda(lse, "lse", (torch.float32,), 2).shape) != (B, H) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous, [B, q_heads]")
     if ws is None:
-        ws = workspace(q8_attn_decode_workspace_size(B, H, cache.kv_heads, D), q.device)
+        ws = _new(stream, lambda: workspace(q8_attn_decode_workspace_size(B, H, cache.kv_heads, D), q.device))
     st = lib().q8_attn_decode(cache._ref, q.data_ptr(), sq[0] if B > 1 else H * D, H, table.data_ptr(), table.shape[1],
                               lens.data_ptr(), B, D ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
                               lse.data_ptr(), _p(ws), 0 if ws is None else ws.numel(), _p(dev_status), _stream(stream))
@@ -541,19 +557,19 @@ def q8_moe(x, logits, q13, s13, q2, s2, top_k, renorm=True, y=None, ids=None, we
     if T > 0 and (x.stride(1) != 1 or logits.stride(1) != 1):
         raise ValueError("x and logits must have unit inner stride")
     if y is None:
-        y = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        y = _new(stream, lambda: torch.empty((T, H), dtype=torch.float32, device=x.device))
     elif tuple(_cuda(y, "y", (torch.float32,), 2).shape) != (T, H) or y.stride(1) != 1:
         raise ValueError("y must be [T, H] with unit inner stride")
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+        ids = _new(stream, lambda: torch.empty((T, top_k), dtype=torch.int32, device=x.device))
     elif tuple(_cuda(ids, "ids", (torch.int32,), 2).shape) != (T, top_k) or not ids.is_contiguous():
         raise ValueError("ids must be contiguous, [T, top_k]")
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+        weights = _new(stream, lambda: torch.empty((T, top_k), dtype=torch.float32, device=x.device))
     elif tuple(_cuda(weights, "weights", (torch.float32,), 2).shape) != (T, top_k) or not weights.is_contiguous():
         raise ValueError("weights must be contiguous, [T, top_k]")
     if ws is None:
-        ws = workspace(q8_moe_workspace_size(T, E, H, F, top_k), x.device)
+        ws = _new(stream, lambda: workspace(q8_moe_workspace_size(T, E, H, F, top_k), x.device))
     one = T <= 1
     st = lib().q8_moe(x.data_ptr(), H if one else x.stride(0), logits.data_ptr(), E if one else logits.stride(0), T, E, top_k,
                       int(renorm), q13.data_ptr(), s13.data_ptr(), q2.data_ptr(), s2.data_ptr(), H, F, y.data_ptr(),
@@ -587,11 +603,11 @@ def q8_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
             _per_row(top_p, "top_p", n, torch.float32), _per_row(min_p, "min_p", n, torch.float32),
             _per_row(u, "u", n, torch.float32)]
     if token is None:
-        token = torch.empty(n, dtype=torch.int32, device=logits.device)
+        token = _new(stream, lambda: torch.empty(n, dtype=torch.int32, device=logits.device))
     if logprob is None:
-        logprob = torch.empty(n, dtype=torch.float32, device=logits.device)
+        logprob = _new(stream, lambda: torch.empty(n, dtype=torch.float32, device=logits.device))
     if kept is None:
-        kept = torch.empty(n, dtype=torch.int32, device=logits.device)
+        kept = _new(stream, lambda: torch.empty(n, dtype=torch.int32, device=logits.device))
     st = lib().q8_sample(logits.data_ptr(), _ROW_DTYPES[logits.dtype], logits.stride(0) if n > 1 else V, n, V, *args,
                          _per_row(token, "token", n, torch.int32), _per_row(logprob, "logprob", n, torch.float32),
                          _per_row(kept, "kept", n, torch.int32), _p(dev_status), _stream(stream))

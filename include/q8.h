@@ -585,9 +585,10 @@ size_t q8_moe_workspace_size(int32_t T, int32_t E, int64_t H, int64_t F, int32_t
  *   token  : int32 [rows]; -1 where no word is left
  *   logprob: float [rows], log(w_token / W), -inf where there is none; may be NULL
  *   kept   : int32 [rows], how many words of mass > 0 were left; may be NULL
- * 1 <= V <= 2^20.  No workspace.
+ * 1 <= V <= 2^19 (a row's slices lie in the shared memory of a cluster of 16
+ * CTAs).  No workspace.
  */
-#define Q8_SAMPLE_MAX_V (1 << 20)
+#define Q8_SAMPLE_MAX_V (1 << 19)
 q8_status q8_sample(const void *logits, int32_t dtype, int64_t ld, int32_t rows, int64_t V, const float *temperature,
                     const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
                     float *logprob, int32_t *kept, uint32_t *dev_status, q8_stream_t stream);

@@ -126,7 +126,7 @@ def sample(L, logits=A, dtype=0, ld=100, rows=2, V=100, T=A, k=A, p=A, m=A, u=A,
 def test_sample_validation(L):
     from block_quantized_int8_gb300 import q8
     assert sample(L, dtype=2) == q8.Q8_ERR_ARG
-    for kw in (dict(V=0), dict(V=(1 << 20) + 1, ld=1 << 21), dict(ld=99), dict(rows=-1)):
+    for kw in (dict(V=0), dict(V=(1 << 19) + 1, ld=1 << 21), dict(ld=99), dict(rows=-1)):
         assert sample(L, **kw) == q8.Q8_ERR_SHAPE, kw
     for a in ("logits", "u", "tok"):
         assert sample(L, **{a: None}) == q8.Q8_ERR_ARG, a

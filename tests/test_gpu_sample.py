@@ -62,7 +62,7 @@ def test_vocabularies(V):
 
 
 def test_largest_vocabulary():
-    l, u, r = rows(2, 1 << 20, 1)
+    l, u, r = rows(2, 1 << 19, 1)
     check(l, u, k=[0, 300], p=[0.9, 0.9])
 
 
