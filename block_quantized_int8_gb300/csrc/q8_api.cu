@@ -475,14 +475,14 @@ q8_status q8_attn_decode(const q8_kv_cache *cache, const uint16_t *q, int64_t ld
 
 static q8_status check_moe_shape(int32_t T, int32_t E, int64_t H, int64_t F, int32_t top_k) {
     if (T < 0 || T > Q8_SKINNY_MAX_M || E < 1 || E > Q8_MOE_MAX_EXPERTS) return Q8_ERR_SHAPE;
-    if (H < 32 || F < 32 || H % 32 != 0 || F % 32 != 0 || H > (1 << 20) || F > (1 << 20)) return Q8_ERR_SHAPE;
+    if (H < 32 || F < 32 || H % 32 != 0 || F % 32 != 0 || H > Q8_MOE_MAX_HIDDEN || F > Q8_MOE_MAX_FFN) return Q8_ERR_SHAPE;
     if (top_k < 1 || top_k > E || top_k > Q8_MOE_MAX_TOP_K) return Q8_ERR_ARG;
     return Q8_OK;
 }
 
 size_t q8_moe_workspace_size(int32_t T, int32_t E, int64_t H, int64_t F, int32_t top_k) {
     if (check_moe_shape(T, E, H, F, top_k) != Q8_OK || T == 0) return 0;
-    return moe_workspace(T, static_cast<int>(F), top_k);
+    return moe_workspace(T, static_cast<int>(H), static_cast<int>(F), top_k);
 }
 
 q8_status q8_moe(const uint16_t *x, int64_t ldx, const float *logits, int64_t ldl, int32_t T, int32_t E, int32_t top_k,
@@ -497,7 +497,7 @@ q8_status q8_moe(const uint16_t *x, int64_t ldx, const float *logits, int64_t ld
     if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(q13, 16) || !aligned(s13, 16) || !aligned(q2, 16) || !aligned(s2, 16) ||
         !aligned(logits, 4) || !aligned(y, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(dev_status, 4))
         return Q8_ERR_ALIGN;
-    const size_t need = moe_workspace(T, static_cast<int>(F), top_k);
+    const size_t need = moe_workspace(T, static_cast<int>(H), static_cast<int>(F), top_k);
     if (!ws || ws_bytes < need) return Q8_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return Q8_ERR_ALIGN;
     const DeviceInfo *di;

@@ -191,7 +191,7 @@ struct MoeArgs {
     int64_t ldx, ldl, ldy;
     int32_t T, E, H, F, top_k, renorm;
 };
-size_t moe_workspace(int T, int F, int top_k);
+size_t moe_workspace(int T, int H, int F, int top_k);
 q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStream_t stream);
 
 // ---- decode step: the next token ---------------------------------------------------

@@ -1,31 +1,40 @@
-// q8_moe.cu -- a mixture-of-experts layer for a few tokens (T <= 32) in two
-// kernels: routing, gate and up products and SwiGLU in the first; down
-// products and the weighted sum over experts in the second.
+// q8_moe.cu -- a mixture-of-experts layer for a few tokens (T <= 32): routing,
+// gate and up products and SwiGLU in one kernel, down products in a second, and
+// a small one for the weighted sum over each token's experts.
 //
 // Mathematics.  Token t takes the top_k experts of largest logit (ties: the
 // lower index), w_j = exp(l_j - l_max) / z with z summed over the chosen (or
 // all) experts; y_t = sum_j w_j W2_e(silu(W1_e x_t) * (W3_e x_t)).
 //
 // Bound: the chosen experts' weights, 1.0625 bytes each, read once for all
-// tokens that chose them.  Both kernels are streams of 16-row x 256-column
-// weight tiles through shared memory (16-byte asynchronous copies, a ring of
-// stages per CTA) and m16n8k16 warp MMAs: 16 weight rows by 8 tokens, one
-// block of 32 at a time, whose fp32 result is multiplied by the block's scale
-// as in the matmuls.  The host does not know which experts are chosen: every
-// CTA works the routing out for itself from the logits (a few hundred cycles
-// a token) and cuts the same list of work into equal runs.
+// tokens that chose them (for up to 16; an expert with more is read again,
+// from L2).  Both kernels are streams of 16-row weight tiles against a few
+// tokens' vectors: m16n8k16 warp MMAs of 16 weight rows by 8 tokens, one block
+// of 32 columns at a time, whose fp32 result is multiplied by the block's
+// scale as in the matmuls.
 //
-// gate/up kernel: a task is 32 hidden units of one expert, 8 per warp: MMA
-// rows 0..7 are gate rows and 8..15 the same units' up rows, so a thread holds
-// both factors of its unit and SwiGLU needs no exchange.  x is bf16 as given
-// (products exact).
-// Between the kernels a hidden unit must not lose what fp32 outputs keep, so
-// it is stored as the sum of two binary16 values (22 bits), scaled by a power
-// of two per token and block of 32 units.
-// down kernel: a unit of work is 64 output rows x 256 hidden units of one
-// expert; CTA c takes units [c * per, (c + 1) * per) of the list ordered by
-// output rows, then expert, so a CTA's sums stay with it; output rows shared
-// by CTAs are left in the workspace and joined in CTA order by the last.
+// One CTA of 16 warps per SM.  The tokens' vectors of an expert lie in shared
+// memory as binary16 for as long as the CTA works on it; weights come through
+// a ring of each warp's own (16-byte asynchronous copies of 16 rows x 128
+// columns), so warps wait for one another only where the CTA moves on past
+// the experts it has in shared memory.  (A first form with the vectors in the
+// ring, and so a CTA barrier per 128 columns, took 2.4 times as long.)  The host
+// does not know which experts are chosen: every CTA of the first kernel works the
+// routing out for itself from the logits, the others read it, and every CTA cuts
+// the same list of tasks into equal runs.
+// Where a CTA's tasks do not fill its warps evenly, 2, 4 or 8 warps share one,
+// each a range of its columns.
+//
+// gate/up kernel: a task is 8 hidden units of one expert: MMA rows 0..7 are
+// their gate rows, 8..15 their up rows, so a thread holds both factors of its
+// unit and SwiGLU needs no exchange.  x (bf16) is scaled by a power of two per
+// token to a largest value in [2^14, 2^15): exact in binary16 down to 2^-39 of it.
+// Hidden units go to the workspace in fp32.
+// down kernel: a task is 16 output rows of one expert over a segment of 512 or
+// 1024 hidden units.  The hidden units, scaled likewise per token and segment,
+// are taken as the sum of two binary16 values (22 bits), so fp32 outputs keep
+// their digits.  Each task leaves its tokens' rows in the workspace; the third
+// kernel adds them up in the order of the token's experts and segments.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -38,17 +47,24 @@ namespace q8 {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxT = 32;
 constexpr int kMaxE = 512;
 constexpr int kMaxPairs = kMaxT * 16;  // tokens x chosen experts
-constexpr int kChunk = 256;            // columns of a stage
+constexpr int kGroup = 16;             // most tokens of an entry: an expert with more is listed again
+constexpr int kNT = kGroup / 8;        // MMA tiles of 8 tokens
+constexpr int kMaxEntries = kMaxE + kMaxPairs / 8;
+constexpr int kChunk = 128;            // columns of a stage
+constexpr int kBlocks = kChunk / 32;
 constexpr int kTile = 16 * kChunk;     // bytes of a warp's codes in a stage
-constexpr int kScaleTile = 16 * 32;    // bytes of its scales: rows of up to 20, 32 apart
-constexpr int kWeights = kWarps * (kTile + kScaleTile);
-constexpr int kMaxGrid = 1024;
-constexpr int kDownRows = kWarps * 16;
+constexpr int kScalePitch = 16;        // a row's scales take up to 12 bytes
+constexpr int kStage = kTile + 16 * kScalePitch;
+constexpr int kMaxStages = 8;
+constexpr int kSmem = 227 * 1024 - 7 * 1024;  // beside the routing
+constexpr int kJoin = kWarps * 32 * 4 * kNT * 4;  // sums of warps that share a task
+// What the vectors of one entry may take: two stages of every warp stay beside them.
+constexpr int kMostX = kSmem - kWarps * 2 * kStage;
 
 struct MoeParams {
     const uint16_t *x;      // bf16 [T][ldx]
@@ -58,26 +74,31 @@ struct MoeParams {
     float *y;               // [T][ldy]
     int32_t *ids;           // [T][top_k] or null
     float *weights;         // [T][top_k] or null
-    uint16_t *hi, *lo;      // binary16 [pairs][F]: the hidden units' two parts
-    float *fac;             // [pairs][F / 32]: the factor that undoes a block's scaling
-    uint32_t *tickets;      // [kMaxGrid]
-    float *parts;           // [2 * kMaxGrid][T * kDownRows]
+    float *hidden;          // [pairs][F]
+    float *z;               // [segments][pairs][H]: the experts' outputs
+    void *routing;          // the first kernel's, for the others
     uint32_t *status;
     int64_t ldx, ldl, ldy;
     int32_t T, E, H, F, top_k, renorm;
-    int32_t stages, tok_rows;  // ring; token rows of a stage (T rounded up to 8)
+    int32_t cap;            // tokens of an entry: 8 or 16
 };
 
-// The routing as every CTA holds it.
-struct Routing {
-    uint32_t mask[kMaxE];       // tokens that chose the expert
-    uint16_t expert[kMaxE];     // the chosen experts, in order
-    uint16_t base[kMaxE + 1];   // first pair of each
-    uint8_t token[kMaxPairs];   // the pairs' tokens, by expert, then token
-    float weight[kMaxPairs];    // and weights
-    int16_t id[kMaxPairs];      // [T][top_k]
-    float w[kMaxPairs];         // [T][top_k]
-    int32_t used;               // chosen experts
+// The routing: entries of an expert and up to `cap` of its tokens, by expert,
+// then token; a pair is a token of an entry.
+struct alignas(16) Routing {
+    uint16_t expert[kMaxEntries];
+    uint16_t base[kMaxEntries + 1];  // first pair of each entry
+    uint8_t token[kMaxPairs];        // the pairs' tokens
+    int16_t pair[kMaxPairs];         // [T][top_k]: the pair of each choice, -1 for none
+    float w[kMaxPairs];              // [T][top_k]: its weight
+    int32_t used;                    // entries
+    int32_t most;                    // tokens of the largest
+};
+// What only making it needs; lies where the ring comes later.
+struct Making {
+    uint32_t mask[kMaxE];    // tokens that chose the expert
+    uint16_t first[kMaxE];   // first pair of the expert
+    int16_t id[kMaxPairs];   // [T][top_k]
 };
 
 // A total order of floats as unsigned integers; NaN below everything.
@@ -88,532 +109,605 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 
-__device__ void route(const MoeParams &p, Routing &r, bool report) {
+// One warp's token: its top_k experts by repeated maximum of NK keys a lane.
+template <int NK>
+__device__ void route_token(const MoeParams &p, Routing &r, Making &mk, int t, bool report) {
+    const int lane = threadIdx.x & 31;
+    const float *row = p.logits + t * p.ldl;
+    float v[NK];
+    uint32_t key[NK];
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) v[i] = lane + 32 * i < p.E ? row[lane + 32 * i] : -INFINITY;
+    // this lane's best: the largest key, the lowest index of equal ones
+    uint32_t m = 0;
+    int mi = 0;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        nan = nan || v[i] != v[i];
+        key[i] = order_key(v[i]);
+        if (key[i] > m) m = key[i], mi = lane + 32 * i;
+    }
+    if (report && __any_sync(0xffffffffu, nan) && lane == 0 && p.status) atomicOr(p.status, Q8_DEV_NONFINITE);
+    uint32_t got = 0;  // lane j: the j-th choice
+    int id = -1;
+    for (int j = 0; j < p.top_k; ++j) {
+        const uint32_t best = __reduce_max_sync(0xffffffffu, m);
+        if (best <= kKeyNegInf) break;  // nothing left to choose
+        const uint32_t who = __ballot_sync(0xffffffffu, m == best);
+        int e;
+        if (who & (who - 1))  // equal logits in several lanes
+            e = __reduce_min_sync(0xffffffffu, m == best ? mi : kMaxE);
+        else
+            e = __shfl_sync(0xffffffffu, mi, __ffs(who) - 1);
+        if (lane == j) got = best, id = e;
+        if (m == best && mi == e) {  // its lane takes it out
+            m = 0;
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                if (lane + 32 * i == e) key[i] = 0;
+                if (key[i] > m) m = key[i], mi = lane + 32 * i;
+            }
+        }
+    }
+    const float l = __uint_as_float((got & 0x80000000u) ? got ^ 0x80000000u : ~got);
+    const float top = __shfl_sync(0xffffffffu, l, 0);
+    const float mine = id < 0 ? 0.f : (l == top ? 1.f : expf(l - top));
+    float z = mine;
+    if (!p.renorm) {
+        z = 0.f;
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+            if (lane + 32 * i < p.E && v[i] == v[i]) z += v[i] == top ? 1.f : expf(v[i] - top);
+    }
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if (lane < p.top_k) {
+        mk.id[t * p.top_k + lane] = static_cast<int16_t>(id);
+        r.w[t * p.top_k + lane] = id < 0 ? 0.f : __fdiv_rn(mine, z);
+        if (id >= 0) atomicOr(&mk.mask[id], 1u << t);
+    }
+}
+
+__device__ void route(const MoeParams &p, Routing &r, Making &mk, bool report) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int e = tid; e < p.E; e += kThreads) r.mask[e] = 0;
+    for (int e = tid; e < p.E; e += kThreads) mk.mask[e] = 0;
     __syncthreads();
     for (int t = warp; t < p.T; t += kWarps) {
-        const float *row = p.logits + t * p.ldl;
-        uint32_t key[kMaxE / 32];
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < kMaxE / 32; ++i) {
-            const int e = lane + 32 * i;
-            key[i] = 0;
-            if (e < p.E) {
-                const float v = row[e];
-                key[i] = order_key(v);
-                nan = nan || v != v;
-            }
-        }
-        if (report && __any_sync(0xffffffffu, nan) && lane == 0 && p.status) atomicOr(p.status, Q8_DEV_NONFINITE);
-        float top = 0.f, z = 0.f, mine = 0.f;
-        int mine_id = -1;
-        for (int j = 0; j < p.top_k; ++j) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < kMaxE / 32; ++i) m = max(m, key[i]);
-            const uint32_t best = __reduce_max_sync(0xffffffffu, m);
-            if (best <= kKeyNegInf) break;  // nothing left to choose
-            int at = kMaxE;
-#pragma unroll
-            for (int i = kMaxE / 32 - 1; i >= 0; --i)
-                if (key[i] == best) at = lane + 32 * i;
-            const int e = __reduce_min_sync(0xffffffffu, at);
-#pragma unroll
-            for (int i = 0; i < kMaxE / 32; ++i)
-                if (lane + 32 * i == e) key[i] = 0;
-            const float v = __uint_as_float((best & 0x80000000u) ? best ^ 0x80000000u : ~best);
-            if (j == 0) top = v;
-            const float ex = v == top ? 1.f : expf(v - top);
-            if (p.renorm) z += ex;
-            if (lane == j) mine = ex, mine_id = e;
-            if (lane == 0) atomicOr(&r.mask[e], 1u << t);
-        }
-        if (!p.renorm) {
-            for (int e = lane; e < p.E; e += 32) {
-                const float v = row[e];
-                if (v == v) z += v == top ? 1.f : expf(v - top);
-            }
-            for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        }
-        if (lane < p.top_k) {
-            r.id[t * p.top_k + lane] = static_cast<int16_t>(mine_id);
-            r.w[t * p.top_k + lane] = mine_id < 0 ? 0.f : __fdiv_rn(mine, z);
-        }
+        if (p.E <= 32)
+            route_token<1>(p, r, mk, t, report);
+        else if (p.E <= 128)
+            route_token<4>(p, r, mk, t, report);
+        else
+            route_token<kMaxE / 32>(p, r, mk, t, report);
     }
     __syncthreads();
     if (warp == 0) {
-        int used = 0, pairs = 0;
+        int used = 0, pairs = 0, most = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
-            const uint32_t m = e < p.E ? r.mask[e] : 0u;
-            const uint32_t some = __ballot_sync(0xffffffffu, m != 0);
-            int n = __popc(m), run = n;
+            const int n = e < p.E ? __popc(mk.mask[e]) : 0, parts = (n + p.cap - 1) / p.cap;
+            int run = n, erun = parts;
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += v;
+                const int v = __shfl_up_sync(0xffffffffu, run, o), ev = __shfl_up_sync(0xffffffffu, erun, o);
+                if (lane >= o) run += v, erun += ev;
             }
-            if (m) {
-                const int i = used + __popc(some & ((1u << lane) - 1));
-                r.expert[i] = static_cast<uint16_t>(e);
-                r.base[i] = static_cast<uint16_t>(pairs + run - n);
+            if (n > 0) mk.first[e] = static_cast<uint16_t>(pairs + run - n);
+            for (int i = 0; i < parts; ++i) {
+                r.expert[used + erun - parts + i] = static_cast<uint16_t>(e);
+                r.base[used + erun - parts + i] = static_cast<uint16_t>(pairs + run - n + i * p.cap);
             }
-            used += __popc(some);
+            most = max(most, min(n, p.cap));
+            used += __shfl_sync(0xffffffffu, erun, 31);
             pairs += __shfl_sync(0xffffffffu, run, 31);
         }
+        most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) {
             r.base[used] = static_cast<uint16_t>(pairs);
             r.used = used;
+            r.most = most;
         }
     }
     __syncthreads();
-    for (int i = warp; i < r.used; i += kWarps) {
-        const int e = r.expert[i];
-        const uint32_t m = r.mask[e];
-        if ((m >> lane) & 1) {
-            const int at = r.base[i] + __popc(m & ((1u << lane) - 1));
-            r.token[at] = static_cast<uint8_t>(lane);
-            for (int j = 0; j < p.top_k; ++j)
-                if (r.id[lane * p.top_k + j] == e) r.weight[at] = r.w[lane * p.top_k + j];
+    for (int i = tid; i < p.T * p.top_k; i += kThreads) {
+        const int e = mk.id[i], t = i / p.top_k;
+        int at = -1;
+        if (e >= 0) {
+            at = mk.first[e] + __popc(mk.mask[e] & ((1u << t) - 1));
+            r.token[at] = static_cast<uint8_t>(t);
         }
+        r.pair[i] = static_cast<int16_t>(at);
     }
     __syncthreads();
 }
 
-// 16-byte chunk c of a weight tile's row r, and of a token row n: placed so
-// that the MMA operand reads hit every bank once.
-__device__ __forceinline__ uint32_t weight_at(int r, int c) {
-    const uint32_t m = r * (kChunk / 16) + c;
-    return (m ^ ((m >> 3) & 7)) * 16;
+// Chunk c (16 bytes) of a weight tile's row r: placed so that the MMA operand
+// reads hit every bank once.
+__device__ __forceinline__ uint32_t weight_at(int r, int c) { return (r * 8 + (c ^ ((r & 3) << 1))) * 16; }
+// Bytes from one token's vector to the next, for the same reason: 64 past a multiple of 128
+// for 2-byte values, 16 past one for the two parts of a value (4 bytes).
+template <bool DOWN>
+__device__ __forceinline__ int pitch_of(int columns) {
+    return DOWN ? columns * 4 + 16 : columns * 2 + ((columns * 2) % 128 == 0 ? 64 : 0);
 }
-__device__ __forceinline__ uint32_t token_at(int n, int c) { return (n * 32 + (c ^ ((n & 1) << 2))) * 16; }
 
-// One warp's weight tile: 16 rows (8 from row0, 8 from row8) x 256 columns
-// from col, of a [rows][K] matrix.
-__device__ __forceinline__ void load_tile(uint32_t codes, uint32_t scales, const int8_t *q, const uint16_t *s, int64_t row0,
-                                          int64_t row8, int K, int col, int lane) {
-    const int c = lane & 15;
-    if (col + c * 16 < K) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 2 * i + (lane >> 4);
-            const int64_t row = r < 8 ? row0 + r : row8 + (r - 8);
-            cp_async16(codes + weight_at(r, c), q + row * K + col + c * 16);
-        }
+// A warp's weight tiles as they come: 16 rows (8 from row0, 8 from row8) of a
+// [rows][K] matrix, 128 columns at a time.  Pointers move with the columns.
+struct TileLoad {
+    const int8_t *a, *b;   // this lane's place in rows 0..7 and 8..15
+    const uint16_t *s;     // this lane's row of scales (lanes 0..15), at the stage's columns
+    int64_t row0, row8;
+    int col;
+
+    __device__ __forceinline__ void begin(const int8_t *q, const uint16_t *sc, int64_t r0, int64_t r8, int K, int c0, int lane) {
+        row0 = r0, row8 = r8, col = c0;
+        a = q + (r0 + (lane >> 3)) * K + c0 + (lane & 7) * 16;
+        b = q + (r8 + (lane >> 3)) * K + c0 + (lane & 7) * 16;
+        s = sc + (lane < 8 ? r0 + lane : r8 + (lane & 7)) * (K >> 5) + (c0 >> 5);
     }
-    const int nb = K >> 5;
-    if ((K & 255) == 0) {
-        if (lane < 16) {
-            const int64_t row = lane < 8 ? row0 + lane : row8 + (lane - 8);
-            cp_async16(scales + lane * 32, s + row * nb + (col >> 5));
+    // codes: this lane's first chunk in the stage; scales: the warp's
+    __device__ __forceinline__ void load(uint32_t codes, uint32_t scales, const uint16_t *sc, int K, int lane) {
+        if (col + (lane & 7) * 16 < K) {
+            cp_async16(codes, a);
+            cp_async16(codes + 4 * kChunk, a + 4 * K);
+            cp_async16(codes + 8 * kChunk, b);
+            cp_async16(codes + 12 * kChunk, b + 4 * K);
         }
-    } else {
-        // rows of scales start at any 2-byte offset: take the aligned words
-        // that hold this chunk's (the array ends on a word: rows % 32 == 0)
-        const int words = min(5, (min(8, nb - (col >> 5)) + 2) >> 1);
+        if ((K & (kChunk - 1)) == 0) {
+            if (lane < 16) cp_async8(scales + lane * kScalePitch, s);
+        } else {
+            // rows of scales start at any 2-byte offset: take the aligned words
+            // that hold this chunk's (the array ends on a word: rows % 32 == 0)
+            constexpr int kWords = kBlocks / 2 + 1;
+            const int nb = K >> 5, words = min(kWords, (min(kBlocks, nb - (col >> 5)) + 2) >> 1);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int j = i * 32 + lane;
-            const int r = j / 5, wd = j - r * 5;
-            if (r < 16 && wd < words) {
-                const int64_t row = r < 8 ? row0 + r : row8 + (r - 8);
-                const int64_t at = (row * nb + (col >> 5)) & ~int64_t(1);
-                if (at + wd * 2 < (row + 1) * nb) cp_async4(scales + r * 32 + wd * 4, s + at + wd * 2);
+            for (int i = 0; i < (16 * kWords + 31) / 32; ++i) {
+                const int j = i * 32 + lane;
+                const int r = j / kWords, wd = j - r * kWords;
+                if (r < 16 && wd < words) {
+                    const int64_t row = r < 8 ? row0 + r : row8 + (r - 8);
+                    const int64_t at = (row * nb + (col >> 5)) & ~int64_t(1);
+                    if (at + wd * 2 < (row + 1) * nb) cp_async4(scales + r * kScalePitch + wd * 4, sc + at + wd * 2);
+                }
             }
         }
+        a += kChunk, b += kChunk, s += kBlocks, col += kChunk;
     }
-}
+};
 
-// The 8 scales of a row's chunk, as four pairs.
-__device__ __forceinline__ void row_scales(uint32_t scales, int r, bool odd, uint32_t *w) {
-    const uint4 a = lds128(scales + r * 32);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-    if (odd) {
-        const uint32_t last = lds32(scales + r * 32 + 16);
-        w[0] = __funnelshift_r(a.x, a.y, 16);
-        w[1] = __funnelshift_r(a.y, a.z, 16);
-        w[2] = __funnelshift_r(a.z, a.w, 16);
-        w[3] = __funnelshift_r(a.w, last, 16);
+// The scales of a row's chunk, as pairs.
+struct Scales {
+    uint32_t w[kBlocks / 2];
+    __device__ __forceinline__ void get(uint32_t at, bool odd) {
+        const uint4 a = lds128(at);
+        w[0] = odd ? __funnelshift_r(a.x, a.y, 16) : a.x;
+        w[1] = odd ? __funnelshift_r(a.y, a.z, 16) : a.y;
     }
-}
-__device__ __forceinline__ float pick_scale(const uint32_t *w, int b) {
-    return f16_bits_to_f32((b & 1) ? w[b >> 1] >> 16 : w[b >> 1] & 0xFFFFu);
-}
+    __device__ __forceinline__ float of(int b) const {
+        const __half2 h = *reinterpret_cast<const __half2 *>(&w[b >> 1]);
+        return (b & 1) ? __high2float(h) : __low2float(h);
+    }
+};
 
+// Waits for the oldest stage: of `stages` (2, 3, 4, 6 or 8), all but two may still be under way.
 __device__ __forceinline__ void wait_stage(int stages) {
-    // groups still under way: all but the oldest of stages - 1
-    switch (stages) {
-        case 2: cp_async_wait<0>(); break;
-        case 3: cp_async_wait<1>(); break;
-        case 4: cp_async_wait<2>(); break;
-        case 5: cp_async_wait<3>(); break;
-        default: cp_async_wait<4>(); break;
+    if (stages == 4)
+        cp_async_wait<2>();
+    else if (stages == 3)
+        cp_async_wait<1>();
+    else if (stages == 6)
+        cp_async_wait<4>();
+    else if (stages == 8)
+        cp_async_wait<6>();
+    else
+        cp_async_wait<0>();
+}
+
+constexpr int kRow8 = 8 * kChunk;  // from a tile's row g to row g + 8
+// 16 rows x 32 columns of codes as two binary16 MMA operands (8 columns a lane).
+struct Codes {
+    uint32_t a[4], b[4];
+    __device__ __forceinline__ void get(uint32_t at) {
+        const uint2 w0 = lds64(at), w1 = lds64(at + kRow8);
+        codes4_to_f16x2(w0.x, a[0], a[2]);
+        codes4_to_f16x2(w1.x, a[1], a[3]);
+        codes4_to_f16x2(w0.y, b[0], b[2]);
+        codes4_to_f16x2(w1.y, b[1], b[3]);
+    }
+    // d = (these codes) x, x this lane's 8 values
+    __device__ __forceinline__ void mul(float *d, const uint4 &x) const {
+        mma_f16_16816_new(d[0], d[1], d[2], d[3], a[0], a[1], a[2], a[3], x.x, x.y);
+        mma_f16_16816(d[0], d[1], d[2], d[3], b[0], b[1], b[2], b[3], x.z, x.w);
+    }
+    // the same with x in two parts: values 0..3 (high, low), then 4..7
+    __device__ __forceinline__ void mul2(float *d, const uint4 &x, const uint4 &y) const {
+        mma_f16_16816_new(d[0], d[1], d[2], d[3], a[0], a[1], a[2], a[3], x.z, x.w);
+        mma_f16_16816(d[0], d[1], d[2], d[3], b[0], b[1], b[2], b[3], y.z, y.w);
+        mma_f16_16816(d[0], d[1], d[2], d[3], a[0], a[1], a[2], a[3], x.x, x.y);
+        mma_f16_16816(d[0], d[1], d[2], d[3], b[0], b[1], b[2], b[3], y.x, y.y);
+    }
+};
+// 2^(14 - e) and 2^(e - 14) for a largest magnitude m of exponent e: m goes to [2^14, 2^15)
+// (zero, subnormal and non-finite m keep factors in range)
+__device__ __forceinline__ int scale_exponent(float m) { return min(max(static_cast<int>(__float_as_uint(m) >> 23), 30), 240); }
+__device__ __forceinline__ float scale_up(int ex) { return __uint_as_float(static_cast<uint32_t>(268 - ex) << 23); }
+__device__ __forceinline__ float scale_down(int ex) { return __uint_as_float(static_cast<uint32_t>(ex - 14) << 23); }
+
+
+// A stage: acc += (tile) x for N MMA tiles of tokens; x is this lane's place in the vectors (token
+// g, its 8 of each block's columns), tok8 on for token g + 8.  ALL: the stage holds kBlocks blocks
+// (no test in the way of overlapping them).
+template <bool DOWN, int N, bool ALL>
+__device__ __forceinline__ void stage_product(uint32_t codes, const uint32_t (&code_at)[kBlocks], const Scales &s0, const Scales &s1,
+                                              int nb, uint32_t x, int tok8, float (&acc)[kNT][4]) {
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+        if (!ALL && b >= nb) break;
+        Codes w;
+        w.get(codes + code_at[b]);
+        const float f0 = s0.of(b), f1 = s1.of(b);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float d[4];
+            const uint32_t from = x + b * (DOWN ? 128 : 64) + i * tok8;
+            if constexpr (DOWN)
+                w.mul2(d, lds128(from), lds128(from + 16));
+            else
+                w.mul(d, lds128(from));
+            acc[i][0] = fmaf(f0, d[0], acc[i][0]);
+            acc[i][1] = fmaf(f0, d[1], acc[i][1]);
+            acc[i][2] = fmaf(f1, d[2], acc[i][2]);
+            acc[i][3] = fmaf(f1, d[3], acc[i][3]);
+        }
     }
 }
 
-__global__ void __launch_bounds__(kThreads) moe_gate_up_kernel(const __grid_constant__ MoeParams p) {
+// A token's x in shared memory, bf16 as copied there, to binary16 of x 2^(14 - e) in place (a
+// warp's work; loops are kept short: this code runs once, and what it costs is fetching it).
+__device__ int scale_x(uint32_t at, int n) {
+    const int lane = threadIdx.x & 31;
+    uint32_t m = 0;  // the largest magnitude's bits, in either half
+#pragma unroll 2
+    for (int c = lane; c < n / 8; c += 32) {
+        const uint4 v = lds128(at + c * 16);
+        m = __vmaxu2(__vmaxu2(m, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu)), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    }
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+    const int e = scale_exponent(__uint_as_float(m << 16));
+    const float up = scale_up(e);
+#pragma unroll 2
+    for (int c = lane; c < n / 8; c += 32) {
+        const uint4 v = lds128(at + c * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = f32x2_to_f16x2(bf16lo_f32(w[i]) * up, bf16hi_f32(w[i]) * up);
+        sts128(at + c * 16, make_uint4(h[0], h[1], h[2], h[3]));
+    }
+    return e;
+}
+// Hidden units likewise: four fp32 values become their four high parts and four low parts.
+__device__ int scale_hidden(uint32_t at, int n) {
+    const int lane = threadIdx.x & 31;
+    float m = 0.f;
+#pragma unroll 2
+    for (int c = lane; c < n / 4; c += 32) {
+        const uint4 v = lds128(at + c * 16);
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(__uint_as_float(v.x)), fabsf(__uint_as_float(v.y))),
+                           fmaxf(fabsf(__uint_as_float(v.z)), fabsf(__uint_as_float(v.w)))));
+    }
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int e = scale_exponent(m);
+    const float up = scale_up(e);
+#pragma unroll 2
+    for (int c = lane; c < n / 4; c += 32) {
+        const uint4 v = lds128(at + c * 16);
+        const float x[4] = {__uint_as_float(v.x) * up, __uint_as_float(v.y) * up, __uint_as_float(v.z) * up, __uint_as_float(v.w) * up};
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            h[i] = f32x2_to_f16x2(x[2 * i], x[2 * i + 1]);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+            l[i] = f32x2_to_f16x2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
+        }
+        sts128(at + c * 16, make_uint4(h[0], h[1], l[0], l[1]));
+    }
+    return e;
+}
+
+// Hidden units of a segment of the down kernel: F in equal parts (of whole chunks) of at most
+// 1024, or 512 where an entry has more than 8 tokens.
+__device__ __forceinline__ int segment_of(int most, int F) {
+    const int n = (F + (most <= 8 ? 1023 : 511)) / (most <= 8 ? 1024 : 512);
+    return ((F + n - 1) / n + kChunk - 1) / kChunk * kChunk;
+}
+
+template <bool DOWN>
+__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ MoeParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Routing r;
-    __shared__ float s_max[kWarps][kMaxT];
+    __shared__ int s_ex[2][kGroup];  // the exponents that the vectors in shared memory were scaled by
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    pdl_launch_dependents();
-    route(p, r, blockIdx.x == 0);
-    if (blockIdx.x == 0) {
-        for (int i = tid; i < p.T * p.top_k; i += kThreads) {
-            if (p.ids) p.ids[i] = r.id[i];
-            if (p.weights) p.weights[i] = r.w[i];
-        }
-    }
-    const int blocks = p.F >> 5, chunks = (p.H + kChunk - 1) / kChunk;
-    const int64_t tasks = static_cast<int64_t>(r.used) * blocks;
-    const int64_t t0 = tasks * blockIdx.x / gridDim.x, t1 = tasks * (blockIdx.x + 1) / gridDim.x;
-    if (t0 >= t1) return;
-
-    const int stage_bytes = kWeights + p.tok_rows * 512;
-    const uint32_t ring = smem_addr(smem);
-    const int64_t total = (t1 - t0) * chunks;
-    int64_t loaded = 0;
-    int ld_i = static_cast<int>(t0 / blocks), ld_b = static_cast<int>(t0 % blocks), ld_c = 0, ld_slot = 0;
-    auto load = [&]() {
-        if (loaded < total) {
-            const uint32_t st = ring + ld_slot * stage_bytes;
-            const int64_t rows = static_cast<int64_t>(r.expert[ld_i]) * 2 * p.F;
-            const int unit = ld_b * 32 + warp * 8, col = ld_c * kChunk;
-            load_tile(st + warp * kTile, st + kWarps * kTile + warp * kScaleTile, p.q13, p.s13, rows + unit, rows + p.F + unit,
-                      p.H, col, lane);
-            const int base = r.base[ld_i], n = r.base[ld_i + 1] - base;
-            if (col + lane * 8 < p.H)
-                for (int i = warp; i < n; i += kWarps)
-                    cp_async16(st + kWeights + token_at(i, lane), p.x + r.token[base + i] * p.ldx + col + lane * 8);
-            ++loaded;
-            if (++ld_c == chunks) {
-                ld_c = 0;
-                if (++ld_b == blocks) ld_b = 0, ++ld_i;
-            }
-        }
-        ld_slot = ld_slot + 1 == p.stages ? 0 : ld_slot + 1;
-        cp_async_commit();
-    };
-    for (int i = 0; i < p.stages - 1; ++i) load();
-
-    int slot = 0, ei = static_cast<int>(t0 / blocks), blk = static_cast<int>(t0 % blocks);
-    const bool odd0 = ((p.H >> 5) & 1) != 0;
-    for (int64_t task = t0; task < t1; ++task) {
-        const int base = r.base[ei], n = r.base[ei + 1] - base, nt = (n + 7) >> 3;
-        float acc[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        const int64_t rows = static_cast<int64_t>(r.expert[ei]) * 2 * p.F;
-        const bool oddg = odd0 && ((rows + blk * 32 + warp * 8 + g) & 1), oddu = odd0 && ((rows + p.F + blk * 32 + warp * 8 + g) & 1);
-        for (int c = 0; c < chunks; ++c) {
-            wait_stage(p.stages);
-            __syncthreads();
-            load();
-            const uint32_t st = ring + slot * stage_bytes, codes = st + warp * kTile;
-            const uint32_t sc = st + kWarps * kTile + warp * kScaleTile, xs = st + kWeights;
-            uint32_t sg[4], su[4];
-            row_scales(sc, g, oddg, sg);
-            row_scales(sc, g + 8, oddu, su);
-            const int nb = min(8, (p.H >> 5) - c * 8);
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                if (b < nb) {
-                    const uint2 w0 = lds64(codes + weight_at(g, 2 * b + (t >> 1)) + (t & 1) * 8);
-                    const uint2 w1 = lds64(codes + weight_at(g + 8, 2 * b + (t >> 1)) + (t & 1) * 8);
-                    uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-                    codes4_to_bf16x2(w0.x, a0, a2);
-                    codes4_to_bf16x2(w1.x, a1, a3);
-                    codes4_to_bf16x2(w0.y, b0, b2);
-                    codes4_to_bf16x2(w1.y, b1, b3);
-                    const float f0 = pick_scale(sg, b), f1 = pick_scale(su, b);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (i < nt) {
-                            const uint4 xv = lds128(xs + token_at(i * 8 + g, 4 * b + t));
-                            float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
-                            mma_bf16_16816(d0, d1, d2, d3, a0, a1, a2, a3, xv.x, xv.y);
-                            mma_bf16_16816(d0, d1, d2, d3, b0, b1, b2, b3, xv.z, xv.w);
-                            acc[i][0] = fmaf(f0, d0, acc[i][0]);
-                            acc[i][1] = fmaf(f0, d1, acc[i][1]);
-                            acc[i][2] = fmaf(f1, d2, acc[i][2]);
-                            acc[i][3] = fmaf(f1, d3, acc[i][3]);
-                        }
-                    }
-                }
-            }
-            slot = slot + 1 == p.stages ? 0 : slot + 1;
-        }
-        // SwiGLU; the largest hidden unit of each token's block of 32 (four warps)
-        float act[4][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float a = acc[i][j];
-                act[i][j] = a / (1.0f + expf(-a)) * acc[i][2 + j];
-                if (i < nt) {
-                    float m = fabsf(act[i][j]);
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    if (g == 0) s_max[warp][i * 8 + 2 * t + j] = m;
-                }
-            }
-        }
+    constexpr int kWords = sizeof(Routing) / 16;
+    static_assert(kWords <= kThreads, "a thread copies 16 bytes of the routing");
+    if constexpr (DOWN) {
+        pdl_wait_prior();
+        if (tid < kWords) reinterpret_cast<uint4 *>(&r)[tid] = __ldcg(static_cast<const uint4 *>(p.routing) + tid);
+        pdl_launch_dependents();  // the third kernel may read the routing (the first has ended) before its wait
         __syncthreads();
-        const int unit = blk * 32 + warp * 8 + g;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int tok = i * 8 + 2 * t + j;
-                if (tok < n) {
-                    const float m = fmaxf(fmaxf(s_max[0][tok], s_max[1][tok]), fmaxf(s_max[2][tok], s_max[3][tok]));
-                    // the largest to [2^14, 2^15); a block of zeros or of non-finite units keeps a factor in range
-                    const int ex = min(max(static_cast<int>(__float_as_uint(m) >> 23), 30), 240);
-                    const float v = act[i][j] * __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
-                    const __half h = __float2half_rn(v);
-                    const __half l = __float2half_rn(v - __half2float(h));
-                    const int64_t at = static_cast<int64_t>(base + tok) * p.F + unit;
-                    p.hi[at] = __half_as_ushort(h);
-                    p.lo[at] = __half_as_ushort(l);
-                    if (warp == 0 && g == 0)
-                        p.fac[static_cast<int64_t>(base + tok) * blocks + blk] = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
-                }
+    } else {
+        pdl_launch_dependents();
+        Making &mk = *reinterpret_cast<Making *>(smem);
+        route(p, r, mk, blockIdx.x == 0);
+        if (blockIdx.x == 0) {
+            for (int i = tid; i < p.T * p.top_k; i += kThreads) {
+                if (p.ids) p.ids[i] = mk.id[i];
+                if (p.weights) p.weights[i] = r.w[i];
             }
+            if (tid < kWords) static_cast<uint4 *>(p.routing)[tid] = reinterpret_cast<const uint4 *>(&r)[tid];
+            __syncthreads();
         }
-        if (++blk == blocks) blk = 0, ++ei;
     }
-    cp_async_wait<0>();
-}
+    if (r.used == 0) return;
 
-__global__ void __launch_bounds__(kThreads) moe_down_kernel(const __grid_constant__ MoeParams p) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Routing r;
-    __shared__ uint32_t s_last;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    route(p, r, false);
-    const int chunks = (p.F + kChunk - 1) / kChunk, tiles = (p.H + kDownRows - 1) / kDownRows, blocks = p.F >> 5;
-    const int64_t item = static_cast<int64_t>(r.used) * chunks;  // units of one tile of output rows
-    const int64_t total = item * tiles;
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(1));
-    const int64_t u0 = per * blockIdx.x, u1 = min(u0 + per, total);
-    const int stage_bytes = kWeights + p.tok_rows * (1024 + 32);
-    const uint32_t ring = smem_addr(smem);
-    float *const s_y = reinterpret_cast<float *>(smem + p.stages * stage_bytes);  // [T][kDownRows]
+    // ---- the list of tasks: group (an entry, for DOWN with a segment) major, then tiles of rows --
+    const int K = DOWN ? p.F : p.H;                          // columns of the weights
+    const int rows8 = (r.most + 7) & ~7;
+    const int seg = DOWN ? segment_of(r.most, K) : K;        // columns of a group
+    const int nseg = (K + seg - 1) / seg;
+    const int tiles = DOWN ? p.H / 16 : p.F / 8;
+    const int groups = r.used * nseg;
+    const uint32_t tasks = static_cast<uint32_t>(groups) * tiles;
+    const uint32_t t0 = static_cast<uint32_t>(static_cast<uint64_t>(tasks) * blockIdx.x / gridDim.x);
+    const uint32_t t1 = static_cast<uint32_t>(static_cast<uint64_t>(tasks) * (blockIdx.x + 1) / gridDim.x);
+    if (t0 >= t1) return;
+    const int mine = static_cast<int>(t1 - t0);
 
-    int64_t loaded = u0;
-    int ld_rt = 0, ld_i = 0, ld_c = 0, ld_slot = 0;
-    if (u0 < u1) {
-        ld_rt = static_cast<int>(u0 / item);
-        const int64_t in = u0 - ld_rt * item;
-        ld_i = static_cast<int>(in / chunks);
-        ld_c = static_cast<int>(in - static_cast<int64_t>(ld_i) * chunks);
+    // ---- shared memory: one or two groups' vectors, the ring, sums of warps that share ------------
+    const int pitch = pitch_of<DOWN>(DOWN ? seg : K), tok8 = 8 * pitch, x_bytes = rows8 * pitch;
+    // warps to a task: what makes the rounds of tasks shortest, a chunk's time for joining included
+    int share = 1;
+    {
+        const int chunks = (min(seg, K) + kChunk - 1) / kChunk;
+        int best = (mine + kWarps - 1) / kWarps * chunks;
+        for (int s = 2; s <= 8; s *= 2) {
+            const int cost = (mine * s + kWarps - 1) / kWarps * ((chunks + s - 1) / s + 1);
+            if (cost < best && x_bytes + kJoin + kWarps * 2 * kStage <= kSmem) best = cost, share = s;
+        }
     }
-    int rt = ld_rt, ei = ld_i, ch = ld_c;
-    // weights do not depend on the first kernel, hidden units do
-    auto load_weights = [&](uint32_t st, int a_rt, int a_i, int a_c) {
-        const int row = a_rt * kDownRows + warp * 16;
-        if (row < p.H) {
-            const int64_t rows = static_cast<int64_t>(r.expert[a_i]) * p.H + row;
-            load_tile(st + warp * kTile, st + kWarps * kTile + warp * kScaleTile, p.q2, p.s2, rows, rows + 8, p.F, a_c * kChunk, lane);
-        }
+    const int teams = kWarps / share, team = warp / share, part = warp - team * share;
+    const int join = share > 1 ? kJoin : 0;
+    const int busy = min(mine, teams) * share;
+    const int bufs = 2 * x_bytes + join + busy * 3 * kStage <= kSmem ? 2 : 1;
+    int stages = min((kSmem - bufs * x_bytes - join) / (busy * kStage), kMaxStages);
+    stages -= stages == 5 || stages == 7 ? 1 : 0;
+    const uint32_t xs = smem_addr(smem), ring = xs + bufs * x_bytes + warp * stages * kStage, ring_end = ring + stages * kStage;
+    float *const s_join = reinterpret_cast<float *>(smem + bufs * x_bytes + busy * stages * kStage);
+    const bool works = team < mine;
+
+    // ---- this warp's weights: tasks team, team + teams, ...; of each group's columns its share ----
+    auto chunk0 = [&](int columns) { return (columns + kChunk - 1) / kChunk * part / share; };
+    auto chunk1 = [&](int columns) { return (columns + kChunk - 1) / kChunk * (part + 1) / share; };
+    struct At {
+        int task;          // of this CTA
+        int group, tile;
     };
-    auto load_hidden = [&](uint32_t st, int a_i, int a_c) {
-        const int base = r.base[a_i], n = r.base[a_i + 1] - base, col = a_c * kChunk;
-        const uint32_t hs = st + kWeights;
-        if (col + lane * 8 < p.F)
-            for (int i = warp; i < n; i += kWarps) {
-                const int64_t at = static_cast<int64_t>(base + i) * p.F + col + lane * 8;
-                cp_async16(hs + token_at(i, lane), p.hi + at);
-                cp_async16(hs + p.tok_rows * 512 + token_at(i, lane), p.lo + at);
-            }
-        const int nb = min(8, blocks - a_c * 8);
-        for (int j = tid; j < n * 8; j += kThreads)
-            if ((j & 7) < nb)
-                cp_async4(hs + p.tok_rows * 1024 + (j & 7) * (p.tok_rows * 4) + (j >> 3) * 4,
-                          p.fac + static_cast<int64_t>(base + (j >> 3)) * blocks + a_c * 8 + (j & 7));
+    auto enter = [&](At &a) {
+        const uint32_t n = t0 + a.task;
+        a.group = static_cast<int>(n / tiles);
+        a.tile = static_cast<int>(n - a.group * tiles);
     };
-    auto step = [&](int &a_rt, int &a_i, int &a_c) {
-        if (++a_c == chunks) {
-            a_c = 0;
-            if (++a_i == r.used) a_i = 0, ++a_rt;
-        }
+    auto next = [&](At &a) {
+        a.task += teams;
+        a.tile += teams;
+        while (a.tile >= tiles) a.tile -= tiles, ++a.group;
     };
+    auto columns_of = [&](int group) { return DOWN ? min(seg, K - group % nseg * seg) : K; };
+    At ld = {team, 0, 0};
+    if (works) enter(ld);
+    TileLoad tile;
+    int ld_left = 0;  // chunks of the task still to load; 0: begin the next
+    uint32_t ld_at = ring;
+    const uint32_t code_to = weight_at(lane >> 3, lane & 7);
+    const int8_t *const q = DOWN ? p.q2 : p.q13;
+    const uint16_t *const sc = DOWN ? p.s2 : p.s13;
     auto load = [&]() {
-        if (loaded < u1) {
-            const uint32_t st = ring + ld_slot * stage_bytes;
-            load_weights(st, ld_rt, ld_i, ld_c);
-            load_hidden(st, ld_i, ld_c);
-            ++loaded;
-            step(ld_rt, ld_i, ld_c);
+        while (ld_left == 0 && ld.task < mine) {
+            const int cols = columns_of(ld.group), c0 = chunk0(cols);
+            ld_left = chunk1(cols) - c0;
+            const int64_t e = r.expert[DOWN ? ld.group / nseg : ld.group];
+            const int from = (DOWN ? ld.group % nseg * seg : 0) + c0 * kChunk;
+            if constexpr (DOWN) {
+                const int64_t row = e * p.H + ld.tile * 16;
+                tile.begin(q, sc, row, row + 8, K, from, lane);
+            } else {
+                const int64_t row = e * 2 * p.F + ld.tile * 8;
+                tile.begin(q, sc, row, row + p.F, K, from, lane);
+            }
+            next(ld);
         }
-        ld_slot = ld_slot + 1 == p.stages ? 0 : ld_slot + 1;
+        if (ld_left > 0) {
+            tile.load(ld_at + code_to, ld_at + kTile, sc, K, lane);
+            --ld_left;
+        }
+        ld_at = ld_at + kStage == ring_end ? ring : ld_at + kStage;
         cp_async_commit();
     };
-    pdl_wait_prior();
-    if (r.used == 0) {
-        for (int64_t i = blockIdx.x * kThreads + tid; i < static_cast<int64_t>(p.T) * p.H; i += gridDim.x * kThreads)
-            p.y[i / p.H * p.ldy + i % p.H] = 0.f;
-        return;
-    }
-    if (u0 >= u1) return;
-    for (int i = 0; i < p.stages - 1; ++i) load();
+    if (works)
+#pragma unroll 1
+        for (int i = 0; i < stages - 1; ++i) load();
 
-    const bool odd = ((p.F >> 5) & 1) != 0;
-    int slot = 0;
-    int64_t u = u0;
-    while (u < u1) {
-        const int64_t seg0 = u, tile0 = rt * item, tile1 = tile0 + item, end = min(u1, tile1);
-        const int this_rt = rt;
-        for (int i = lane; i < p.T * 16; i += 32) s_y[(i >> 4) * kDownRows + warp * 16 + (i & 15)] = 0.f;
+    uint32_t code_at[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) code_at[b] = weight_at(g, 2 * b + (t >> 1)) + (t & 1) * 8;
+    // rows of a tile start at even places, so the parity of a row's first scale is that of g
+    const bool odd = ((K >> 5) & 1) != 0 && (g & 1);
+    uint32_t at = ring;
+    At now = {team, 0, 0};
+    enter(now);
+    const int g_last = static_cast<int>((t1 - 1) / tiles);
+    for (int gb = static_cast<int>(t0 / tiles); gb <= g_last; gb += bufs) {
+        // ---- the vectors of groups gb .. gb + bufs - 1, a warp a token -----------------------------
+        if (gb != static_cast<int>(t0 / tiles)) __syncthreads();  // nobody reads the ones before any more
+        auto vectors = [&](auto take) {
+#pragma unroll 1
+            for (int i = warp; i < bufs * kGroup; i += kWarps) {
+                const int buf = i / kGroup, k = i - buf * kGroup, group = gb + buf;
+                if (group > g_last) break;
+                const int entry = DOWN ? group / nseg : group, base = r.base[entry];
+                if (k < r.base[entry + 1] - base) take(buf, k, group, base + k, xs + buf * x_bytes + k * pitch);
+            }
+        };
+        vectors([&](int, int, int group, int pr, uint32_t to) {
+            const void *from;
+            int n;  // 16-byte copies
+            if constexpr (DOWN) {
+                from = p.hidden + static_cast<int64_t>(pr) * p.F + group % nseg * seg;
+                n = columns_of(group) / 4;
+            } else {
+                from = p.x + r.token[pr] * p.ldx;
+                n = p.H / 8;
+            }
+#pragma unroll 1
+            for (int c = lane; c < n; c += 32) cp_async16(to + c * 16, static_cast<const uint4 *>(from) + c);
+        });
+        cp_async_commit();
+        cp_async_wait<0>();
         __syncwarp();
-        while (u < end) {
-            const int base = r.base[ei], n = r.base[ei + 1] - base, nt = (n + 7) >> 3;
-            const int64_t row0 = static_cast<int64_t>(r.expert[ei]) * p.H + rt * kDownRows + warp * 16;
-            const bool odd0 = odd && ((row0 + g) & 1);
-            const int this_e = ei;
-            float acc[4][4];
+        vectors([&](int buf, int k, int group, int, uint32_t to) {
+            const int e = DOWN ? scale_hidden(to, columns_of(group)) : scale_x(to, p.H);
+            if (lane == 0) s_ex[buf][k] = e;
+        });
+        __syncthreads();
+
+        for (; now.task < mine && now.group < gb + bufs; next(now)) {
+            const int entry = DOWN ? now.group / nseg : now.group;
+            const int base = r.base[entry], n = r.base[entry + 1] - base, buf = now.group - gb;
+            const int cols = columns_of(now.group), c0 = chunk0(cols), c1 = chunk1(cols);
+            uint32_t x = xs + buf * x_bytes + g * pitch + (t * 16 + c0 * (kChunk * 2)) * (DOWN ? 2 : 1);
+            float acc[kNT][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-            do {
-                wait_stage(p.stages);
-                __syncthreads();
-                load();
-                const uint32_t st = ring + slot * stage_bytes, codes = st + warp * kTile;
-                const uint32_t sc = st + kWarps * kTile + warp * kScaleTile, hs = st + kWeights;
-                const uint32_t fs = hs + p.tok_rows * 1024 + 8 * t;
-                uint32_t s0[4], s1[4];
-                row_scales(sc, g, odd0, s0);
-                row_scales(sc, g + 8, odd0, s1);
-                const int nb = min(8, blocks - ch * 8);
+            for (int i = 0; i < kNT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+            for (int c = c0; c < c1; ++c) {
+                wait_stage(stages);
+                __syncwarp();
+                load();  // into the stage that the step before this one read
+                Scales s0, s1;
+                s0.get(at + kTile + g * kScalePitch, odd);
+                s1.get(at + kTile + (g + 8) * kScalePitch, odd);
+                const int nb = min(kBlocks, (cols >> 5) - c * kBlocks);
+                if (n <= 8)
+                    nb == kBlocks ? stage_product<DOWN, 1, true>(at, code_at, s0, s1, nb, x, tok8, acc)
+                                  : stage_product<DOWN, 1, false>(at, code_at, s0, s1, nb, x, tok8, acc);
+                else
+                    nb == kBlocks ? stage_product<DOWN, kNT, true>(at, code_at, s0, s1, nb, x, tok8, acc)
+                                  : stage_product<DOWN, kNT, false>(at, code_at, s0, s1, nb, x, tok8, acc);
+                x += kChunk * (DOWN ? 4 : 2);
+                at = at + kStage == ring_end ? ring : at + kStage;
+            }
+            if (share > 1) {  // add the shares up, in the order of the columns
+                float *const to = s_join + (warp * 32 + lane) * 4 * kNT;
+                auto meet = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * share) : "memory"); };
+                if (part > 0) {
 #pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    if (b < nb) {
-                        const uint2 w0 = lds64(codes + weight_at(g, 2 * b + (t >> 1)) + (t & 1) * 8);
-                        const uint2 w1 = lds64(codes + weight_at(g + 8, 2 * b + (t >> 1)) + (t & 1) * 8);
-                        uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-                        codes4_to_f16x2(w0.x, a0, a2);
-                        codes4_to_f16x2(w1.x, a1, a3);
-                        codes4_to_f16x2(w0.y, b0, b2);
-                        codes4_to_f16x2(w1.y, b1, b3);
-                        const float f0 = pick_scale(s0, b), f1 = pick_scale(s1, b);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (i < nt) {
-                                const uint32_t at = hs + token_at(i * 8 + g, 4 * b + t);
-                                const uint4 hv = lds128(at), lv = lds128(at + p.tok_rows * 512);
-                                const uint2 fv = lds64(fs + b * (p.tok_rows * 4) + i * 32);
-                                float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
-                                mma_f16_16816(d0, d1, d2, d3, a0, a1, a2, a3, lv.x, lv.y);
-                                mma_f16_16816(d0, d1, d2, d3, b0, b1, b2, b3, lv.z, lv.w);
-                                mma_f16_16816(d0, d1, d2, d3, a0, a1, a2, a3, hv.x, hv.y);
-                                mma_f16_16816(d0, d1, d2, d3, b0, b1, b2, b3, hv.z, hv.w);
-                                const float c0 = __uint_as_float(fv.x), c1 = __uint_as_float(fv.y);
-                                acc[i][0] = fmaf(f0 * c0, d0, acc[i][0]);
-                                acc[i][1] = fmaf(f0 * c1, d1, acc[i][1]);
-                                acc[i][2] = fmaf(f1 * c0, d2, acc[i][2]);
-                                acc[i][3] = fmaf(f1 * c1, d3, acc[i][3]);
-                            }
-                        }
-                    }
+                    for (int i = 0; i < kNT; ++i) *reinterpret_cast<float4 *>(to + 4 * i) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
                 }
-                slot = slot + 1 == p.stages ? 0 : slot + 1;
-                ++u;
-                step(rt, ei, ch);
-            } while (u < end && ei == this_e && ch != 0);
-            // this expert's share of the rows, weighted
+                meet();
+                if (part == 0) {
+                    for (int w = 1; w < share; ++w)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < kNT; ++i) {
+                            const float4 v = *reinterpret_cast<const float4 *>(to + w * 32 * 4 * kNT + 4 * i);
+                            acc[i][0] += v.x, acc[i][1] += v.y, acc[i][2] += v.z, acc[i][3] += v.w;
+                        }
+                }
+                meet();
+                if (part > 0) continue;
+            }
+#pragma unroll
+            for (int i = 0; i < kNT; ++i) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int k = i * 8 + 2 * t + j;
                     if (k < n) {
-                        float *at = s_y + r.token[base + k] * kDownRows + warp * 16 + g;
-                        const float w = r.weight[base + k];
-                        at[0] = fmaf(w, acc[i][j], at[0]);
-                        at[8] = fmaf(w, acc[i][2 + j], at[8]);
+                        const float down = scale_down(s_ex[buf][k]);
+                        const float v0 = acc[i][j] * down, v1 = acc[i][2 + j] * down;
+                        if constexpr (DOWN) {
+                            float *const to = p.z + (static_cast<int64_t>(now.group % nseg) * (p.T * p.top_k) + base + k) * p.H +
+                                              now.tile * 16 + g;
+                            to[0] = v0;
+                            to[8] = v1;
+                        } else {
+                            p.hidden[static_cast<int64_t>(base + k) * p.F + now.tile * 8 + g] = v0 / (1.0f + expf(-v0)) * v1;
+                        }
                     }
                 }
-            __syncwarp();
-        }
-        const int row = this_rt * kDownRows;
-        const int rows = min(kDownRows, p.H - row);
-        __syncthreads();
-        if (seg0 == tile0 && end == tile1) {
-            for (int i = tid; i < p.T * kDownRows; i += kThreads) {
-                const int tok = i / kDownRows, k = i - tok * kDownRows;
-                if (k < rows) p.y[tok * p.ldy + row + k] = s_y[i];
-            }
-        } else {
-            const int c0 = static_cast<int>(tile0 / per), c1 = static_cast<int>((tile1 - 1) / per);
-            const int64_t size = static_cast<int64_t>(p.T) * kDownRows;
-            float *const mine = p.parts + (2 * blockIdx.x + (seg0 == tile0 ? 1 : 0)) * size;
-            for (int i = tid; i < size; i += kThreads) mine[i] = s_y[i];
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const uint32_t k = atomicAdd(p.tickets + c0, 1u);
-                s_last = k == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
-                if (s_last) p.tickets[c0] = 0u;
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                for (int i = tid; i < size; i += kThreads) {
-                    const int tok = i / kDownRows, k = i - tok * kDownRows;
-                    float sum = 0.f;
-#pragma unroll 8
-                    for (int c = c0; c <= c1; ++c) sum += __ldcg(p.parts + (2 * c + (c == c0 ? 1 : 0)) * size + i);
-                    if (k < rows) p.y[tok * p.ldy + row + k] = sum;
-                }
             }
         }
-        __syncthreads();
     }
     cp_async_wait<0>();
+}
+
+// y_t = the sum over the token's experts and segments, in that order.  A thread takes four
+// columns of one token.  A kernel of its own: where the CTA that completed 16 rows added
+// them up, the last CTA of all had most of the rows left to itself (hundreds of us).
+constexpr int kSumThreads = 128;
+__global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(const __grid_constant__ MoeParams p) {
+    const int t = blockIdx.y, c = (blockIdx.x * kSumThreads + threadIdx.x) * 4;
+    const Routing &r = *static_cast<const Routing *>(p.routing);
+    const int pairs = p.T * p.top_k, used = r.used, nseg = (p.F + segment_of(r.most, p.F) - 1) / segment_of(r.most, p.F);
+    const float *const w = r.w + t * p.top_k;
+    const int16_t *const pair = r.pair + t * p.top_k;
+    constexpr int kAt = 8;  // choices at once: their loads are under way together
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < p.top_k; j0 += kAt) {
+        int at[kAt];
+        float wj[kAt];
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) {
+            at[j] = j0 + j < p.top_k ? pair[j0 + j] : -1;
+            wj[j] = j0 + j < p.top_k ? w[j0 + j] : 0.f;
+        }
+        if (j0 == 0) pdl_wait_prior();  // for the experts' outputs
+        if (c >= p.H) return;
+        for (int s = 0; s < nseg && used > 0; ++s) {
+            float4 v[kAt];
+#pragma unroll
+            for (int j = 0; j < kAt; ++j)
+                v[j] = __ldcs(reinterpret_cast<const float4 *>(p.z + (static_cast<int64_t>(s) * pairs + max(at[j], 0)) * p.H + c));
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                if (at[j] < 0) continue;
+                sum.x = fmaf(wj[j], v[j].x, sum.x), sum.y = fmaf(wj[j], v[j].y, sum.y);
+                sum.z = fmaf(wj[j], v[j].z, sum.z), sum.w = fmaf(wj[j], v[j].w, sum.w);
+            }
+        }
+    }
+    float *const y = p.y + t * p.ldy + c;
+    y[0] = sum.x, y[1] = sum.y, y[2] = sum.z, y[3] = sum.w;  // rows of y are 4-byte aligned
 }
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct MoeLayout {
-    size_t hi, lo, fac, parts, total;
+    size_t hidden, z, total;  // after the routing
 };
-MoeLayout layout_of(int T, int F, int top_k) {
-    const size_t pairs = static_cast<size_t>(T) * top_k;
+MoeLayout layout_of(int T, int H, int F, int top_k) {
+    const size_t pairs = static_cast<size_t>(T) * top_k, segments = (F + 511) / 512;
     MoeLayout m;
-    m.hi = kMaxGrid * 4;
-    m.lo = m.hi + up256(pairs * F * 2);
-    m.fac = m.lo + up256(pairs * F * 2);
-    m.parts = m.fac + up256(pairs * (F / 32) * 4);
-    m.total = m.parts + static_cast<size_t>(2) * kMaxGrid * T * kDownRows * 4;
+    m.hidden = up256(sizeof(Routing));
+    m.z = m.hidden + up256(pairs * F * 4);
+    m.total = m.z + up256(segments * pairs * H * 4);
     return m;
 }
 
-constexpr int kSmemPerSm = 227 * 1024, kStaticSmem = 12 * 1024;
-
-// Stages and CTAs per SM: as many CTAs as leave each a ring of three stages,
-// at most 3; then as many stages as fit, at most 6.
-struct Shape {
-    int ctas, stages;
-    size_t smem;
-};
-Shape shape_of(int stage, int extra) {
-    for (int ctas = 3; ctas >= 1; --ctas) {
-        const int room = kSmemPerSm / ctas - kStaticSmem - extra;
-        const int stages = room / stage;
-        if (stages >= 3 || ctas == 1) {
-            const int n = stages > 6 ? 6 : stages;
-            return {ctas, n, static_cast<size_t>(n) * stage + extra};
-        }
-    }
-    return {0, 0, 0};
-}
+static_assert(sizeof(Routing) <= 6 * 1024, "kSmem leaves room for the routing");
+static_assert(sizeof(Making) <= kSmem, "the routing is made in the ring's memory");
+static_assert(8 * (2 * Q8_MOE_MAX_HIDDEN + 64) <= kMostX, "eight tokens' vectors fit beside two stages of every warp");
+static_assert(kGroup * (4 * 512 + 16) <= kMostX && 8 * (4 * 1024 + 16) <= kMostX, "and so does a segment's");
 
 }  // namespace
 
-size_t moe_workspace(int T, int F, int top_k) { return layout_of(T, F, top_k).total; }
+size_t moe_workspace(int T, int H, int F, int top_k) { return layout_of(T, H, F, top_k).total; }
 
 q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStream_t stream) {
     const DeviceInfo *di = device_info();
@@ -621,43 +715,31 @@ q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStrea
     static std::atomic<uint64_t> ready{0};
     const uint64_t bit = 1ull << (di->device & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        const int most = kSmemPerSm - kStaticSmem;
-        if (cudaFuncSetAttribute(moe_gate_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-            cudaFuncSetAttribute(moe_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+        if (cudaFuncSetAttribute(moe_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(moe_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
             return Q8_ERR_CUDA;
         ready.fetch_or(bit);
     }
-    const MoeLayout m = layout_of(a.T, a.F, a.top_k);
+    const MoeLayout m = layout_of(a.T, a.H, a.F, a.top_k);
     uint8_t *w = static_cast<uint8_t *>(ws);
     MoeParams p = {};
     p.x = a.x, p.logits = a.logits, p.q13 = a.q13, p.s13 = a.s13, p.q2 = a.q2, p.s2 = a.s2;
     p.y = a.y, p.ids = a.ids, p.weights = a.weights;
-    p.tickets = reinterpret_cast<uint32_t *>(w);
-    p.hi = reinterpret_cast<uint16_t *>(w + m.hi), p.lo = reinterpret_cast<uint16_t *>(w + m.lo);
-    p.fac = reinterpret_cast<float *>(w + m.fac), p.parts = reinterpret_cast<float *>(w + m.parts);
+    p.routing = w;
+    p.hidden = reinterpret_cast<float *>(w + m.hidden), p.z = reinterpret_cast<float *>(w + m.z);
     p.status = dev_status;
     p.ldx = a.ldx, p.ldl = a.ldl, p.ldy = a.ldy;
     p.T = a.T, p.E = a.E, p.H = a.H, p.F = a.F, p.top_k = a.top_k, p.renorm = a.renorm;
-    p.tok_rows = (a.T + 7) & ~7;
-    const int64_t used = static_cast<int64_t>(a.T) * a.top_k < a.E ? static_cast<int64_t>(a.T) * a.top_k : a.E;
-
-    const Shape up = shape_of(kWeights + p.tok_rows * 512, 0);
-    p.stages = up.stages;
-    int64_t grid = static_cast<int64_t>(up.ctas) * di->sm_count, need = used * (a.F / 32);
-    if (grid > kMaxGrid) grid = kMaxGrid;
-    if (grid > need) grid = need;
-    if (launch_kernel(moe_gate_up_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), up.smem, stream, false, p) != cudaSuccess)
+    p.cap = kGroup * (2 * a.H + 64) <= kMostX ? kGroup : 8;
+    const int64_t pairs = static_cast<int64_t>(a.T) * a.top_k, entries = pairs < a.E ? pairs : a.E + pairs / p.cap;
+    auto grid_of = [&](int64_t tasks) { return dim3(static_cast<unsigned>(tasks < di->sm_count ? tasks : di->sm_count)); };
+    if (launch_kernel(moe_kernel<false>, grid_of(entries * (a.F / 8)), dim3(kThreads), kSmem, stream, false, p) != cudaSuccess)
         return Q8_ERR_CUDA;
-
-    const Shape down = shape_of(kWeights + p.tok_rows * (1024 + 32), a.T * kDownRows * 4);
-    p.stages = down.stages;
-    grid = static_cast<int64_t>(down.ctas) * di->sm_count;
-    need = used * ((a.F + kChunk - 1) / kChunk) * ((a.H + kDownRows - 1) / kDownRows);
-    if (grid > kMaxGrid) grid = kMaxGrid;
-    if (grid > need) grid = need;
-    if (launch_kernel(moe_down_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), down.smem, stream, true, p) != cudaSuccess)
+    if (launch_kernel(moe_kernel<true>, grid_of(entries * (a.H / 16) * ((a.F + 511) / 512)), dim3(kThreads), kSmem, stream, true, p) !=
+        cudaSuccess)
         return Q8_ERR_CUDA;
-    return Q8_OK;
+    const dim3 sums((a.H / 4 + kSumThreads - 1) / kSumThreads, a.T);
+    return launch_kernel(moe_sum_kernel, sums, dim3(kSumThreads), 0, stream, true, p) == cudaSuccess ? Q8_OK : Q8_ERR_CUDA;
 }
 
 }  // namespace q8

@@ -549,15 +549,18 @@ size_t q8_attn_decode_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_
  *   y       : float [T][ldy], ldy >= H
  *   ids     : int32 [T][top_k] the chosen experts, -1 for none; may be NULL
  *   weights : float [T][top_k] their w_j; may be NULL
- *   ws      : q8_moe_workspace_size() bytes, 256-byte aligned, zeroed once;
- *             not for two calls that may run at the same time
- * H and F multiples of 32; 1 <= E <= 512; 1 <= top_k <= min(16, E).
+ *   ws      : q8_moe_workspace_size() bytes, 256-byte aligned, no zeroing
+ *             needed; not for two calls that may run at the same time
+ * H and F multiples of 32, H <= 8192 (eight tokens' vectors lie in shared memory), F <= 65536;
+ * 1 <= E <= 512; 1 <= top_k <= min(16, E).
  * Products are exact and summed in fp32; hidden units are kept to 22 bits.
- * The second kernel is a programmatic dependent of the first; work before
- * the call in the stream is complete before either reads anything.
+ * The call's later kernels are programmatic dependents of its first; work
+ * before the call in the stream is complete before any reads anything.
  */
 #define Q8_MOE_MAX_EXPERTS 512
 #define Q8_MOE_MAX_TOP_K 16
+#define Q8_MOE_MAX_HIDDEN 8192
+#define Q8_MOE_MAX_FFN 65536
 q8_status q8_moe(const uint16_t *x, int64_t ldx, const float *logits, int64_t ldl, int32_t T, int32_t E, int32_t top_k,
                  int32_t renorm, const int8_t *q13, const uint16_t *s13, const int8_t *q2, const uint16_t *s2, int64_t H,
                  int64_t F, float *y, int64_t ldy, int32_t *ids, float *weights, void *ws, size_t ws_bytes,

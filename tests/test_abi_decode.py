@@ -100,7 +100,7 @@ def moe(L, x=A, ldx=64, logits=A, ldl=8, T=3, E=8, k=2, q13=A, s13=A, q2=A, s2=A
 def test_moe_validation(L):
     from block_quantized_int8_gb300 import q8
     for kw in (dict(T=-1), dict(T=33), dict(E=0), dict(E=513), dict(H=48), dict(F=0), dict(H=0), dict(F=33), dict(ldx=63),
-               dict(ldl=7), dict(ldy=63), dict(H=1 << 21)):
+               dict(ldl=7), dict(ldy=63), dict(H=8224, ldx=8224, ldy=8224), dict(F=65568)):
         assert moe(L, **kw) == q8.Q8_ERR_SHAPE, kw
     for kw in (dict(k=0), dict(k=9), dict(k=17, E=32, ldl=32)):
         assert moe(L, **kw) == q8.Q8_ERR_ARG, kw

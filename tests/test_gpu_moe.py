@@ -114,7 +114,6 @@ def test_repeats_and_graph_replays_with_other_logits():
     for _ in range(20):
         q8.q8_moe(x, lg, *dev, 4, y=out, ws=ws)
         assert torch.equal(out, y)
-    assert not ws[:4096].any()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         q8.q8_moe(x, lg, *dev, 4, y=out, ws=ws)
