@@ -20,8 +20,9 @@
 // the experts it has in shared memory.  (A first form with the vectors in the
 // ring, and so a CTA barrier per 128 columns, took 2.4 times as long.)  The host
 // does not know which experts are chosen: every CTA of the first kernel works the
-// routing out for itself from the logits, the others read it, and every CTA cuts
-// the same list of tasks into equal runs.
+// routing out for itself from the logits, and so does every CTA of the second, while
+// the first still runs (the third reads it); every CTA cuts the same list of tasks
+// into equal runs.
 // Where a CTA's tasks do not fill its warps evenly, 2, 4 or 8 warps share one,
 // each a range of its columns.
 //
@@ -109,16 +110,13 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 
-// One warp's token: its top_k experts by repeated maximum of NK keys a lane.
+// One warp's token: its top_k experts by repeated maximum of NK keys a lane (v: the logits of
+// experts lane, lane + 32, ...; -inf past the last).
 template <int NK>
-__device__ void route_token(const MoeParams &p, Routing &r, Making &mk, int t, bool report) {
+__device__ void route_token(const MoeParams &p, Routing &r, Making &mk, int t, const float (&v)[NK], bool report) {
     const int lane = threadIdx.x & 31;
-    const float *row = p.logits + t * p.ldl;
-    float v[NK];
     uint32_t key[NK];
     bool nan = false;
-#pragma unroll
-    for (int i = 0; i < NK; ++i) v[i] = lane + 32 * i < p.E ? row[lane + 32 * i] : -INFINITY;
     // this lane's best: the largest key, the lowest index of equal ones
     uint32_t m = 0;
     int mi = 0;
@@ -168,43 +166,63 @@ __device__ void route_token(const MoeParams &p, Routing &r, Making &mk, int t, b
     }
 }
 
+template <int NK>
+__device__ void route_tokens(const MoeParams &p, Routing &r, Making &mk, bool report) {
+    static_assert(kMaxT <= 2 * kWarps, "a warp routes at most two tokens");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float v[2][NK];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+            v[q][i] = warp + q * kWarps < p.T && lane + 32 * i < p.E ? p.logits[(warp + q * kWarps) * p.ldl + lane + 32 * i] : -INFINITY;
+#pragma unroll 1
+    for (int q = 0; q < 2; ++q) {
+        if (warp + q * kWarps >= p.T) break;
+        route_token<NK>(p, r, mk, warp + q * kWarps, v[0], report);
+#pragma unroll
+        for (int i = 0; i < NK; ++i) v[0][i] = v[1][i];
+    }
+}
+
 __device__ void route(const MoeParams &p, Routing &r, Making &mk, bool report) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int e = tid; e < p.E; e += kThreads) mk.mask[e] = 0;
     __syncthreads();
-    for (int t = warp; t < p.T; t += kWarps) {
-        if (p.E <= 32)
-            route_token<1>(p, r, mk, t, report);
-        else if (p.E <= 128)
-            route_token<4>(p, r, mk, t, report);
-        else
-            route_token<kMaxE / 32>(p, r, mk, t, report);
-    }
+    if (p.E <= 32)
+        route_tokens<1>(p, r, mk, report);
+    else if (p.E <= 128)
+        route_tokens<4>(p, r, mk, report);
+    else
+        route_tokens<kMaxE / 32>(p, r, mk, report);
     __syncthreads();
-    if (warp == 0) {
-        int used = 0, pairs = 0, most = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int n = e < p.E ? __popc(mk.mask[e]) : 0, parts = (n + p.cap - 1) / p.cap;
-            int run = n, erun = parts;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, run, o), ev = __shfl_up_sync(0xffffffffu, erun, o);
-                if (lane >= o) run += v, erun += ev;
-            }
-            if (n > 0) mk.first[e] = static_cast<uint16_t>(pairs + run - n);
-            for (int i = 0; i < parts; ++i) {
-                r.expert[used + erun - parts + i] = static_cast<uint16_t>(e);
-                r.base[used + erun - parts + i] = static_cast<uint16_t>(pairs + run - n + i * p.cap);
-            }
-            most = max(most, min(n, p.cap));
-            used += __shfl_sync(0xffffffffu, erun, 31);
-            pairs += __shfl_sync(0xffffffffu, run, 31);
+    if (warp == 0) {  // a lane takes `each` neighbouring experts
+        const int each = (p.E + 31) / 32, e0 = lane * each, e1 = min(e0 + each, p.E);
+        int n = 0, parts = 0, most = 0;
+        for (int e = e0; e < e1; ++e) {
+            const int k = __popc(mk.mask[e]);
+            n += k, parts += (k + p.cap - 1) / p.cap, most = max(most, min(k, p.cap));
+        }
+        int run = n, erun = parts;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, run, o), ev = __shfl_up_sync(0xffffffffu, erun, o);
+            if (lane >= o) run += v, erun += ev;
         }
         most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) {
-            r.base[used] = static_cast<uint16_t>(pairs);
-            r.used = used;
+        if (lane == 31) {
+            r.base[erun] = static_cast<uint16_t>(run);
+            r.used = erun;
             r.most = most;
+        }
+        int at = erun - parts, pair = run - n;
+        for (int e = e0; e < e1; ++e) {
+            const int k = __popc(mk.mask[e]);
+            mk.first[e] = static_cast<uint16_t>(pair);
+            for (int i = 0; i < k; i += p.cap, ++at) {
+                r.expert[at] = static_cast<uint16_t>(e);
+                r.base[at] = static_cast<uint16_t>(pair + i);
+            }
+            pair += k;
         }
     }
     __syncthreads();
@@ -429,24 +447,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     constexpr int kWords = sizeof(Routing) / 16;
     static_assert(kWords <= kThreads, "a thread copies 16 bytes of the routing");
-    if constexpr (DOWN) {
-        pdl_wait_prior();
-        if (tid < kWords) reinterpret_cast<uint4 *>(&r)[tid] = __ldcg(static_cast<const uint4 *>(p.routing) + tid);
-        pdl_launch_dependents();  // the third kernel may read the routing (the first has ended) before its wait
-        __syncthreads();
-    } else {
-        pdl_launch_dependents();
-        Making &mk = *reinterpret_cast<Making *>(smem);
-        route(p, r, mk, blockIdx.x == 0);
-        if (blockIdx.x == 0) {
-            for (int i = tid; i < p.T * p.top_k; i += kThreads) {
-                if (p.ids) p.ids[i] = mk.id[i];
-                if (p.weights) p.weights[i] = r.w[i];
-            }
-            if (tid < kWords) static_cast<uint4 *>(p.routing)[tid] = reinterpret_cast<const uint4 *>(&r)[tid];
-            __syncthreads();
+    if (!DOWN) pdl_launch_dependents();
+    Making &mk = *reinterpret_cast<Making *>(smem);
+    route(p, r, mk, !DOWN && blockIdx.x == 0);
+    if (!DOWN && blockIdx.x == 0) {
+        for (int i = tid; i < p.T * p.top_k; i += kThreads) {
+            if (p.ids) p.ids[i] = mk.id[i];
+            if (p.weights) p.weights[i] = r.w[i];
         }
+        if (tid < kWords) static_cast<uint4 *>(p.routing)[tid] = reinterpret_cast<const uint4 *>(&r)[tid];
+        __syncthreads();
     }
+    if (DOWN && r.used == 0) pdl_wait_prior();  // this kernel ends no earlier than the first
     if (r.used == 0) return;
 
     // ---- the list of tasks: group (an entry, for DOWN with a segment) major, then tiles of rows --
@@ -459,7 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     const uint32_t tasks = static_cast<uint32_t>(groups) * tiles;
     const uint32_t t0 = static_cast<uint32_t>(static_cast<uint64_t>(tasks) * blockIdx.x / gridDim.x);
     const uint32_t t1 = static_cast<uint32_t>(static_cast<uint64_t>(tasks) * (blockIdx.x + 1) / gridDim.x);
-    if (t0 >= t1) return;
+    if (t0 >= t1) {
+        if (DOWN) pdl_wait_prior();
+        return;
+    }
     const int mine = static_cast<int>(t1 - t0);
 
     // ---- shared memory: one or two groups' vectors, the ring, sums of warps that share ------------
@@ -535,6 +550,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     if (works)
 #pragma unroll 1
         for (int i = 0; i < stages - 1; ++i) load();
+    if constexpr (DOWN) {
+        // the weights could come while the first kernel ran, the hidden units not; the third kernel
+        // may read the first's routing before its own wait
+        pdl_wait_prior();
+        pdl_launch_dependents();
+    }
 
     uint32_t code_at[kBlocks];
 #pragma unroll
@@ -730,7 +751,9 @@ q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStrea
     p.status = dev_status;
     p.ldx = a.ldx, p.ldl = a.ldl, p.ldy = a.ldy;
     p.T = a.T, p.E = a.E, p.H = a.H, p.F = a.F, p.top_k = a.top_k, p.renorm = a.renorm;
-    p.cap = kGroup * (2 * a.H + 64) <= kMostX ? kGroup : 8;
+    // entries of up to 16 tokens where the experts have more than 8 each on the average; else of 8, so
+    // that a much liked expert is two entries' work for two CTAs and not a slow one for one
+    p.cap = a.T * a.top_k > 8 * a.E && kGroup * (2 * a.H + 64) <= kMostX ? kGroup : 8;
     const int64_t pairs = static_cast<int64_t>(a.T) * a.top_k, entries = pairs < a.E ? pairs : a.E + pairs / p.cap;
     auto grid_of = [&](int64_t tasks) { return dim3(static_cast<unsigned>(tasks < di->sm_count ? tasks : di->sm_count)); };
     if (launch_kernel(moe_kernel<false>, grid_of(entries * (a.F / 8)), dim3(kThreads), kSmem, stream, false, p) != cudaSuccess)
