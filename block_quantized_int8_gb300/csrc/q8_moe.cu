@@ -1,6 +1,6 @@
-// q8_moe.cu -- a mixture-of-experts layer for a few tokens (T <= 32): routing,
-// gate and up products and SwiGLU in one kernel, down products in a second, and
-// a small one for the weighted sum over each token's experts.
+// q8_moe.cu -- a mixture-of-experts layer for a few tokens (T <= 32) in one
+// kernel: routing, gate and up products with SwiGLU, down products, and the
+// weighted sum over each token's experts.
 //
 // Mathematics.  Token t takes the top_k experts of largest logit (ties: the
 // lower index), w_j = exp(l_j - l_max) / z with z summed over the chosen (or
@@ -8,7 +8,7 @@
 //
 // Bound: the chosen experts' weights, 1.0625 bytes each, read once for all
 // tokens that chose them (for up to 16; an expert with more is read again,
-// from L2).  Both kernels are streams of 16-row weight tiles against a few
+// from L2).  Both products are streams of 16-row weight tiles against a few
 // tokens' vectors: m16n8k16 warp MMAs of 16 weight rows by 8 tokens, one block
 // of 32 columns at a time, whose fp32 result is multiplied by the block's
 // scale as in the matmuls.
@@ -19,25 +19,27 @@
 // columns), so warps wait for one another only where the CTA moves on past
 // the experts it has in shared memory.  (A first form with the vectors in the
 // ring, and so a CTA barrier per 128 columns, took 2.4 times as long.)  The host
-// does not know which experts are chosen: every CTA of the first kernel works the
-// routing out for itself from the logits, and so does every CTA of the second, while
-// the first still runs (the third reads it); every CTA cuts the same list of tasks
-// into equal runs.
+// does not know which experts are chosen: every CTA works the routing out for
+// itself from the logits and cuts the same lists of tasks into equal runs.  Between
+// the products, and before the sum, all CTAs wait for one another (a cooperative
+// launch): as three kernels the call took 157 us in place of 152 for 32 tokens, most
+// of the difference each kernel's own beginning.
 // Where a CTA's tasks do not fill its warps evenly, 2, 4 or 8 warps share one,
 // each a range of its columns.
 //
-// gate/up kernel: a task is 8 hidden units of one expert: MMA rows 0..7 are
+// gate/up: a task is 8 hidden units of one expert: MMA rows 0..7 are
 // their gate rows, 8..15 their up rows, so a thread holds both factors of its
 // unit and SwiGLU needs no exchange.  x (bf16) is scaled by a power of two per
 // token to a largest value in [2^14, 2^15): exact in binary16 down to 2^-39 of it.
 // Hidden units go to the workspace in fp32.
-// down kernel: a task is 16 output rows of one expert over a segment of 512 or
+// down: a task is 16 output rows of one expert over a segment of 512 or
 // 1024 hidden units.  The hidden units, scaled likewise per token and segment,
 // are taken as the sum of two binary16 values (22 bits), so fp32 outputs keep
-// their digits.  Each task leaves its tokens' rows in the workspace; the third
-// kernel adds them up in the order of the token's experts and segments.
+// their digits.  Each task leaves its tokens' rows in the workspace, and
+// they are added up in the order of the token's experts and segments.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "q8_async.cuh"
@@ -77,7 +79,7 @@ struct MoeParams {
     float *weights;         // [T][top_k] or null
     float *hidden;          // [pairs][F]
     float *z;               // [segments][pairs][H]: the experts' outputs
-    void *routing;          // the first kernel's, for the others
+    uint32_t *counters;     // CTAs that have made their hidden units, and their outputs
     uint32_t *status;
     int64_t ldx, ldl, ldy;
     int32_t T, E, H, F, top_k, renorm;
@@ -432,35 +434,18 @@ __device__ int scale_hidden(uint32_t at, int n) {
     return e;
 }
 
-// Hidden units of a segment of the down kernel: F in equal parts (of whole chunks) of at most
+// Hidden units of a segment of the down product: F in equal parts (of whole chunks) of at most
 // 1024, or 512 where an entry has more than 8 tokens.
 __device__ __forceinline__ int segment_of(int most, int F) {
     const int n = (F + (most <= 8 ? 1023 : 511)) / (most <= 8 ? 1024 : 512);
     return ((F + n - 1) / n + kChunk - 1) / kChunk * kChunk;
 }
 
-template <bool DOWN>
-__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ MoeParams p) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Routing r;
-    __shared__ int s_ex[2][kGroup];  // the exponents that the vectors in shared memory were scaled by
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    constexpr int kWords = sizeof(Routing) / 16;
-    static_assert(kWords <= kThreads, "a thread copies 16 bytes of the routing");
-    if (!DOWN) pdl_launch_dependents();
-    Making &mk = *reinterpret_cast<Making *>(smem);
-    route(p, r, mk, !DOWN && blockIdx.x == 0);
-    if (!DOWN && blockIdx.x == 0) {
-        for (int i = tid; i < p.T * p.top_k; i += kThreads) {
-            if (p.ids) p.ids[i] = mk.id[i];
-            if (p.weights) p.weights[i] = r.w[i];
-        }
-        if (tid < kWords) static_cast<uint4 *>(p.routing)[tid] = reinterpret_cast<const uint4 *>(&r)[tid];
-        __syncthreads();
-    }
-    if (DOWN && r.used == 0) pdl_wait_prior();  // this kernel ends no earlier than the first
-    if (r.used == 0) return;
-
+// One of the two products.  `ready` is called, by every thread, once the first weights are on
+// their way, and says whether what the vectors are made of is there (false: give up).
+template <bool DOWN, typename Ready>
+__device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int (&s_ex)[2][kGroup], uint8_t *smem, Ready ready) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // ---- the list of tasks: group (an entry, for DOWN with a segment) major, then tiles of rows --
     const int K = DOWN ? p.F : p.H;                          // columns of the weights
     const int rows8 = (r.most + 7) & ~7;
@@ -471,10 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     const uint32_t tasks = static_cast<uint32_t>(groups) * tiles;
     const uint32_t t0 = static_cast<uint32_t>(static_cast<uint64_t>(tasks) * blockIdx.x / gridDim.x);
     const uint32_t t1 = static_cast<uint32_t>(static_cast<uint64_t>(tasks) * (blockIdx.x + 1) / gridDim.x);
-    if (t0 >= t1) {
-        if (DOWN) pdl_wait_prior();
-        return;
-    }
+    if (t0 >= t1) return ready();
     const int mine = static_cast<int>(t1 - t0);
 
     // ---- shared memory: one or two groups' vectors, the ring, sums of warps that share ------------
@@ -550,11 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     if (works)
 #pragma unroll 1
         for (int i = 0; i < stages - 1; ++i) load();
-    if constexpr (DOWN) {
-        // the weights could come while the first kernel ran, the hidden units not; the third kernel
-        // may read the first's routing before its own wait
-        pdl_wait_prior();
-        pdl_launch_dependents();
+    if (!ready()) {
+        cp_async_wait<0>();
+        return false;
     }
 
     uint32_t code_at[kBlocks];
@@ -666,56 +646,104 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         }
     }
     cp_async_wait<0>();
+    return true;
 }
 
-// y_t = the sum over the token's experts and segments, in that order.  A thread takes four
-// columns of one token.  A kernel of its own: where the CTA that completed 16 rows added
-// them up, the last CTA of all had most of the rows left to itself (hundreds of us).
-constexpr int kSumThreads = 128;
-__global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(const __grid_constant__ MoeParams p) {
-    const int t = blockIdx.y, c = (blockIdx.x * kSumThreads + threadIdx.x) * 4;
-    const Routing &r = *static_cast<const Routing *>(p.routing);
-    const int pairs = p.T * p.top_k, used = r.used, nseg = (p.F + segment_of(r.most, p.F) - 1) / segment_of(r.most, p.F);
-    const float *const w = r.w + t * p.top_k;
-    const int16_t *const pair = r.pair + t * p.top_k;
-    constexpr int kAt = 8;  // choices at once: their loads are under way together
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < p.top_k; j0 += kAt) {
-        int at[kAt];
-        float wj[kAt];
-#pragma unroll
-        for (int j = 0; j < kAt; ++j) {
-            at[j] = j0 + j < p.top_k ? pair[j0 + j] : -1;
-            wj[j] = j0 + j < p.top_k ? w[j0 + j] : 0.f;
-        }
-        if (j0 == 0) pdl_wait_prior();  // for the experts' outputs
-        if (c >= p.H) return;
-        for (int s = 0; s < nseg && used > 0; ++s) {
-            float4 v[kAt];
-#pragma unroll
-            for (int j = 0; j < kAt; ++j)
-                v[j] = __ldcs(reinterpret_cast<const float4 *>(p.z + (static_cast<int64_t>(s) * pairs + max(at[j], 0)) * p.H + c));
-#pragma unroll
-            for (int j = 0; j < kAt; ++j) {
-                if (at[j] < 0) continue;
-                sum.x = fmaf(wj[j], v[j].x, sum.x), sum.y = fmaf(wj[j], v[j].y, sum.y);
-                sum.z = fmaf(wj[j], v[j].z, sum.z), sum.w = fmaf(wj[j], v[j].w, sum.w);
+// ---- all CTAs of the launch (a cooperative one: they all run) --------------------------------------
+__device__ __forceinline__ void arrive(uint32_t *counter) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        atomicAdd(counter, 1u);
+    }
+}
+__device__ __forceinline__ bool wait_all(const uint32_t *counter, uint32_t *status, int &s_ok) {
+    if (threadIdx.x == 0) {
+        const uint64_t begun = globaltimer_ns();
+        uint32_t n;
+        bool late = false;
+        while (true) {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(counter) : "memory");
+            if (n >= gridDim.x) break;
+            if (globaltimer_ns() - begun > kWaitLimitNs) {
+                late = true;
+                break;
             }
         }
+        if (late && status) atomicOr(status, Q8_DEV_TIMEOUT);
+        s_ok = late ? 0 : 1;
     }
-    float *const y = p.y + t * p.ldy + c;
-    y[0] = sum.x, y[1] = sum.y, y[2] = sum.z, y[3] = sum.w;  // rows of y are 4-byte aligned
+    __syncthreads();
+    return s_ok != 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ MoeParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Routing r;
+    __shared__ int s_ex[2][kGroup];  // the exponents that the vectors in shared memory were scaled by
+    __shared__ int s_ok[2];
+    const int tid = threadIdx.x;
+    // counters[0] is zero here; counters[1] is what the call before left, and nobody counts with it
+    // until this CTA has arrived at counters[0]
+    if (blockIdx.x == 0 && tid == 0) p.counters[1] = 0;
+    Making &mk = *reinterpret_cast<Making *>(smem);
+    route(p, r, mk, blockIdx.x == 0);
+    if (blockIdx.x == 0) {
+        for (int i = tid; i < p.T * p.top_k; i += kThreads) {
+            if (p.ids) p.ids[i] = mk.id[i];
+            if (p.weights) p.weights[i] = r.w[i];
+        }
+        __syncthreads();
+    }
+    phase<false>(p, r, s_ex, smem, [] { return true; });
+    arrive(&p.counters[0]);
+    // the down weights come while the last hidden units are made
+    if (!phase<true>(p, r, s_ex, smem, [&] { return wait_all(&p.counters[0], p.status, s_ok[0]); })) return;
+    arrive(&p.counters[1]);
+    const int nseg = (p.F + segment_of(r.most, p.F) - 1) / segment_of(r.most, p.F);
+    if (!wait_all(&p.counters[1], p.status, s_ok[1])) return;
+    if (blockIdx.x == 0 && tid == 0) p.counters[0] = 0;
+
+    // ---- y_t = the sum over the token's experts and segments, in that order; four columns of one
+    // token a thread ----------------------------------------------------------------------------------
+    constexpr int kAt = 8;  // choices at once: their loads are under way together
+    const int pairs = p.T * p.top_k, quarter = p.H / 4;
+    for (int i = blockIdx.x * kThreads + tid; i < p.T * quarter; i += gridDim.x * kThreads) {
+        const int t = i / quarter, c = (i - t * quarter) * 4;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = 0; j0 < p.top_k; j0 += kAt) {
+            for (int s = 0; s < nseg; ++s) {
+                float4 v[kAt];
+#pragma unroll
+                for (int j = 0; j < kAt; ++j) {
+                    const int at = j0 + j < p.top_k ? r.pair[t * p.top_k + j0 + j] : -1;
+                    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (at >= 0) v[j] = __ldcg(reinterpret_cast<const float4 *>(p.z + (static_cast<int64_t>(s) * pairs + at) * p.H + c));
+                }
+#pragma unroll
+                for (int j = 0; j < kAt; ++j) {
+                    const float w = j0 + j < p.top_k ? r.w[t * p.top_k + j0 + j] : 0.f;
+                    if (w == 0.f) continue;  // not chosen: its place holds nothing
+                    sum.x = fmaf(w, v[j].x, sum.x), sum.y = fmaf(w, v[j].y, sum.y);
+                    sum.z = fmaf(w, v[j].z, sum.z), sum.w = fmaf(w, v[j].w, sum.w);
+                }
+            }
+        }
+        float *const y = p.y + t * p.ldy + c;
+        y[0] = sum.x, y[1] = sum.y, y[2] = sum.z, y[3] = sum.w;  // rows of y are 4-byte aligned
+    }
 }
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct MoeLayout {
-    size_t hidden, z, total;  // after the routing
+    size_t hidden, z, total;  // after the counters
 };
 MoeLayout layout_of(int T, int H, int F, int top_k) {
     const size_t pairs = static_cast<size_t>(T) * top_k, segments = (F + 511) / 512;
     MoeLayout m;
-    m.hidden = up256(sizeof(Routing));
+    m.hidden = 256;
     m.z = m.hidden + up256(pairs * F * 4);
     m.total = m.z + up256(segments * pairs * H * 4);
     return m;
@@ -736,9 +764,7 @@ q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStrea
     static std::atomic<uint64_t> ready{0};
     const uint64_t bit = 1ull << (di->device & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(moe_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(moe_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-            return Q8_ERR_CUDA;
+        if (cudaFuncSetAttribute(moe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return Q8_ERR_CUDA;
         ready.fetch_or(bit);
     }
     const MoeLayout m = layout_of(a.T, a.H, a.F, a.top_k);
@@ -746,7 +772,7 @@ q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStrea
     MoeParams p = {};
     p.x = a.x, p.logits = a.logits, p.q13 = a.q13, p.s13 = a.s13, p.q2 = a.q2, p.s2 = a.s2;
     p.y = a.y, p.ids = a.ids, p.weights = a.weights;
-    p.routing = w;
+    p.counters = reinterpret_cast<uint32_t *>(w);
     p.hidden = reinterpret_cast<float *>(w + m.hidden), p.z = reinterpret_cast<float *>(w + m.z);
     p.status = dev_status;
     p.ldx = a.ldx, p.ldl = a.ldl, p.ldy = a.ldy;
@@ -755,14 +781,18 @@ q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStrea
     // that a much liked expert is two entries' work for two CTAs and not a slow one for one
     p.cap = a.T * a.top_k > 8 * a.E && kGroup * (2 * a.H + 64) <= kMostX ? kGroup : 8;
     const int64_t pairs = static_cast<int64_t>(a.T) * a.top_k, entries = pairs < a.E ? pairs : a.E + pairs / p.cap;
-    auto grid_of = [&](int64_t tasks) { return dim3(static_cast<unsigned>(tasks < di->sm_count ? tasks : di->sm_count)); };
-    if (launch_kernel(moe_kernel<false>, grid_of(entries * (a.F / 8)), dim3(kThreads), kSmem, stream, false, p) != cudaSuccess)
-        return Q8_ERR_CUDA;
-    if (launch_kernel(moe_kernel<true>, grid_of(entries * (a.H / 16) * ((a.F + 511) / 512)), dim3(kThreads), kSmem, stream, true, p) !=
-        cudaSuccess)
-        return Q8_ERR_CUDA;
-    const dim3 sums((a.H / 4 + kSumThreads - 1) / kSumThreads, a.T);
-    return launch_kernel(moe_sum_kernel, sums, dim3(kSumThreads), 0, stream, true, p) == cudaSuccess ? Q8_OK : Q8_ERR_CUDA;
+    const int64_t tasks = entries * std::max<int64_t>(a.F / 8, static_cast<int64_t>(a.H / 16) * ((a.F + 511) / 512));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tasks < di->sm_count ? tasks : di->sm_count));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // its CTAs wait for one another
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, moe_kernel, p) == cudaSuccess ? Q8_OK : Q8_ERR_CUDA;
 }
 
 }  // namespace q8

@@ -549,13 +549,14 @@ size_t q8_attn_decode_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_
  *   y       : float [T][ldy], ldy >= H
  *   ids     : int32 [T][top_k] the chosen experts, -1 for none; may be NULL
  *   weights : float [T][top_k] their w_j; may be NULL
- *   ws      : q8_moe_workspace_size() bytes, 256-byte aligned, no zeroing
- *             needed; not for two calls that may run at the same time
+ *   ws      : q8_moe_workspace_size() bytes, 256-byte aligned, zeroed once (and
+ *             again after a Q8_DEV_TIMEOUT); not for two calls that may run at
+ *             the same time
  * H and F multiples of 32, H <= 8192 (eight tokens' vectors lie in shared memory), F <= 65536;
  * 1 <= E <= 512; 1 <= top_k <= min(16, E).
  * Products are exact and summed in fp32; hidden units are kept to 22 bits.
- * The call's later kernels are programmatic dependents of its first; work
- * before the call in the stream is complete before any reads anything.
+ * One cooperative launch of one CTA per SM, whose CTAs wait for one another
+ * twice (bounded; Q8_DEV_TIMEOUT).
  */
 #define Q8_MOE_MAX_EXPERTS 512
 #define Q8_MOE_MAX_TOP_K 16
