@@ -105,10 +105,34 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return (m ^ ((m >> 3) & 7)) * 16;
 }
 
-// Where a CTA is in the list of items: the sequence, its head (key head *
-// splits + run of heads), the unit within the item.
+// The NB scales of a token: as pairs, and widened.
+template <int NB>
+__device__ __forceinline__ void raw_scales(uint32_t at, uint32_t (&w)[NB / 2]) {
+    if constexpr (NB == 8) {
+        const uint4 v = lds128(at);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (NB == 4) {
+        const uint2 v = lds64(at);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = lds32(at);
+    }
+}
+template <int NB>
+__device__ __forceinline__ void token_scales(uint32_t at, float (&f)[NB]) {
+    uint32_t w[NB / 2];
+    raw_scales<NB>(at, w);
+#pragma unroll
+    for (int b = 0; b < NB / 2; ++b) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[b]));
+        f[2 * b] = v.x, f[2 * b + 1] = v.y;
+    }
+}
+
+// Where a CTA is in the list of items.
 struct Walk {
-    int b, hh, unit, units;  // units of this sequence's items
+    int b, unit, units;      // units of this sequence's items
+    int kvh, run;            // the item: key head, and run of its query heads
     int len, first;          // tokens, and the first one seen
     int base;                // first token of unit 0 (a multiple of 16)
 };
@@ -136,8 +160,10 @@ __device__ __forceinline__ void enter(const AttnParams &p, Walk &w) {
 __device__ __forceinline__ void advance(const AttnParams &p, Walk &w) {
     if (++w.unit < w.units) return;
     w.unit = 0;
-    if (++w.hh < p.kv_heads * p.splits) return;
-    w.hh = 0;
+    if (++w.run < p.splits) return;
+    w.run = 0;
+    if (++w.kvh < p.kv_heads) return;
+    w.kvh = 0;
     do {
         ++w.b;
         enter(p, w);
@@ -221,8 +247,9 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
         }
         enter(p, wk);
         const long long in = u0 - before;
-        wk.hh = static_cast<int>(in / wk.units);
-        wk.unit = static_cast<int>(in - static_cast<long long>(wk.hh) * wk.units);
+        const int item = static_cast<int>(in / wk.units);
+        wk.kvh = item / p.splits, wk.run = item - wk.kvh * p.splits;
+        wk.unit = static_cast<int>(in - static_cast<long long>(item) * wk.units);
     }
 
     // ---- this warp's pipeline ------------------------------------------------------
@@ -232,6 +259,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     int ld_slot = 0;
     int ld_page = -1;          // page of the tile to load next, read one step ahead
     uint32_t held = 0;         // bit i: slot i holds a tile
+    const int page_mask = (1 << p.page_shift) - 1;
     auto tile_of = [&](const Walk &w) { return w.base + w.unit * kUnitTokens + warp * 16; };
     auto fetch_page = [&]() {
         ld_page = -1;
@@ -240,6 +268,9 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             if (tok < ld.len) ld_page = p.table[static_cast<int64_t>(ld.b) * p.table_width + (tok >> p.page_shift)];
         }
     };
+    // 16-byte chunk m of a tile lies at m ^ ((m >> 3) & 7): for this lane's chunks lane + 32 i,
+    // one place for even i and one for odd
+    const uint32_t even = (lane ^ (lane >> 3)) * 16, odd = even ^ 64;
     auto load = [&]() {
         if (ld_left > 0) {
             const int tok = tile_of(ld);
@@ -248,22 +279,18 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             // a page outside the cache: its tokens are left out
             if (!ok && tok < ld.len && lane == 0 && p.status) atomicOr(p.status, Q8_DEV_BAD_INDEX);
             if (ok) {
-                const int kvh = ld.hh / p.splits;
-                const int64_t row = ((static_cast<int64_t>(ld_page) * p.kv_heads + kvh) << p.page_shift) +
-                                    (tok & ((1 << p.page_shift) - 1));
+                const int64_t row = ((static_cast<int64_t>(ld_page) * p.kv_heads + ld.kvh) << p.page_shift) + (tok & page_mask);
                 const uint32_t st = ring + ld_slot * C::kStage;
-                const int8_t *kc = p.kq + row * D, *vc = p.vq + row * D;
+                const int8_t *kc = p.kq + row * D + lane * 16, *vc = p.vq + row * D + lane * 16;
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
-                    const int m = i * 32 + lane;
-                    const uint32_t at = (m ^ ((m >> 3) & 7)) * 16;
-                    cp_async16(st + at, kc + m * 16);
-                    cp_async16(st + C::kCodes + at, vc + m * 16);
+                    const uint32_t to = st + ((i & 1) ? odd : even) + i * 512;
+                    cp_async16(to, kc + i * 512);
+                    cp_async16(to + C::kCodes, vc + i * 512);
                 }
                 if (lane < D / 8) {
                     const bool is_v = lane >= D / 16;
-                    const int c = is_v ? lane - D / 16 : lane;
-                    const uint8_t *src = reinterpret_cast<const uint8_t *>((is_v ? p.vs : p.ks) + row * NB) + c * 16;
+                    const uint8_t *src = reinterpret_cast<const uint8_t *>(is_v ? p.vs : p.ks) + row * (NB * 2) + (is_v ? lane - D / 16 : lane) * 16;
                     cp_async16(st + 2 * C::kCodes + lane * 16, src);
                 }
             }
@@ -277,6 +304,19 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     fetch_page();
     for (int i = 0; i < C::kStages - 1; ++i) load();
 
+    // ---- where this lane reads in a tile ----------------------------------------------
+    // keys: tokens r0 and r0 + 8, 8 codes of each block; values: tokens ra, rb, ra + 8, rb + 8, 4 of each
+    const int r0 = token_of<D>(g), ra = token_of<D>(2 * t), rb = token_of<D>(2 * t + 1);
+    constexpr uint32_t kEight = 8 * D;  // bytes from a token to the eighth after it (the same place modulo 8 lines)
+    uint32_t key_at[NB], va_at[NB], vb_at[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        key_at[b] = chunk_at<D>(r0, 2 * b + (t >> 1)) + (t & 1) * 8;
+        va_at[b] = C::kCodes + chunk_at<D>(ra, 2 * b + (g >> 2)) + (g & 3) * 4;
+        vb_at[b] = C::kCodes + chunk_at<D>(rb, 2 * b + (g >> 2)) + (g & 3) * 4;
+    }
+    constexpr uint32_t kFlip = D == 64 ? 64u : 0u;  // at 64 dimensions 8 tokens are 4 lines: the chunk's place changes
+
     // ---- items ---------------------------------------------------------------------
     long long left = u1 - u0;
     long long item0 = u0 - wk.unit;  // first unit of the current item in the list
@@ -284,9 +324,8 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     while (left > 0) {
         const int seg_first = wk.unit;
         const int seg = static_cast<int>(min(left, static_cast<long long>(wk.units - wk.unit)));
-        const int kvh = wk.hh / p.splits, run = wk.hh - kvh * p.splits;
-        const int head0 = kvh * p.group + run * C::HG;          // first query head of the item
-        const int nheads = min(C::HG, p.group - run * C::HG);
+        const int head0 = wk.kvh * p.group + wk.run * C::HG;    // first query head of the item
+        const int nheads = min(C::HG, p.group - wk.run * C::HG);
         // this lane's query fragments: head g (+ 8 per n-tile), 8 dimensions of each block
         uint32_t qf[NT][NB][4];
         float fac[NT][2];  // scores of head 2t, 2t + 1: MMA result -> log2 units (or softcap's argument)
@@ -323,9 +362,11 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             fac[n][1] = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
         }
         float m[NT][2], l[NT][2], o[NT][D / 16][4];
+        float ref[NT][2], top[NT][2];  // m, or 0 where nothing was seen; the score that moves it
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            m[n][0] = m[n][1] = -INFINITY;
+            m[n][0] = m[n][1] = top[n][0] = top[n][1] = -INFINITY;
+            ref[n][0] = ref[n][1] = 0.f;
             l[n][0] = l[n][1] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
@@ -339,94 +380,101 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             load();  // into the slot that the step before this one read
             const uint32_t st = ring + slot * C::kStage;
             if (live) {
-                const int r0 = token_of<D>(g);
                 // ---- scores: 16 tokens x 8 NT heads
                 float acc[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-                const uint32_t sk = st + 2 * C::kCodes;
+                const uint32_t sk = st + 2 * C::kCodes, sv = sk + C::kScales;
+                float s0[NB], s1[NB];
+                token_scales<NB>(sk + r0 * NB * 2, s0);
+                token_scales<NB>(sk + (r0 + 8) * NB * 2, s1);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    const uint32_t in = (t & 1) * 8;
-                    const uint2 w0 = lds64(st + chunk_at<D>(r0, 2 * b + (t >> 1)) + in);
-                    const uint2 w1 = lds64(st + chunk_at<D>(r0 + 8, 2 * b + (t >> 1)) + in);
+                    const uint2 w0 = lds64(st + key_at[b]);
+                    const uint2 w1 = lds64(st + ((key_at[b] + kEight) ^ kFlip));
                     uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
                     codes4_to_f16x2(w0.x, a0, a2);
                     codes4_to_f16x2(w1.x, a1, a3);
                     codes4_to_f16x2(w0.y, b0, b2);
                     codes4_to_f16x2(w1.y, b1, b3);
-                    const uint32_t sc = lds32(sk + (r0 * NB + b) * 2 & ~3u), sd = lds32(sk + ((r0 + 8) * NB + b) * 2 & ~3u);
-                    const float s0 = f16_bits_to_f32((b & 1) ? sc >> 16 : sc & 0xFFFFu);
-                    const float s1 = f16_bits_to_f32((b & 1) ? sd >> 16 : sd & 0xFFFFu);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
-                        mma_f16_16816(d0, d1, d2, d3, a0, a1, a2, a3, qf[n][b][0], qf[n][b][1]);
+                        float d0, d1, d2, d3;
+                        mma_f16_16816_new(d0, d1, d2, d3, a0, a1, a2, a3, qf[n][b][0], qf[n][b][1]);
                         mma_f16_16816(d0, d1, d2, d3, b0, b1, b2, b3, qf[n][b][2], qf[n][b][3]);
-                        acc[n][0] = fmaf(s0, d0, acc[n][0]);
-                        acc[n][1] = fmaf(s0, d1, acc[n][1]);
-                        acc[n][2] = fmaf(s1, d2, acc[n][2]);
-                        acc[n][3] = fmaf(s1, d3, acc[n][3]);
+                        acc[n][0] = fmaf(s0[b], d0, acc[n][0]);
+                        acc[n][1] = fmaf(s0[b], d1, acc[n][1]);
+                        acc[n][2] = fmaf(s1[b], d2, acc[n][2]);
+                        acc[n][3] = fmaf(s1[b], d3, acc[n][3]);
                     }
                 }
+                // value scales of tokens ra, rb, ra + 8, rb + 8
+                uint32_t x[4][NB / 2];
+                raw_scales<NB>(sv + ra * NB * 2, x[0]);
+                raw_scales<NB>(sv + rb * NB * 2, x[1]);
+                raw_scales<NB>(sv + (ra + 8) * NB * 2, x[2]);
+                raw_scales<NB>(sv + (rb + 8) * NB * 2, x[3]);
                 // ---- weights
-                const bool whole = tok >= wk.first && tok + 16 <= wk.len;
-                const bool in0 = whole || (tok + r0 >= wk.first && tok + r0 < wk.len);
-                const bool in1 = whole || (tok + r0 + 8 >= wk.first && tok + r0 + 8 < wk.len);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[n][i] *= fac[n][i & 1];
+                if (p.softcap > 0.f) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[n][i] = p.softcap * kLog2e * tanhf(acc[n][i]);
+                }
+                if (tok < wk.first || tok + 16 > wk.len) {  // some tokens are not seen: no weight, and no value
+                    auto seen = [&](int r) { return tok + r >= wk.first && tok + r < wk.len; };
+                    const bool in0 = seen(r0), in1 = seen(r0 + 8);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[n][i] = (i < 2 ? in0 : in1) ? acc[n][i] : -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = seen(((i & 1) ? rb : ra) + ((i & 2) ? 8 : 0));
+#pragma unroll
+                        for (int b = 0; b < NB / 2; ++b) x[i][b] = in ? x[i][b] : 0u;
+                    }
+                }
                 bool grows = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x = acc[n][i] * fac[n][i & 1];
-                        if (p.softcap > 0.f) x = p.softcap * kLog2e * tanhf(x);
-                        x = (i < 2 ? in0 : in1) ? x : -INFINITY;
-                        acc[n][i] = x;
-                        grows = grows || x > m[n][i & 1] + kGrow;
-                    }
+                    for (int j = 0; j < 2; ++j) grows = grows || fmaxf(acc[n][j], acc[n][2 + j]) > top[n][j];
                 if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float x = fmaxf(acc[n][j], acc[n][2 + j]);
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                            x = fmaxf(x, m[n][j]);
-                            const float f = m[n][j] == -INFINITY ? 0.f : ex2(m[n][j] - x);
-                            m[n][j] = x;
+                            float y = fmaxf(acc[n][j], acc[n][2 + j]);
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                            y = fmaxf(y, m[n][j]);
+                            const float f = m[n][j] == -INFINITY ? 0.f : ex2(m[n][j] - y);
+                            m[n][j] = y;
+                            ref[n][j] = y == -INFINITY ? 0.f : y;
+                            top[n][j] = y + kGrow;
                             l[n][j] *= f;
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) o[n][i][j] *= f, o[n][i][2 + j] *= f;
                         }
                 }
-                uint32_t pf[NT][2];
-                const uint32_t sv = sk + C::kScales;
-                const int ra = token_of<D>(2 * t), rb = token_of<D>(2 * t + 1);
-                // value scales of tokens (ra, rb) and (ra + 8, rb + 8), as pairs
-                uint32_t s01[NB], s89[NB];
-                uint32_t top = 0;
-                {
-                    uint32_t x[4][NB / 2];
+                // a scale above 512 (or a negative one, which the quantizer does not make) in either half
+                uint32_t most = __vmaxu2(__vmaxu2(x[0][0], x[1][0]), __vmaxu2(x[2][0], x[3][0]));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = ((i & 1) ? rb : ra) + ((i & 2) ? 8 : 0);
-                        const bool in = whole || (tok + r >= wk.first && tok + r < wk.len);
+                for (int b = 1; b < NB / 2; ++b)
+                    most = __vmaxu2(most, __vmaxu2(__vmaxu2(x[0][b], x[1][b]), __vmaxu2(x[2][b], x[3][b])));
+                const bool big = __any_sync(0xffffffffu, __vmaxu2(most, 0x60006000u) != 0x60006000u);
+                uint32_t s01[NB], s89[NB];  // as pairs (ra, rb), (ra + 8, rb + 8)
 #pragma unroll
-                        for (int b = 0; b < NB / 2; ++b) {
-                            x[i][b] = in ? lds32(sv + r * NB * 2 + b * 4) : 0u;
-                            const uint32_t lo = x[i][b] & 0x7FFFu, hi = (x[i][b] >> 16) & 0x7FFFu;
-                            top = max(top, max(lo, hi));
-                        }
-                    }
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        s01[b] = __byte_perm(x[0][b / 2], x[1][b / 2], (b & 1) ? 0x7632 : 0x5410);
-                        s89[b] = __byte_perm(x[2][b / 2], x[3][b / 2], (b & 1) ? 0x7632 : 0x5410);
-                    }
+                for (int b = 0; b < NB; ++b) {
+                    s01[b] = __byte_perm(x[0][b / 2], x[1][b / 2], (b & 1) ? 0x7632 : 0x5410);
+                    s89[b] = __byte_perm(x[2][b / 2], x[3][b / 2], (b & 1) ? 0x7632 : 0x5410);
                 }
-                const bool big = __any_sync(0xffffffffu, top > 0x6000u);  // a scale above 512
                 if (big) {
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
@@ -434,38 +482,33 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                         s89[b] = hmul2(s89[b], 0x18001800u);
                     }
                 }
-                const float up = big ? 512.f : 1.f;
+                uint32_t pf[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float ref = m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1];
-                        w[i] = ex2(acc[n][i] - ref);
-                    }
+                    for (int i = 0; i < 4; ++i) w[i] = ex2(acc[n][i] - ref[n][i & 1]);
                     l[n][0] += w[0] + w[2];
                     l[n][1] += w[1] + w[3];
-                    pf[n][0] = movmatrix(f32x2_to_f16x2(w[0] * up, w[1] * up));
-                    pf[n][1] = movmatrix(f32x2_to_f16x2(w[2] * up, w[3] * up));
+                    if (big) w[0] *= 512.f, w[1] *= 512.f, w[2] *= 512.f, w[3] *= 512.f;
+                    pf[n][0] = movmatrix(f32x2_to_f16x2(w[0], w[1]));
+                    pf[n][1] = movmatrix(f32x2_to_f16x2(w[2], w[3]));
                 }
                 // ---- weighted values
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    const uint32_t vb = st + C::kCodes + (g & 3) * 4;
-                    const int c = 2 * b + (g >> 2);
-                    const uint32_t wa = lds32(vb + chunk_at<D>(ra, c)) ^ 0x80808080u;
-                    const uint32_t wb = lds32(vb + chunk_at<D>(rb, c)) ^ 0x80808080u;
-                    const uint32_t wc = lds32(vb + chunk_at<D>(ra + 8, c)) ^ 0x80808080u;
-                    const uint32_t wd = lds32(vb + chunk_at<D>(rb + 8, c)) ^ 0x80808080u;
+                    const uint32_t wa = lds32(st + va_at[b]) ^ 0x80808080u, wb = lds32(st + vb_at[b]) ^ 0x80808080u;
+                    const uint32_t wc = lds32(st + ((va_at[b] + kEight) ^ kFlip)) ^ 0x80808080u;
+                    const uint32_t wd = lds32(st + ((vb_at[b] + kEight) ^ kFlip)) ^ 0x80808080u;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {  // dimensions 32 b + 4 g + 2 i, + 1
-                        const uint32_t x = __byte_perm(wa, wb, i ? 0x7362 : 0x5140);
-                        const uint32_t y = __byte_perm(wc, wd, i ? 0x7362 : 0x5140);
+                        const uint32_t y = __byte_perm(wa, wb, i ? 0x7362 : 0x5140);
+                        const uint32_t z = __byte_perm(wc, wd, i ? 0x7362 : 0x5140);
                         const uint32_t k1152 = 0x64806480u;
-                        const uint32_t a0 = hmul2(hsub2(__byte_perm(x, 0x64646464u, 0x4140), k1152), s01[b]);
-                        const uint32_t a1 = hmul2(hsub2(__byte_perm(x, 0x64646464u, 0x4342), k1152), s01[b]);
-                        const uint32_t a2 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4140), k1152), s89[b]);
-                        const uint32_t a3 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4342), k1152), s89[b]);
+                        const uint32_t a0 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4140), k1152), s01[b]);
+                        const uint32_t a1 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4342), k1152), s01[b]);
+                        const uint32_t a2 = hmul2(hsub2(__byte_perm(z, 0x64646464u, 0x4140), k1152), s89[b]);
+                        const uint32_t a3 = hmul2(hsub2(__byte_perm(z, 0x64646464u, 0x4342), k1152), s89[b]);
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             mma_f16_16816(o[n][2 * b + i][0], o[n][2 * b + i][1], o[n][2 * b + i][2], o[n][2 * b + i][3],
