@@ -14,7 +14,7 @@
 // query is then exact in binary16 down to 2^-31 of that value.  A warp MMA
 // (m16n8k16) multiplies 16 tokens x 32 codes by 8 query heads; the block's
 // scale multiplies its fp32 result, as in the matmuls.
-// Weighted sum: O^T = V^T P, 32 dimensions x 16 tokens by 8 heads.  The
+// Weighted sum: O^T = V^T P, 16 dimensions x 16 tokens by 8 heads.  The
 // weight is rounded to binary16, the value s * code too (2^-11 each at most,
 // against 2^-8 of the bf16 result), sums are fp32.  Value scales above 512 could
 // overflow s * code: such a tile takes s 2^-9 and p 2^9.
@@ -29,8 +29,8 @@
 // the device); CTA c takes units [c * per, (c + 1) * per) of the list of all
 // (sequence, key head, group of query heads) items, so CTAs carry the same
 // load whatever the lengths.  An item within one CTA is finished there; the
-// others leave (m, l, O) in the workspace and the last CTA to arrive joins
-// them in CTA order.
+// others leave (m, l, O) in the workspace, where they are joined in CTA order, in
+// bunches and then the bunches, each by the last CTA to arrive.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -49,6 +49,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnitTokens = kWarps * 16;
 constexpr int kMaxGrid = 1024;    // CTAs a launch may have (sizes the workspace)
 constexpr int kMinUnits = 4;      // units a CTA takes at least
+constexpr int kBunch = 32;        // most parts joined at once
 constexpr float kGrow = 4.0f;     // log2 growth of a score that moves the reference
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -59,7 +60,7 @@ struct AttnParams {
     const int32_t *table, *lens;
     uint16_t *out;
     float *lse;
-    uint32_t *tickets;  // [kMaxGrid]
+    uint32_t *tickets;  // [2][2 * kMaxGrid]: by the first part of a bunch, of an item
     float *parts;       // [2 * kMaxGrid][HG * (D + 2)]
     uint32_t *status;
     int64_t ldq;
@@ -68,6 +69,16 @@ struct AttnParams {
     float scale, softcap;
 };
 
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t *p, uint32_t v) {
+    uint32_t old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
@@ -92,7 +103,8 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
 // The token (0 .. 7) that MMA row f stands for; rows f + 8 stand for token
 // + 8.  Chunks of 16 bytes are stored at chunk ^ (128-byte line & 7); these
 // orders make both access patterns hit all banks once: keys (rows f = 0..3
-// and 4..7, two chunks each) and values (rows 0, 2, 4, 6 and 1, 3, 5, 7).
+// and 4..7, two chunks each) and values (rows 0, 2, 4, 6 and 1, 3, 5, 7, two
+// neighbouring lanes' chunks each).
 template <int D>
 __device__ __forceinline__ int token_of(int f) {
     constexpr uint32_t order = D == 64 ? 0x37265140u : (D == 128 ? 0x57136420u : 0x67453210u);
@@ -126,6 +138,18 @@ __device__ __forceinline__ void token_scales(uint32_t at, float (&f)[NB]) {
     for (int b = 0; b < NB / 2; ++b) {
         const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[b]));
         f[2 * b] = v.x, f[2 * b + 1] = v.y;
+    }
+}
+
+// N codes of one token, as offsets from -128.
+template <int N>
+__device__ __forceinline__ void run_codes(uint32_t at, uint32_t (&w)[N / 4]) {
+    if constexpr (N == 16) {
+        const uint4 v = lds128(at);
+        w[0] = v.x ^ 0x80808080u, w[1] = v.y ^ 0x80808080u, w[2] = v.z ^ 0x80808080u, w[3] = v.w ^ 0x80808080u;
+    } else {
+        const uint2 v = lds64(at);
+        w[0] = v.x ^ 0x80808080u, w[1] = v.y ^ 0x80808080u;
     }
 }
 
@@ -179,7 +203,7 @@ struct Cfg {
     static constexpr int kStages = D == 256 ? 3 : (D == 128 ? 4 : 6);
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kOPitch = D + 8;
-    static constexpr int kJoin = (HG * kOPitch + 2 * kWarps * HG + 2 * HG) * 4;
+    static constexpr int kJoin = (HG * kOPitch + 2 * kWarps * HG + 2 * HG + kBunch * HG) * 4;
     static constexpr int kSmem = kRing + kJoin;
     static constexpr int kPart = HG * (D + 2);     // floats of one partial result
 };
@@ -189,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     using C = Cfg<D, NT>;
     constexpr int NB = D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_scan[kWarps];
+    __shared__ long long s_scan[2 * kWarps];
     __shared__ uint32_t s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -198,18 +222,28 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     float *const s_l = s_m + kWarps * C::HG;
     float *const s_mm = s_l + kWarps * C::HG;     // [HG] joined
     float *const s_ll = s_mm + C::HG;
+    float *const s_f = s_ll + C::HG;              // [kBunch][HG]
 
     // ---- the list: how long it is, and where this CTA begins --------------------
     const int heads = p.kv_heads * p.splits;
-    long long total = 0;
-    for (int b = tid; b < p.batch; b += kThreads) total += seq_units(p, seq_len(p, b, blockIdx.x == 0));
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) s_scan[warp] = total;
+    long long total = 0, n_items = 0;
+    for (int b = tid; b < p.batch; b += kThreads) {
+        const int n = seq_units(p, seq_len(p, b, blockIdx.x == 0));
+        total += n, n_items += n > 0 ? 1 : 0;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        n_items += __shfl_xor_sync(0xffffffffu, n_items, o);
+    }
+    if (lane == 0) s_scan[warp] = total, s_scan[kWarps + warp] = n_items;
     __syncthreads();
-    total = 0;
-    for (int w = 0; w < kWarps; ++w) total += s_scan[w];
-    total *= heads;
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinUnits));
+    total = n_items = 0;
+    for (int w = 0; w < kWarps; ++w) total += s_scan[w], n_items += s_scan[kWarps + w];
+    total *= heads, n_items *= heads;
+    // at least kMinUnits, and of longer items (on the average) half, up to 2 kMinUnits: a part more to
+    // join costs as much as a few units
+    const long long half = n_items > 0 ? total / n_items / 2 : 0;
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, min(max(half, static_cast<long long>(kMinUnits)), 2ll * kMinUnits));
     const long long u0 = per * blockIdx.x, u1 = min(u0 + per, total);
 
     // sequences of no tokens have no units: write their answer
@@ -305,16 +339,21 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     for (int i = 0; i < C::kStages - 1; ++i) load();
 
     // ---- where this lane reads in a tile ----------------------------------------------
-    // keys: tokens r0 and r0 + 8, 8 codes of each block; values: tokens ra, rb, ra + 8, rb + 8, 4 of each
+    // keys: tokens r0 and r0 + 8, 8 codes of each block; values: of tokens ra, rb, ra + 8, rb + 8 the
+    // dimensions kRun g .. kRun (g + 1) - 1 of each kRun * 8, which lie in one block
     const int r0 = token_of<D>(g), ra = token_of<D>(2 * t), rb = token_of<D>(2 * t + 1);
+    constexpr int kRun = D == 64 ? 8 : 16, kRuns = D / (8 * kRun);
     constexpr uint32_t kEight = 8 * D;  // bytes from a token to the eighth after it (the same place modulo 8 lines)
-    uint32_t key_at[NB], va_at[NB], vb_at[NB];
+    uint32_t key_at[NB], va_at[kRuns], vb_at[kRuns];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        key_at[b] = chunk_at<D>(r0, 2 * b + (t >> 1)) + (t & 1) * 8;
-        va_at[b] = C::kCodes + chunk_at<D>(ra, 2 * b + (g >> 2)) + (g & 3) * 4;
-        vb_at[b] = C::kCodes + chunk_at<D>(rb, 2 * b + (g >> 2)) + (g & 3) * 4;
+    for (int b = 0; b < NB; ++b) key_at[b] = chunk_at<D>(r0, 2 * b + (t >> 1)) + (t & 1) * 8;
+#pragma unroll
+    for (int k = 0; k < kRuns; ++k) {
+        const int d = kRun * (8 * k + g);
+        va_at[k] = C::kCodes + chunk_at<D>(ra, d / 16) + d % 16;
+        vb_at[k] = C::kCodes + chunk_at<D>(rb, d / 16) + d % 16;
     }
+    const int vs_at = (kRun * g / 32) * 2;  // bytes to the scale of a token's first run; the next is kRun * 8 / 32 on
     constexpr uint32_t kFlip = D == 64 ? 64u : 0u;  // at 64 dimensions 8 tokens are 4 lines: the chunk's place changes
 
     // ---- items ---------------------------------------------------------------------
@@ -408,12 +447,14 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                         acc[n][3] = fmaf(s1[b], d3, acc[n][3]);
                     }
                 }
-                // value scales of tokens ra, rb, ra + 8, rb + 8
-                uint32_t x[4][NB / 2];
-                raw_scales<NB>(sv + ra * NB * 2, x[0]);
-                raw_scales<NB>(sv + rb * NB * 2, x[1]);
-                raw_scales<NB>(sv + (ra + 8) * NB * 2, x[2]);
-                raw_scales<NB>(sv + (rb + 8) * NB * 2, x[3]);
+                // value scales of tokens (ra, rb) and (ra + 8, rb + 8), as pairs
+                uint32_t s01[kRuns], s89[kRuns];
+#pragma unroll
+                for (int k = 0; k < kRuns; ++k) {
+                    const uint32_t from = sv + vs_at + k * (kRun * 8 / 32) * 2;
+                    s01[k] = lds16(from + ra * NB * 2) | lds16(from + rb * NB * 2) << 16;
+                    s89[k] = lds16(from + (ra + 8) * NB * 2) | lds16(from + (rb + 8) * NB * 2) << 16;
+                }
                 // ---- weights
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -432,12 +473,10 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[n][i] = (i < 2 ? in0 : in1) ? acc[n][i] : -INFINITY;
+                    const uint32_t m01 = (seen(ra) ? 0xFFFFu : 0u) | (seen(rb) ? 0xFFFF0000u : 0u);
+                    const uint32_t m89 = (seen(ra + 8) ? 0xFFFFu : 0u) | (seen(rb + 8) ? 0xFFFF0000u : 0u);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool in = seen(((i & 1) ? rb : ra) + ((i & 2) ? 8 : 0));
-#pragma unroll
-                        for (int b = 0; b < NB / 2; ++b) x[i][b] = in ? x[i][b] : 0u;
-                    }
+                    for (int k = 0; k < kRuns; ++k) s01[k] &= m01, s89[k] &= m89;
                 }
                 bool grows = false;
 #pragma unroll
@@ -464,22 +503,15 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                         }
                 }
                 // a scale above 512 (or a negative one, which the quantizer does not make) in either half
-                uint32_t most = __vmaxu2(__vmaxu2(x[0][0], x[1][0]), __vmaxu2(x[2][0], x[3][0]));
+                uint32_t most = 0x60006000u;
 #pragma unroll
-                for (int b = 1; b < NB / 2; ++b)
-                    most = __vmaxu2(most, __vmaxu2(__vmaxu2(x[0][b], x[1][b]), __vmaxu2(x[2][b], x[3][b])));
-                const bool big = __any_sync(0xffffffffu, __vmaxu2(most, 0x60006000u) != 0x60006000u);
-                uint32_t s01[NB], s89[NB];  // as pairs (ra, rb), (ra + 8, rb + 8)
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    s01[b] = __byte_perm(x[0][b / 2], x[1][b / 2], (b & 1) ? 0x7632 : 0x5410);
-                    s89[b] = __byte_perm(x[2][b / 2], x[3][b / 2], (b & 1) ? 0x7632 : 0x5410);
-                }
+                for (int k = 0; k < kRuns; ++k) most = __vmaxu2(most, __vmaxu2(s01[k], s89[k]));
+                const bool big = __any_sync(0xffffffffu, most != 0x60006000u);
                 if (big) {
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        s01[b] = hmul2(s01[b], 0x18001800u);  // 2^-9
-                        s89[b] = hmul2(s89[b], 0x18001800u);
+                    for (int k = 0; k < kRuns; ++k) {
+                        s01[k] = hmul2(s01[k], 0x18001800u);  // 2^-9
+                        s89[k] = hmul2(s89[k], 0x18001800u);
                     }
                 }
                 uint32_t pf[NT][2];
@@ -494,25 +526,29 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                     pf[n][0] = movmatrix(f32x2_to_f16x2(w[0], w[1]));
                     pf[n][1] = movmatrix(f32x2_to_f16x2(w[2], w[3]));
                 }
-                // ---- weighted values
+                // ---- weighted values: MMA rows g and g + 8 of tile q are this lane's dimensions 2 q and
+                // 2 q + 1 of its run
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint32_t wa = lds32(st + va_at[b]) ^ 0x80808080u, wb = lds32(st + vb_at[b]) ^ 0x80808080u;
-                    const uint32_t wc = lds32(st + ((va_at[b] + kEight) ^ kFlip)) ^ 0x80808080u;
-                    const uint32_t wd = lds32(st + ((vb_at[b] + kEight) ^ kFlip)) ^ 0x80808080u;
+                for (int k = 0; k < kRuns; ++k) {
+                    uint32_t wa[kRun / 4], wb[kRun / 4], wc[kRun / 4], wd[kRun / 4];
+                    run_codes<kRun>(st + va_at[k], wa);
+                    run_codes<kRun>(st + vb_at[k], wb);
+                    run_codes<kRun>(st + ((va_at[k] + kEight) ^ kFlip), wc);
+                    run_codes<kRun>(st + ((vb_at[k] + kEight) ^ kFlip), wd);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {  // dimensions 32 b + 4 g + 2 i, + 1
-                        const uint32_t y = __byte_perm(wa, wb, i ? 0x7362 : 0x5140);
-                        const uint32_t z = __byte_perm(wc, wd, i ? 0x7362 : 0x5140);
+                    for (int q = 0; q < kRun / 2; ++q) {
+                        const uint32_t y = __byte_perm(wa[q / 2], wb[q / 2], (q & 1) ? 0x7362 : 0x5140);
+                        const uint32_t z = __byte_perm(wc[q / 2], wd[q / 2], (q & 1) ? 0x7362 : 0x5140);
                         const uint32_t k1152 = 0x64806480u;
-                        const uint32_t a0 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4140), k1152), s01[b]);
-                        const uint32_t a1 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4342), k1152), s01[b]);
-                        const uint32_t a2 = hmul2(hsub2(__byte_perm(z, 0x64646464u, 0x4140), k1152), s89[b]);
-                        const uint32_t a3 = hmul2(hsub2(__byte_perm(z, 0x64646464u, 0x4342), k1152), s89[b]);
+                        const uint32_t a0 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4140), k1152), s01[k]);
+                        const uint32_t a1 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4342), k1152), s01[k]);
+                        const uint32_t a2 = hmul2(hsub2(__byte_perm(z, 0x64646464u, 0x4140), k1152), s89[k]);
+                        const uint32_t a3 = hmul2(hsub2(__byte_perm(z, 0x64646464u, 0x4342), k1152), s89[k]);
+                        constexpr int kTiles = kRun / 2;
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            mma_f16_16816(o[n][2 * b + i][0], o[n][2 * b + i][1], o[n][2 * b + i][2], o[n][2 * b + i][3],
-                                          a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                            mma_f16_16816(o[n][k * kTiles + q][0], o[n][k * kTiles + q][1], o[n][k * kTiles + q][2],
+                                          o[n][k * kTiles + q][3], a0, a1, a2, a3, pf[n][0], pf[n][1]);
                     }
                 }
             }
@@ -545,27 +581,37 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             s_mm[tid] = mm;
             s_ll[tid] = ll;
         }
-        for (int w = 0; w < kWarps; ++w) {
+        // each warp adds its sums to one quarter of the dimensions after another, beginning with its
+        // own: quarter q takes warps q, q + 1, ... in that order
+        float f[NT][2];
+#pragma unroll 1
+        for (int turn = 0; turn < kWarps; ++turn) {
             __syncthreads();
-            if (warp != w) continue;
+            if (turn == 0) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int h = n * 8 + 2 * t + j;
-                    const float f = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - s_mm[h]);
+                    for (int j = 0; j < 2; ++j) f[n][j] = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - s_mm[n * 8 + 2 * t + j]);
+            }
+            const int quarter = (warp + kWarps - turn) % kWarps;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        float2 *at = reinterpret_cast<float2 *>(s_o + h * C::kOPitch + 32 * (i >> 1) + 4 * g + 2 * (i & 1));
-                        float2 v = make_float2(o[n][i][j] * f, o[n][i][2 + j] * f);
-                        if (w > 0) {
+            for (int i = 0; i < D / 16; ++i) {
+                if (i / (D / 64) != quarter) continue;
+                const int d = kRun * (8 * (i / (kRun / 2)) + g) + 2 * (i % (kRun / 2));
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float2 *at = reinterpret_cast<float2 *>(s_o + (n * 8 + 2 * t + j) * C::kOPitch + d);
+                        float2 v = make_float2(o[n][i][j] * f[n][j], o[n][i][2 + j] * f[n][j]);
+                        if (turn > 0) {
                             const float2 old = *at;
                             v.x += old.x;
                             v.y += old.y;
                         }
                         *at = v;
                     }
-                }
+            }
         }
         __syncthreads();
 
@@ -574,9 +620,9 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             for (int i = tid; i < nheads * (D / 4); i += kThreads) {
                 const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
                 const float ll = s_ll[h], r = ll == 0.f ? 0.f : 1.f / ll;
-                const float *src = s_o + h * C::kOPitch + d;
-                const __nv_bfloat162 x = __floats2bfloat162_rn(src[0] * r, src[1] * r);
-                const __nv_bfloat162 y = __floats2bfloat162_rn(src[2] * r, src[3] * r);
+                const float4 o4 = *reinterpret_cast<const float4 *>(s_o + h * C::kOPitch + d);
+                const __nv_bfloat162 x = __floats2bfloat162_rn(o4.x * r, o4.y * r);
+                const __nv_bfloat162 y = __floats2bfloat162_rn(o4.z * r, o4.w * r);
                 uint2 v;
                 v.x = *reinterpret_cast<const uint32_t *>(&x);
                 v.y = *reinterpret_cast<const uint32_t *>(&y);
@@ -591,55 +637,87 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
         if (seg == wk.units) {
             answer();
         } else {
+            // CTAs c0 .. c1 have a part each.  The last of a bunch of neighbours joins theirs into one, the
+            // last bunch of the item those: with all of them left to the item's last CTA, 57 parts took
+            // 20 us at the end of a long sequence.
             const int c0 = static_cast<int>(item0 / per), c1 = static_cast<int>((item0 + wk.units - 1) / per);
-            float *const mine = p.parts + static_cast<int64_t>(2 * blockIdx.x + (seg_first == 0 ? 1 : 0)) * C::kPart;
-            for (int i = tid; i < C::HG * (D / 4); i += kThreads) {
-                const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-                *reinterpret_cast<float4 *>(mine + h * D + d) = *reinterpret_cast<const float4 *>(s_o + h * C::kOPitch + d);
-            }
-            if (tid < C::HG) {
-                mine[C::HG * D + tid] = s_mm[tid];
-                mine[C::HG * D + C::HG + tid] = s_ll[tid];
-            }
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const uint32_t n = atomicAdd(p.tickets + c0, 1u);
-                s_last = n == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
-                if (s_last) p.tickets[c0] = 0u;
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                auto part = [&](int c) { return p.parts + static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * C::kPart; };
+            auto slot_of = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };
+            auto part = [&](int c) { return p.parts + static_cast<int64_t>(slot_of(c)) * C::kPart; };
+            auto leave = [&](float *to) {
+                for (int i = tid; i < C::HG * (D / 4); i += kThreads) {
+                    const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+                    __stcg(reinterpret_cast<float4 *>(to + h * D + d), *reinterpret_cast<const float4 *>(s_o + h * C::kOPitch + d));
+                }
                 if (tid < C::HG) {
-                    float mm = -INFINITY, ll = 0.f;
-                    for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(part(c) + C::HG * D + tid));
-                    for (int c = c0; c <= c1; ++c) {
-                        const float mc = __ldcg(part(c) + C::HG * D + tid), lc = __ldcg(part(c) + C::HG * D + C::HG + tid);
-                        ll += mc == -INFINITY ? lc : lc * ex2(mc - mm);
-                    }
-                    s_mm[tid] = mm;
-                    s_ll[tid] = ll;
+                    __stcg(to + C::HG * D + tid, s_mm[tid]);
+                    __stcg(to + C::HG * D + C::HG + tid, s_ll[tid]);
+                }
+            };
+            // counts this CTA in; true for the last of n (one thread's fence, after the barrier: a fence
+            // waits for the copies its thread has under way)
+            auto last_of = [&](uint32_t *ticket, int n) -> bool {
+                __syncthreads();
+                if (tid == 0) {
+                    s_last = atomic_add_acq_rel(ticket, 1u) == static_cast<uint32_t>(n - 1) ? 1u : 0u;
+                    if (s_last) *ticket = 0u;
                 }
                 __syncthreads();
-                for (int i = tid; i < nheads * (D / 4); i += kThreads) {
+                return s_last != 0;
+            };
+            // s_o, s_mm, s_ll <- the parts of CTAs a, a + step, ... (n of them, at most kBunch), in that order
+            auto join = [&](int a, int step, int n) {
+                for (int i = tid; i < n * C::HG; i += kThreads) s_f[i] = __ldcg(part(a + i / C::HG * step) + C::HG * D + i % C::HG);
+                __syncthreads();
+                if (tid < C::HG) {
+                    float mm = -INFINITY;
+                    for (int c = 0; c < n; ++c) mm = fmaxf(mm, s_f[c * C::HG + tid]);
+                    s_mm[tid] = mm;
+                }
+                __syncthreads();
+                for (int i = tid; i < n * C::HG; i += kThreads) {
+                    const float mc = s_f[i];
+                    s_f[i] = mc == -INFINITY ? 1.f : ex2(mc - s_mm[i % C::HG]);
+                }
+                __syncthreads();
+                for (int i = tid; i < C::HG * (D / 4) + C::HG; i += kThreads) {
+                    if (i >= C::HG * (D / 4)) {
+                        const int h = i - C::HG * (D / 4);
+                        float ll = 0.f;
+#pragma unroll 8
+                        for (int c = 0; c < n; ++c) ll = fmaf(__ldcg(part(a + c * step) + C::HG * D + C::HG + h), s_f[c * C::HG + h], ll);
+                        s_ll[h] = ll;
+                        continue;
+                    }
                     const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-                    const float mm = s_mm[h];
                     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-                    for (int c = c0; c <= c1; ++c) {
-                        const float *q = part(c);
-                        const float mc = __ldcg(q + C::HG * D + h);
-                        const float f = mc == -INFINITY ? 1.f : ex2(mc - mm);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(q + h * D + d));
+                    for (int c = 0; c < n; ++c) {
+                        const float f = s_f[c * C::HG + h];
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(a + c * step) + h * D + d));
                         sum.x = fmaf(v.x, f, sum.x), sum.y = fmaf(v.y, f, sum.y);
                         sum.z = fmaf(v.z, f, sum.z), sum.w = fmaf(v.w, f, sum.w);
                     }
                     *reinterpret_cast<float4 *>(s_o + h * C::kOPitch + d) = sum;
                 }
                 __syncthreads();
-                answer();
+            };
+            const int c = static_cast<int>(blockIdx.x), n = c1 - c0 + 1;
+            int bunch = 8;
+            while (bunch * bunch < n) bunch *= 2;  // 1024 CTAs at most: 32
+            const int first = c0 + (c - c0) / bunch * bunch, in_bunch = min(bunch, c1 - first + 1);
+            const int bunches = (n + bunch - 1) / bunch;
+            leave(part(c));
+            if (last_of(p.tickets + slot_of(first), in_bunch)) {
+                join(first, 1, in_bunch);
+                if (bunches == 1) {
+                    answer();
+                } else {
+                    leave(part(first));
+                    if (last_of(p.tickets + 2 * kMaxGrid + slot_of(c0), bunches)) {
+                        join(c0, bunch, bunches);
+                        answer();
+                    }
+                }
             }
         }
         __syncthreads();
@@ -691,7 +769,7 @@ q8_status launch(const AttnParams &p, int64_t most_units, const DeviceInfo *di, 
 // Counters, then two partial results per CTA.
 size_t attn_workspace(int q_heads, int kv_heads, int head_dim) {
     const int hg = 8 * tiles_of(q_heads / kv_heads, head_dim);
-    return static_cast<size_t>(kMaxGrid) * 4 + static_cast<size_t>(2) * kMaxGrid * hg * (head_dim + 2) * 4;
+    return static_cast<size_t>(4) * kMaxGrid * 4 + static_cast<size_t>(2) * kMaxGrid * hg * (head_dim + 2) * 4;
 }
 
 q8_status launch_attn(const q8_kv_cache &c, const AttnArgs &a, void *ws, uint32_t *dev_status, cudaStream_t stream) {
@@ -701,7 +779,7 @@ q8_status launch_attn(const q8_kv_cache &c, const AttnArgs &a, void *ws, uint32_
     p.kq = c.kq, p.vq = c.vq, p.ks = c.ks, p.vs = c.vs;
     p.q = a.q, p.table = a.table, p.lens = a.lens, p.out = a.out, p.lse = a.lse;
     p.tickets = static_cast<uint32_t *>(ws);
-    p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kMaxGrid * 4);
+    p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 4 * kMaxGrid * 4);
     p.status = dev_status;
     p.ldq = a.ldq;
     p.batch = a.batch, p.q_heads = a.q_heads, p.kv_heads = c.kv_heads;

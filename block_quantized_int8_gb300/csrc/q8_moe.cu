@@ -651,12 +651,8 @@ __device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int 
 
 // ---- all CTAs of the launch (a cooperative one: they all run) --------------------------------------
 __device__ __forceinline__ void arrive(uint32_t *counter) {
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        atomicAdd(counter, 1u);
-    }
+    if (threadIdx.x == 0) asm volatile("red.add.release.gpu.global.u32 [%0], 1;" ::"l"(counter) : "memory");
 }
 __device__ __forceinline__ bool wait_all(const uint32_t *counter, uint32_t *status, int &s_ok) {
     if (threadIdx.x == 0) {
