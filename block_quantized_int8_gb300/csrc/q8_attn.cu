@@ -49,7 +49,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnitTokens = kWarps * 16;
 constexpr int kMaxGrid = 1024;    // CTAs a launch may have (sizes the workspace)
 constexpr int kMinUnits = 4;      // units a CTA takes at least
-constexpr int kBunch = 32;        // most parts joined at once
+constexpr int kEndUnits = 2;      // what ending an item (joining warps, giving the answer) takes, in units' time
 constexpr float kGrow = 4.0f;     // log2 growth of a score that moves the reference
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -203,7 +203,7 @@ struct Cfg {
     static constexpr int kStages = D == 256 ? 3 : (D == 128 ? 4 : 6);
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kOPitch = D + 8;
-    static constexpr int kJoin = (HG * kOPitch + 2 * kWarps * HG + 2 * HG + kBunch * HG) * 4;
+    static constexpr int kJoin = (HG * kOPitch + 2 * kWarps * HG + 2 * HG) * 4;
     static constexpr int kSmem = kRing + kJoin;
     static constexpr int kPart = HG * (D + 2);     // floats of one partial result
 };
@@ -222,14 +222,13 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     float *const s_l = s_m + kWarps * C::HG;
     float *const s_mm = s_l + kWarps * C::HG;     // [HG] joined
     float *const s_ll = s_mm + C::HG;
-    float *const s_f = s_ll + C::HG;              // [kBunch][HG]
 
-    // ---- the list: how long it is, and where this CTA begins --------------------
+    // ---- the list: an item takes its units and kEndUnits; how long that is, and where this CTA begins ----
     const int heads = p.kv_heads * p.splits;
     long long total = 0, n_items = 0;
     for (int b = tid; b < p.batch; b += kThreads) {
         const int n = seq_units(p, seq_len(p, b, blockIdx.x == 0));
-        total += n, n_items += n > 0 ? 1 : 0;
+        total += n > 0 ? n + kEndUnits : 0, n_items += n > 0 ? 1 : 0;
     }
     for (int o = 16; o > 0; o >>= 1) {
         total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -256,14 +255,17 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     }
     if (u0 >= u1) return;
 
-    // the sequence that holds unit u0: each warp scans for itself, 32 at a time
+    // the sequence at place u0 of the list: each warp scans for itself, 32 at a time
     Walk wk;
+    long long left = u1 - u0;  // of this CTA's stretch of the list, from its next unit on
+    long long item0;           // where the item begins
     {
         long long before = 0;
         int b0 = 0;
         while (true) {
             const int b = b0 + lane;
-            long long n = b < p.batch ? static_cast<long long>(seq_units(p, seq_len(p, b, false))) * heads : 0;
+            const int units = b < p.batch ? seq_units(p, seq_len(p, b, false)) : 0;
+            const long long n = units > 0 ? static_cast<long long>(units + kEndUnits) * heads : 0;
             long long run = n;
             for (int o = 1; o < 32; o <<= 1) {
                 const long long v = __shfl_up_sync(0xffffffffu, run, o);
@@ -281,15 +283,23 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
         }
         enter(p, wk);
         const long long in = u0 - before;
-        const int item = static_cast<int>(in / wk.units);
+        const int cost = wk.units + kEndUnits, item = static_cast<int>(in / cost);
         wk.kvh = item / p.splits, wk.run = item - wk.kvh * p.splits;
-        wk.unit = static_cast<int>(in - static_cast<long long>(item) * wk.units);
+        wk.unit = static_cast<int>(in - static_cast<long long>(item) * cost);
+        item0 = u0 - wk.unit;
+        if (wk.unit >= wk.units) {  // at the end of an item that others work on: begin with the next
+            left -= cost - wk.unit;
+            item0 += cost;
+            if (left <= 0) return;
+            wk.unit = wk.units - 1;
+            advance(p, wk);
+        }
     }
 
     // ---- this warp's pipeline ------------------------------------------------------
     const uint32_t ring = smem_addr(smem) + warp * C::kStages * C::kStage;
     Walk ld = wk;              // the next unit to load
-    long long ld_left = u1 - u0;
+    long long ld_left = left;
     int ld_slot = 0;
     int ld_page = -1;          // page of the tile to load next, read one step ahead
     uint32_t held = 0;         // bit i: slot i holds a tile
@@ -328,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                     cp_async16(st + 2 * C::kCodes + lane * 16, src);
                 }
             }
-            --ld_left;
+            ld_left -= ld.unit + 1 < ld.units ? 1 : 1 + kEndUnits;
             if (ld_left > 0) advance(p, ld);
             fetch_page();
         }
@@ -357,8 +367,6 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     constexpr uint32_t kFlip = D == 64 ? 64u : 0u;  // at 64 dimensions 8 tokens are 4 lines: the chunk's place changes
 
     // ---- items ---------------------------------------------------------------------
-    long long left = u1 - u0;
-    long long item0 = u0 - wk.unit;  // first unit of the current item in the list
     int slot = 0;
     while (left > 0) {
         const int seg_first = wk.unit;
@@ -616,26 +624,22 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
         __syncthreads();
 
         // ---- give the item's answer, or leave a part of it --------------------------------
-        auto answer = [&]() {
-            for (int i = tid; i < nheads * (D / 4); i += kThreads) {
-                const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-                const float ll = s_ll[h], r = ll == 0.f ? 0.f : 1.f / ll;
-                const float4 o4 = *reinterpret_cast<const float4 *>(s_o + h * C::kOPitch + d);
-                const __nv_bfloat162 x = __floats2bfloat162_rn(o4.x * r, o4.y * r);
-                const __nv_bfloat162 y = __floats2bfloat162_rn(o4.z * r, o4.w * r);
-                uint2 v;
-                v.x = *reinterpret_cast<const uint32_t *>(&x);
-                v.y = *reinterpret_cast<const uint32_t *>(&y);
-                *reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(wk.b) * p.q_heads + head0 + h) * D + d) = v;
-            }
-            if (p.lse && tid < nheads) {
-                const float mm = s_mm[tid], ll = s_ll[tid];
-                p.lse[static_cast<int64_t>(wk.b) * p.q_heads + head0 + tid] =
-                    ll == 0.f ? -INFINITY : fmaf(mm, 0.69314718055994531f, logf(ll));
-            }
+        auto answer = [&](int h, int d, float mm, float ll, float4 v) {  // four dimensions of a head
+            const float r = ll == 0.f ? 0.f : 1.f / ll;
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v.x * r, v.y * r);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(v.z * r, v.w * r);
+            const int64_t row = static_cast<int64_t>(wk.b) * p.q_heads + head0 + h;
+            *reinterpret_cast<uint2 *>(p.out + row * D + d) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+            if (p.lse && d == 0) p.lse[row] = ll == 0.f ? -INFINITY : fmaf(mm, 0.69314718055994531f, logf(ll));
         };
+        const int quads = nheads * (D / 4);
+        auto own = [&](int h, int d) { return *reinterpret_cast<const float4 *>(s_o + h * C::kOPitch + d); };
         if (seg == wk.units) {
-            answer();
+            for (int i = tid; i < quads; i += kThreads) {
+                const int h = i / (D / 4), d = i % (D / 4) * 4;
+                answer(h, d, s_mm[h], s_ll[h], own(h, d));
+            }
         } else {
             // CTAs c0 .. c1 have a part each.  The last of a bunch of neighbours joins theirs into one, the
             // last bunch of the item those: with all of them left to the item's last CTA, 57 parts took
@@ -643,15 +647,9 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             const int c0 = static_cast<int>(item0 / per), c1 = static_cast<int>((item0 + wk.units - 1) / per);
             auto slot_of = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };
             auto part = [&](int c) { return p.parts + static_cast<int64_t>(slot_of(c)) * C::kPart; };
-            auto leave = [&](float *to) {
-                for (int i = tid; i < C::HG * (D / 4); i += kThreads) {
-                    const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-                    __stcg(reinterpret_cast<float4 *>(to + h * D + d), *reinterpret_cast<const float4 *>(s_o + h * C::kOPitch + d));
-                }
-                if (tid < C::HG) {
-                    __stcg(to + C::HG * D + tid, s_mm[tid]);
-                    __stcg(to + C::HG * D + C::HG + tid, s_ll[tid]);
-                }
+            auto leave = [&](float *to, int h, int d, float mm, float ll, float4 v) {
+                __stcg(reinterpret_cast<float4 *>(to + h * D + d), v);
+                if (d == 0) __stcg(reinterpret_cast<float2 *>(to + C::HG * D) + h, make_float2(mm, ll));
             };
             // counts this CTA in; true for the last of n (one thread's fence, after the barrier: a fence
             // waits for the copies its thread has under way)
@@ -664,66 +662,81 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                 __syncthreads();
                 return s_last != 0;
             };
-            // s_o, s_mm, s_ll <- the parts of CTAs a, a + step, ... (n of them, at most kBunch), in that order
-            auto join = [&](int a, int step, int n) {
-                for (int i = tid; i < n * C::HG; i += kThreads) s_f[i] = __ldcg(part(a + i / C::HG * step) + C::HG * D + i % C::HG);
-                __syncthreads();
-                if (tid < C::HG) {
-                    float mm = -INFINITY;
-                    for (int c = 0; c < n; ++c) mm = fmaxf(mm, s_f[c * C::HG + tid]);
-                    s_mm[tid] = mm;
-                }
-                __syncthreads();
-                for (int i = tid; i < n * C::HG; i += kThreads) {
-                    const float mc = s_f[i];
-                    s_f[i] = mc == -INFINITY ? 1.f : ex2(mc - s_mm[i % C::HG]);
-                }
-                __syncthreads();
-                for (int i = tid; i < C::HG * (D / 4) + C::HG; i += kThreads) {
-                    if (i >= C::HG * (D / 4)) {
-                        const int h = i - C::HG * (D / 4);
-                        float ll = 0.f;
-#pragma unroll 8
-                        for (int c = 0; c < n; ++c) ll = fmaf(__ldcg(part(a + c * step) + C::HG * D + C::HG + h), s_f[c * C::HG + h], ll);
-                        s_ll[h] = ll;
-                        continue;
+            // the parts of CTAs a, a + step, ... (n of them) joined in that order, eight under way at a time
+            auto join = [&](int a, int step, int n, int h, int d, float &mm, float &ll, float4 &v) {
+                mm = -INFINITY, ll = 0.f, v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                for (int c = 0; c < n; c += 8) {
+                    float2 ml[8];
+                    float4 x[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float *from = part(a + min(c + k, n - 1) * step);
+                        ml[k] = __ldcg(reinterpret_cast<const float2 *>(from + C::HG * D) + h);
+                        x[k] = __ldcg(reinterpret_cast<const float4 *>(from + h * D + d));
                     }
-                    const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int c = 0; c < n; ++c) {
-                        const float f = s_f[c * C::HG + h];
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(a + c * step) + h * D + d));
-                        sum.x = fmaf(v.x, f, sum.x), sum.y = fmaf(v.y, f, sum.y);
-                        sum.z = fmaf(v.z, f, sum.z), sum.w = fmaf(v.w, f, sum.w);
+                    float top = mm;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].x);
+                    auto weight = [&](float m1) { return m1 == -INFINITY ? (top == -INFINITY ? 1.f : 0.f) : ex2(m1 - top); };
+                    const float f0 = weight(mm);
+                    ll *= f0, v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (c + k >= n) continue;
+                        const float f1 = weight(ml[k].x);
+                        ll = fmaf(ml[k].y, f1, ll);
+                        v.x = fmaf(x[k].x, f1, v.x), v.y = fmaf(x[k].y, f1, v.y);
+                        v.z = fmaf(x[k].z, f1, v.z), v.w = fmaf(x[k].w, f1, v.w);
                     }
-                    *reinterpret_cast<float4 *>(s_o + h * C::kOPitch + d) = sum;
+                    mm = top;
                 }
-                __syncthreads();
             };
             const int c = static_cast<int>(blockIdx.x), n = c1 - c0 + 1;
             int bunch = 8;
             while (bunch * bunch < n) bunch *= 2;  // 1024 CTAs at most: 32
             const int first = c0 + (c - c0) / bunch * bunch, in_bunch = min(bunch, c1 - first + 1);
             const int bunches = (n + bunch - 1) / bunch;
-            leave(part(c));
+            for (int i = tid; i < quads; i += kThreads) {
+                const int h = i / (D / 4), d = i % (D / 4) * 4;
+                leave(part(c), h, d, s_mm[h], s_ll[h], own(h, d));
+            }
             if (last_of(p.tickets + slot_of(first), in_bunch)) {
-                join(first, 1, in_bunch);
-                if (bunches == 1) {
-                    answer();
-                } else {
-                    leave(part(first));
+                for (int i = tid; i < quads; i += kThreads) {
+                    const int h = i / (D / 4), d = i % (D / 4) * 4;
+                    float mm, ll;
+                    float4 v;
+                    join(first, 1, in_bunch, h, d, mm, ll, v);
+                    if (bunches == 1) {
+                        answer(h, d, mm, ll, v);
+                    } else {
+                        // it goes to the first part's place, once every thread has read that
+                        *reinterpret_cast<float4 *>(s_o + h * C::kOPitch + d) = v;
+                        if (d == 0) s_mm[h] = mm, s_ll[h] = ll;
+                    }
+                }
+                if (bunches > 1) {
+                    __syncthreads();
+                    for (int i = tid; i < quads; i += kThreads) {
+                        const int h = i / (D / 4), d = i % (D / 4) * 4;
+                        leave(part(first), h, d, s_mm[h], s_ll[h], own(h, d));
+                    }
                     if (last_of(p.tickets + 2 * kMaxGrid + slot_of(c0), bunches)) {
-                        join(c0, bunch, bunches);
-                        answer();
+                        for (int i = tid; i < quads; i += kThreads) {
+                            const int h = i / (D / 4), d = i % (D / 4) * 4;
+                            float mm, ll;
+                            float4 v;
+                            join(c0, bunch, bunches, h, d, mm, ll, v);
+                            answer(h, d, mm, ll, v);
+                        }
                     }
                 }
             }
         }
         __syncthreads();
 
-        left -= seg;
-        item0 += wk.units;
+        left -= seg + kEndUnits;
+        item0 += wk.units + kEndUnits;
         if (left > 0) {
             wk.unit = wk.units - 1;
             advance(p, wk);
