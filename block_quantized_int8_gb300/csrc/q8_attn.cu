@@ -49,7 +49,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnitTokens = kWarps * 16;
 constexpr int kMaxGrid = 1024;    // CTAs a launch may have (sizes the workspace)
 constexpr int kMinUnits = 4;      // units a CTA takes at least
-constexpr int kEndUnits = 2;      // what ending an item (joining warps, giving the answer) takes, in units' time
+constexpr int kEndUnits = 4;      // what ending an item (joining warps, giving the answer) takes, in units' time
 constexpr float kGrow = 4.0f;     // log2 growth of a score that moves the reference
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -200,7 +200,8 @@ struct Cfg {
     static constexpr int kCodes = 16 * D;          // bytes of a tile's key (or value) codes
     static constexpr int kScales = D;              // bytes of its scales: 16 * (D / 32) * 2
     static constexpr int kStage = 2 * (kCodes + kScales);
-    static constexpr int kStages = D == 256 ? 3 : (D == 128 ? 4 : 6);
+    static constexpr int kStages = D == 256 ? 3 : (D == 128 ? (NT == 1 ? 3 : 4) : 6);
+    static constexpr int kCtas = D == 256 ? 2 : (D == 64 && NT == 1 ? 4 : 3);  // CTAs an SM that registers must allow
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kOPitch = D + 8;
     static constexpr int kJoin = (HG * kOPitch + 2 * kWarps * HG + 2 * HG) * 4;
@@ -209,7 +210,7 @@ struct Cfg {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const __grid_constant__ AttnParams p) {
     using C = Cfg<D, NT>;
     constexpr int NB = D / 32;
     extern __shared__ __align__(128) uint8_t smem[];

@@ -14,10 +14,14 @@
 //
 // The row is not sorted: the words kept are a prefix of the ranking, and what
 // is needed is where it ends.
-//  - top-k up to 128: the row is cut into 256 groups; at least k words are no
-//    smaller than the k-th largest group maximum, and few more are.  The
-//    maxima come with the row's largest logit, so one pass gathers those words
-//    and one CTA sorts them and draws; only they need their exponential.
+//  - few words: the row is cut into 128 groups.  At least k words are no smaller than
+//    the k-th largest group maximum, and few more are (top-k up to 64).  For more
+//    words the maxima are taken over every 4th or 16th word, and the rank among them
+//    is where 1.5 k words (1400 for top-p alone) are expected.  The maxima come with
+//    the row's largest logit, so one pass gathers the words above that bound and one
+//    CTA sorts them and draws.  Whether they are enough is then known exactly (top-k:
+//    their number; top-p: their mass against that of the whole row, summed in a pass
+//    of its own); where not, the searches below follow.
 //  - larger top-k: a histogram of counts over 2048 equal steps of the distance
 //    from the largest logit (down to exp(-28) or the row's smallest logit) finds
 //    the step that holds the k-th word.
@@ -58,8 +62,10 @@ constexpr int kBins = 2048;
 constexpr int kList = 2048;        // words one CTA sorts
 constexpr int kPer = kList / kThreads;
 constexpr int kMaxCluster = 16;
-constexpr int kGroups = 256;       // of a row, for the bound on its k-th logit
-constexpr int kFastK = 128;
+constexpr int kGroups = 128;       // of a row, for a bound on its k-th logit
+constexpr int kFewK = 64;          // top-k whose bound is exact
+constexpr int kManyK = 1000;       // and whose words, half as many more expected, fit the list
+constexpr int kListP = 1400;       // words asked for where only top-p counts
 constexpr int kCopies = 4;         // bulk copies of a slice
 constexpr float kUnit = 1.0f / 1099511627776.0f;  // 2^-40
 
@@ -85,11 +91,13 @@ struct alignas(16) Shared {
     alignas(16) float groups[kGroups];         // of all CTAs, written by each
     unsigned long long sub_mass[kMaxCluster];  // per CTA, written by each
     uint32_t sub_count[kMaxCluster];
-    float minima[kMaxCluster];
+    float maxima[kMaxCluster], minima[kMaxCluster];
     unsigned long long warp_mass[kWarps];
     uint32_t warp_count[kWarps];
-    float warp_min[kWarps];
+    float warp_min[kWarps], warp_max[kWarps];
+    float thread_groups[kGroups];              // this CTA's, of at most 32 threads
     float bound;
+    uint32_t enough;
     // what a search found, in the CTA that found it
     uint32_t digit, before_count, in_count;
     unsigned long long before_mass, in_mass;
@@ -244,8 +252,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         return v != v ? -INFINITY : v;
     };
 
+    // ---- the row's knobs, and which words the bound is made from ----------------------------
+    float temp = p.temperature ? p.temperature[row] : 1.0f;
+    int k = p.top_k ? p.top_k[row] : 0;
+    const float top_p = p.top_p ? p.top_p[row] : 1.0f, min_p = p.min_p ? p.min_p[row] : 0.0f;
+    const float u = p.u[row];
+    if (!(temp > 0.0f)) temp = 1.0f, k = 1;
+    if (k <= 0 || k > p.V) k = p.V;
+    // words to gather; 0: no list
+    const int list = k <= kFewK ? k : (k <= kManyK ? k + k / 2 : (k == p.V && top_p < 1.0f ? kListP : 0));
+    const int every = list <= kFewK ? 1 : (list <= 4 * kFewK ? 4 : 16);
+
     // ---- the slice; the row's largest and smallest logits -----------------------------
-    float top = -INFINITY, low = INFINITY;
+    float top = -INFINITY, low = INFINITY, some = -INFINITY;  // some: of every 4th or 16th word
     bool nan = false;
     auto look = [&](float v) -> float {
         const bool bad = v != v;
@@ -272,10 +291,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             for (int j = 0; j < 4; ++j) {
                 const int b = b0 + j * kThreads;
                 if (b < body) {
-                    dst[2 * b] = make_float4(look(bf16lo_f32(q[j].x)), look(bf16hi_f32(q[j].x)), look(bf16lo_f32(q[j].y)),
-                                             look(bf16hi_f32(q[j].y)));
-                    dst[2 * b + 1] = make_float4(look(bf16lo_f32(q[j].z)), look(bf16hi_f32(q[j].z)), look(bf16lo_f32(q[j].w)),
+                    const float4 v = make_float4(look(bf16lo_f32(q[j].x)), look(bf16hi_f32(q[j].x)), look(bf16lo_f32(q[j].y)),
+                                                 look(bf16hi_f32(q[j].y)));
+                    const float4 w = make_float4(look(bf16lo_f32(q[j].z)), look(bf16hi_f32(q[j].z)), look(bf16lo_f32(q[j].w)),
                                                  look(bf16hi_f32(q[j].w)));
+                    dst[2 * b] = v, dst[2 * b + 1] = w;
+                    if (every == 4 || (j & 1) == 0) some = fmaxf(some, every == 4 ? fmaxf(v.x, w.x) : v.x);
                 }
             }
         }
@@ -293,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         __syncthreads();
         bool late = false;
         float4 *const run = reinterpret_cast<float4 *>(vals + head);
+        int turn = 0;
         for (int c = 0; c < kCopies; ++c) {
             late = !mbar_wait_bounded(&s.bars[c], 0) || late;
             const int b1 = part(c + 1);
@@ -301,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 const float4 q = run[b];
                 const float4 v = make_float4(look(q.x), look(q.y), look(q.z), look(q.w));
                 if (q.x != q.x || q.y != q.y || q.z != q.z || q.w != q.w) run[b] = v;
+                if (every == 4 || (turn++ & 3) == 0) some = fmaxf(some, v.x);
             }
         }
         if (late) {
@@ -309,41 +332,46 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
     }
     if (nan && p.status) atomicOr(p.status, Q8_DEV_NONFINITE);
-    // the largest of each of this CTA's kGroups / ranks groups of threads
-    const int group = kThreads * ranks / kGroups;  // threads of a group: a power of two, 2 .. 32
-    for (int o = 1; o < group; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-    if (lane == 0) s.warp_min[warp] = low;
+    // the largest of each of this CTA's kGroups / ranks groups of 4 ranks threads, first of runs of
+    // at most 32; the largest and smallest of all
+    if (every == 1) some = top;
+    const int part = min(4 * ranks, 32);
+    for (int o = 1; o < part; o <<= 1) some = fmaxf(some, __shfl_xor_sync(0xffffffffu, some, o));
+    for (int o = 16; o > 0; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    }
+    if (tid % part == 0) s.thread_groups[tid / part] = some;
+    if (lane == 0) s.warp_min[warp] = low, s.warp_max[warp] = top;
     if (tid == 0) s.listed = 0;
     cluster.barrier_wait();
-    if (tid % group < ranks) {
-        // a group's threads write its maximum to the CTAs, the lanes in turn
-        for (int c = tid % group; c < ranks; c += group)
-            cluster.map_shared_rank(&s, c)->groups[rank * (kGroups / ranks) + tid / group] = top;
-    }
     __syncthreads();
-    if (warp == 0) {
-        low = s.warp_min[lane % kWarps];
-        for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-        if (lane < ranks) cluster.map_shared_rank(&s, lane)->minima[rank] = low;
+    if (tid < kGroups) {  // a thread writes one group's maximum to one CTA
+        const int g = tid / ranks;
+        some = s.thread_groups[4 * ranks > 32 ? 2 * g : g];
+        if (4 * ranks > 32) some = fmaxf(some, s.thread_groups[2 * g + 1]);
+        cluster.map_shared_rank(&s, tid % ranks)->groups[rank * (kGroups / ranks) + g] = some;
+    } else if (warp == kGroups / 32) {
+        low = s.warp_min[lane % kWarps], top = s.warp_max[lane % kWarps];
+        for (int o = 16; o > 0; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+        }
+        if (lane < ranks) {
+            Shared *o = cluster.map_shared_rank(&s, lane);
+            o->minima[rank] = low, o->maxima[rank] = top;
+        }
     }
     cluster.sync();
-    top = s.groups[lane], low = s.minima[lane % ranks];
-#pragma unroll
-    for (int i = 32; i < kGroups; i += 32) top = fmaxf(top, s.groups[i + lane]);
-    for (int o = 16; o > 0; o >>= 1) {
+    top = s.maxima[lane % ranks], low = s.minima[lane % ranks];
+    for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
     }
 
     Row r;
     r.top = top;
-    r.temp = p.temperature ? p.temperature[row] : 1.0f;
-    int k = p.top_k ? p.top_k[row] : 0;
-    if (!(r.temp > 0.0f)) r.temp = 1.0f, k = 1;
-    if (k <= 0 || k > p.V) k = p.V;
-    const float top_p = p.top_p ? p.top_p[row] : 1.0f, min_p = p.min_p ? p.min_p[row] : 0.0f;
-    const float u = p.u[row];
+    r.temp = temp;
 
     auto nothing = [&]() {
         if (rank == 0 && tid == 0) {
@@ -357,10 +385,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         return;
     }
 
-    // CTA 0's list gets every word for which in(i) holds; false, for all threads, if they are too
-    // many.  Leaves a barrier open (all have looked at CTA 0's count): settle() closes it, CTA 0
-    // before it ends.
-    auto gather = [&](auto in, bool from_memory) -> bool {
+    // CTA 0's list gets every word for which in(i) holds (those that fit; `listed` counts all).
+    auto gather = [&](auto in, bool from_memory) {
         Shared *o = cluster.map_shared_rank(&s, 0);
         for (int i0 = tid; i0 - tid < n; i0 += 32 * kThreads) {
             uint32_t hits = 0;  // of this thread's next 32 words
@@ -387,11 +413,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 }
         }
         cluster.sync();
-        const bool fits = o->listed <= kList;
-        cluster.barrier_arrive();
-        return fits;
     };
-    auto settle = [&]() { cluster.barrier_wait(); };
     // Sorts the list of CTA 0 by (key, index).
     auto sort = [&](int count) {
         int m = 128;
@@ -417,15 +439,70 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     auto draw_from_list = [&](unsigned long long want) {
         const int count = static_cast<int>(s.listed);
         sort(count);
-        const int words_of = count <= 128 ? 1 : kPer;  // words per thread
+        if (count <= 128) {  // one warp, four words a lane
+            if (warp == 0) {
+                unsigned long long w[4], sum = 0;
+                float e[4];
+                uint32_t idx[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = lane * 4 + j;
+                    const unsigned long long x = i < count && i < k ? s.list[i] : ~0ull;
+                    idx[j] = static_cast<uint32_t>(x);
+                    e[j] = x != ~0ull ? r.weight(unkey(static_cast<uint32_t>(x >> 32))) : 0.f;
+                    w[j] = mass_of(e[j]);
+                    sum += w[j];
+                }
+                unsigned long long before = sum;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned long long v = __shfl_up_sync(0xffffffffu, before, o);
+                    if (lane >= o) before += v;
+                }
+                if (top_p < 1.0f && want == 0) want = mass_wanted(top_p, __shfl_sync(0xffffffffu, before, 31));
+                before -= sum;
+                sum = 0;
+                uint32_t words = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = w[j] != 0 && (!(top_p < 1.0f) || before < want) && e[j] >= min_p;
+                    before += w[j];
+                    // by index: 20 bits of index above 41 of mass
+                    s.list[lane * 4 + j] = in ? static_cast<unsigned long long>(idx[j]) << 41 | w[j] : ~0ull;
+                    sum += in ? w[j] : 0ull;
+                    words += in ? 1u : 0u;
+                }
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                words = __reduce_add_sync(0xffffffffu, words);
+                if (lane == 0) s.warp_mass[0] = sum, s.warp_count[0] = words;
+            }
+            __syncthreads();
+            const unsigned long long all = s.warp_mass[0], low41 = (1ull << 41) - 1;
+            if (all == 0) {
+                nothing();
+            } else if (tid < count) {
+                const unsigned long long x = s.list[tid], place = place_of(u, all);
+                unsigned long long before = 0;
+#pragma unroll 8
+                for (int j = 0; j < count; ++j) {
+                    const unsigned long long y = s.list[j];
+                    before += y < x ? y & low41 : 0ull;
+                }
+                if (x != ~0ull && before <= place && place < before + (x & low41)) {
+                    p.token[row] = static_cast<int32_t>(x >> 41);
+                    if (p.logprob) p.logprob[row] = log_share(x & low41, all);
+                    if (p.kept) p.kept[row] = static_cast<int32_t>(s.warp_count[0]);
+                }
+            }
+            return;
+        }
         unsigned long long w[kPer], sum = 0;
         float e[kPer];
         uint32_t idx[kPer];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            const int i = tid * words_of + j;
+            const int i = tid * kPer + j;
             w[j] = 0, e[j] = 0.f, idx[j] = 0;
-            if (j < words_of && i < count && i < k) {
+            if (i < count && i < k) {
                 const unsigned long long x = s.list[i];
                 idx[j] = static_cast<uint32_t>(x);
                 e[j] = r.weight(unkey(static_cast<uint32_t>(x >> 32)));
@@ -501,30 +578,72 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
     };
 
-    // ---- top-k of few -------------------------------------------------------------------
-    if (k <= kFastK) {
-        // the k-th largest group maximum: the one with fewer than k before it and no more than k - 1 equal ones ahead
-        static_assert(kThreads == 2 * kGroups, "two threads a group");
-        const float x = s.groups[tid >> 1];
-        int at = 0;
-#pragma unroll 8
-        for (int j = (tid & 1) * (kGroups / 2); j < ((tid & 1) + 1) * (kGroups / 2); j += 4) {
-            const float4 y = *reinterpret_cast<const float4 *>(&s.groups[j]);
-            const int me = tid >> 1;
-            at += (y.x > x || (y.x == x && j < me)) + (y.y > x || (y.y == x && j + 1 < me)) +
-                  (y.z > x || (y.z == x && j + 2 < me)) + (y.w > x || (y.w == x && j + 3 < me));
+    // ---- a list of few words ----------------------------------------------------------------
+    if (list > 0) {
+        unsigned long long want = 0;
+        if (k == p.V) {  // what top-p asks for, of the mass of the row
+            unsigned long long m = 0, mb;
+            uint32_t cb, c_all;
+            for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
+                float e[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e[j] = r.weight(i0 + j * kThreads < n ? vals[i0 + j * kThreads] : -INFINITY);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m += mass_of(e[j]);
+            }
+            scan_cta(s, m, 0u, mb, cb, m, c_all);
+            if (tid < ranks) cluster.map_shared_rank(&s, tid)->sub_mass[rank] = m;
         }
-        at += __shfl_xor_sync(0xffffffffu, at, 1);
-        if (at == k - 1) s.bound = x;
-        __syncthreads();
-        const float bound = s.bound;
-        if (gather([&](int i) { return vals[i] >= bound && vals[i] > -INFINITY; }, false)) {
-            if (rank == 0) draw_from_list(0ull);
-            settle();
+        float bound = -INFINITY;
+        if (p.V > kList) {
+            // the wanted one in the ranking of the group maxima (equal ones by their place): four
+            // threads count what comes before one maximum
+            static_assert(kThreads == 4 * kGroups, "four threads a group");
+            const int place = every == 1 ? k : min(kGroups, max(1, static_cast<int>(ceilf(kGroups * (1.0f - expf(-static_cast<float>(list) / (every * kGroups)))))));
+            const int me = tid >> 2, j0 = (tid & 3) * (kGroups / 4);
+            const float x = s.groups[me];
+            int at = 0;
+#pragma unroll
+            for (int j = j0; j < j0 + kGroups / 4; j += 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(&s.groups[j]);
+                at += (y.x > x || (y.x == x && j < me)) + (y.y > x || (y.y == x && j + 1 < me)) +
+                      (y.z > x || (y.z == x && j + 2 < me)) + (y.w > x || (y.w == x && j + 3 < me));
+            }
+            at += __shfl_xor_sync(0xffffffffu, at, 1);
+            at += __shfl_xor_sync(0xffffffffu, at, 2);
+            if (at == place - 1) s.bound = x;
+            __syncthreads();
+            bound = s.bound;
+        }
+        gather([&](int i) { return vals[i] >= bound && vals[i] > -INFINITY; }, false);
+        if (k == p.V) {
+            unsigned long long total = 0;
+            for (int c = 0; c < ranks; ++c) total += s.sub_mass[c];
+            want = mass_wanted(top_p, total);
+        }
+        if (rank == 0) {  // are they enough?
+            const uint32_t listed = s.listed;
+            __syncthreads();  // before it may be set back below
+            bool enough = listed <= kList && (bound == -INFINITY || listed >= static_cast<uint32_t>(k));
+            if (k == p.V && listed <= kList) {
+                unsigned long long m = 0, mb;
+                uint32_t cb, c_all;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const uint32_t i = tid + j * kThreads;
+                    if (i < listed) m += mass_of(r.weight(unkey(static_cast<uint32_t>(s.list[i] >> 32))));
+                }
+                scan_cta(s, m, 0u, mb, cb, m, c_all);
+                enough = m >= want;
+            }
+            if (tid < ranks) cluster.map_shared_rank(&s, tid)->enough = enough ? 1u : 0u;
+            if (!enough && tid == 0) s.listed = 0;
+        }
+        cluster.sync();
+        if (s.enough) {
+            if (rank == 0) draw_from_list(want);
             return;
         }
-        settle();
-        if (rank == 0 && tid == 0) s.listed = 0;
     }
 
     // ---- searches over the whole row ------------------------------------------------------
@@ -630,7 +749,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // weight(key): a word's share of `want`.
     auto end_in_step = [&](auto in, bool from_memory, unsigned long long before0, unsigned long long want, auto weight) {
         gather(in, from_memory);
-        settle();
         if (rank == 0) {
             const int count = min(static_cast<int>(s.listed), kList);
             sort(count);
@@ -742,7 +860,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             if (f.before_count + f.in_count <= kList) {
                 gather([&](int i) { const int b = step_of(vals[i]); return b >= 0 && b <= bin; }, false);
                 if (rank == 0) draw_from_list(0ull);
-                settle();
                 return;
             }
             auto in = [&](int i) { return step_of(vals[i]) == bin; };
@@ -836,7 +953,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             if (f.before_count + f.in_count <= kList) {
                 gather([&](int i) { return vals[i] >= least && bin_of(vals[i]) <= bin; }, true);
                 if (rank == 0) k = p.V, draw_from_list(want);
-                settle();
                 return;
             }
             auto in = [&](int i) { return vals[i] >= least && bin_of(vals[i]) == bin; };
