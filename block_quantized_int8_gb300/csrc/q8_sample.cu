@@ -130,52 +130,6 @@ __device__ __forceinline__ unsigned long long mass_of(float e) {
     return m >> min(-shift, 31);
 }
 
-// Ascending sort of n words (a power of two, 128 .. kList): four neighbours a
-// thread, exchanged in registers, by shuffles within a warp and through shared
-// memory across warps.
-__device__ void sort_list(unsigned long long *v, int n) {
-    const int tid = threadIdx.x;
-    const bool mine = tid * kPer < n;
-    unsigned long long x[kPer];
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) x[j] = mine ? v[tid * kPer + j] : 0ull;
-    for (int size = 2; size <= n; size <<= 1) {
-        for (int step = size >> 1; step > 0; step >>= 1) {
-            if (step >= 32 * kPer) {
-                __syncthreads();
-                if (mine)
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j) v[tid * kPer + j] = x[j];
-                __syncthreads();
-            }
-            if (mine) {
-                unsigned long long y[kPer];
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    if (step >= 32 * kPer)
-                        y[j] = v[(tid * kPer + j) ^ step];
-                    else if (step >= kPer)
-                        y[j] = __shfl_xor_sync(0xffffffffu, x[j], step / kPer);
-                    else
-                        y[j] = step == 1 ? x[j ^ 1] : x[j ^ 2];
-                }
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int i = tid * kPer + j;
-                    const bool small = ((i & step) == 0) == ((i & size) == 0);  // this place takes the smaller
-                    x[j] = (small == (x[j] < y[j])) ? x[j] : y[j];
-                }
-            }
-        }
-    }
-    __syncthreads();
-    if (mine)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) v[tid * kPer + j] = x[j];
-    __syncthreads();
-}
-
 // Exclusive running sums of m and c over the threads of the CTA, and the totals.
 __device__ void scan_cta(Shared &s, unsigned long long m, uint32_t c, unsigned long long &m_before, uint32_t &c_before,
                          unsigned long long &m_all, uint32_t &c_all) {
@@ -200,6 +154,55 @@ __device__ void scan_cta(Shared &s, unsigned long long m, uint32_t c, unsigned l
         c_all += s.warp_count[w];
     }
     m_before = mr - m + mb, c_before = cr - c + cb;
+}
+
+// Ascending sort of n <= kList different words of s.list into kBins buckets by bin(word), which
+// does not fall from one word to a larger one; within a bucket by counting.  (A bitonic sort
+// of 2048 took 20,000 cycles and more.)  s.count is used.
+template <typename Bin>
+__device__ void sort_buckets(Shared &s, int n, Bin bin) {
+    const int tid = threadIdx.x;
+    unsigned long long x[kPer];
+    int b[kPer];
+    uint32_t at[kPer];
+    for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = tid + j * kThreads;
+        x[j] = i < n ? s.list[i] : 0ull;
+        b[j] = i < n ? bin(x[j]) : -1;
+        at[j] = b[j] >= 0 ? atomicAdd(&s.count[b[j]], 1u) : 0u;
+    }
+    __syncthreads();
+    // where each bucket begins
+    uint32_t c[kBins / kThreads], sum = 0, before, all;
+    unsigned long long mb, ma;
+#pragma unroll
+    for (int j = 0; j < kBins / kThreads; ++j) c[j] = s.count[tid * (kBins / kThreads) + j], sum += c[j];
+    scan_cta(s, 0ull, sum, mb, before, ma, all);
+#pragma unroll
+    for (int j = 0; j < kBins / kThreads; ++j) {
+        s.count[tid * (kBins / kThreads) + j] = before;
+        before += c[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+        if (b[j] >= 0) s.list[s.count[b[j]] + at[j]] = x[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        if (b[j] < 0) continue;
+        const uint32_t i0 = s.count[b[j]], i1 = b[j] + 1 < kBins ? s.count[b[j] + 1] : static_cast<uint32_t>(n);
+        at[j] = i0;
+        for (uint32_t i = i0; i < i1; ++i) at[j] += s.list[i] < x[j] ? 1u : 0u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+        if (b[j] >= 0) s.list[at[j]] = x[j];
+    __syncthreads();
 }
 
 // log(w / all): through 1 - (all - w) / all where the word has most of the mass
@@ -416,8 +419,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     };
     // Sorts the list of CTA 0 by (key, index).
     auto sort = [&](int count) {
-        int m = 128;
-        while (m < count) m <<= 1;
         if (count <= 128) {  // each word's place is how many come before it
             unsigned long long x = 0;
             int at = 0;
@@ -428,10 +429,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             __syncthreads();
             if (tid < count) s.list[at] = x;
             __syncthreads();
-        } else {
-            for (int i = count + tid; i < m; i += kThreads) s.list[i] = ~0ull;
-            sort_list(s.list, m);
+            return;
         }
+        // buckets by the distance from the list's largest logit
+        float hi = -INFINITY, lo = INFINITY;
+        for (int i = tid; i < count; i += kThreads) {
+            const float l = unkey(static_cast<uint32_t>(s.list[i] >> 32));
+            hi = fmaxf(hi, l), lo = fminf(lo, l);
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        }
+        if (lane == 0) s.warp_max[warp] = hi, s.warp_min[warp] = lo;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) hi = fmaxf(hi, s.warp_max[w]), lo = fminf(lo, s.warp_min[w]);
+        const float span = hi - lo, per = span > 0.0f && span < INFINITY ? __fdiv_rn(static_cast<float>(kBins - 1), span) : 0.0f;
+        sort_buckets(s, count, [&](unsigned long long x) {
+            const float l = unkey(static_cast<uint32_t>(x >> 32));
+            return l == hi ? 0 : static_cast<int>(fminf((hi - l) * per, static_cast<float>(kBins - 1)));
+        });
     };
 
     // The whole draw from the list of CTA 0: the row's first words, at least as many as can be
@@ -557,7 +574,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             }
             return;
         }
-        sort(static_cast<int>(all_words));
+        const float per_word = __fdiv_rn(static_cast<float>(kBins), static_cast<float>(p.V));
+        sort_buckets(s, static_cast<int>(all_words),
+                     [&](unsigned long long x) { return min(static_cast<int>(static_cast<float>(x >> 41) * per_word), kBins - 1); });
         kept = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -579,6 +598,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     };
 
     // ---- a list of few words ----------------------------------------------------------------
+    unsigned long long row_mass = 0;  // of all words, where it is known
     if (list > 0) {
         unsigned long long want = 0;
         if (k == p.V) {  // what top-p asks for, of the mass of the row
@@ -617,9 +637,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         gather([&](int i) { return vals[i] >= bound && vals[i] > -INFINITY; }, false);
         if (k == p.V) {
-            unsigned long long total = 0;
-            for (int c = 0; c < ranks; ++c) total += s.sub_mass[c];
-            want = mass_wanted(top_p, total);
+            for (int c = 0; c < ranks; ++c) row_mass += s.sub_mass[c];
+            want = mass_wanted(top_p, row_mass);
         }
         if (rank == 0) {  // are they enough?
             const uint32_t listed = s.listed;
@@ -920,15 +939,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // bins of e: exponent and 5 fraction bits, the largest first
     auto bin_of = [](float e) -> int { return e > 0.f ? static_cast<int>(min((0x3F800000u - __float_as_uint(e)) >> 18, kBins - 1u)) : kBins; };
     if (top_p < 1.0f) {
-        unsigned long long mb, m_all;
-        uint32_t cb, c_all;
-        scan_cta(s, total, 0u, mb, cb, m_all, c_all);
-        cluster.sync();
-        if (tid < ranks) cluster.map_shared_rank(&s, tid)->sub_mass[rank] = m_all;
         clear();
-        cluster.sync();
-        total = 0;
-        for (int c = 0; c < ranks; ++c) total += s.sub_mass[c];
+        if (row_mass != 0) {
+            total = row_mass;
+        } else {
+            unsigned long long mb, m_all;
+            uint32_t cb, c_all;
+            scan_cta(s, total, 0u, mb, cb, m_all, c_all);
+            cluster.sync();
+            if (tid < ranks) cluster.map_shared_rank(&s, tid)->sub_mass[rank] = m_all;
+            cluster.sync();
+            total = 0;
+            for (int c = 0; c < ranks; ++c) total += s.sub_mass[c];
+        }
         const unsigned long long want = mass_wanted(top_p, total);
         // words below this e have together less than total - want, or each no mass
         const float share = __fdiv_rn(static_cast<float>(total - min(want, total)), static_cast<float>(p.V));
