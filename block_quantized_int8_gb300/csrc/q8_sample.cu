@@ -28,8 +28,7 @@
 //  - top-p without a small top-k: every word's e replaces its logit in shared
 //    memory and the masses are summed.  Words below (1 - p) / V of that sum lie
 //    past the end together, so only the others enter a histogram of masses by
-//    e's leading bits (exponent and 5 fraction bits), which finds the bin that
-//    holds the end.
+//    e's leading bits, which finds the bin that holds the end.
 // If the words up to the end of that step or bin are at most 2048, they are
 // gathered and drawn from by one CTA.  Otherwise the words of that step alone are
 // gathered and sorted to find the last one kept (their logits read again, since
@@ -698,26 +697,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // false, for all threads, if it never is.
     auto locate = [&](int bins, bool by_mass, unsigned long long want, Place &f) -> bool {
         cluster.sync();
-        // CTA `rank` adds up its share of the bins over all CTAs, up to four neighbours a thread
+        // CTA `rank` adds up its share of the bins over all CTAs: several threads a bin where there are
+        // enough (each takes some of the CTAs, the first of them the sum), up to four bins a thread where not
         const int share = bins / ranks, b0 = rank * share, each = (share + kThreads - 1) / kThreads;
+        const int helpers = each > 1 ? 1 : min(4, kThreads / share), me = tid / helpers, sub = tid % helpers;
         uint32_t cnt[kBins / kThreads] = {};
         unsigned long long mas[kBins / kThreads] = {};
         uint32_t c_sum = 0;
         unsigned long long m_sum = 0;
 #pragma unroll
         for (int j = 0; j < kBins / kThreads; ++j) {
-            const int b = tid * each + j;
+            const int b = me * each + j;
             if (j < each && b < share) {
-#pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c)
-                    if (c < ranks) {
-                        const Shared *o = cluster.map_shared_rank(&s, c);
-                        cnt[j] += o->count[b0 + b];
-                        if (by_mass) mas[j] += static_cast<unsigned long long>(o->mass_hi[b0 + b]) << 32 | o->mass_lo[b0 + b];
-                    }
-                c_sum += cnt[j];
-                m_sum += mas[j];
+#pragma unroll 4
+                for (int c = sub; c < ranks; c += helpers) {
+                    const Shared *o = cluster.map_shared_rank(&s, c);
+                    cnt[j] += o->count[b0 + b];
+                    if (by_mass) mas[j] += static_cast<unsigned long long>(o->mass_hi[b0 + b]) << 32 | o->mass_lo[b0 + b];
+                }
             }
+        }
+        for (int q = 1; q < helpers; q <<= 1) {  // then each > 1 does not hold: one bin a thread
+            cnt[0] += __shfl_xor_sync(0xffffffffu, cnt[0], q);
+            mas[0] += __shfl_xor_sync(0xffffffffu, mas[0], q);
+        }
+#pragma unroll
+        for (int j = 0; j < kBins / kThreads; ++j) {
+            if (sub != 0) cnt[j] = 0, mas[j] = 0;
+            c_sum += cnt[j];
+            m_sum += mas[j];
         }
         unsigned long long mb, m_all;
         uint32_t cb, c_all;
@@ -744,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 const unsigned long long have = by_mass ? mb : cb;
                 const unsigned long long with = by_mass ? mb + mas[j] : static_cast<unsigned long long>(cb) + cnt[j];
                 if (have < want && with >= want) {
-                    s.digit = b0 + tid * each + j;
+                    s.digit = b0 + me * each + j;
                     s.before_count = cb, s.in_count = cnt[j];
                     s.before_mass = mb, s.in_mass = mas[j];
                 }
@@ -889,17 +897,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
     }
 
-    // ---- e in place of the logits, 0 for words that top-k leaves out -------------------------
-    unsigned long long sum = 0;  // of this thread's run
-    uint32_t count = 0;
-    auto tally = [&](float e) -> unsigned long long {
-        const unsigned long long w = mass_of(e), in = e >= min_p ? w : 0ull;
-        sum += in;
-        count += in != 0 ? 1u : 0u;
-        return w;
-    };
-    // each lane starts elsewhere in its run, so that a warp's reads hit all banks
-    const int turn = run > 0 ? lane % run : 0;
+    // ---- e in place of the logits, 0 for words that top-k leaves out; with no filter they stay ----
+    const bool all_words_in = k == p.V && !(top_p < 1.0f);
     unsigned long long total = 0;
     if (ranked) {
         uint32_t eq = ties_before([&](int i) { return rank_key(vals[i]); });
@@ -908,27 +907,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             const float e = key < last || (key == last && eq < ties) ? r.weight(vals[i]) : 0.f;
             eq += key == last ? 1u : 0u;
             vals[i] = e;
-            total += tally(e);
+            total += mass_of(e);
         }
         ranked = false;
-    } else {
-        int j = turn;
-        for (int q = 0; q < run; q += 4) {
+    } else if (!all_words_in) {
+        for (int w0 = tid; w0 < n; w0 += 4 * kThreads) {
             float e[4];
-            int at[4];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                at[h] = q + h < run ? i0 + j : n;
-                const float l = at[h] < i1 ? vals[at[h]] : -INFINITY;
-                e[h] = rank_key(l) <= last ? r.weight(l) : 0.f;
-                j = j + 1 == run ? 0 : j + 1;
+            for (int j = 0; j < 4; ++j) {
+                const float l = w0 + j * kThreads < n ? vals[w0 + j * kThreads] : -INFINITY;
+                e[j] = rank_key(l) <= last ? r.weight(l) : 0.f;
             }
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-                if (at[h] < i1) {
-                    vals[at[h]] = e[h];
-                    total += tally(e[h]);
-                }
+            for (int j = 0; j < 4; ++j) {
+                if (w0 + j * kThreads < n) vals[w0 + j * kThreads] = e[j];
+                total += mass_of(e[j]);
+            }
         }
     }
 
@@ -936,8 +930,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     uint32_t eq_before = 0;
     int end_bin = kBins;       // words past this bin are out
     bool edge = false;         // words of this bin are in up to `last`
-    // bins of e: exponent and 5 fraction bits, the largest first
-    auto bin_of = [](float e) -> int { return e > 0.f ? static_cast<int>(min((0x3F800000u - __float_as_uint(e)) >> 18, kBins - 1u)) : kBins; };
+    // bins of e, the largest first: its leading bits, as many as leave the least e a bin
+    int shift = 23;
+    auto bin_of = [&](float e) -> int { return e > 0.f ? static_cast<int>(min((0x3F800000u - __float_as_uint(e)) >> shift, kBins - 1u)) : kBins; };
     if (top_p < 1.0f) {
         clear();
         if (row_mass != 0) {
@@ -956,6 +951,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         // words below this e have together less than total - want, or each no mass
         const float share = __fdiv_rn(static_cast<float>(total - min(want, total)), static_cast<float>(p.V));
         const float least = fmaxf(share * 0.999f, 1.0f) * kUnit;
+        while (shift > 0 && (0x3F800000u - __float_as_uint(least)) >> (shift - 1) < static_cast<uint32_t>(kBins)) --shift;
         for (int w0 = warp * 32; w0 < n; w0 += kThreads * 4) {
             float e[4];
 #pragma unroll
@@ -988,28 +984,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (edge && ranked) eq_before = ties_before([&](int i) { return bin_of(vals[i]) == end_bin ? rank_key(logit(i)) : 0xFFFFFFFFu; });
     }
     auto keep = [&](int i, uint32_t eq) -> float {
-        const float e = vals[i];
+        const float e = all_words_in ? r.weight(vals[i]) : vals[i];
+        if (!edge) return e;
         const int b = bin_of(e);
-        if (b < end_bin || !edge) return e;
-        if (b > end_bin) return 0.f;
+        if (b != end_bin) return b < end_bin ? e : 0.f;
         const uint32_t key = rank_key(logit(i));
         return key < last || (key == last && eq < ties) ? e : 0.f;
     };
-    if (edge) {
-        sum = 0, count = 0;
-        if (ranked) {
-            uint32_t eq = eq_before;
-            for (int i = i0; i < i1; ++i) {
-                tally(keep(i, eq));
-                if (bin_of(vals[i]) == end_bin) eq += rank_key(logit(i)) == last ? 1u : 0u;
-            }
-        } else {
-            int j = turn;
-#pragma unroll 4
-            for (int q = 0; q < run; ++q) {
-                if (i0 + j < i1) tally(keep(i0 + j, 0u));
+    unsigned long long sum = 0;  // of this thread's run
+    uint32_t count = 0;
+    auto tally = [&](float e) {
+        const unsigned long long w = e >= min_p ? mass_of(e) : 0ull;
+        sum += w;
+        count += w != 0 ? 1u : 0u;
+    };
+    __syncthreads();
+    if (edge && ranked) {
+        uint32_t eq = eq_before;
+        for (int i = i0; i < i1; ++i) {
+            tally(keep(i, eq));
+            if (bin_of(vals[i]) == end_bin) eq += rank_key(logit(i)) == last ? 1u : 0u;
+        }
+    } else {
+        // each lane starts elsewhere in its run, so that a warp's reads hit all banks
+        int j = run > 0 ? lane % run : 0;
+        for (int q = 0; q < run; q += 4) {
+            float e[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                e[h] = q + h < run && i0 + j < i1 ? keep(i0 + j, 0u) : 0.f;
                 j = j + 1 == run ? 0 : j + 1;
             }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) tally(e[h]);
         }
     }
 
