@@ -401,11 +401,16 @@ def q8_gemm(q, s, x, y=None, dev_status=None, stream=None, tile=0, splits=0):
 
 # ---------------------------------------------------------------------------
 # the rest of a decode step
+#
+# These calls take 10 to 20 us of kernel at their smallest, so what the host spends on them
+# counts: arguments are looked at in one expression, and one by one (for the message) only
+# where that fails.
 # ---------------------------------------------------------------------------
+_I8, _I32, _I64, _F32, _BF16 = torch.int8, torch.int32, torch.int64, torch.float32, torch.bfloat16
+
+
 def _new(stream, make):
     """make() with its allocations (and zeroing) ordered on the call's stream."""
-    if stream is None:
-        return make()
     with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
         return make()
 
@@ -446,50 +451,63 @@ class KvCache:
 _ROW_DTYPES = {torch.float32: Q8_DTYPE_F32, torch.bfloat16: Q8_DTYPE_BF16}
 
 
-def _kv_rows(cache, t, name, n, dtype=None):
+def _kv_rows(cache, t, name, n, dtype):
     """The row stride of [n, kv_heads * head_dim] or [n, kv_heads, head_dim] rows (heads contiguous)."""
-    if not t.is_cuda or t.dtype not in _ROW_DTYPES or (dtype is not None and t.dtype != dtype):
+    if not t.is_cuda or t.dtype not in _ROW_DTYPES or t.dtype is not dtype:
         raise TypeError(f"{name} must be a float32 or bfloat16 CUDA tensor, keys and values alike")
-    row = cache.kv_heads * cache.head_dim
-    sh, sd = tuple(t.shape), t.stride()
-    if sh == (n, cache.kv_heads, cache.head_dim):
-        ok = sd[2] == 1 and (sd[1] == cache.head_dim or cache.kv_heads == 1)
+    sh, sd, h, d = t.shape, t.stride(), cache.kv_heads, cache.head_dim
+    if sh == (n, h, d):
+        ok = sd[2] == 1 and (sd[1] == d or h == 1)
     else:
-        ok = sh == (n, row) and sd[1] == 1
+        ok = sh == (n, h * d) and sd[1] == 1
     if not ok and n > 0:
-        raise ValueError(f"{name} must hold {n} rows of {cache.kv_heads} x {cache.head_dim} values, each row contiguous")
-    return sd[0] if n > 1 else row
+        raise ValueError(f"{name} must hold {n} rows of {h} x {d} values, each row contiguous")
+    return sd[0] if n > 1 else h * d
+
+
+def _slots(slots):
+    if not (slots.is_cuda and slots.dtype is _I64 and slots.dim() == 1):
+        _cuda(slots, "slots", (_I64,), 1)
+    n = slots.shape[0]
+    if n > 1 and slots.stride(0) != 1:
+        raise ValueError("slots must be contiguous")
+    return n
 
 
 def q8_kv_append(cache, k, v, slots, dev_status=None, stream=None):
     """Quantize the rows k, v ([T, kv_heads, head_dim] or [T, kv_heads * head_dim], fp32 or
     bf16) into the cache's slots (int64 [T]; negative: skipped)."""
-    _cuda(slots, "slots", (torch.int64,), 1)
-    n = slots.shape[0]
-    if n > 1 and slots.stride(0) != 1:
-        raise ValueError("slots must be contiguous")
-    ldk, ldv = _kv_rows(cache, k, "k", n), _kv_rows(cache, v, "v", n, k.dtype)
-    st = lib().q8_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[k.dtype], slots.data_ptr(), n,
-                            _p(dev_status), _stream(stream))
-    _check(st, "q8_kv_append")
+    n, t = _slots(slots), k.dtype
+    ldk, ldv = _kv_rows(cache, k, "k", n, t), _kv_rows(cache, v, "v", n, t)
+    st = lib().q8_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[t], slots.data_ptr(), n,
+                            None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    if st:
+        _check(st, "q8_kv_append")
 
 
 def q8_kv_read(cache, slots, k=None, v=None, dtype=torch.float32, dev_status=None, stream=None):
     """The values of the cache's slots: (k, v), each [T, kv_heads, head_dim] in `dtype`
     (or in the given rows' own type); a negative slot gives zeros."""
-    _cuda(slots, "slots", (torch.int64,), 1)
-    n = slots.shape[0]
-    if n > 1 and slots.stride(0) != 1:
-        raise ValueError("slots must be contiguous")
-    shape = (n, cache.kv_heads, cache.head_dim)
-    if k is None:
-        k = _new(stream, lambda: torch.empty(shape, dtype=dtype if v is None else v.dtype, device=cache.device))
-    if v is None:
-        v = _new(stream, lambda: torch.empty(shape, dtype=k.dtype, device=cache.device))
-    ldk, ldv = _kv_rows(cache, k, "k", n), _kv_rows(cache, v, "v", n, k.dtype)
-    st = lib().q8_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[k.dtype],
-                          _p(dev_status), _stream(stream))
-    _check(st, "q8_kv_read")
+    n, h, d = _slots(slots), cache.kv_heads, cache.head_dim
+    if k is not None or v is not None:
+        dtype = (v if k is None else k).dtype
+    if dtype not in _ROW_DTYPES:
+        raise TypeError("the values are given as float32 or bfloat16")
+    row = h * d
+    if k is not None:
+        ldk = _kv_rows(cache, k, "k", n, dtype)
+    else:
+        k, ldk = torch.empty((n, h, d), dtype=dtype, device=cache.device) if stream is None else _new(
+            stream, lambda: torch.empty((n, h, d), dtype=dtype, device=cache.device)), row
+    if v is not None:
+        ldv = _kv_rows(cache, v, "v", n, dtype)
+    else:
+        v, ldv = torch.empty((n, h, d), dtype=dtype, device=cache.device) if stream is None else _new(
+            stream, lambda: torch.empty((n, h, d), dtype=dtype, device=cache.device)), row
+    st = lib().q8_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[dtype],
+                          None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    if st:
+        _check(st, "q8_kv_read")
     return k, v
 
 
@@ -503,31 +521,39 @@ def q8_attn_decode(q, cache, table, lens, scale=None, softcap=0.0, window=0, out
     table int32 [B, pages of a sequence], lens int32 [B] (the new token included).
     Returns (out bf16 [B, q_heads, head_dim], lse fp32 [B, q_heads]).  scale defaults to
     1 / sqrt(head_dim); softcap 0: none; window 0: all tokens."""
-    _cuda(q, "q", (torch.bfloat16,), 3)
-    _cuda(table, "table", (torch.int32,), 2)
-    _cuda(lens, "lens", (torch.int32,), 1)
-    B, H, D = q.shape
-    if D != cache.head_dim or table.shape[0] != B or lens.shape[0] != B:
-        raise ValueError("q is [B, q_heads, head_dim] with the cache's head_dim, table [B, pages], lens [B]")
     sq = q.stride()
+    if not (q.is_cuda and table.is_cuda and lens.is_cuda and q.dtype is _BF16 and table.dtype is _I32 and lens.dtype is _I32
+            and len(sq) == 3 and table.dim() == 2 and lens.dim() == 1):
+        _cuda(q, "q", (_BF16,), 3)
+        _cuda(table, "table", (_I32,), 2)
+        _cuda(lens, "lens", (_I32,), 1)
+    B, H, D = q.shape
+    n, width = table.shape
+    if D != cache.head_dim or n != B or lens.shape[0] != B:
+        raise ValueError("q is [B, q_heads, head_dim] with the cache's head_dim, table [B, pages], lens [B]")
     if (sq[2] != 1 or (H > 1 and sq[1] != D)) and B > 0:
         raise ValueError("each row of q must be contiguous")
-    if not table.is_contiguous() or not lens.is_contiguous():
+    if not (table.is_contiguous() and lens.is_contiguous()):
         raise ValueError("table and lens must be contiguous")
     if out is None:
-        out = _new(stream, lambda: torch.empty((B, H, D), dtype=torch.bfloat16, device=q.device))
-    elif _cuda(out, "out", (torch.bfloat16,), 3).shape != q.shape or not out.is_contiguous():
+        out = torch.empty((B, H, D), dtype=_BF16, device=cache.device) if stream is None else _new(
+            stream, lambda: torch.empty((B, H, D), dtype=_BF16, device=cache.device))
+    elif _cuda(out, "out", (_BF16,), 3).shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape")
     if lse is None:
-        lse = _new(stream, lambda: torch.empty((B, H), dtype=torch.float32, device=q.device))
-    elif tuple(_cuda(lse, "lse", (torch.float32,), 2).shape) != (B, H) or not lse.is_contiguous():
+        lse = torch.empty((B, H), dtype=_F32, device=cache.device) if stream is None else _new(
+            stream, lambda: torch.empty((B, H), dtype=_F32, device=cache.device))
+    elif _cuda(lse, "lse", (_F32,), 2).shape != (B, H) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous, [B, q_heads]")
     if ws is None:
-        ws = _new(stream, lambda: workspace(q8_attn_decode_workspace_size(B, H, cache.kv_heads, D), q.device))
-    st = lib().q8_attn_decode(cache._ref, q.data_ptr(), sq[0] if B > 1 else H * D, H, table.data_ptr(), table.shape[1],
-                              lens.data_ptr(), B, D ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
-                              lse.data_ptr(), _p(ws), 0 if ws is None else ws.numel(), _p(dev_status), _stream(stream))
-    _check(st, "q8_attn_decode")
+        nbytes = q8_attn_decode_workspace_size(B, H, cache.kv_heads, D)
+        ws = workspace(nbytes, q.device) if stream is None else _new(stream, lambda: workspace(nbytes, q.device))
+    st = lib().q8_attn_decode(cache._ref, q.data_ptr(), sq[0] if B > 1 else H * D, H, table.data_ptr(), width, lens.data_ptr(), B,
+                              D ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), lse.data_ptr(),
+                              *((None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())),
+                              None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    if st:
+        _check(st, "q8_attn_decode")
     return out, lse
 
 
@@ -540,51 +566,62 @@ def q8_moe(x, logits, q13, s13, q2, s2, top_k, renorm=True, y=None, ids=None, we
     """A mixture-of-experts layer for T <= 32 tokens: x bf16 [T, H], router logits fp32 [T, E],
     experts' gate and up rows (q13 int8 [E, 2 F, H], s13) and down rows (q2 int8 [E, H, F], s2).
     Returns (y fp32 [T, H], ids int32 [T, top_k], weights fp32 [T, top_k])."""
-    _cuda(x, "x", (torch.bfloat16,), 2)
-    _cuda(logits, "logits", (torch.float32,), 2)
-    _cuda(q13, "q13", (torch.int8,), 3)
-    _cuda(q2, "q2", (torch.int8,), 3)
-    _cuda(s13, "s13", _B16, 3)
-    _cuda(s2, "s2", _B16, 3)
+    sx, sl = x.stride(), logits.stride()
+    if not (x.is_cuda and logits.is_cuda and q13.is_cuda and s13.is_cuda and q2.is_cuda and s2.is_cuda and x.dtype is _BF16
+            and logits.dtype is _F32 and q13.dtype is _I8 and q2.dtype is _I8 and s13.dtype in _B16 and s2.dtype in _B16
+            and len(sx) == 2 and len(sl) == 2):
+        _cuda(x, "x", (_BF16,), 2)
+        _cuda(logits, "logits", (_F32,), 2)
+        for name, t, types in (("q13", q13, (_I8,)), ("q2", q2, (_I8,)), ("s13", s13, _B16), ("s2", s2, _B16)):
+            _cuda(t, name, types, 3)
     T, H = x.shape
-    E, F = logits.shape[1], q2.shape[2]
-    if tuple(q13.shape) != (E, 2 * F, H) or tuple(q2.shape) != (E, H, F) or logits.shape[0] != T:
+    n, E = logits.shape
+    F = q2.shape[-1]
+    if n != T or q13.shape != (E, 2 * F, H) or q2.shape != (E, H, F):
         raise ValueError("x is [T, H], logits [T, E], q13 [E, 2 F, H] and q2 [E, H, F]")
-    if tuple(s13.shape) != (E, 2 * F, H // 32) or tuple(s2.shape) != (E, H, F // 32):
+    if s13.shape != (E, 2 * F, H // 32) or s2.shape != (E, H, F // 32):
         raise ValueError("s13 and s2 hold a scale per 32 codes")
     if not (q13.is_contiguous() and s13.is_contiguous() and q2.is_contiguous() and s2.is_contiguous()):
         raise ValueError("the experts' tensors must be contiguous")
-    if T > 0 and (x.stride(1) != 1 or logits.stride(1) != 1):
+    if T > 0 and (sx[1] != 1 or sl[1] != 1):
         raise ValueError("x and logits must have unit inner stride")
+    dev = x.device
     if y is None:
-        y = _new(stream, lambda: torch.empty((T, H), dtype=torch.float32, device=x.device))
-    elif tuple(_cuda(y, "y", (torch.float32,), 2).shape) != (T, H) or y.stride(1) != 1:
-        raise ValueError("y must be [T, H] with unit inner stride")
+        y, ldy = torch.empty((T, H), dtype=_F32, device=dev) if stream is None else _new(
+            stream, lambda: torch.empty((T, H), dtype=_F32, device=dev)), H
+    else:
+        if _cuda(y, "y", (_F32,), 2).shape != (T, H) or y.stride(1) != 1:
+            raise ValueError("y must be [T, H] with unit inner stride")
+        ldy = H if T <= 1 else y.stride(0)
     if ids is None:
-        ids = _new(stream, lambda: torch.empty((T, top_k), dtype=torch.int32, device=x.device))
-    elif tuple(_cuda(ids, "ids", (torch.int32,), 2).shape) != (T, top_k) or not ids.is_contiguous():
+        ids = torch.empty((T, top_k), dtype=_I32, device=dev) if stream is None else _new(
+            stream, lambda: torch.empty((T, top_k), dtype=_I32, device=dev))
+    elif _cuda(ids, "ids", (_I32,), 2).shape != (T, top_k) or not ids.is_contiguous():
         raise ValueError("ids must be contiguous, [T, top_k]")
     if weights is None:
-        weights = _new(stream, lambda: torch.empty((T, top_k), dtype=torch.float32, device=x.device))
-    elif tuple(_cuda(weights, "weights", (torch.float32,), 2).shape) != (T, top_k) or not weights.is_contiguous():
+        weights = torch.empty((T, top_k), dtype=_F32, device=dev) if stream is None else _new(
+            stream, lambda: torch.empty((T, top_k), dtype=_F32, device=dev))
+    elif _cuda(weights, "weights", (_F32,), 2).shape != (T, top_k) or not weights.is_contiguous():
         raise ValueError("weights must be contiguous, [T, top_k]")
     if ws is None:
-        ws = _new(stream, lambda: workspace(q8_moe_workspace_size(T, E, H, F, top_k), x.device))
+        nbytes = q8_moe_workspace_size(T, E, H, F, top_k)
+        ws = workspace(nbytes, dev) if stream is None else _new(stream, lambda: workspace(nbytes, dev))
     one = T <= 1
-    st = lib().q8_moe(x.data_ptr(), H if one else x.stride(0), logits.data_ptr(), E if one else logits.stride(0), T, E, top_k,
-                      int(renorm), q13.data_ptr(), s13.data_ptr(), q2.data_ptr(), s2.data_ptr(), H, F, y.data_ptr(),
-                      H if one else y.stride(0), ids.data_ptr(), weights.data_ptr(), _p(ws), 0 if ws is None else ws.numel(),
-                      _p(dev_status), _stream(stream))
-    _check(st, "q8_moe")
+    st = lib().q8_moe(x.data_ptr(), H if one else sx[0], logits.data_ptr(), E if one else sl[0], T, E, top_k, 1 if renorm else 0,
+                      q13.data_ptr(), s13.data_ptr(), q2.data_ptr(), s2.data_ptr(), H, F, y.data_ptr(), ldy, ids.data_ptr(),
+                      weights.data_ptr(), *((None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())),
+                      None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    if st:
+        _check(st, "q8_moe")
     return y, ids, weights
 
 
 def _per_row(t, name, n, dtype):
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != dtype:
+    if not (t.is_cuda and t.dtype is dtype):
         raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must hold one value per row, contiguous")
     return t.data_ptr()
 
@@ -596,20 +633,25 @@ def q8_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     None.  Returns (token int32, logprob fp32, kept int32), each [rows]."""
     if not logits.is_cuda or logits.dtype not in _ROW_DTYPES:
         raise TypeError("logits must be a float32 or bfloat16 CUDA tensor")
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    sl = logits.stride()
+    if len(sl) != 2 or (logits.shape[1] > 1 and sl[1] != 1):
         raise ValueError("logits must be [rows, V] with unit inner stride")
     n, V = logits.shape
-    args = [_per_row(temperature, "temperature", n, torch.float32), _per_row(top_k, "top_k", n, torch.int32),
-            _per_row(top_p, "top_p", n, torch.float32), _per_row(min_p, "min_p", n, torch.float32),
-            _per_row(u, "u", n, torch.float32)]
+    dev = logits.device
     if token is None:
-        token = _new(stream, lambda: torch.empty(n, dtype=torch.int32, device=logits.device))
+        token = torch.empty(n, dtype=_I32, device=dev) if stream is None else _new(
+            stream, lambda: torch.empty(n, dtype=_I32, device=dev))
     if logprob is None:
-        logprob = _new(stream, lambda: torch.empty(n, dtype=torch.float32, device=logits.device))
+        logprob = torch.empty(n, dtype=_F32, device=dev) if stream is None else _new(
+            stream, lambda: torch.empty(n, dtype=_F32, device=dev))
     if kept is None:
-        kept = _new(stream, lambda: torch.empty(n, dtype=torch.int32, device=logits.device))
-    st = lib().q8_sample(logits.data_ptr(), _ROW_DTYPES[logits.dtype], logits.stride(0) if n > 1 else V, n, V, *args,
-                         _per_row(token, "token", n, torch.int32), _per_row(logprob, "logprob", n, torch.float32),
-                         _per_row(kept, "kept", n, torch.int32), _p(dev_status), _stream(stream))
-    _check(st, "q8_sample")
+        kept = torch.empty(n, dtype=_I32, device=dev) if stream is None else _new(
+            stream, lambda: torch.empty(n, dtype=_I32, device=dev))
+    st = lib().q8_sample(logits.data_ptr(), _ROW_DTYPES[logits.dtype], sl[0] if n > 1 else V, n, V,
+                         _per_row(temperature, "temperature", n, _F32), _per_row(top_k, "top_k", n, _I32),
+                         _per_row(top_p, "top_p", n, _F32), _per_row(min_p, "min_p", n, _F32), _per_row(u, "u", n, _F32),
+                         _per_row(token, "token", n, _I32), _per_row(logprob, "logprob", n, _F32), _per_row(kept, "kept", n, _I32),
+                         None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    if st:
+        _check(st, "q8_sample")
     return token, logprob, kept
