@@ -16,8 +16,10 @@
 // is needed is where it ends.
 //  - few words: the row is cut into 128 groups.  At least k words are no smaller than
 //    the k-th largest group maximum, and few more are (top-k up to 64).  For more
-//    words the maxima are taken over every 4th or 16th word, and the rank among them
-//    is where 1.5 k words (1400 for top-p alone) are expected.  The maxima come with
+//    words the rank among the maxima is where 1.5 k words (1400 for top-p alone) are
+//    expected: with f of the groups above the bound, -log(1 - f) words a group.  From
+//    256 words on the maxima are of every 4th word, which keeps f away from 1: the
+//    number of words found then strays by an eighth or less.  The maxima come with
 //    the row's largest logit, so one pass gathers the words above that bound and one
 //    CTA sorts them and draws.  Whether they are enough is then known exactly (top-k:
 //    their number; top-p: their mass against that of the whole row, summed in a pass
@@ -263,10 +265,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (k <= 0 || k > p.V) k = p.V;
     // words to gather; 0: no list
     const int list = k <= kFewK ? k : (k <= kManyK ? k + k / 2 : (k == p.V && top_p < 1.0f ? kListP : 0));
-    const int every = list <= kFewK ? 1 : (list <= 4 * kFewK ? 4 : 16);
+    const int every = list <= 2 * kGroups ? 1 : 4;
 
     // ---- the slice; the row's largest and smallest logits -----------------------------
-    float top = -INFINITY, low = INFINITY, some = -INFINITY;  // some: of every 4th or 16th word
+    float top = -INFINITY, low = INFINITY, some = -INFINITY;  // some: of every 4th word
     bool nan = false;
     auto look = [&](float v) -> float {
         const bool bad = v != v;
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                     const float4 w = make_float4(look(bf16lo_f32(q[j].z)), look(bf16hi_f32(q[j].z)), look(bf16lo_f32(q[j].w)),
                                                  look(bf16hi_f32(q[j].w)));
                     dst[2 * b] = v, dst[2 * b + 1] = w;
-                    if (every == 4 || (j & 1) == 0) some = fmaxf(some, every == 4 ? fmaxf(v.x, w.x) : v.x);
+                    some = fmaxf(some, fmaxf(v.x, w.x));
                 }
             }
         }
@@ -316,7 +318,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         __syncthreads();
         bool late = false;
         float4 *const run = reinterpret_cast<float4 *>(vals + head);
-        int turn = 0;
         for (int c = 0; c < kCopies; ++c) {
             late = !mbar_wait_bounded(&s.bars[c], 0) || late;
             const int b1 = part(c + 1);
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 const float4 q = run[b];
                 const float4 v = make_float4(look(q.x), look(q.y), look(q.z), look(q.w));
                 if (q.x != q.x || q.y != q.y || q.z != q.z || q.w != q.w) run[b] = v;
-                if (every == 4 || (turn++ & 3) == 0) some = fmaxf(some, v.x);
+                some = fmaxf(some, v.x);
             }
         }
         if (late) {
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             // the wanted one in the ranking of the group maxima (equal ones by their place): four
             // threads count what comes before one maximum
             static_assert(kThreads == 4 * kGroups, "four threads a group");
-            const int place = every == 1 ? k : min(kGroups, max(1, static_cast<int>(ceilf(kGroups * (1.0f - expf(-static_cast<float>(list) / (every * kGroups)))))));
+            const int place = k <= kFewK ? k : min(kGroups, max(1, static_cast<int>(ceilf(kGroups * (1.0f - expf(-static_cast<float>(list) / (every * kGroups)))))));
             const int me = tid >> 2, j0 = (tid & 3) * (kGroups / 4);
             const float x = s.groups[me];
             int at = 0;
@@ -1096,13 +1097,17 @@ q8_status launch_sample(const SampleArgs &a, uint32_t *dev_status, cudaStream_t 
     }
     SampleParams p = {a.logits, a.temperature, a.top_p, a.min_p, a.u, a.top_k, a.token, a.kept, a.logprob, dev_status,
                       a.ld, a.V, 0};
-    // CTAs per row: slices of 8192 words for a few rows, where the passes' latency is what counts,
-    // and of 16384 (two CTAs an SM) for many; 16 of them (more than every device promises, but
-    // this one has) for a few rows, and where a slice would not fit otherwise
-    const int least = a.rows <= 8 ? 8192 : 16384;
-    const int most = a.rows <= 8 || a.V > (1 << 18) ? kMaxCluster : kMaxCluster / 2;
+    // CTAs per row: slices of at most 8192 words while all rows' CTAs find an SM of their own, else
+    // of 16384 (two CTAs an SM) where 16 CTAs or fewer can have that.  16 is more than every
+    // device promises, but this one has it; such clusters need 16 free SMs of one GPC, so they
+    // find fewer.  With top-k 50, in us: 131071 words, 16 CTAs and 8: 11.2 and 12.8 for one row,
+    // 20.1 and 15.7 for 16, 50 and 30 for 64.  32000 words, 4 and 2: 11.3 and 12.3 for 16 rows, 13.9
+    // and 12.9 for 64, 26 and 16 for 128 (8 CTAs: 10.9 for one row, but top-p alone 24 in place
+    // of 19).  262144 words, 16 and 8: 12.8 and 15.3 for one row, 59 and 60 for 64.
     int ranks = 1;
-    while (ranks < most && a.V > least * ranks) ranks *= 2;
+    while (ranks < kMaxCluster && a.V > 8192 * ranks) ranks *= 2;
+    const int64_t places = ranks == kMaxCluster ? di->sm_count * 2 / 3 : di->sm_count;
+    if (ranks > 1 && a.rows * int64_t{ranks} > places && a.V <= 8192 * ranks) ranks /= 2;
     p.slice = ((a.V + 7 + ranks - 1) / ranks + 7) & ~7;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
