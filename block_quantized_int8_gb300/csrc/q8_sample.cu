@@ -21,14 +21,15 @@
 //    256 words on the maxima are of every 4th word, which keeps f away from 1: the
 //    number of words found then strays by an eighth or less.  The maxima come with
 //    the row's largest logit, so one pass gathers the words above that bound and one
-//    CTA sorts them and draws.  Whether they are enough is then known exactly (top-k:
-//    their number; top-p: their mass against that of the whole row, summed in a pass
-//    of its own); where not, the searches below follow.
+//    CTA sorts them and draws.  Whether they are enough is known exactly (top-k: their
+//    number; top-p: their mass against that of the whole row, summed before they are
+//    gathered, when every word's e takes its logit's place); where not, the searches
+//    below follow.
 //  - larger top-k: a histogram of counts over 2048 equal steps of the distance
 //    from the largest logit (down to exp(-28) or the row's smallest logit) finds
 //    the step that holds the k-th word.
 //  - top-p without a small top-k: every word's e replaces its logit in shared
-//    memory and the masses are summed.  Words below (1 - p) / V of that sum lie
+//    memory (if it has not yet) and the masses are summed.  Words below (1 - p) / V of that sum lie
 //    past the end together, so only the others enter a histogram of masses by
 //    e's leading bits, which finds the bin that holds the end.
 // If the words up to the end of that step or bin are at most 2048, they are
@@ -93,7 +94,8 @@ struct alignas(16) Shared {
     unsigned long long sub_mass[kMaxCluster];  // per CTA, written by each
     uint32_t sub_count[kMaxCluster];
     float maxima[kMaxCluster], minima[kMaxCluster];
-    unsigned long long warp_mass[kWarps];
+    unsigned long long sub_above[kMaxCluster];
+    unsigned long long warp_mass[kWarps], warp_above[kWarps];
     uint32_t warp_count[kWarps];
     float warp_min[kWarps], warp_max[kWarps];
     float thread_groups[kGroups];              // this CTA's, of at most 32 threads
@@ -598,22 +600,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     };
 
     // ---- a list of few words ----------------------------------------------------------------
-    unsigned long long row_mass = 0;  // of all words, where it is known
+    unsigned long long row_mass = 0;  // of all words, where their e are in place
     if (list > 0) {
-        unsigned long long want = 0;
-        if (k == p.V) {  // what top-p asks for, of the mass of the row
-            unsigned long long m = 0, mb;
-            uint32_t cb, c_all;
-            for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
-                float e[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) e[j] = r.weight(i0 + j * kThreads < n ? vals[i0 + j * kThreads] : -INFINITY);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) m += mass_of(e[j]);
-            }
-            scan_cta(s, m, 0u, mb, cb, m, c_all);
-            if (tid < ranks) cluster.map_shared_rank(&s, tid)->sub_mass[rank] = m;
-        }
         float bound = -INFINITY;
         if (p.V > kList) {
             // the wanted one in the ranking of the group maxima (equal ones by their place): four
@@ -635,33 +623,59 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             __syncthreads();
             bound = s.bound;
         }
-        gather([&](int i) { return vals[i] >= bound && vals[i] > -INFINITY; }, false);
         if (k == p.V) {
-            for (int c = 0; c < ranks; ++c) row_mass += s.sub_mass[c];
-            want = mass_wanted(top_p, row_mass);
-        }
-        if (rank == 0) {  // are they enough?
-            const uint32_t listed = s.listed;
-            __syncthreads();  // before it may be set back below
-            bool enough = listed <= kList && (bound == -INFINITY || listed >= static_cast<uint32_t>(k));
-            if (k == p.V && listed <= kList) {
-                unsigned long long m = 0, mb;
-                uint32_t cb, c_all;
+            // e in place of the logits, and whether the mass above the bound is what top-p asks for
+            const float least = r.weight(bound);
+            unsigned long long m = 0, a = 0;
+            uint32_t c = 0;
+            for (int j0 = tid; j0 < n; j0 += 4 * kThreads) {
+                float e[4];
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const uint32_t i = tid + j * kThreads;
-                    if (i < listed) m += mass_of(r.weight(unkey(static_cast<uint32_t>(s.list[i] >> 32))));
+                for (int j = 0; j < 4; ++j) e[j] = r.weight(j0 + j * kThreads < n ? vals[j0 + j * kThreads] : -INFINITY);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j0 + j * kThreads < n) vals[j0 + j * kThreads] = e[j];
+                    const unsigned long long w = mass_of(e[j]);
+                    m += w;
+                    if (e[j] >= least && e[j] > 0.f) a += w, ++c;
                 }
-                scan_cta(s, m, 0u, mb, cb, m, c_all);
-                enough = m >= want;
             }
-            if (tid < ranks) cluster.map_shared_rank(&s, tid)->enough = enough ? 1u : 0u;
-            if (!enough && tid == 0) s.listed = 0;
-        }
-        cluster.sync();
-        if (s.enough) {
-            if (rank == 0) draw_from_list(want);
-            return;
+            for (int o = 16; o > 0; o >>= 1) {
+                m += __shfl_xor_sync(0xffffffffu, m, o);
+                a += __shfl_xor_sync(0xffffffffu, a, o);
+            }
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (lane == 0) s.warp_mass[warp] = m, s.warp_above[warp] = a, s.warp_count[warp] = c;
+            __syncthreads();
+            if (tid < ranks) {
+                m = 0, a = 0, c = 0;
+                for (int w = 0; w < kWarps; ++w) m += s.warp_mass[w], a += s.warp_above[w], c += s.warp_count[w];
+                Shared *o = cluster.map_shared_rank(&s, tid);
+                o->sub_mass[rank] = m, o->sub_above[rank] = a, o->sub_count[rank] = c;
+            }
+            cluster.sync();
+            a = 0, c = 0;
+            for (int o = 0; o < ranks; ++o) row_mass += s.sub_mass[o], a += s.sub_above[o], c += s.sub_count[o];
+            const unsigned long long want = mass_wanted(top_p, row_mass);
+            if (c <= kList && a >= want) {
+                gather([&](int i) { return vals[i] >= least && vals[i] > 0.f; }, true);
+                if (rank == 0) draw_from_list(want);
+                return;
+            }
+        } else {
+            gather([&](int i) { return vals[i] >= bound && vals[i] > -INFINITY; }, false);
+            if (rank == 0) {  // are they enough?
+                const uint32_t listed = s.listed;
+                __syncthreads();  // before it may be set back below
+                const bool enough = listed <= kList && (bound == -INFINITY || listed >= static_cast<uint32_t>(k));
+                if (tid < ranks) cluster.map_shared_rank(&s, tid)->enough = enough ? 1u : 0u;
+                if (!enough && tid == 0) s.listed = 0;
+            }
+            cluster.sync();
+            if (s.enough) {
+                if (rank == 0) draw_from_list(0ull);
+                return;
+            }
         }
     }
 
@@ -911,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             total += mass_of(e);
         }
         ranked = false;
-    } else if (!all_words_in) {
+    } else if (!all_words_in && row_mass == 0) {
         for (int w0 = tid; w0 < n; w0 += 4 * kThreads) {
             float e[4];
 #pragma unroll
