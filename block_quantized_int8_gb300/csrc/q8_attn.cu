@@ -48,8 +48,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnitTokens = kWarps * 16;
 constexpr int kMaxGrid = 1024;    // CTAs a launch may have (sizes the workspace)
-constexpr int kMinUnits = 4;      // units a CTA takes at least
-constexpr int kEndUnits = 4;      // what ending an item (joining warps, giving the answer) takes, in units' time
+constexpr int kMinUnits = 2;      // units a CTA takes at least; 3 and 4 gain in one short case what they lose in another
 constexpr float kGrow = 4.0f;     // log2 growth of a score that moves the reference
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -200,13 +199,20 @@ struct Cfg {
     static constexpr int kCodes = 16 * D;          // bytes of a tile's key (or value) codes
     static constexpr int kScales = D;              // bytes of its scales: 16 * (D / 32) * 2
     static constexpr int kStage = 2 * (kCodes + kScales);
-    static constexpr int kStages = D == 256 ? 3 : (D == 128 ? (NT == 1 ? 3 : 4) : 6);
-    static constexpr int kCtas = D == 256 ? 2 : (D == 64 && NT == 1 ? 4 : 3);  // CTAs an SM that registers must allow
+    // as deep as the CTAs that registers allow leave room for; a stage more or fewer is within 3 % (66.4 us
+    // with 4 for 48 ragged sequences, 65.2 with 3, which leave room for 3 CTAs in place of 2), but for 16
+    // heads of 128 dimensions (28.4 us with 4, 30.4 with 3)
+    static constexpr int kStages = D == 256 ? 2 : (D == 128 && NT == 1 ? 3 : 4);
+    static constexpr int kCtas = D == 256 ? 2 : 3;  // CTAs an SM that registers must allow
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kOPitch = D + 8;
     static constexpr int kJoin = (HG * kOPitch + 2 * kWarps * HG + 2 * HG) * 4;
     static constexpr int kSmem = kRing + kJoin;
     static constexpr int kPart = HG * (D + 2);     // floats of one partial result
+    // What ending an item (joining the warps, leaving a part or the answer) takes, in units' time.
+    // With 0, 2, 4, 6, 8 units 48 ragged sequences (8 heads, 128 dimensions) take 71, 65.7, 64.2, 64.9, 66.2
+    // us; with 2, 4, 6, 8 others with 16 heads 104, 86.1, 82.6, 83.4.
+    static constexpr int kEndUnits = NT == 1 ? 4 : 6;
 };
 
 template <int D, int NT>
@@ -214,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
     using C = Cfg<D, NT>;
     constexpr int NB = D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_scan[2 * kWarps];
+    __shared__ long long s_scan[kWarps];
     __shared__ uint32_t s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -226,24 +232,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
 
     // ---- the list: an item takes its units and kEndUnits; how long that is, and where this CTA begins ----
     const int heads = p.kv_heads * p.splits;
-    long long total = 0, n_items = 0;
+    long long total = 0;
     for (int b = tid; b < p.batch; b += kThreads) {
         const int n = seq_units(p, seq_len(p, b, blockIdx.x == 0));
-        total += n > 0 ? n + kEndUnits : 0, n_items += n > 0 ? 1 : 0;
+        total += n > 0 ? n + C::kEndUnits : 0;
     }
-    for (int o = 16; o > 0; o >>= 1) {
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-        n_items += __shfl_xor_sync(0xffffffffu, n_items, o);
-    }
-    if (lane == 0) s_scan[warp] = total, s_scan[kWarps + warp] = n_items;
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) s_scan[warp] = total;
     __syncthreads();
-    total = n_items = 0;
-    for (int w = 0; w < kWarps; ++w) total += s_scan[w], n_items += s_scan[kWarps + w];
-    total *= heads, n_items *= heads;
-    // at least kMinUnits, and of longer items (on the average) half, up to 2 kMinUnits: a part more to
-    // join costs as much as a few units
-    const long long half = n_items > 0 ? total / n_items / 2 : 0;
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, min(max(half, static_cast<long long>(kMinUnits)), 2ll * kMinUnits));
+    total = 0;
+    for (int w = 0; w < kWarps; ++w) total += s_scan[w];
+    total *= heads;
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinUnits));
     const long long u0 = per * blockIdx.x, u1 = min(u0 + per, total);
 
     // sequences of no tokens have no units: write their answer
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
         while (true) {
             const int b = b0 + lane;
             const int units = b < p.batch ? seq_units(p, seq_len(p, b, false)) : 0;
-            const long long n = units > 0 ? static_cast<long long>(units + kEndUnits) * heads : 0;
+            const long long n = units > 0 ? static_cast<long long>(units + C::kEndUnits) * heads : 0;
             long long run = n;
             for (int o = 1; o < 32; o <<= 1) {
                 const long long v = __shfl_up_sync(0xffffffffu, run, o);
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
         }
         enter(p, wk);
         const long long in = u0 - before;
-        const int cost = wk.units + kEndUnits, item = static_cast<int>(in / cost);
+        const int cost = wk.units + C::kEndUnits, item = static_cast<int>(in / cost);
         wk.kvh = item / p.splits, wk.run = item - wk.kvh * p.splits;
         wk.unit = static_cast<int>(in - static_cast<long long>(item) * cost);
         item0 = u0 - wk.unit;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
                     cp_async16(st + 2 * C::kCodes + lane * 16, src);
                 }
             }
-            ld_left -= ld.unit + 1 < ld.units ? 1 : 1 + kEndUnits;
+            ld_left -= ld.unit + 1 < ld.units ? 1 : 1 + C::kEndUnits;
             if (ld_left > 0) advance(p, ld);
             fetch_page();
         }
@@ -736,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
         }
         __syncthreads();
 
-        left -= seg + kEndUnits;
-        item0 += wk.units + kEndUnits;
+        left -= seg + C::kEndUnits;
+        item0 += wk.units + C::kEndUnits;
         if (left > 0) {
             wk.unit = wk.units - 1;
             advance(p, wk);
@@ -752,10 +752,13 @@ int ilog2(int64_t v) {
     return s;
 }
 
-// Query heads that share one pass over the keys: 16 where a group has more
-// than 8 (the keys and values are then read once for all of them), else 8;
-// at 256 dimensions 16 heads' sums would not fit the registers.
-int tiles_of(int group, int head_dim) { return head_dim <= 128 && group > 8 ? 2 : 1; }
+// Query heads that share one pass over the keys and values: 8, or 16 where a group has more than
+// 8 and the cache is long (`units` of 64 tokens, over all sequences, key heads and 16 heads).  Then
+// half as many bytes count; in a short one more items of half the work do.  At 256 dimensions 16
+// heads' sums would not fit the registers.  With 16 and 8, 64 / 4 heads of 128 dimensions: 86 and 97 us
+// for 48 sequences (36,000 units), 70.6 and 74.7 for 16 (24,000), 41 and 40 (12,000), 28.5 and 25.5
+// (6,000), 17.5 and 13.9 for two (400).
+int tiles_of(int group, int head_dim, int64_t units) { return head_dim <= 128 && group > 8 && units > 10000 ? 2 : 1; }
 
 template <int D, int NT>
 q8_status launch(const AttnParams &p, int64_t most_units, const DeviceInfo *di, cudaStream_t stream) {
@@ -782,7 +785,7 @@ q8_status launch(const AttnParams &p, int64_t most_units, const DeviceInfo *di, 
 
 // Counters, then two partial results per CTA.
 size_t attn_workspace(int q_heads, int kv_heads, int head_dim) {
-    const int hg = 8 * tiles_of(q_heads / kv_heads, head_dim);
+    const int hg = 8 * tiles_of(q_heads / kv_heads, head_dim, INT64_MAX);
     return static_cast<size_t>(4) * kMaxGrid * 4 + static_cast<size_t>(2) * kMaxGrid * hg * (head_dim + 2) * 4;
 }
 
@@ -798,13 +801,14 @@ q8_status launch_attn(const q8_kv_cache &c, const AttnArgs &a, void *ws, uint32_
     p.ldq = a.ldq;
     p.batch = a.batch, p.q_heads = a.q_heads, p.kv_heads = c.kv_heads;
     p.group = a.q_heads / c.kv_heads;
-    const int nt = tiles_of(p.group, c.head_dim);
-    p.splits = (p.group + 8 * nt - 1) / (8 * nt);
     p.table_width = a.table_width, p.pages = c.pages, p.page_shift = ilog2(c.page_size);
     p.window = a.window, p.scale = a.scale, p.softcap = a.softcap;
     int64_t span = static_cast<int64_t>(a.table_width) * c.page_size;
     if (a.window > 0 && span > a.window + 15) span = a.window + 15;
-    const int64_t most = (span + kUnitTokens - 1) / kUnitTokens * a.batch * p.kv_heads * p.splits;
+    const int64_t units = (span + kUnitTokens - 1) / kUnitTokens * a.batch * p.kv_heads;
+    const int nt = tiles_of(p.group, c.head_dim, units * ((p.group + 15) / 16));
+    p.splits = (p.group + 8 * nt - 1) / (8 * nt);
+    const int64_t most = units * p.splits;
     if (c.head_dim == 64) return nt == 1 ? launch<64, 1>(p, most, di, stream) : launch<64, 2>(p, most, di, stream);
     if (c.head_dim == 128) return nt == 1 ? launch<128, 1>(p, most, di, stream) : launch<128, 2>(p, most, di, stream);
     return launch<256, 1>(p, most, di, stream);

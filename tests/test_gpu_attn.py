@@ -100,6 +100,19 @@ def test_page_sizes_and_tile_ends(ps):
     run_case(128, 2, 4, ps, [1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 0, 1000], seed=ps)
 
 
+@pytest.mark.parametrize("D,group,window,softcap", [(64, 9, 0, 0.0), (64, 16, 50, 0.0), (64, 32, 0, 20.0), (128, 12, 0, 0.0),
+                                                    (128, 16, 100, 30.0), (128, 20, 0, 0.0)])
+def test_groups_of_tables_for_long_sequences(D, group, window, softcap):
+    # a table wide enough for 16 heads to share a pass (without a window), whatever the lengths are
+    lens = [0, 77, 1, 2300, 64]
+    cache, kv, vv = filled_cache(5 * 3 + 2, 1024, 2, D, D + group)
+    r = np.random.default_rng(group)
+    table = np.full((5, 1100 // 16 + 1), -1)
+    table[:, :3] = r.permutation(17)[:15].reshape(5, 3)
+    q = bf16_of(r.standard_normal((5, 2 * group, D)) * 1.5).cuda()
+    check(cache, kv, vv, q, table, lens, window=window, softcap=softcap)
+
+
 def test_one_token_and_none():
     run_case(128, 3, 2, 16, [0, 1, 0], seed=3)
     run_case(64, 1, 1, 16, [0], seed=4)
