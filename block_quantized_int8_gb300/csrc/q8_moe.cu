@@ -32,8 +32,8 @@
 // unit and SwiGLU needs no exchange.  x (bf16) is scaled by a power of two per
 // token to a largest value in [2^14, 2^15): exact in binary16 down to 2^-39 of it.
 // Hidden units go to the workspace in fp32.
-// down: a task is 16 output rows of one expert over a segment of 512 or
-// 1024 hidden units.  The hidden units, scaled likewise per token and segment,
+// down: a task is 16 output rows of one expert over a segment of its hidden
+// units.  The hidden units, scaled likewise per token and segment,
 // are taken as the sum of two binary16 values (22 bits), so fp32 outputs keep
 // their digits.  Each task leaves its tokens' rows in the workspace, and
 // they are added up in the order of the token's experts and segments.
@@ -435,9 +435,13 @@ __device__ int scale_hidden(uint32_t at, int n) {
 }
 
 // Hidden units of a segment of the down product: F in equal parts (of whole chunks) of at most
-// 1024, or 512 where an entry has more than 8 tokens.
+// 1024, or 512 where an entry has more than 8 tokens (whose vectors take twice the room); up
+// to 1536 units are one segment.  At 1376 units one takes 71.7 us and two 74.7 (7 tokens, 6
+// of 64 experts); at 4096, where more rows of vectors are waited for at once, parts of 1024
+// take 59.3 and of 1408 61.1, of 2048 65 (32 tokens, 2 of 8); parts of 512 were 4 to 12 % slower
+// than of 1024 everywhere.
 __device__ __forceinline__ int segment_of(int most, int F) {
-    const int n = (F + (most <= 8 ? 1023 : 511)) / (most <= 8 ? 1024 : 512);
+    const int n = most > 8 ? (F + 511) / 512 : (F <= 1536 ? 1 : (F + 1023) / 1024);
     return ((F + n - 1) / n + kChunk - 1) / kChunk * kChunk;
 }
 
@@ -462,6 +466,7 @@ __device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int 
     // ---- shared memory: one or two groups' vectors, the ring, sums of warps that share ------------
     const int pitch = pitch_of<DOWN>(DOWN ? seg : K), tok8 = 8 * pitch, x_bytes = rows8 * pitch;
     // warps to a task: what makes the rounds of tasks shortest, a chunk's time for joining included
+    // (one token, 2 of 16 experts of 1536 x 4096: 22.6 us, and 25.0 with one warp to a task)
     int share = 1;
     {
         const int chunks = (min(seg, K) + kChunk - 1) / kChunk;
@@ -474,9 +479,10 @@ __device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int 
     const int teams = kWarps / share, team = warp / share, part = warp - team * share;
     const int join = share > 1 ? kJoin : 0;
     const int busy = min(mine, teams) * share;
+    // two groups' vectors where the ring keeps three stages: half as many waits for the whole CTA (7
+    // tokens, 6 of 64 experts: 75 us and with one 83; 32 tokens, 8 of 128: 151 and 162)
     const int bufs = 2 * x_bytes + join + busy * 3 * kStage <= kSmem ? 2 : 1;
-    int stages = min((kSmem - bufs * x_bytes - join) / (busy * kStage), kMaxStages);
-    stages -= stages == 5 || stages == 7 ? 1 : 0;
+    const int stages = min((kSmem - bufs * x_bytes - join) / (busy * kStage), kMaxStages);
     const uint32_t xs = smem_addr(smem), ring = xs + bufs * x_bytes + warp * stages * kStage, ring_end = ring + stages * kStage;
     float *const s_join = reinterpret_cast<float *>(smem + bufs * x_bytes + busy * stages * kStage);
     const bool works = team < mine;
@@ -748,7 +754,7 @@ MoeLayout layout_of(int T, int H, int F, int top_k) {
 static_assert(sizeof(Routing) <= 6 * 1024, "kSmem leaves room for the routing");
 static_assert(sizeof(Making) <= kSmem, "the routing is made in the ring's memory");
 static_assert(8 * (2 * Q8_MOE_MAX_HIDDEN + 64) <= kMostX, "eight tokens' vectors fit beside two stages of every warp");
-static_assert(kGroup * (4 * 512 + 16) <= kMostX && 8 * (4 * 1024 + 16) <= kMostX, "and so does a segment's");
+static_assert(kGroup * (4 * 512 + 16) <= kMostX && 8 * (4 * 1536 + 16) <= kMostX, "and so does a segment's");
 
 }  // namespace
 
@@ -774,7 +780,8 @@ q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStrea
     p.ldx = a.ldx, p.ldl = a.ldl, p.ldy = a.ldy;
     p.T = a.T, p.E = a.E, p.H = a.H, p.F = a.F, p.top_k = a.top_k, p.renorm = a.renorm;
     // entries of up to 16 tokens where the experts have more than 8 each on the average; else of 8, so
-    // that a much liked expert is two entries' work for two CTAs and not a slow one for one
+    // that a much liked expert is two entries' work for two CTAs and not a slow one for one (32
+    // tokens, 8 of 128 experts: 151 us, 183 with entries of 16; 2 of 8 experts of 1536 x 4096: 59.6 and 60.9)
     p.cap = a.T * a.top_k > 8 * a.E && kGroup * (2 * a.H + 64) <= kMostX ? kGroup : 8;
     const int64_t pairs = static_cast<int64_t>(a.T) * a.top_k, entries = pairs < a.E ? pairs : a.E + pairs / p.cap;
     const int64_t tasks = entries * std::max<int64_t>(a.F / 8, static_cast<int64_t>(a.H / 16) * ((a.F + 511) / 512));
