@@ -308,18 +308,18 @@ struct Scales {
     }
 };
 
-// Waits for the oldest stage: of `stages` (2, 3, 4, 6 or 8), all but two may still be under way.
-__device__ __forceinline__ void wait_stage(int stages) {
-    if (stages == 4)
-        cp_async_wait<2>();
-    else if (stages == 3)
-        cp_async_wait<1>();
-    else if (stages == 6)
-        cp_async_wait<4>();
-    else if (stages == 8)
-        cp_async_wait<6>();
-    else
-        cp_async_wait<0>();
+// Waits until at most n (below kMaxStages) of this thread's last groups of copies are under way.
+__device__ __forceinline__ void wait_but(int n) {
+    switch (n) {
+    case 1: cp_async_wait<1>(); break;
+    case 2: cp_async_wait<2>(); break;
+    case 3: cp_async_wait<3>(); break;
+    case 4: cp_async_wait<4>(); break;
+    case 5: cp_async_wait<5>(); break;
+    case 6: cp_async_wait<6>(); break;
+    case 7: cp_async_wait<7>(); break;
+    default: cp_async_wait<0>();
+    }
 }
 
 constexpr int kRow8 = 8 * kChunk;  // from a tile's row g to row g + 8
@@ -535,13 +535,11 @@ __device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int 
         ld_at = ld_at + kStage == ring_end ? ring : ld_at + kStage;
         cp_async_commit();
     };
-    if (works)
+    auto begin = [&]() {
+        if (works)
 #pragma unroll 1
-        for (int i = 0; i < stages - 1; ++i) load();
-    if (!ready()) {
-        cp_async_wait<0>();
-        return false;
-    }
+            for (int i = 0; i < stages - 1; ++i) load();
+    };
 
     uint32_t code_at[kBlocks];
 #pragma unroll
@@ -551,10 +549,17 @@ __device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int 
     uint32_t at = ring;
     At now = {team, 0, 0};
     enter(now);
-    const int g_last = static_cast<int>((t1 - 1) / tiles);
-    for (int gb = static_cast<int>(t0 / tiles); gb <= g_last; gb += bufs) {
+    const int g_first = static_cast<int>(t0 / tiles), g_last = static_cast<int>((t1 - 1) / tiles);
+    for (int gb = g_first; gb <= g_last; gb += bufs) {
         // ---- the vectors of groups gb .. gb + bufs - 1, a warp a token -----------------------------
-        if (gb != static_cast<int>(t0 / tiles)) __syncthreads();  // nobody reads the ones before any more
+        if (gb != g_first) __syncthreads();  // nobody reads the ones before any more
+        if (DOWN && gb == g_first) {  // weights first: these vectors are not there yet
+            begin();
+            if (!ready()) {
+                cp_async_wait<0>();
+                return false;
+            }
+        }
         auto vectors = [&](auto take) {
 #pragma unroll 1
             for (int i = warp; i < bufs * kGroup; i += kWarps) {
@@ -578,7 +583,12 @@ __device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int 
             for (int c = lane; c < n; c += 32) cp_async16(to + c * 16, static_cast<const uint4 *>(from) + c);
         });
         cp_async_commit();
-        cp_async_wait<0>();
+        if (!DOWN && gb == g_first) {  // vectors first: they need not wait for the weights behind them
+            begin();
+            wait_but(works ? stages - 1 : 0);
+        } else {
+            cp_async_wait<0>();
+        }
         __syncwarp();
         vectors([&](int buf, int k, int group, int, uint32_t to) {
             const int e = DOWN ? scale_hidden(to, columns_of(group)) : scale_x(to, p.H);
@@ -595,7 +605,7 @@ __device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int 
 #pragma unroll
             for (int i = 0; i < kNT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
             for (int c = c0; c < c1; ++c) {
-                wait_stage(stages);
+                wait_but(stages - 2);
                 __syncwarp();
                 load();  // into the stage that the step before this one read
                 Scales s0, s1;
