@@ -458,8 +458,8 @@ __device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int 
     const int tiles = DOWN ? p.H / 16 : p.F / 8;
     const int groups = r.used * nseg;
     const uint32_t tasks = static_cast<uint32_t>(groups) * tiles;
-    const uint32_t t0 = static_cast<uint32_t>(static_cast<uint64_t>(tasks) * blockIdx.x / gridDim.x);
-    const uint32_t t1 = static_cast<uint32_t>(static_cast<uint64_t>(tasks) * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t run = tasks / gridDim.x, more = tasks - run * gridDim.x;  // the first `more` CTAs take one more
+    const uint32_t t0 = run * blockIdx.x + min(blockIdx.x, more), t1 = t0 + run + (blockIdx.x < more ? 1 : 0);
     if (t0 >= t1) return ready();
     const int mine = static_cast<int>(t1 - t0);
 
@@ -719,27 +719,27 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 
     // ---- y_t = the sum over the token's experts and segments, in that order; four columns of one
     // token a thread ----------------------------------------------------------------------------------
-    constexpr int kAt = 8;  // choices at once: their loads are under way together
+    constexpr int kAt = 8;  // summands at once: their loads are under way together
     const int pairs = p.T * p.top_k, quarter = p.H / 4;
     for (int i = blockIdx.x * kThreads + tid; i < p.T * quarter; i += gridDim.x * kThreads) {
         const int t = i / quarter, c = (i - t * quarter) * 4;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j0 = 0; j0 < p.top_k; j0 += kAt) {
-            for (int s = 0; s < nseg; ++s) {
-                float4 v[kAt];
+        for (int choice = 0, seg = 0; choice < p.top_k;) {
+            float4 v[kAt];
+            float w[kAt];
 #pragma unroll
-                for (int j = 0; j < kAt; ++j) {
-                    const int at = j0 + j < p.top_k ? r.pair[t * p.top_k + j0 + j] : -1;
-                    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (at >= 0) v[j] = __ldcg(reinterpret_cast<const float4 *>(p.z + (static_cast<int64_t>(s) * pairs + at) * p.H + c));
-                }
+            for (int j = 0; j < kAt; ++j) {
+                const int at = choice < p.top_k ? r.pair[t * p.top_k + choice] : -1;
+                w[j] = at >= 0 ? r.w[t * p.top_k + choice] : 0.f;
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (at >= 0) v[j] = __ldcg(reinterpret_cast<const float4 *>(p.z + (static_cast<int64_t>(seg) * pairs + at) * p.H + c));
+                if (++seg == nseg) seg = 0, ++choice;
+            }
 #pragma unroll
-                for (int j = 0; j < kAt; ++j) {
-                    const float w = j0 + j < p.top_k ? r.w[t * p.top_k + j0 + j] : 0.f;
-                    if (w == 0.f) continue;  // not chosen: its place holds nothing
-                    sum.x = fmaf(w, v[j].x, sum.x), sum.y = fmaf(w, v[j].y, sum.y);
-                    sum.z = fmaf(w, v[j].z, sum.z), sum.w = fmaf(w, v[j].w, sum.w);
-                }
+            for (int j = 0; j < kAt; ++j) {
+                if (w[j] == 0.f) continue;  // not chosen: its place holds nothing
+                sum.x = fmaf(w[j], v[j].x, sum.x), sum.y = fmaf(w[j], v[j].y, sum.y);
+                sum.z = fmaf(w[j], v[j].z, sum.z), sum.w = fmaf(w[j], v[j].w, sum.w);
             }
         }
         float *const y = p.y + t * p.ldy + c;
