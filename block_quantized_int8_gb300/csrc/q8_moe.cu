@@ -562,8 +562,8 @@ __device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int 
         }
         auto vectors = [&](auto take) {
 #pragma unroll 1
-            for (int i = warp; i < bufs * kGroup; i += kWarps) {
-                const int buf = i / kGroup, k = i - buf * kGroup, group = gb + buf;
+            for (int i = warp; i < bufs * rows8; i += kWarps) {
+                const int buf = i >= rows8 ? 1 : 0, k = i - buf * rows8, group = gb + buf;
                 if (group > g_last) break;
                 const int entry = DOWN ? group / nseg : group, base = r.base[entry];
                 if (k < r.base[entry + 1] - base) take(buf, k, group, base + k, xs + buf * x_bytes + k * pitch);
