@@ -73,6 +73,15 @@ def test_rows(n):
           m=r.choice([0.0, 0.1], n))
 
 
+@pytest.mark.parametrize("n,V", [(153, 3001), (512, 700), (513, 700), (80, 20000)])
+def test_rows_of_mixed_knobs_beyond_one_wave(n, V):
+    # greedy rows, short and long lists, top-p alone and none, in any order
+    l, u, r = rows(n, V, n + V, sd=4.0)
+    kind = r.integers(0, 6, n)
+    check(l, u, np.where(kind == 0, 0.0, 0.8), np.array([0, 20, 1500, 0, 0, 40])[kind],
+          np.array([1.0, 1.0, 0.9, 0.95, 1.0, 0.5])[kind], np.where(kind == 4, 0.01, 0.0))
+
+
 def test_defaults_are_the_plain_distribution():
     from block_quantized_int8_gb300 import q8
     l, u, r = rows(40, 700, 9)
