@@ -345,10 +345,13 @@ struct Codes {
     }
     // the same with x in two parts: values 0..3 (high, low), then 4..7
     __device__ __forceinline__ void mul2(float *d, const uint4 &x, const uint4 &y) const {
-        mma_f16_16816_new(d[0], d[1], d[2], d[3], a[0], a[1], a[2], a[3], x.z, x.w);
-        mma_f16_16816(d[0], d[1], d[2], d[3], b[0], b[1], b[2], b[3], y.z, y.w);
-        mma_f16_16816(d[0], d[1], d[2], d[3], a[0], a[1], a[2], a[3], x.x, x.y);
+        float l[4];
+        mma_f16_16816_new(d[0], d[1], d[2], d[3], a[0], a[1], a[2], a[3], x.x, x.y);
+        mma_f16_16816_new(l[0], l[1], l[2], l[3], a[0], a[1], a[2], a[3], x.z, x.w);
         mma_f16_16816(d[0], d[1], d[2], d[3], b[0], b[1], b[2], b[3], y.x, y.y);
+        mma_f16_16816(l[0], l[1], l[2], l[3], b[0], b[1], b[2], b[3], y.z, y.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] += l[i];
     }
 };
 // 2^(14 - e) and 2^(e - 14) for a largest magnitude m of exponent e: m goes to [2^14, 2^15)
