@@ -623,9 +623,8 @@ __device__ __forceinline__ bool phase(const MoeParams &p, const Routing &r, int 
                 if (n <= 8)
                     nb == kBlocks ? stage_product<DOWN, 1, true>(at, code_at, s0, s1, nb, x, tok8, acc)
                                   : stage_product<DOWN, 1, false>(at, code_at, s0, s1, nb, x, tok8, acc);
-                else
-                    nb == kBlocks ? stage_product<DOWN, kNT, true>(at, code_at, s0, s1, nb, x, tok8, acc)
-                                  : stage_product<DOWN, kNT, false>(at, code_at, s0, s1, nb, x, tok8, acc);
+                else  // one form: a second would cost the others more, in instructions to fetch, than it gives
+                    stage_product<DOWN, kNT, false>(at, code_at, s0, s1, nb, x, tok8, acc);
                 x += kChunk * (DOWN ? 4 : 2);
                 at = at + kStage == ring_end ? ring : at + kStage;
             }
