@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             // 2^e with amax * 2^e in [2^14, 2^15); exponents kept where 2^e and 2^-e are normal
             int ex = static_cast<int>(__float_as_uint(amax) >> 23);
-            ex = min(max(ex, 30), 240);
+            ex = min(max(ex, 30), 254);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - ex) << 23);
             const float down = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
 #pragma unroll

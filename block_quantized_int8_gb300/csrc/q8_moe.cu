@@ -356,7 +356,7 @@ struct Codes {
 };
 // 2^(14 - e) and 2^(e - 14) for a largest magnitude m of exponent e: m goes to [2^14, 2^15)
 // (zero, subnormal and non-finite m keep factors in range)
-__device__ __forceinline__ int scale_exponent(float m) { return min(max(static_cast<int>(__float_as_uint(m) >> 23), 30), 240); }
+__device__ __forceinline__ int scale_exponent(float m) { return min(max(static_cast<int>(__float_as_uint(m) >> 23), 30), 254); }
 __device__ __forceinline__ float scale_up(int ex) { return __uint_as_float(static_cast<uint32_t>(268 - ex) << 23); }
 __device__ __forceinline__ float scale_down(int ex) { return __uint_as_float(static_cast<uint32_t>(ex - 14) << 23); }
 

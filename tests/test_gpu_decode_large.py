@@ -87,3 +87,14 @@ def test_rows_of_logits_further_apart_than_2_31():
     logits = torch.empty(ld + V, dtype=torch.float32, device="cuda").as_strided((n, V), (ld, 1))
     logits.copy_(torch.from_numpy((r.standard_normal((n, V)) * 2.5).astype(np.float32)))
     sample.check(logits, r.random(n).astype(np.float32), k=[0, 40], p=[0.9, 1.0])
+
+
+def test_queries_near_the_end_of_the_range():
+    cache, kv, vv = attn.filled_cache(6, 16, 1, 128, 10)
+    r = np.random.default_rng(2)
+    q = attn.bf16_of(r.standard_normal((1, 2, 128)) * 2.0 ** 124).cuda()
+    attn.check(cache, kv, vv, q, np.arange(6).reshape(1, 6), [90], scale=2.0 ** -126)
+
+
+def test_hidden_units_near_the_end_of_the_range():
+    moe.run(4, 4, 128, 128, 2, seed=5, xs=2.0 ** 61)
