@@ -11,11 +11,10 @@
 // 2) bytes in and 1.0625 out for the write, the reverse for the read.  A lane
 // holds 16 bytes of a row (4 fp32 or 8 bf16 values), so a warp's accesses to
 // the rows are 512 contiguous bytes; 8 or 4 lanes own a block.  Each thread takes the same
-// place of the keys and of the values and is done (a grid of resident CTAs that loop,
-// with two or four such units under way in a thread, was slower at every size: 16 against
-// 14 us for the write and 21 against 19 for the read of 8192 tokens x 1024 values).
-// Measured there: 13.4 us, 3.8 TB/s, for the write from bf16 and 19.1 us, 4.4 TB/s, for the
-// read in fp32; 2.1 and 1.7 us for one token.
+// place of the keys and of the values and is done (a grid of resident CTAs that loop was slower at
+// every size).  Where there are more such units than run at once, a thread reads two (8192 tokens x 1024
+// values in fp32: 16.7 us, 5.1 TB/s, with one 18.7; 1024 tokens 3.3 and 3.1; one token 1.9 and 1.7).  Writing
+// two was slower at every size (8192 tokens 13.1 us and 13.0, 3.9 TB/s, from bf16; one token 2.7 and 2.1).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -27,7 +26,8 @@ namespace q8 {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr uint32_t kMany = 1 << 19;  // units from which on a thread reads two
 
 struct KvParams {
     int8_t *codes[2];      // keys, values
@@ -180,35 +180,42 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     }
 }
 
-template <typename T>
+template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvParams p) {
     constexpr int W = Unit<T>::W;
-    const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
-    if (u >= p.units) return;
-    Place o;
-    const bool live = place<W>(p, u, o);
-    uint2 c[2];
-    float s[2];
+    const uint32_t u = (blockIdx.x * kThreads + (threadIdx.x & ~31u)) * N + (threadIdx.x & 31);  // and u + 32, ...
+    Place o[N];
+    bool live[N];
+    uint2 c[N][2];
+    float s[N][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        c[i] = make_uint2(0u, 0u);
-        s[i] = 0.f;
-        if (live) {
-            if constexpr (W == 4)
-                c[i].x = *reinterpret_cast<const uint32_t *>(p.codes[i] + o.code);
-            else
-                c[i] = *reinterpret_cast<const uint2 *>(p.codes[i] + o.code);
-            s[i] = f16_bits_to_f32(p.scales[i][o.code >> 5]);
+    for (int n = 0; n < N; ++n) live[n] = u + 32 * n < p.units && place<W>(p, u + 32 * n, o[n]);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            c[n][i] = make_uint2(0u, 0u);
+            s[n][i] = 0.f;
+            if (live[n]) {
+                if constexpr (W == 4)
+                    c[n][i].x = *reinterpret_cast<const uint32_t *>(p.codes[i] + o[n].code);
+                else
+                    c[n][i] = *reinterpret_cast<const uint2 *>(p.codes[i] + o[n].code);
+                s[n][i] = f16_bits_to_f32(p.scales[i][o[n].code >> 5]);
+            }
         }
-    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float x[W];
-        codes4_to_f32(c[i].x, x[0], x[1], x[2], x[3]);
-        if constexpr (W == 8) codes4_to_f32(c[i].y, x[4], x[5], x[6], x[7]);
+    for (int n = 0; n < N; ++n) {
+        if (u + 32 * n >= p.units) return;
 #pragma unroll
-        for (int j = 0; j < W; ++j) x[j] *= s[i];
-        *reinterpret_cast<uint4 *>(static_cast<T *>(p.out[i]) + o.token * p.ld[i] + o.at) = Unit<T>::narrow(x);
+        for (int i = 0; i < 2; ++i) {
+            float x[W];
+            codes4_to_f32(c[n][i].x, x[0], x[1], x[2], x[3]);
+            if constexpr (W == 8) codes4_to_f32(c[n][i].y, x[4], x[5], x[6], x[7]);
+#pragma unroll
+            for (int j = 0; j < W; ++j) x[j] *= s[n][i];
+            *reinterpret_cast<uint4 *>(static_cast<T *>(p.out[i]) + o[n].token * p.ld[i] + o[n].at) = Unit<T>::narrow(x);
+        }
     }
 }
 
@@ -245,17 +252,13 @@ q8_status launch_kv(const q8_kv_cache &c, bool append, const void *k, const void
         p.in[0] = static_cast<const uint8_t *>(k) + offk, p.in[1] = static_cast<const uint8_t *>(v) + offv;
         p.out[0] = const_cast<void *>(p.in[0]), p.out[1] = const_cast<void *>(p.in[1]);
         const unsigned grid = (p.units + kThreads - 1) / kThreads;
-        if (append) {
-            if (dtype == Q8_DTYPE_F32)
-                kv_append_kernel<float><<<grid, kThreads, 0, stream>>>(p);
-            else
-                kv_append_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(p);
-        } else {
-            if (dtype == Q8_DTYPE_F32)
-                kv_read_kernel<float><<<grid, kThreads, 0, stream>>>(p);
-            else
-                kv_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(p);
-        }
+        const bool f32 = dtype == Q8_DTYPE_F32;
+        if (append)
+            (f32 ? kv_append_kernel<float> : kv_append_kernel<__nv_bfloat16>)<<<grid, kThreads, 0, stream>>>(p);
+        else if (p.units < kMany)
+            (f32 ? kv_read_kernel<float, 1> : kv_read_kernel<__nv_bfloat16, 1>)<<<grid, kThreads, 0, stream>>>(p);
+        else
+            (f32 ? kv_read_kernel<float, 2> : kv_read_kernel<__nv_bfloat16, 2>)<<<(grid + 1) / 2, kThreads, 0, stream>>>(p);
         if (cudaGetLastError() != cudaSuccess) return Q8_ERR_CUDA;
     }
     return Q8_OK;

@@ -98,3 +98,21 @@ def test_queries_near_the_end_of_the_range():
 
 def test_hidden_units_near_the_end_of_the_range():
     moe.run(4, 4, 128, 128, 2, seed=5, xs=2.0 ** 61)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,heads,D", [(8193, 5, 64), (8195, 4, 128), (4099, 3, 256)])
+def test_reading_many_tokens(oracle, dtype, T, heads, D):
+    from block_quantized_int8_gb300 import q8
+    cache = q8.KvCache.empty(-(-T // 64) + 1, 64, heads, D)
+    r = np.random.default_rng(T)
+    x = [torch.from_numpy(r.standard_normal((T, heads * D)).astype(np.float32)).to(dtype) for _ in range(2)]
+    slots = r.permutation(T + 64)[:T].astype(np.int64)
+    slots[::97] = -1
+    at = torch.from_numpy(slots).cuda()
+    q8.q8_kv_append(cache, *(a.cuda() for a in x), at)
+    for a, g in zip(x, q8.q8_kv_read(cache, at, dtype=dtype)):
+        cq, sq, _ = oracle.quantize_rows(a.float().numpy())
+        want = torch.from_numpy(ref.values(cq, sq).astype(np.float32)).to(dtype)
+        want[::97] = 0
+        assert torch.equal(g.cpu().view(T, heads * D), want)
