@@ -119,21 +119,38 @@ __device__ __forceinline__ uint32_t rank_key(float v) {
 }
 __device__ __forceinline__ float unkey(uint32_t key) { return __uint_as_float((key & 0x80000000u) ? key : ~key & 0x7FFFFFFFu); }
 
+// e of a row's words.  A pass is bound by its instructions and branches, so the quotient (l - top) / T
+// is made without either's slow parts: both are multiplied by a power of two that brings T into
+// [1, 2) (exact), and with y = 1 / T rounded to nearest two corrections q + (d - q T) y of q = d y give
+// d / T rounded to nearest (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990).  Below -2^40 e is 0; where d is small enough for a step to underflow, e is 1.
 struct Row {
-    float top, temp;
+    float top, temp, scale, rcp;
+    bool rare;  // T has no such power, or is infinite
+    __device__ __forceinline__ Row(float l, float t) {
+        const uint32_t bits = __float_as_uint(t), exponent = bits >> 23;
+        rare = exponent < 1 || exponent > 253;
+        top = l;
+        temp = rare ? t : __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
+        scale = rare ? 1.0f : __uint_as_float((254 - exponent) << 23);
+        rcp = __frcp_rn(temp);
+    }
+    __device__ __noinline__ float slow(float l) const { return l == top ? 1.0f : (l == -INFINITY ? 0.0f : expf(__fdiv_rn(l - top, temp))); }
     __device__ __forceinline__ float weight(float l) const {
-        // a division by 1 is left out: the quotient is the same
-        const float d = l - top, q = temp == 1.0f ? d : __fdiv_rn(d, temp);
-        return l == top ? 1.0f : (l == -INFINITY ? 0.0f : expf(q));
+        if (rare) return slow(l);
+        const float d = fmaxf((l - top) * scale, -0x1p40f);
+        float q = d * rcp;
+        q = fmaf(fmaf(-q, temp, d), rcp, q);
+        q = fmaf(fmaf(-q, temp, d), rcp, q);
+        const float e = expf(q);
+        return l == top ? 1.0f : e;
     }
 };
 // floor(e 2^40) for 0 <= e <= 1 from e's own bits: 64-bit conversions are slow here (the pass
 // over 16384 words took 20,000 cycles with two of them a word)
 __device__ __forceinline__ unsigned long long mass_of(float e) {
     const uint32_t b = __float_as_uint(e), m = (b & 0x7FFFFFu) | 0x800000u;
-    const int shift = static_cast<int>(b >> 23) - 110;  // e = m 2^(exponent - 150)
-    if (shift >= 0) return static_cast<unsigned long long>(m) << shift;
-    return m >> min(-shift, 31);
+    return (static_cast<unsigned long long>(m) << 17) >> min(127 - static_cast<int>(b >> 23), 63);  // e = m 2^(exponent - 150)
 }
 
 // Exclusive running sums of m and c over the threads of the CTA, and the totals.
@@ -395,9 +412,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
     }
 
-    Row r;
-    r.top = top;
-    r.temp = temp;
+    const Row r(top, temp);
 
     auto nothing = [&]() {
         if (rank == 0 && tid == 0) {
