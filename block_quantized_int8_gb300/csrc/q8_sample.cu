@@ -44,8 +44,10 @@
 // in shared memory, so the logits are read from memory once.  Bound: by
 // latency for few rows (passes over shared memory with cluster barriers, about
 // 1000 cycles each, between them), by the passes' instructions for many.
-// Measured: one row of 262,144 words 11.7 us with top-k 50, 17 without a filter, 38
-// with top-p 0.95 alone; 64 rows of 131,071 words 31, 48 and 96 us, 49 with mixed knobs.
+// Measured: one row of 262,144 words 12 us with top-k 50, 16 without a filter, 43
+// with top-p 0.95 alone (12,566 words kept); 64 rows of 131,071 words 30, 45 and 93 us,
+// 48 with mixed knobs.  A pass that weighs every word takes 70 instructions a word, the
+// histogram of masses twice as many.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -1148,7 +1150,7 @@ q8_status launch_sample(const SampleArgs &a, uint32_t *dev_status, cudaStream_t 
     SampleParams p = {a.logits, a.temperature, a.top_p, a.min_p, a.u, a.top_k, a.token, a.kept, a.logprob, dev_status,
                       a.ld, a.V, 0, 0};
     // CTAs per row: slices of at most 8192 words while all rows' CTAs find an SM of their own, else
-    // of 16384 (two CTAs an SM) where 16 CTAs or fewer can have that.  16 is more than every
+    // of 16384 (two CTAs an SM) where that is possible with half as many.  16 is more than every
     // device promises, but this one has it; such clusters need 16 free SMs of one GPC, so they
     // find fewer.  With top-k 50, in us: 131071 words, 16 CTAs and 8: 11.2 and 12.8 for one row,
     // 20.1 and 15.7 for 16, 50 and 30 for 64.  32000 words, 4 and 2: 11.3 and 12.3 for 16 rows, 13.9
