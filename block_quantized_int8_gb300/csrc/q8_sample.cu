@@ -126,6 +126,8 @@ __device__ __forceinline__ float unkey(uint32_t key) { return __uint_as_float((k
 // [1, 2) (exact), and with y = 1 / T rounded to nearest two corrections q + (d - q T) y of q = d y give
 // d / T rounded to nearest (Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990).  Below -2^40 e is 0; where d is small enough for a step to underflow, e is 1.
+// Every step is monotone, expf too (looked at for all neighbouring floats from 0 to -104), so e
+// ranks words as their logits do but where it is equal.
 struct Row {
     float top, temp, scale, rcp;
     bool rare;  // T has no such power, or is infinite
