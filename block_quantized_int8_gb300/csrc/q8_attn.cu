@@ -16,8 +16,9 @@
 // scale multiplies its fp32 result, as in the matmuls.
 // Weighted sum: O^T = V^T P, 16 dimensions x 16 tokens by 8 heads.  The
 // weight is rounded to binary16, the value s * code too (2^-11 each at most,
-// against 2^-8 of the bf16 result), sums are fp32.  Value scales above 512 could
-// overflow s * code: such a tile takes s 2^-9 and p 2^9.
+// against 2^-8 of the bf16 result), sums are fp32.
+// Value scales from 512 on could overflow s * code: their tokens are added in a turn
+// of their own, with s 2^-9 and O 2^-9, both exact.
 //
 // Bound: bytes of the cache, 2.125 per dimension and token, each read once
 // for up to 16 query heads; beyond 8 query heads to a key head by the
@@ -515,18 +516,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
                             for (int i = 0; i < D / 16; ++i) o[n][i][j] *= f, o[n][i][2 + j] *= f;
                         }
                 }
-                // a scale above 512 (or a negative one, which the quantizer does not make) in either half
-                uint32_t most = 0x60006000u;
+                // a scale of 512 or more in either half (of any sign, though the quantizer makes none below zero)
+                uint32_t most = 0x5FFF5FFFu;
 #pragma unroll
-                for (int k = 0; k < kRuns; ++k) most = __vmaxu2(most, __vmaxu2(s01[k], s89[k]));
-                const bool big = __any_sync(0xffffffffu, most != 0x60006000u);
-                if (big) {
-#pragma unroll
-                    for (int k = 0; k < kRuns; ++k) {
-                        s01[k] = hmul2(s01[k], 0x18001800u);  // 2^-9
-                        s89[k] = hmul2(s89[k], 0x18001800u);
-                    }
-                }
+                for (int k = 0; k < kRuns; ++k) most = __vmaxu2(most, __vmaxu2(s01[k] & 0x7FFF7FFFu, s89[k] & 0x7FFF7FFFu));
+                const bool big = __any_sync(0xffffffffu, most != 0x5FFF5FFFu);
                 uint32_t pf[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -535,35 +529,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
                     for (int i = 0; i < 4; ++i) w[i] = ex2(acc[n][i] - ref[n][i & 1]);
                     l[n][0] += w[0] + w[2];
                     l[n][1] += w[1] + w[3];
-                    if (big) w[0] *= 512.f, w[1] *= 512.f, w[2] *= 512.f, w[3] *= 512.f;
                     pf[n][0] = movmatrix(f32x2_to_f16x2(w[0], w[1]));
                     pf[n][1] = movmatrix(f32x2_to_f16x2(w[2], w[3]));
                 }
                 // ---- weighted values: MMA rows g and g + 8 of tile q are this lane's dimensions 2 q and
                 // 2 q + 1 of its run
+                auto add_values = [&](const uint32_t (&t01)[kRuns], const uint32_t (&t89)[kRuns]) {
 #pragma unroll
-                for (int k = 0; k < kRuns; ++k) {
-                    uint32_t wa[kRun / 4], wb[kRun / 4], wc[kRun / 4], wd[kRun / 4];
-                    run_codes<kRun>(st + va_at[k], wa);
-                    run_codes<kRun>(st + vb_at[k], wb);
-                    run_codes<kRun>(st + ((va_at[k] + kEight) ^ kFlip), wc);
-                    run_codes<kRun>(st + ((vb_at[k] + kEight) ^ kFlip), wd);
+                    for (int k = 0; k < kRuns; ++k) {
+                        uint32_t wa[kRun / 4], wb[kRun / 4], wc[kRun / 4], wd[kRun / 4];
+                        run_codes<kRun>(st + va_at[k], wa);
+                        run_codes<kRun>(st + vb_at[k], wb);
+                        run_codes<kRun>(st + ((va_at[k] + kEight) ^ kFlip), wc);
+                        run_codes<kRun>(st + ((vb_at[k] + kEight) ^ kFlip), wd);
 #pragma unroll
-                    for (int q = 0; q < kRun / 2; ++q) {
-                        const uint32_t y = __byte_perm(wa[q / 2], wb[q / 2], (q & 1) ? 0x7362 : 0x5140);
-                        const uint32_t z = __byte_perm(wc[q / 2], wd[q / 2], (q & 1) ? 0x7362 : 0x5140);
-                        const uint32_t k1152 = 0x64806480u;
-                        const uint32_t a0 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4140), k1152), s01[k]);
-                        const uint32_t a1 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4342), k1152), s01[k]);
-                        const uint32_t a2 = hmul2(hsub2(__byte_perm(z, 0x64646464u, 0x4140), k1152), s89[k]);
-                        const uint32_t a3 = hmul2(hsub2(__byte_perm(z, 0x64646464u, 0x4342), k1152), s89[k]);
-                        constexpr int kTiles = kRun / 2;
+                        for (int q = 0; q < kRun / 2; ++q) {
+                            const uint32_t y = __byte_perm(wa[q / 2], wb[q / 2], (q & 1) ? 0x7362 : 0x5140);
+                            const uint32_t z = __byte_perm(wc[q / 2], wd[q / 2], (q & 1) ? 0x7362 : 0x5140);
+                            const uint32_t k1152 = 0x64806480u;
+                            const uint32_t a0 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4140), k1152), t01[k]);
+                            const uint32_t a1 = hmul2(hsub2(__byte_perm(y, 0x64646464u, 0x4342), k1152), t01[k]);
+                            const uint32_t a2 = hmul2(hsub2(__byte_perm(z, 0x64646464u, 0x4140), k1152), t89[k]);
+                            const uint32_t a3 = hmul2(hsub2(__byte_perm(z, 0x64646464u, 0x4342), k1152), t89[k]);
+                            constexpr int kTiles = kRun / 2;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16_16816(o[n][k * kTiles + q][0], o[n][k * kTiles + q][1], o[n][k * kTiles + q][2],
+                                              o[n][k * kTiles + q][3], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                        }
+                    }
+                };
+                if (big) {  // the tokens of large scales by themselves, then the others (one loop around both took 3 % more)
+                    auto scale_o = [&](float f) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            mma_f16_16816(o[n][k * kTiles + q][0], o[n][k * kTiles + q][1], o[n][k * kTiles + q][2],
-                                          o[n][k * kTiles + q][3], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) o[n][i][0] *= f, o[n][i][1] *= f, o[n][i][2] *= f, o[n][i][3] *= f;
+                    };
+                    uint32_t t01[kRuns], t89[kRuns];
+#pragma unroll
+                    for (int k = 0; k < kRuns; ++k) {
+                        const uint32_t m01 = __vcmpgeu2(s01[k] & 0x7FFF7FFFu, 0x60006000u), m89 = __vcmpgeu2(s89[k] & 0x7FFF7FFFu, 0x60006000u);
+                        t01[k] = hmul2(s01[k] & m01, 0x18001800u);  // 2^-9
+                        t89[k] = hmul2(s89[k] & m89, 0x18001800u);
+                        s01[k] &= ~m01, s89[k] &= ~m89;
                     }
+                    scale_o(0x1p-9f);
+                    add_values(t01, t89);
+                    scale_o(0x1p9f);
                 }
+                add_values(s01, s89);
             }
             slot = slot + 1 == C::kStages ? 0 : slot + 1;
         }

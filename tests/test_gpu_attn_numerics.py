@@ -1,0 +1,75 @@
+"""Where the roundings of q8_attn_decode could show: large value scales beside small ones, and
+weights far below the largest.
+
+Tolerance, from the arithmetic: the result is rounded once to bf16 (2^-9 of it), a dequantised
+value once to binary16 (2^-12 of it), a weight too (2^-12 of it, or 2^-36 of the largest weight
+where that is more), and a score's fp32 sums move a weight by less than 2^-18 (1 + sum|q k| scale)
+of itself, its share by twice that."""
+import numpy as np
+import pytest
+import torch
+
+import decode_ref as ref
+import test_gpu_attn as attn
+
+pytestmark = pytest.mark.gpu
+
+
+def planes_to_cache(kq, ks, vq, vs):
+    from block_quantized_int8_gb300 import q8
+    ks, vs = ks.astype(np.float16), vs.astype(np.float16)
+    cache = q8.KvCache(*(torch.from_numpy(a).cuda() for a in (kq, ks, vq, vs)))
+    return cache, ref.values(kq, ks.view(np.uint16)), ref.values(vq, vs.view(np.uint16))
+
+
+def check(cache, kv, vv, q, table, n):
+    """One sequence of n tokens in the pages `table`, scale 1; every head against binary64."""
+    from block_quantized_int8_gb300 import q8
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = q8.q8_attn_decode(q, cache, torch.tensor([table], dtype=torch.int32, device="cuda"),
+                                 torch.tensor([n], dtype=torch.int32, device="cuda"), scale=1.0, dev_status=st)
+    out, lse, qn = attn.f64(out)[0], attn.f64(lse)[0], attn.f64(q)[0]
+    assert int(st.item()) == 0
+    pos = np.arange(n)
+    pg, off = np.asarray(table)[pos // cache.page_size], pos % cache.page_size
+    group = qn.shape[0] // cache.kv_heads
+    for h in range(qn.shape[0]):
+        k, v = kv[pg, h // group, off], vv[pg, h // group, off]
+        o, e, pv, big = ref.attention(qn[h], k, v, 1.0)
+        fine = 2.0 ** -18 * (1 + big)
+        assert abs(lse[h] - e) <= fine
+        s = k @ qn[h]
+        tol = 2.0 ** -9 * np.abs(o) + (2.0 ** -11 + 2 * fine) * pv + 2.0 ** -36 * np.abs(v).sum(0) / np.exp(s - s.max()).sum()
+        bad = np.abs(out[h] - o) > tol
+        assert not bad.any(), (h, np.abs(out[h] - o).max(), tol[bad].min(), o[bad][:4], out[h][bad][:4])
+
+
+def tokens(D, heads, pages, ps, scores, r):
+    """Keys whose score with a query of ones / 1024 is about scores[token], values of codes 64 .. 127."""
+    kq = np.full((pages, heads, ps, D), 127, dtype=np.int8)
+    ks = np.broadcast_to((scores * 1024.0 / (127.0 * D)).reshape(pages, 1, ps, 1), (pages, heads, ps, D // 32)).copy()
+    vq = r.integers(64, 128, (pages, heads, ps, D), dtype=np.int8)
+    q = torch.full((1, heads, D), 2.0 ** -10, dtype=torch.bfloat16, device="cuda")
+    return kq, ks, vq, q
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("large", [512.0, 600.0, 60000.0])
+def test_small_value_scales_beside_large_ones(D, large):
+    # one token of every tile has large values and next to no weight (2^-40): the others' digits stay
+    r = np.random.default_rng(D)
+    scores = np.full(16 * 16, 28.0)
+    scores[3::16] = 0.25
+    kq, ks, vq, q = tokens(D, 2, 16, 16, scores, r)
+    vs = r.uniform(0.9, 1.1, (16, 2, 16, D // 32)) * 1.4e-4
+    vs[:, :, 3] = large
+    check(*planes_to_cache(kq, ks, vq, vs), q.repeat(1, 2, 1), list(range(16)), 250)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_the_lowest_code_at_a_scale_of_512(D):
+    # 512 * -128 is beyond binary16; a cache may come from elsewhere than q8_kv_append
+    r = np.random.default_rng(D)
+    kq, ks, vq, q = tokens(D, 1, 4, 16, r.uniform(1.0, 2.0, 64), r)
+    vq[:] = -128
+    check(*planes_to_cache(kq, ks, vq, np.full((4, 1, 16, D // 32), 512.0)), q, [2, 0, 3, 1], 64)
