@@ -7,16 +7,21 @@
 // into (max m, l1 2^(m1 - m) + l2 2^(m2 - m), ...), which is how the warps of
 // a CTA and the CTAs of a sequence are put together, in a fixed order.  The
 // reference is moved only when a score passes it by 4 (a vote, no shuffles
-// otherwise): any m gives the same quotient, and weights stay below 2^4.
+// otherwise): any m gives the same quotient.  A warp weighs by 2^(s' - m + 11),
+// so that weights, below 2^15, use binary16's range downwards; the factor 2^11 of
+// l and O goes out in the quotient.
 //
 // Scores: keys' codes are exact in binary16, and each query head is scaled by
 // a power of two so that its largest value lies in [2^14, 2^15): the bf16
 // query is then exact in binary16 down to 2^-31 of that value.  A warp MMA
 // (m16n8k16) multiplies 16 tokens x 32 codes by 8 query heads; the block's
 // scale multiplies its fp32 result, as in the matmuls.
-// Weighted sum: O^T = V^T P, 16 dimensions x 16 tokens by 8 heads.  The
-// weight is rounded to binary16, the value s * code too (2^-11 each at most,
-// against 2^-8 of the bf16 result), sums are fp32.
+// Weighted sum: O^T = V^T P, 16 dimensions x 16 tokens by 8 heads, sums in fp32.
+// Two roundings to binary16, for one MMA a tile, against 2^-8 of the bf16 result: the value
+// s * code by 2^-11 of itself at most, the weight by 2^-11 of itself down to 2^-25 of the
+// warp's largest and by 2^-36 of that below, which for 2^18 tokens makes 2^-18.
+// (With the largest at 1, weights lost digits from 2^-14 on and vanished at 2^-25, out of
+// O but not out of l.)
 // Value scales from 512 on could overflow s * code: their tokens are added in a turn
 // of their own, with s 2^-9 and O 2^-9, both exact.
 //
@@ -55,6 +60,7 @@ constexpr int kUnitTokens = kWarps * 16;
 constexpr int kMaxGrid = 1024;    // CTAs a launch may have (sizes the workspace)
 constexpr int kMinUnits = 2;      // units a CTA takes at least; 3 and 4 gain in one short case what they lose in another
 constexpr float kGrow = 4.0f;     // log2 growth of a score that moves the reference
+constexpr float kLift = 11.0f;    // log2 of a weight at the reference: 2^(kLift + kGrow) is within binary16
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
             fac[n][1] = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
         }
         float m[NT][2], l[NT][2], o[NT][D / 16][4];
-        float ref[NT][2], top[NT][2];  // m, or 0 where nothing was seen; the score that moves it
+        float ref[NT][2], top[NT][2];  // m - kLift, or 0 where nothing was seen; the score that moves it
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n][0] = m[n][1] = top[n][0] = top[n][1] = -INFINITY;
@@ -509,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
                             y = fmaxf(y, m[n][j]);
                             const float f = m[n][j] == -INFINITY ? 0.f : ex2(m[n][j] - y);
                             m[n][j] = y;
-                            ref[n][j] = y == -INFINITY ? 0.f : y;
+                            ref[n][j] = y == -INFINITY ? 0.f : y - kLift;
                             top[n][j] = y + kGrow;
                             l[n][j] *= f;
 #pragma unroll
@@ -651,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
             const int64_t row = static_cast<int64_t>(wk.b) * p.q_heads + head0 + h;
             *reinterpret_cast<uint2 *>(p.out + row * D + d) =
                 make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-            if (p.lse && d == 0) p.lse[row] = ll == 0.f ? -INFINITY : fmaf(mm, 0.69314718055994531f, logf(ll));
+            if (p.lse && d == 0) p.lse[row] = ll == 0.f ? -INFINITY : fmaf(mm, 0.69314718055994531f, logf(ll * 0x1p-11f));
         };
         const int quads = nheads * (D / 4);
         auto own = [&](int h, int d) { return *reinterpret_cast<const float4 *>(s_o + h * C::kOPitch + d); };

@@ -517,8 +517,10 @@ q8_status q8_kv_read(const q8_kv_cache *cache, const int64_t *slots, int64_t T, 
  *   out   : bf16 [batch][q_heads][head_dim], 16-byte aligned
  *   lse   : float [batch][q_heads], log(sum_t exp(s_t)); may be NULL
  * A sequence of no tokens gives out = 0 and lse = -inf.  Sums, the running
- * maximum and lse are fp32; key codes enter exactly, weights and dequantised
- * values are rounded to binary16 (2^-11 relative at most) before their product.
+ * maximum and lse are fp32; key codes enter exactly.  Before their product a
+ * dequantised value is rounded to binary16 (by 2^-11 of itself at most) and a
+ * token's weight too: by 2^-11 of itself down to 2^-25 of the largest weight
+ * around it, and by 2^-36 of that largest below.
  *   ws    : q8_attn_decode_workspace_size() bytes, 256-byte aligned, zeroed
  *           once; the kernel leaves its counters zero.  Not for two calls
  *           that may run at the same time.
