@@ -129,23 +129,23 @@ __device__ __forceinline__ float unkey(uint32_t key) { return __uint_as_float((k
 // Every step is monotone, expf too (looked at for all neighbouring floats from 0 to -104), so e
 // ranks words as their logits do but where it is equal.
 struct Row {
-    float top, temp, scale, rcp;
+    float top, divisor, scale, rcp;  // divisor: T over the power of two, in [1, 2) (T itself where rare)
     bool rare;  // T has no such power, or is infinite
     __device__ __forceinline__ Row(float l, float t) {
         const uint32_t bits = __float_as_uint(t), exponent = bits >> 23;
         rare = exponent < 1 || exponent > 253;
         top = l;
-        temp = rare ? t : __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
+        divisor = rare ? t : __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
         scale = rare ? 1.0f : __uint_as_float((254 - exponent) << 23);
-        rcp = __frcp_rn(temp);
+        rcp = __frcp_rn(divisor);
     }
-    __device__ __noinline__ float slow(float l) const { return l == top ? 1.0f : (l == -INFINITY ? 0.0f : expf(__fdiv_rn(l - top, temp))); }
+    __device__ __noinline__ float slow(float l) const { return l == top ? 1.0f : (l == -INFINITY ? 0.0f : expf(__fdiv_rn(l - top, divisor))); }
     __device__ __forceinline__ float weight(float l) const {
         if (rare) return slow(l);
         const float d = fmaxf((l - top) * scale, -0x1p40f);
         float q = d * rcp;
-        q = fmaf(fmaf(-q, temp, d), rcp, q);
-        q = fmaf(fmaf(-q, temp, d), rcp, q);
+        q = fmaf(fmaf(-q, divisor, d), rcp, q);
+        q = fmaf(fmaf(-q, divisor, d), rcp, q);
         const float e = expf(q);
         return l == top ? 1.0f : e;
     }
@@ -916,8 +916,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
     if (k < p.V) {
         // steps of the distance from the top: monotone in l, as a difference, a product and a
-        // truncation are, each rounded one way
-        const float far = 28.0f * r.temp, range = fminf(far, top - low);
+        // truncation are, each rounded one way.  Past 28 T words have no mass (exp(-28) < 2^-40)
+        const float far = 28.0f * temp, range = fminf(far, top - low);
         const float per = range > 0.0f && range < INFINITY ? __fdiv_rn(static_cast<float>(kBins - 1), range) : 0.0f;
         auto step_of = [&](float l) -> int {
             const float d = top - l;
