@@ -303,7 +303,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // ---- the row's knobs, and which words the bound is made from ----------------------------
     float temp = p.temperature ? p.temperature[row] : 1.0f;
     int k = p.top_k ? p.top_k[row] : 0;
-    const float top_p = p.top_p ? p.top_p[row] : 1.0f, min_p = p.min_p ? p.min_p[row] : 0.0f;
+    float top_p = p.top_p ? p.top_p[row] : 1.0f;
+    if (!(top_p < 1.0f)) top_p = 1.0f;  // all words
+    const float min_p = p.min_p ? p.min_p[row] : 0.0f;
     const float u = p.u[row];
     if (!(temp > 0.0f)) temp = 1.0f, k = 1;
     if (k <= 0 || k > p.V) k = p.V;
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             __syncthreads();
             bound = s.bound;
         }
-        if (k == p.V) {
+        if (k == p.V && top_p < 1.0f) {
             // e in place of the logits, and whether the mass above the bound is what top-p asks for
             const float least = r.weight(bound);
             unsigned long long m = 0, a = 0;

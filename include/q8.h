@@ -578,7 +578,7 @@ size_t q8_moe_workspace_size(int32_t T, int32_t E, int64_t H, int64_t F, int32_t
  *   are ranked by logit, descending; equal logits by index, ascending.
  *     top-k  keeps the first top_k (<= 0 or > V: all);
  *     top-p  keeps, of those, the words before which less than
- *            ceil(top_p * their sum) lies (top_p >= 1: all; always at least one);
+ *            ceil(top_p * their sum) lies (top_p >= 1 or NaN: all; always at least one);
  *     min-p  keeps, of those, the words with e_i >= min_p;
  *   with W the sum of what is left and r = floor(u * W) (binary64, u binary32),
  *   the token is the first word in index order whose running sum passes r.

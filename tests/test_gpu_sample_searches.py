@@ -39,3 +39,17 @@ def test_top_k_among_many_equal_words(T, k):
     l[1, r.permutation(20000)[:2]] = 0.0
     l[2] += r.integers(0, 2, 20000).astype(np.float32) * T
     sample.check(l, r.random(3).astype(np.float32), T=T, k=k, p=[1.0, 1.0, 0.7])
+
+
+@pytest.mark.parametrize("V", [1, 2, 64, 65, 500, 1000, 1001, 3000])
+@pytest.mark.parametrize("p", [1.0, 1.0 + 2.0 ** -23, 1.5, 1e30, np.inf, np.nan])
+def test_top_p_of_one_and_more_keeps_all_words(V, p):
+    # the same draw as without top-p, whether or not the vocabulary fits a list; logits of both signs
+    l, u, r = sample.rows(6, V, V)
+    l[1] += 20.0
+    l[2] -= 20.0
+    l[3, : V // 2] = -np.inf
+    for k in (0, V, 40):
+        a = sample.draw(l, u, T=[1.0, 0.7, 1.3, 1.0, 0.0, 2.0], k=k, p=p)
+        b = sample.check(l, u, T=[1.0, 0.7, 1.3, 1.0, 0.0, 2.0], k=k)
+        assert all(np.array_equal(x, y) for x, y in zip(a, b)), (k, a, b)
