@@ -55,6 +55,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <vector>
 
 #include "q8_dev.cuh"
@@ -133,8 +134,11 @@ struct TDesc {
 // A row block whose items are shared between CTAs: its partials and ticket
 // live in the workspace under a split id; `sharers` CTAs contribute, and the
 // one holding class 0 writes its running sum through class `pe`.
+// The largest array comes last: an array that began at byte 32132 of the parameters was read
+// wrongly through an index known only at run time (pe: 0, where a constant index or a pointer
+// read the 1 that the host had written), so that a row block's sum took in a partial that the
+// call had not made -- whatever an earlier call had left there.
 struct TParams {
-    TMaps m[Q8_MAX_BATCH];
     TDesc d[Q8_MAX_BATCH];
     uint32_t *status;
     uint32_t *tickets;   // [split id][8 warps], zero between launches
@@ -152,8 +156,10 @@ struct TParams {
     int16_t last_sid[kMaxGrid];   // split id of a CTA's last row block, -1 if whole
     uint8_t sharers[kMaxGrid];
     int8_t pe[kMaxGrid];
+    TMaps m[Q8_MAX_BATCH];
 };
 static_assert(sizeof(TParams) <= 32764, "kernel parameters exceed the 32764-byte limit");
+static_assert(offsetof(TParams, m) <= 16384, "indexed parameters begin far below the limit");
 
 __host__ __device__ __forceinline__ int class_lo(int KC, int C, int c) { return (c * KC) / C; }
 
