@@ -58,6 +58,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnitTokens = kWarps * 16;
 constexpr int kMaxGrid = 1024;    // CTAs a launch may have (sizes the workspace)
+constexpr size_t kTicketBytes = size_t{4} * kMaxGrid * 4;
 constexpr int kMinUnits = 2;      // units a CTA takes at least; 3 and 4 gain in one short case what they lose in another
 constexpr float kGrow = 4.0f;     // log2 growth of a score that moves the reference
 constexpr float kLift = 11.0f;    // log2 of a weight at the reference: 2^(kLift + kGrow) is within binary16
@@ -811,17 +812,21 @@ q8_status launch(const AttnParams &p, int64_t most_units, const DeviceInfo *di, 
 // Counters, then two partial results per CTA.
 size_t attn_workspace(int q_heads, int kv_heads, int head_dim) {
     const int hg = 8 * tiles_of(q_heads / kv_heads, head_dim, INT64_MAX);
-    return static_cast<size_t>(4) * kMaxGrid * 4 + static_cast<size_t>(2) * kMaxGrid * hg * (head_dim + 2) * 4;
+    return kTicketBytes + static_cast<size_t>(2) * kMaxGrid * hg * (head_dim + 2) * 4;
 }
 
 q8_status launch_attn(const q8_kv_cache &c, const AttnArgs &a, void *ws, uint32_t *dev_status, cudaStream_t stream) {
     const DeviceInfo *di = device_info();
     if (!di) return Q8_ERR_CUDA;
+    const WsRange counters = {0, kTicketBytes};
+    const WsRange data = {kTicketBytes, attn_workspace(a.q_heads, c.kv_heads, c.head_dim) - kTicketBytes};
+    const q8_status st = claim_workspace(ws, &counters, 1, &data, 1, stream);
+    if (st != Q8_OK) return st;
     AttnParams p = {};
     p.kq = c.kq, p.vq = c.vq, p.ks = c.ks, p.vs = c.vs;
     p.q = a.q, p.table = a.table, p.lens = a.lens, p.out = a.out, p.lse = a.lse;
     p.tickets = static_cast<uint32_t *>(ws);
-    p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 4 * kMaxGrid * 4);
+    p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kTicketBytes);
     p.status = dev_status;
     p.ldq = a.ldq;
     p.batch = a.batch, p.q_heads = a.q_heads, p.kv_heads = c.kv_heads;

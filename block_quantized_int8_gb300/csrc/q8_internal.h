@@ -23,6 +23,15 @@ const DeviceInfo *device_info();
 // Q8_ERR_CUDA if they cannot be read, Q8_ERR_ARCH for another device.
 q8_status check_arch(const DeviceInfo **out);
 
+// ---- workspaces (q8_workspace.cu) ---------------------------------------------
+struct WsRange {
+    size_t off, len;  // bytes
+};
+// Before a launch that counts with some words of ws (zero before and after it) and writes data to
+// others: clears, in the stream, those counters that are not known to be zero.
+q8_status claim_workspace(void *ws, const WsRange *counters, size_t ncounters, const WsRange *data, size_t ndata,
+                          cudaStream_t stream);
+
 // ---- quantizer --------------------------------------------------------------
 // mode: Q8_QUANT_EXACT (codes from the stored scale) or Q8_QUANT_FL32.
 q8_status launch_quantize(const float *w, int64_t rows, int64_t K, int8_t *q, uint16_t *s,

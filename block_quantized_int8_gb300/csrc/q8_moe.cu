@@ -787,6 +787,10 @@ q8_status launch_moe(const MoeArgs &a, void *ws, uint32_t *dev_status, cudaStrea
         ready.fetch_or(bit);
     }
     const MoeLayout m = layout_of(a.T, a.H, a.F, a.top_k);
+    // counters[0] is zero before and after; counters[1] is left as it is, like data
+    const WsRange counters = {0, sizeof(uint32_t)}, data = {sizeof(uint32_t), m.total - sizeof(uint32_t)};
+    const q8_status st = claim_workspace(ws, &counters, 1, &data, 1, stream);
+    if (st != Q8_OK) return st;
     uint8_t *w = static_cast<uint8_t *>(ws);
     MoeParams p = {};
     p.x = a.x, p.logits = a.logits, p.q13 = a.q13, p.s13 = a.s13, p.q2 = a.q2, p.s2 = a.s2;

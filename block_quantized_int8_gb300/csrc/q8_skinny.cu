@@ -32,8 +32,6 @@
 // No wait in this kernel can block forever: the copy waits give up after a
 // time limit and report Q8_DEV_TIMEOUT; the split-K ticket never waits.
 #include <algorithm>
-#include <mutex>
-#include <unordered_map>
 #include <vector>
 
 #include "q8_dev.cuh"
@@ -542,79 +540,6 @@ size_t skinny_workspace(const q8_linear_desc *descs, int count, int M, SplitPlan
     return need;
 }
 
-namespace {
-
-// The words the kernels count with (split-K tickets, the GEMV's pool
-// counter) are left zero by every launch, but where they sit depends on the
-// call's shapes: another call's partial sums or x copies can cover them.  So
-// the library keeps, per workspace address, the byte ranges that calls
-// enqueued on it may have left nonzero (their partial sums and x copies); a
-// call clears those of its counter ranges that meet one (one memset each,
-// in its stream), and an address seen for the first time is taken as all
-// nonzero.  Calls that write no such data (the GEMV) or repeat the same
-// shapes clear nothing.
-struct Range {
-    size_t off, len;
-};
-std::mutex g_ws_mu;
-std::unordered_map<const void *, std::vector<Range>> g_ws_dirty;
-constexpr size_t kMaxTrackedWorkspaces = 1 << 16;
-constexpr size_t kMaxDirtyRanges = 64;
-
-bool meets(const std::vector<Range> &set, const Range &r) {
-    for (const Range &d : set)
-        if (d.off < r.off + r.len && r.off < d.off + d.len) return true;
-    return false;
-}
-
-// set minus r (pieces of at most two ranges per member)
-void subtract(std::vector<Range> &set, const Range &r) {
-    std::vector<Range> out;
-    for (const Range &d : set) {
-        if (d.off + d.len <= r.off || r.off + r.len <= d.off) {
-            out.push_back(d);
-            continue;
-        }
-        if (d.off < r.off) out.push_back({d.off, r.off - d.off});
-        if (d.off + d.len > r.off + r.len) out.push_back({r.off + r.len, d.off + d.len - (r.off + r.len)});
-    }
-    set.swap(out);
-}
-
-q8_status clear_met_counters(void *ws, const std::vector<Range> &counters, const std::vector<Range> &data,
-                             cudaStream_t stream) {
-    if (ws == nullptr) return Q8_OK;
-    std::lock_guard<std::mutex> lock(g_ws_mu);
-    auto it = g_ws_dirty.find(ws);
-    if (it == g_ws_dirty.end()) {
-        // (a forgotten address is taken as unknown again: cleared on its next use)
-        if (g_ws_dirty.size() >= kMaxTrackedWorkspaces) g_ws_dirty.clear();
-        it = g_ws_dirty.emplace(ws, std::vector<Range>{{0, SIZE_MAX / 2}}).first;
-    }
-    std::vector<Range> &dirty = it->second;
-    for (const Range &r : counters) {
-        if (!meets(dirty, r)) continue;
-        if (cudaMemsetAsync(static_cast<uint8_t *>(ws) + r.off, 0, r.len, stream) != cudaSuccess) return Q8_ERR_CUDA;
-        subtract(dirty, r);
-    }
-    for (const Range &r : data) {
-        subtract(dirty, r);
-        dirty.push_back(r);
-    }
-    // a long history collapses into one range over all of it (more clearing, never less)
-    if (dirty.size() > kMaxDirtyRanges) {
-        size_t lo = SIZE_MAX, hi = 0;
-        for (const Range &d : dirty) {
-            lo = std::min(lo, d.off);
-            hi = std::max(hi, d.off + d.len);
-        }
-        dirty.assign(1, Range{lo, hi - lo});
-    }
-    return Q8_OK;
-}
-
-}  // namespace
-
 q8_status launch_skinny(const q8_linear_desc *all, int all_count, int M, int variant,
                         void *ws, size_t ws_bytes, uint32_t *dev_status, cudaStream_t stream, bool chained) {
     const DeviceInfo *di = device_info();
@@ -652,9 +577,9 @@ q8_status launch_skinny(const q8_linear_desc *all, int all_count, int M, int var
     for (int i = 0; i < count; ++i)
         if (plans[i].bps > ksb_for_m(M)) return Q8_ERR_UNSUPPORTED;
     {
-        // this call's counter words (cleared first where an earlier call on
-        // this workspace may have left data) and the data it writes
-        std::vector<Range> counters, data;
+        // this call's counter words (cleared first where an earlier call may
+        // have left data) and the data it writes
+        std::vector<WsRange> counters, data;
         if (sched_off != SIZE_MAX) counters.push_back({sched_off, 256});
         if (n[kRouteTile] > 0 && tile_off != SIZE_MAX && variant != Q8_VARIANT_BATCH_INVARIANT) {
             size_t toff = 0, tbytes = 0;
@@ -672,7 +597,7 @@ q8_status launch_skinny(const q8_linear_desc *all, int all_count, int M, int var
             data.push_back({gbase + plans[i].part_off,
                             static_cast<size_t>(plans[i].S) * M * static_cast<size_t>(descs[i].N) * 4});
         }
-        const q8_status st = clear_met_counters(ws, counters, data, stream);
+        const q8_status st = claim_workspace(ws, counters.data(), counters.size(), data.data(), data.size(), stream);
         if (st != Q8_OK) return st;
     }
     if (n[kRouteGemv] > 0) {

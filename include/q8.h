@@ -236,13 +236,16 @@ typedef struct q8_linear_desc {
  *           At M = 1 it ends with a 256-byte block whose first word the GEMV
  *           uses as a work counter (it hands its last stages to whichever CTA
  *           is free first) and leaves zero; after a Q8_DEV_TIMEOUT zero the
- *           workspace again.  One workspace may serve later calls of other
- *           shapes (at the same address, in stream order): where the words
- *           a call counts with may hold an earlier call's partial sums or x
- *           copies (or on the first use of an address), the library clears
+ *           workspace again.  One workspace, or parts of it, may serve later
+ *           calls of any kind and shape in stream order (every call that
+ *           takes a workspace: chains, q8_attn_decode and q8_moe too):
+ *           where the words a call counts with may hold what an earlier
+ *           call left (or on the first use of an address), the library clears
  *           them first with one cudaMemsetAsync per range in the call's
  *           stream; M = 1 calls and repeated calls of the same shapes clear
- *           nothing.
+ *           nothing.  What a captured call clears is settled when it is
+ *           captured: a graph that replays between other calls needs a
+ *           workspace that they leave alone.
  * Each output equals, bit for bit, what q8_gemm_skinny returns for that matrix.
  * Outputs must not overlap each other or any input.
  */
@@ -523,7 +526,8 @@ q8_status q8_kv_read(const q8_kv_cache *cache, const int64_t *slots, int64_t T, 
  * around it, and by 2^-36 of that largest below.
  *   ws    : q8_attn_decode_workspace_size() bytes, 256-byte aligned, zeroed
  *           once; the kernel leaves its counters zero.  Not for two calls
- *           that may run at the same time.
+ *           that may run at the same time; may be shared with other calls
+ *           (see q8_linear_batch).
  * The work is split over the sequences' lengths as the device reads them, so
  * a captured graph may be replayed with other lengths.
  */
@@ -553,7 +557,7 @@ size_t q8_attn_decode_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_
  *   weights : float [T][top_k] their w_j; may be NULL
  *   ws      : q8_moe_workspace_size() bytes, 256-byte aligned, zeroed once (and
  *             again after a Q8_DEV_TIMEOUT); not for two calls that may run at
- *             the same time
+ *             the same time; may be shared with other calls (see q8_linear_batch)
  * H and F multiples of 32, H <= 8192 (eight tokens' vectors lie in shared memory), F <= 65536;
  * 1 <= E <= 512; 1 <= top_k <= min(16, E).
  * Products are exact and summed in fp32; hidden units are kept to 22 bits.
