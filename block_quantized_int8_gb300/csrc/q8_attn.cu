@@ -834,7 +834,8 @@ q8_status launch_attn(const q8_kv_cache &c, const AttnArgs &a, void *ws, uint32_
     p.table_width = a.table_width, p.pages = c.pages, p.page_shift = ilog2(c.page_size);
     p.window = a.window, p.scale = a.scale, p.softcap = a.softcap;
     int64_t span = static_cast<int64_t>(a.table_width) * c.page_size;
-    if (a.window > 0 && span > a.window + 15) span = a.window + 15;
+    const int64_t reach = int64_t{a.window} + 15;  // a window may begin anywhere in a tile
+    if (a.window > 0 && span > reach) span = reach;
     const int64_t units = (span + kUnitTokens - 1) / kUnitTokens * a.batch * p.kv_heads;
     const int nt = tiles_of(p.group, c.head_dim, units * ((p.group + 15) / 16));
     p.splits = (p.group + 8 * nt - 1) / (8 * nt);

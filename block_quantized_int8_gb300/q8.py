@@ -549,7 +549,8 @@ def q8_attn_decode(q, cache, table, lens, scale=None, softcap=0.0, window=0, out
         nbytes = q8_attn_decode_workspace_size(B, H, cache.kv_heads, D)
         ws = workspace(nbytes, q.device) if stream is None else _new(stream, lambda: workspace(nbytes, q.device))
     st = lib().q8_attn_decode(cache._ref, q.data_ptr(), sq[0] if B > 1 else H * D, H, table.data_ptr(), width, lens.data_ptr(), B,
-                              D ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), lse.data_ptr(),
+                              D ** -0.5 if scale is None else scale, softcap, window if window < 2 ** 31 else 2 ** 31 - 1,
+                              out.data_ptr(), lse.data_ptr(),
                               *((None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())),
                               None if dev_status is None else dev_status.data_ptr(), _stream(stream))
     if st:
