@@ -411,7 +411,10 @@ _I8, _I32, _I64, _F32, _BF16 = torch.int8, torch.int32, torch.int64, torch.float
 
 def _new(stream, make):
     """make() with its allocations (and zeroing) ordered on the call's stream."""
-    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+    if not isinstance(stream, torch.cuda.Stream):
+        # handle 0 is the default stream (an ExternalStream of 0 is some other, new one)
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
         return make()
 
 
