@@ -189,6 +189,20 @@ def workspace(nbytes: int, device=None) -> torch.Tensor | None:
     return torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
 
 
+def _new(stream, make):
+    """make() with its allocations (and zeroing) ordered on the call's stream."""
+    if not isinstance(stream, torch.cuda.Stream):
+        # handle 0 is the default stream (an ExternalStream of 0 is some other, new one)
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _alloc(stream, make):
+    """As _new, or on the current stream where none is given."""
+    return make() if stream is None else _new(stream, make)
+
+
 # ---------------------------------------------------------------------------
 def q8_quantize_rows(w, q=None, s=None, dev_status=None, stream=None, mode=Q8_QUANT_EXACT):
     """Q8_0-quantize float32 w[rows, K] -> (q int8 [rows, K], s float16 [rows, K/32]);
@@ -198,9 +212,9 @@ def q8_quantize_rows(w, q=None, s=None, dev_status=None, stream=None, mode=Q8_QU
         raise ValueError("w must be contiguous")
     rows, K = w.shape
     if q is None:
-        q = torch.empty((rows, K), dtype=torch.int8, device=w.device)
+        q = _alloc(stream, lambda: torch.empty((rows, K), dtype=torch.int8, device=w.device))
     if s is None:
-        s = torch.empty((rows, max(K // 32, 0)), dtype=torch.float16, device=w.device)
+        s = _alloc(stream, lambda: torch.empty((rows, max(K // 32, 0)), dtype=torch.float16, device=w.device))
     st = lib().q8_quantize_rows_ex(_p(w), rows, K, _p(q), _p(s), int(mode), _p(dev_status), _stream(stream))
     _check(st, "q8_quantize_rows")
     return q, s
@@ -213,9 +227,9 @@ def q8_gguf_to_planar(blocks, rows: int, K: int, q=None, s=None, stream=None):
     if not blocks.is_contiguous() or blocks.numel() != rows * (K // 32) * 34:
         raise ValueError("blocks must be contiguous and hold rows * K/32 blocks of 34 bytes")
     if q is None:
-        q = torch.empty((rows, K), dtype=torch.int8, device=blocks.device)
+        q = _alloc(stream, lambda: torch.empty((rows, K), dtype=torch.int8, device=blocks.device))
     if s is None:
-        s = torch.empty((rows, K // 32), dtype=torch.float16, device=blocks.device)
+        s = _alloc(stream, lambda: torch.empty((rows, K // 32), dtype=torch.float16, device=blocks.device))
     st = lib().q8_gguf_to_planar(_p(blocks), rows, K, _p(q), _p(s), _stream(stream))
     _check(st, "q8_gguf_to_planar")
     return q, s
@@ -227,7 +241,7 @@ def q8_planar_to_gguf(q, s, blocks=None, stream=None):
     _cuda(s, "s", _B16, 2)
     rows, K = q.shape
     if blocks is None:
-        blocks = torch.empty(rows * (K // 32) * 34, dtype=torch.uint8, device=q.device)
+        blocks = _alloc(stream, lambda: torch.empty(rows * (K // 32) * 34, dtype=torch.uint8, device=q.device))
     st = lib().q8_planar_to_gguf(_p(q), _p(s), rows, K, _p(blocks), _stream(stream))
     _check(st, "q8_planar_to_gguf")
     return blocks
@@ -255,10 +269,10 @@ def q8_gemv(q, s, x, y=None, ws=None, dev_status=None, stream=None):
     """y[N] = dequant(q, s) @ x[K] (fp32)."""
     N, K = q.shape
     if y is None:
-        y = torch.empty(N, dtype=torch.float32, device=q.device)
+        y = _alloc(stream, lambda: torch.empty(N, dtype=torch.float32, device=q.device))
     need = q8_workspace_size(N, K, 1)
     if ws is None and need:
-        ws = workspace(need, q.device)
+        ws = _alloc(stream, lambda: workspace(need, q.device))
     st = lib().q8_gemv(_p(q), _p(s), N, K, _p(x), _p(y), _p(ws), 0 if ws is None else ws.numel(),
                        _p(dev_status), _stream(stream))
     _check(st, "q8_gemv")
@@ -270,11 +284,11 @@ def q8_gemm_skinny(q, s, x, y=None, ws=None, dev_status=None, stream=None):
     N, K = q.shape
     M = x.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=q.device)
+        y = _alloc(stream, lambda: torch.empty((M, N), dtype=torch.float32, device=q.device))
     d, _ = _desc(q, s, x, y)
     need = q8_workspace_size(N, K, M)
     if ws is None and need:
-        ws = workspace(need, q.device)
+        ws = _alloc(stream, lambda: workspace(need, q.device))
     st = lib().q8_gemm_skinny(_p(q), _p(s), N, K, _p(x), d.ldx, M, _p(y), d.ldy, _p(ws),
                               0 if ws is None else ws.numel(), _p(dev_status), _stream(stream))
     _check(st, "q8_gemm_skinny")
@@ -289,7 +303,7 @@ def q8_gemm_skinny_noalloc(q, s, x, y=None, dev_status=None, stream=None):
     N, K = q.shape
     M = x.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=q.device)
+        y = _alloc(stream, lambda: torch.empty((M, N), dtype=torch.float32, device=q.device))
     d, _ = _desc(q, s, x, y)
     st = lib().q8_gemm_skinny_noalloc(_p(q), _p(s), N, K, _p(x), d.ldx, M, _p(y), d.ldy,
                                       _p(dev_status), _stream(stream))
@@ -323,7 +337,7 @@ def q8_linear_batch(mats=None, ws=None, variant=Q8_VARIANT_AUTO, dev_status=None
         descs, M = make_descs(mats)
     need = int(lib().q8_linear_batch_workspace_size_ex(descs, len(descs), M, variant))
     if ws is None and need:
-        ws = workspace(need)
+        ws = _alloc(stream, lambda: workspace(need))
     nbytes = 0 if ws is None else ws.numel()
     if chained:
         if variant != Q8_VARIANT_AUTO:
@@ -359,7 +373,7 @@ def q8_linear_chain(steps, M, ws=None, dev_status=None, stream=None):
     step's x made from its y on the device (q8_linear_chain)."""
     need = q8_linear_chain_workspace_size(steps, M)
     if ws is None and need:
-        ws = workspace(need)
+        ws = _alloc(stream, lambda: workspace(need))
     nbytes = 0 if ws is None else ws.numel()
     st = lib().q8_linear_chain(steps, len(steps), M, _p(ws), nbytes, _p(dev_status), _stream(stream))
     _check(st, "q8_linear_chain")
@@ -373,10 +387,10 @@ def q8_gemm_w8a8(q, s, x, y=None, ws=None, dev_status=None, stream=None):
     N, K = q.shape
     M = x.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=q.device)
+        y = _alloc(stream, lambda: torch.empty((M, N), dtype=torch.float32, device=q.device))
     need = int(lib().q8_gemm_w8a8_workspace_size(N, K, M))
     if ws is None and need:
-        ws = workspace(need, q.device)
+        ws = _alloc(stream, lambda: workspace(need, q.device))
     st = lib().q8_gemm_w8a8(_p(q), _p(s), N, K, _p(x), x.stride(0), M, _p(y), y.stride(0), _p(ws),
                             0 if ws is None else ws.numel(), _p(dev_status), _stream(stream))
     _check(st, "q8_gemm_w8a8")
@@ -392,7 +406,7 @@ def q8_gemm(q, s, x, y=None, dev_status=None, stream=None, tile=0, splits=0):
     N, K = q.shape
     M = x.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=q.device)
+        y = _alloc(stream, lambda: torch.empty((M, N), dtype=torch.bfloat16, device=q.device))
     st = lib().q8_gemm_ex(_p(q), _p(s), N, K, _p(x), x.stride(0), M, _p(y), y.stride(0), int(tile), int(splits),
                           _p(dev_status), _stream(stream))
     _check(st, "q8_gemm")
@@ -407,15 +421,6 @@ def q8_gemm(q, s, x, y=None, dev_status=None, stream=None, tile=0, splits=0):
 # where that fails.
 # ---------------------------------------------------------------------------
 _I8, _I32, _I64, _F32, _BF16 = torch.int8, torch.int32, torch.int64, torch.float32, torch.bfloat16
-
-
-def _new(stream, make):
-    """make() with its allocations (and zeroing) ordered on the call's stream."""
-    if not isinstance(stream, torch.cuda.Stream):
-        # handle 0 is the default stream (an ExternalStream of 0 is some other, new one)
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    with torch.cuda.stream(stream):
-        return make()
 
 
 class KvCache:
