@@ -389,6 +389,12 @@ q8_status q8_gemm_ex(const int8_t *q, const uint16_t *s, int64_t N, int64_t K, c
                           reinterpret_cast<cudaStream_t>(stream));
 }
 
+q8_status q8_workspace_zero(void *ws, size_t bytes, q8_stream_t stream) {
+    if (bytes == 0) return Q8_OK;
+    if (!ws) return Q8_ERR_ARG;
+    return cudaMemsetAsync(ws, 0, bytes, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? Q8_OK : Q8_ERR_CUDA;
+}
+
 // ---- decode step ---------------------------------------------------------------
 static q8_status check_cache(const q8_kv_cache *c) {
     if (!c) return Q8_ERR_ARG;

@@ -58,7 +58,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnitTokens = kWarps * 16;
 constexpr int kMaxGrid = 1024;    // CTAs a launch may have (sizes the workspace)
-constexpr size_t kTicketBytes = size_t{4} * kMaxGrid * 4;
+constexpr size_t kTicketBytes = Q8_ATTN_ZEROED_BYTES;
+static_assert(kTicketBytes == size_t{4} * kMaxGrid * 4, "the tickets");
 constexpr int kMinUnits = 2;      // units a CTA takes at least; 3 and 4 gain in one short case what they lose in another
 constexpr float kGrow = 4.0f;     // log2 growth of a score that moves the reference
 constexpr float kLift = 11.0f;    // log2 of a weight at the reference: 2^(kLift + kGrow) is within binary16

@@ -762,7 +762,7 @@ struct MoeLayout {
 MoeLayout layout_of(int T, int H, int F, int top_k) {
     const size_t pairs = static_cast<size_t>(T) * top_k, segments = (F + 511) / 512;
     MoeLayout m;
-    m.hidden = 256;
+    m.hidden = Q8_MOE_ZEROED_BYTES;  // after the counters
     m.z = m.hidden + up256(pairs * F * 4);
     m.total = m.z + up256(segments * pairs * H * 4);
     return m;

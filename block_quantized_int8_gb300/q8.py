@@ -34,6 +34,7 @@ Q8_MAX_BATCH = 64
 Q8_VARIANT_AUTO, Q8_VARIANT_SIMT, Q8_VARIANT_MMA, Q8_VARIANT_BATCH_INVARIANT, Q8_VARIANT_W8A8 = 0, 1, 2, 3, 4
 Q8_GEMM_TILE_AUTO, Q8_GEMM_TILE_256x128, Q8_GEMM_TILE_128x128, Q8_GEMM_TILE_64x128 = 0, 1, 2, 3
 Q8_GEMM_MAX_SPLITS = 8
+Q8_ATTN_ZEROED_BYTES, Q8_MOE_ZEROED_BYTES = 16384, 256
 Q8_QUANT_EXACT, Q8_QUANT_FL32 = 0, 1
 
 EXPORTS = ("q8_quantize_rows", "q8_gemv", "q8_gemm_skinny", "q8_linear_batch", "q8_linear_batch_ex",
@@ -43,7 +44,7 @@ EXPORTS = ("q8_quantize_rows", "q8_gemv", "q8_gemm_skinny", "q8_linear_batch", "
            "q8_stream_read", "q8_stream_read_out_words", "q8_linear_chain", "q8_linear_chain_workspace_size",
            "q8_gemm_w8a8", "q8_gemm_w8a8_workspace_size", "q8_kv_append", "q8_kv_read", "q8_attn_decode",
            "q8_attn_decode_workspace_size", "q8_moe", "q8_moe_workspace_size",
-           "q8_sample")
+           "q8_sample", "q8_workspace_zero")
 Q8_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -127,6 +128,7 @@ def lib():
         L.q8_moe_workspace_size.argtypes = [I32, I32, I64, I64, I32]
         L.q8_moe_workspace_size.restype = SZ
         L.q8_sample.argtypes = [P, I32, I64, I32, I64, P, P, P, P, P, P, P, P, P, P]
+        L.q8_workspace_zero.argtypes = [P, SZ, P]
         L.q8_status_str.argtypes = [ctypes.c_int]
         L.q8_status_str.restype = ctypes.c_char_p
         L.q8_abi_version.restype = I32
@@ -134,7 +136,7 @@ def lib():
                      "q8_linear_batch_ex", "q8_linear_batch_chained", "q8_gguf_to_planar",
                      "q8_planar_to_gguf", "q8_gemm", "q8_gemm_ex", "q8_gemm_skinny_noalloc", "q8_linear_chain", "q8_gemm_w8a8",
                      "q8_kv_append", "q8_kv_read", "q8_attn_decode", "q8_moe",
-                     "q8_sample"):
+                     "q8_sample", "q8_workspace_zero"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -423,6 +425,15 @@ def q8_gemm(q, s, x, y=None, dev_status=None, stream=None, tile=0, splits=0):
 _I8, _I32, _I64, _F32, _BF16 = torch.int8, torch.int32, torch.int64, torch.float32, torch.bfloat16
 
 
+def _counting_workspace(nbytes, zeroed, device):
+    """A workspace of which only the words that the kernels count with are zeroed."""
+    if nbytes == 0:
+        return None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _check(lib().q8_workspace_zero(ws.data_ptr(), zeroed, _stream(None)), "q8_workspace_zero")
+    return ws
+
+
 class KvCache:
     """A paged key-value cache in Q8_0 blocks (q8_kv_cache): codes int8
     [pages, kv_heads, page_size, head_dim], scales 16-bit [..., head_dim / 32].
@@ -555,7 +566,7 @@ def q8_attn_decode(q, cache, table, lens, scale=None, softcap=0.0, window=0, out
         raise ValueError("lse must be contiguous, [B, q_heads]")
     if ws is None:
         nbytes = q8_attn_decode_workspace_size(B, H, cache.kv_heads, D)
-        ws = workspace(nbytes, q.device) if stream is None else _new(stream, lambda: workspace(nbytes, q.device))
+        ws = _alloc(stream, lambda: _counting_workspace(nbytes, Q8_ATTN_ZEROED_BYTES, cache.device))
     st = lib().q8_attn_decode(cache._ref, q.data_ptr(), sq[0] if B > 1 else H * D, H, table.data_ptr(), width, lens.data_ptr(), B,
                               D ** -0.5 if scale is None else scale, softcap, window if window < 2 ** 31 else 2 ** 31 - 1,
                               out.data_ptr(), lse.data_ptr(),
@@ -614,7 +625,7 @@ def q8_moe(x, logits, q13, s13, q2, s2, top_k, renorm=True, y=None, ids=None, we
         raise ValueError("weights must be contiguous, [T, top_k]")
     if ws is None:
         nbytes = q8_moe_workspace_size(T, E, H, F, top_k)
-        ws = workspace(nbytes, dev) if stream is None else _new(stream, lambda: workspace(nbytes, dev))
+        ws = _alloc(stream, lambda: _counting_workspace(nbytes, Q8_MOE_ZEROED_BYTES, dev))
     one = T <= 1
     st = lib().q8_moe(x.data_ptr(), H if one else sx[0], logits.data_ptr(), E if one else sl[0], T, E, top_k, 1 if renorm else 0,
                       q13.data_ptr(), s13.data_ptr(), q2.data_ptr(), s2.data_ptr(), H, F, y.data_ptr(), ldy, ids.data_ptr(),

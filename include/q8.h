@@ -524,13 +524,15 @@ q8_status q8_kv_read(const q8_kv_cache *cache, const int64_t *slots, int64_t T, 
  * dequantised value is rounded to binary16 (by 2^-11 of itself at most) and a
  * token's weight too: by 2^-11 of itself down to 2^-25 of the largest weight
  * around it, and by 2^-36 of that largest below.
- *   ws    : q8_attn_decode_workspace_size() bytes, 256-byte aligned, zeroed
- *           once; the kernel leaves its counters zero.  Not for two calls
+ *   ws    : q8_attn_decode_workspace_size() bytes, 256-byte aligned, the first
+ *           Q8_ATTN_ZEROED_BYTES zeroed once (the kernel counts there and
+ *           leaves them zero; the rest may hold anything).  Not for two calls
  *           that may run at the same time; may be shared with other calls
  *           (see q8_linear_batch).
  * The work is split over the sequences' lengths as the device reads them, so
  * a captured graph may be replayed with other lengths.
  */
+#define Q8_ATTN_ZEROED_BYTES 16384
 q8_status q8_attn_decode(const q8_kv_cache *cache, const uint16_t *q, int64_t ldq, int32_t q_heads,
                          const int32_t *table, int32_t table_width, const int32_t *lens, int32_t batch, float scale,
                          float softcap, int32_t window, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
@@ -555,8 +557,9 @@ size_t q8_attn_decode_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_
  *   y       : float [T][ldy], ldy >= H
  *   ids     : int32 [T][top_k] the chosen experts, -1 for none; may be NULL
  *   weights : float [T][top_k] their w_j; may be NULL
- *   ws      : q8_moe_workspace_size() bytes, 256-byte aligned, zeroed once (and
- *             again after a Q8_DEV_TIMEOUT); not for two calls that may run at
+ *   ws      : q8_moe_workspace_size() bytes, 256-byte aligned, the first
+ *             Q8_MOE_ZEROED_BYTES zeroed once (and again after a
+ *             Q8_DEV_TIMEOUT); not for two calls that may run at
  *             the same time; may be shared with other calls (see q8_linear_batch)
  * H and F multiples of 32, H <= 8192 (eight tokens' vectors lie in shared memory), F <= 65536;
  * 1 <= E <= 512; 1 <= top_k <= min(16, E).
@@ -568,6 +571,7 @@ size_t q8_attn_decode_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_
 #define Q8_MOE_MAX_TOP_K 16
 #define Q8_MOE_MAX_HIDDEN 8192
 #define Q8_MOE_MAX_FFN 65536
+#define Q8_MOE_ZEROED_BYTES 256
 q8_status q8_moe(const uint16_t *x, int64_t ldx, const float *logits, int64_t ldl, int32_t T, int32_t E, int32_t top_k,
                  int32_t renorm, const int8_t *q13, const uint16_t *s13, const int8_t *q2, const uint16_t *s2, int64_t H,
                  int64_t F, float *y, int64_t ldy, int32_t *ids, float *weights, void *ws, size_t ws_bytes,
@@ -602,6 +606,14 @@ size_t q8_moe_workspace_size(int32_t T, int32_t E, int64_t H, int64_t F, int32_t
 q8_status q8_sample(const void *logits, int32_t dtype, int64_t ld, int32_t rows, int64_t V, const float *temperature,
                     const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
                     float *logprob, int32_t *kept, uint32_t *dev_status, q8_stream_t stream);
+
+/*
+ * q8_workspace_zero -- zero the first `bytes` of a workspace, in the stream:
+ * what its first use asks for (all of it, or the Q8_*_ZEROED_BYTES of a call),
+ * for callers whose memory comes unzeroed.  One cudaMemsetAsync.  bytes == 0
+ * is a no-op.
+ */
+q8_status q8_workspace_zero(void *ws, size_t bytes, q8_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
 const char *q8_status_str(q8_status st);
