@@ -45,6 +45,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <cfloat>
 
 #include "q8_async.cuh"
 #include "q8_dev.cuh"
@@ -419,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
             }
             float f = p.scale * down;
             f = p.softcap > 0.f ? f / p.softcap : f * kLog2e;
+            f = fmaxf(fminf(f, FLT_MAX), -FLT_MAX);  // a score of zero stays one
             fac[n][0] = __shfl_sync(0xffffffffu, f, (2 * t) * 4);
             fac[n][1] = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
         }
@@ -833,7 +835,9 @@ q8_status launch_attn(const q8_kv_cache &c, const AttnArgs &a, void *ws, uint32_
     p.batch = a.batch, p.q_heads = a.q_heads, p.kv_heads = c.kv_heads;
     p.group = a.q_heads / c.kv_heads;
     p.table_width = a.table_width, p.pages = c.pages, p.page_shift = ilog2(c.page_size);
-    p.window = a.window, p.scale = a.scale, p.softcap = a.softcap;
+    // c tanh(s / c) is s (1 - (s / c)^2 / 3 + ...): from c = 2^40 on s itself for every score that binary32 can
+    // tell from its neighbours by less than 2^4 (and c log2(e) would overflow near the end of the range)
+    p.window = a.window, p.scale = a.scale, p.softcap = a.softcap < 0x1p40f ? a.softcap : 0.f;
     int64_t span = static_cast<int64_t>(a.table_width) * c.page_size;
     const int64_t reach = int64_t{a.window} + 15;  // a window may begin anywhere in a tile
     if (a.window > 0 && span > reach) span = reach;

@@ -20,3 +20,21 @@ def test_a_window_that_says_unbounded(window):
     got = q8.q8_attn_decode(q, cache, table, lens, window=window)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     attn.check(cache, kv, vv, q, table.cpu().numpy(), [5600, 3333], window=window)
+
+
+@pytest.mark.parametrize("softcap", [2.0 ** 38, 2.0 ** 40, 1e30, 3.0e38])
+def test_a_cap_far_above_the_scores_is_none(softcap):
+    lens, table = [300, 17], np.arange(40).reshape(2, 20)
+    cache, kv, vv = attn.filled_cache(40, 16, 1, 128, 5)
+    q = attn.bf16_of(np.random.default_rng(2).standard_normal((2, 3, 128)) * 2.0).cuda()
+    attn.check(cache, kv, vv, q, table, lens, softcap=softcap)
+
+
+@pytest.mark.parametrize("softcap,scale", [(1e-45, 1.0), (1e-30, 1.0), (0.0, 3.0e38), (1e-40, -3.0e38)])
+def test_scores_of_zero_stay_zero_however_small_the_cap(softcap, scale):
+    # tokens with a key of zeros: their score is zero and counts like any other's
+    from block_quantized_int8_gb300 import q8
+    cache, kv, vv = attn.filled_cache(8, 16, 1, 64, 6)
+    cache.kq.zero_()
+    q = attn.bf16_of(np.random.default_rng(3).standard_normal((1, 2, 64)) * 2.0 ** 100).cuda()
+    attn.check(cache, 0.0 * kv, vv, q, np.arange(8).reshape(1, 8), [100], softcap=softcap, scale=scale)
