@@ -480,7 +480,38 @@ def chain_rows(torch, q8, ls, peak, ms=(1, 8)):
     return rows
 
 
-def extra_rows(torch, q8, peak):
+def prefill_rows(torch, q8, dev, timed, spread_of, world):
+    """Prefill-shaped GEMMs (compute-bound: TFLOP/s).  q8_gemm loads x by TMA
+    multicast, which is for calls of one GPU: its rows are left out of others."""
+    rows = {}
+    peaks, _ = measured_peaks()
+    tpk = float(peaks.get("bf16_tflops", 1900.0))
+    M = synth.PREFILL_M
+    for (K, N) in synth.SWEEP_SHAPES:
+        q0, s0 = q8.q8_quantize_rows(torch.from_numpy(synth.weights(N, K, 0, f"pf{K}.{N}")).to(dev))
+        x = torch.from_numpy(synth.activations(M, K, 0, f"pfx{K}").view(np.int16)).view(torch.bfloat16).to(dev)
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        if world == 1:
+            t = timed([lambda q0=q0, s0=s0, x=x, y=y: q8.q8_gemm(q0, s0, x, y)], reps=50)
+            tf = 2.0 * M * N * K / t / 1e12
+            rows[f"prefill_gemm_M{M}_K{K}_N{N}"] = {
+                "TFLOP/s": round(tf, 1), "frac": round(tf / tpk, 4), "us": round(t * 1e6, 2),
+                "us_p10": round(spread_of[0][0] * 1e6, 2), "us_p90": round(spread_of[0][1] * 1e6, 2),
+                "GB/s": round(matmul_bytes(N, K, M, 2) / t / 1e9, 1)}
+        # the same shape as W8A8 (int8 warp MMA in 32-row slices; fp32 out):
+        # int8 TOPS, and that rate against the measured bf16 peak
+        y8 = torch.empty((M, N), dtype=torch.float32, device=dev)
+        ws8 = q8.workspace(int(q8.lib().q8_gemm_w8a8_workspace_size(N, K, M)), dev)
+        t = timed([lambda q0=q0, s0=s0, x=x, y8=y8, ws8=ws8: q8.q8_gemm_w8a8(q0, s0, x, y=y8, ws=ws8)], reps=20)
+        tf = 2.0 * M * N * K / t / 1e12
+        rows[f"prefill_w8a8_M{M}_K{K}_N{N}"] = {
+            "TOPS": round(tf, 1), "frac_of_bf16_peak": round(tf / tpk, 4), "us": round(t * 1e6, 2),
+            "us_p10": round(spread_of[0][0] * 1e6, 2), "us_p90": round(spread_of[0][1] * 1e6, 2)}
+        del y8, ws8
+    return rows
+
+
+def extra_rows(torch, q8, peak, world):
     """Context rows: other workloads, each timed with CUDA events on distinct
     weight copies so that no call finds its weights in L2."""
     dev = torch.device("cuda")
@@ -631,30 +662,7 @@ def extra_rows(torch, q8, peak):
         del ys, wsb
     del cps
 
-    # prefill-shaped GEMM on tcgen05 (compute-bound: report TFLOP/s)
-    peaks, _ = measured_peaks()
-    tpk = float(peaks.get("bf16_tflops", 1900.0))
-    M = synth.PREFILL_M
-    for (K, N) in synth.SWEEP_SHAPES:
-        q0, s0 = q8.q8_quantize_rows(torch.from_numpy(synth.weights(N, K, 0, f"pf{K}.{N}")).to(dev))
-        x = torch.from_numpy(synth.activations(M, K, 0, f"pfx{K}").view(np.int16)).view(torch.bfloat16).to(dev)
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        t = timed([lambda q0=q0, s0=s0, x=x, y=y: q8.q8_gemm(q0, s0, x, y)], reps=50)
-        tf = 2.0 * M * N * K / t / 1e12
-        rows[f"prefill_gemm_M{M}_K{K}_N{N}"] = {
-            "TFLOP/s": round(tf, 1), "frac": round(tf / tpk, 4), "us": round(t * 1e6, 2),
-            "us_p10": round(spread_of[0][0] * 1e6, 2), "us_p90": round(spread_of[0][1] * 1e6, 2),
-            "GB/s": round(matmul_bytes(N, K, M, 2) / t / 1e9, 1)}
-        # the same shape as W8A8 (int8 warp MMA in 32-row slices; fp32 out):
-        # int8 TOPS, and that rate against the measured bf16 peak
-        y8 = torch.empty((M, N), dtype=torch.float32, device=dev)
-        ws8 = q8.workspace(int(q8.lib().q8_gemm_w8a8_workspace_size(N, K, M)), dev)
-        t = timed([lambda q0=q0, s0=s0, x=x, y8=y8, ws8=ws8: q8.q8_gemm_w8a8(q0, s0, x, y=y8, ws=ws8)], reps=20)
-        tf = 2.0 * M * N * K / t / 1e12
-        rows[f"prefill_w8a8_M{M}_K{K}_N{N}"] = {
-            "TOPS": round(tf, 1), "frac_of_bf16_peak": round(tf / tpk, 4), "us": round(t * 1e6, 2),
-            "us_p10": round(spread_of[0][0] * 1e6, 2), "us_p90": round(spread_of[0][1] * 1e6, 2)}
-        del y8, ws8
+    rows.update(prefill_rows(torch, q8, dev, timed, spread_of, world))
     torch.cuda.empty_cache()
     return rows
 
@@ -872,6 +880,8 @@ def main():
 
     if args.impl == "reference":
         return reference_arm(args, rank, world)
+    if args.profile and world > 1:
+        ap.error("--profile is for one GPU")
 
     import torch
     torch.cuda.set_device(local_rank)
@@ -926,7 +936,7 @@ def main():
     e2e, h2d, d2h = e2e_gbs(torch, ls, max(20, min(200, args.steps // 10)), bytes_step, chained)
     c_copy, c_read = ceilings(torch, q8)
 
-    rows = {} if (args.no_rows or rank != 0) else extra_rows(torch, q8, peak)
+    rows = {} if (args.no_rows or rank != 0) else extra_rows(torch, q8, peak, world)
     if rows:
         # the same step, plain and chained, captured once into a CUDA graph
         for ch, cn in ((False, "plain"), (True, "chained")):

@@ -365,6 +365,8 @@ size_t q8_linear_chain_workspace_size(const q8_chain_step *steps, int32_t count,
  * on the tested workloads (the bf16 weights round each weight by up to 2^-9
  * relative).  Needs no workspace: when K is split over several CTAs (short N,
  * long K), the partial sums meet in the CTAs' shared memory.
+ * For programs of one GPU: x is loaded by TMA multicast within a cluster (from
+ * this GPU's memory), which has no place in one that runs on several at once.
  */
 q8_status q8_gemm(const int8_t *q, const uint16_t *s, int64_t N, int64_t K,
                   const uint16_t *x, int64_t ldx, int32_t M,
