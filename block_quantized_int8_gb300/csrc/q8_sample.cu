@@ -15,7 +15,7 @@
 // The row is not sorted: the words kept are a prefix of the ranking, and what
 // is needed is where it ends.
 //  - few words: the row is cut into 128 groups.  At least k words are no smaller than
-//    the k-th largest group maximum, and few more are (top-k up to 64).  For more
+//    the k-th largest group maximum, and few more are (top-k up to 96).  For more
 //    words the rank among the maxima is where 1.5 k words (1400 for top-p alone) are
 //    expected: with f of the groups above the bound, -log(1 - f) words a group.  From
 //    256 words on the maxima are of every 4th word, which keeps f away from 1: the
@@ -69,8 +69,16 @@ constexpr int kList = 2048;        // words one CTA sorts
 constexpr int kPer = kList / kThreads;
 constexpr int kMaxCluster = 16;
 constexpr int kGroups = 128;       // of a row, for a bound on its k-th logit
-constexpr int kFewK = 64;          // top-k whose bound is exact
-constexpr int kManyK = 1000;       // and whose words, half as many more expected, fit the list
+// Top-k whose bound is the k-th largest group maximum: up to 3/4 of the groups, above which 1.4 k words
+// are expected, as many as the rule for more words asks for.  With limits of 32, 64, 96 and 112, k = 65 takes
+// 11.6, 11.8, 10.9 and 11.0 us (one row of 32,000 words), 11.8, 11.8, 11.4 and 11.3 (131,071), k = 112 13.1 to 13.4
+// everywhere.
+constexpr int kFewK = kGroups * 3 / 4;
+// Top-k that is looked for through the list at all: 1.5 k words are asked for, and an eighth more still
+// fit.  From 1050 to 1150 words: 131,071 words, one row 17.2 to 17.6 us and 23.7 through the histogram, 64 rows
+// 41 to 43 and 62.5; 262,144 words 19 and 27.8, 81 to 85 and 132; 64 rows of 32,000 words, where the list does
+// not do for one or the other, 32.2 and 26.5.  At 1200 it does not for one row of 262,144 either: 32.5 and 27.8.
+constexpr int kManyK = kList * 9 / 16;
 constexpr int kListP = 1400;       // words asked for where only top-p counts
 constexpr int kCopies = 4;         // bulk copies of a slice
 constexpr float kUnit = 1.0f / 1099511627776.0f;  // 2^-40

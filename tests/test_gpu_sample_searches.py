@@ -53,3 +53,14 @@ def test_top_p_of_one_and_more_keeps_all_words(V, p):
         a = sample.draw(l, u, T=[1.0, 0.7, 1.3, 1.0, 0.0, 2.0], k=k, p=p)
         b = sample.check(l, u, T=[1.0, 0.7, 1.3, 1.0, 0.0, 2.0], k=k)
         assert all(np.array_equal(x, y) for x, y in zip(a, b)), (k, a, b)
+
+
+@pytest.mark.parametrize("V", [2049, 5000, 32003, 131071])
+def test_top_k_around_the_places_where_the_search_changes(V):
+    # by the k-th group maximum up to 96, by a rank among them up to 1152, by the histogram above
+    r = np.random.default_rng(V)
+    k = np.array([1, 63, 64, 65, 95, 96, 97, 127, 128, 129, 170, 171, 999, 1000, 1001, 1151, 1152, 1153, 1366, 2047])
+    l = (r.standard_normal((len(k), V)) * 2.5).astype(np.float32)
+    for p in (1.0, 0.9):
+        tok, lp, kept = sample.check(l, r.random(len(k)).astype(np.float32), T=0.8, k=k, p=p)
+        assert p < 1.0 or np.array_equal(kept, k)
