@@ -51,6 +51,7 @@
 #include <cooperative_groups.h>
 
 #include <atomic>
+#include <cstdlib>
 #include <type_traits>
 
 #include "q8_dev.cuh"
@@ -1145,6 +1146,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 constexpr int kSmem = 227 * 1024 - 1024;
 
+int slice_of(int V, int ranks) { return ((V + 7 + ranks - 1) / ranks + 7) & ~7; }
+bool fits(int V, int ranks) { return sizeof(Shared) + static_cast<size_t>(slice_of(V, ranks)) * 4 <= kSmem; }
+
+// The largest cluster that the current device runs with as much shared memory as a row may take.  16 is more
+// than every device promises, and a part of one may have no 16 free SMs in one place.  0: a CUDA call failed.
+int largest_cluster(const DeviceInfo *di) {
+    static std::atomic<int> found[64];
+    int n = di->device < 64 ? found[di->device].load(std::memory_order_relaxed) : 0;
+    for (int ranks = kMaxCluster; n == 0 && ranks >= 1; ranks /= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.blockDim = dim3(kThreads);
+        cfg.gridDim = dim3(ranks);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = ranks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int active = 0;
+        if (cudaOccupancyMaxActiveClusters(&active, sample_kernel<false>, &cfg) != cudaSuccess) return 0;
+        if (active > 0) n = ranks;
+    }
+    if (n > 0 && di->device < 64) found[di->device].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 }  // namespace
 
 q8_status launch_sample(const SampleArgs &a, uint32_t *dev_status, cudaStream_t stream) {
@@ -1161,21 +1189,29 @@ q8_status launch_sample(const SampleArgs &a, uint32_t *dev_status, cudaStream_t 
     }
     SampleParams p = {a.logits, a.temperature, a.top_p, a.min_p, a.u, a.top_k, a.token, a.kept, a.logprob, dev_status,
                       a.ld, a.V, 0, 0};
+    int most = largest_cluster(di);
+    if (most == 0) return Q8_ERR_CUDA;
+    // Q8_SAMPLE_CLUSTER = 1, 2, 4 or 8 asks for at most that many CTAs a row (as on a device that runs no
+    // more); it never changes the results
+    if (const char *e = std::getenv("Q8_SAMPLE_CLUSTER")) {
+        const int ask = std::atoi(e);
+        if (ask == 1 || ask == 2 || ask == 4 || ask == 8) most = ask < most ? ask : most;
+    }
+    if (!fits(a.V, most)) return Q8_ERR_UNSUPPORTED;
     // CTAs per row: slices of at most 8192 words while all rows' CTAs find an SM of their own, else
-    // of 16384 (two CTAs an SM) where that is possible with half as many.  16 is more than every
-    // device promises, but this one has it; such clusters need 16 free SMs of one GPC, so they
-    // find fewer.  With top-k 50, in us: 131071 words, 16 CTAs and 8: 11.2 and 12.8 for one row,
-    // 20.1 and 15.7 for 16, 50 and 30 for 64.  32000 words, 4 and 2: 11.3 and 12.3 for 16 rows, 13.9
-    // and 12.9 for 64, 26 and 16 for 128 (8 CTAs: 10.9 for one row, but top-p alone 24 in place
+    // of 16384 (two CTAs an SM) where that is possible with half as many.  Clusters of 16 need 16
+    // free SMs of one GPC, so they find fewer.  With top-k 50, in us: 131071 words, 16 CTAs and 8: 11.2 and
+    // 12.8 for one row, 20.1 and 15.7 for 16, 50 and 30 for 64.  32000 words, 4 and 2: 11.3 and 12.3 for 16
+    // rows, 13.9 and 12.9 for 64, 26 and 16 for 128 (8 CTAs: 10.9 for one row, but top-p alone 24 in place
     // of 19).  262144 words, 16 and 8: 12.8 and 15.3 for one row, 59 and 60 for 64.
     int ranks = 1;
-    while (ranks < kMaxCluster && a.V > 8192 * ranks) ranks *= 2;
+    while (ranks < most && a.V > 8192 * ranks) ranks *= 2;
     const int64_t places = ranks == kMaxCluster ? di->sm_count * 2 / 3 : di->sm_count;
     if (ranks > 1 && a.rows * int64_t{ranks} > places && a.V <= 8192 * ranks) ranks /= 2;
     // Rows with knobs of their own, more than run at once: those that take longer begin first (64 rows of
     // 131071 words with mixed knobs: 72 us as they come, 53 so; 64 alike: 30.4 and 30.9).
     p.rows = a.top_k && a.rows <= kThreads && a.rows * int64_t{ranks} > di->sm_count ? a.rows : 0;
-    p.slice = ((a.V + 7 + ranks - 1) / ranks + 7) & ~7;
+    p.slice = slice_of(a.V, ranks);
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(Shared) + static_cast<size_t>(p.slice) * 4;

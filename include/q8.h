@@ -602,7 +602,8 @@ size_t q8_moe_workspace_size(int32_t T, int32_t E, int64_t H, int64_t F, int32_t
  *   logprob: float [rows], log(w_token / W), -inf where there is none; may be NULL
  *   kept   : int32 [rows], how many words of mass > 0 were left; may be NULL
  * 1 <= V <= 2^19 (a row's slices lie in the shared memory of a cluster of 16
- * CTAs).  No workspace.
+ * CTAs; where the device runs only smaller ones, a V that they have no room for
+ * is Q8_ERR_UNSUPPORTED).  No workspace.
  */
 #define Q8_SAMPLE_MAX_V (1 << 19)
 q8_status q8_sample(const void *logits, int32_t dtype, int64_t ld, int32_t rows, int64_t V, const float *temperature,
