@@ -181,6 +181,27 @@ def _cuda(t, name, dtypes, ndim=None):
     return t
 
 
+def _status(t):
+    """The address of a status word, which kernels write to."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.element_size() == 4 and t.numel() > 0):
+        _cuda(t, "dev_status", (t.dtype,))
+        raise TypeError("dev_status must hold a 32-bit word")
+    return t.data_ptr()
+
+
+def _work(ws):
+    """(address, bytes) of a workspace."""
+    if ws is None:
+        return None, 0
+    if not (ws.is_cuda and ws.is_contiguous()):
+        _cuda(ws, "ws", (ws.dtype,))
+        if not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 _B16 = (torch.bfloat16, torch.float16, torch.int16, torch.uint16)
 
 
@@ -217,7 +238,7 @@ def q8_quantize_rows(w, q=None, s=None, dev_status=None, stream=None, mode=Q8_QU
         q = _alloc(stream, lambda: torch.empty((rows, K), dtype=torch.int8, device=w.device))
     if s is None:
         s = _alloc(stream, lambda: torch.empty((rows, max(K // 32, 0)), dtype=torch.float16, device=w.device))
-    st = lib().q8_quantize_rows_ex(_p(w), rows, K, _p(q), _p(s), int(mode), _p(dev_status), _stream(stream))
+    st = lib().q8_quantize_rows_ex(_p(w), rows, K, _p(q), _p(s), int(mode), _status(dev_status), _stream(stream))
     _check(st, "q8_quantize_rows")
     return q, s
 
@@ -269,14 +290,18 @@ def _desc(q, s, x, y):
 
 def q8_gemv(q, s, x, y=None, ws=None, dev_status=None, stream=None):
     """y[N] = dequant(q, s) @ x[K] (fp32)."""
+    _cuda(q, "q", (torch.int8,), 2)
+    _cuda(s, "s", _B16)
+    _cuda(x, "x", _B16)
     N, K = q.shape
     if y is None:
         y = _alloc(stream, lambda: torch.empty(N, dtype=torch.float32, device=q.device))
+    else:
+        _cuda(y, "y", (torch.float32,))
     need = q8_workspace_size(N, K, 1)
     if ws is None and need:
         ws = _alloc(stream, lambda: workspace(need, q.device))
-    st = lib().q8_gemv(_p(q), _p(s), N, K, _p(x), _p(y), _p(ws), 0 if ws is None else ws.numel(),
-                       _p(dev_status), _stream(stream))
+    st = lib().q8_gemv(_p(q), _p(s), N, K, _p(x), _p(y), *_work(ws), _status(dev_status), _stream(stream))
     _check(st, "q8_gemv")
     return y
 
@@ -291,8 +316,7 @@ def q8_gemm_skinny(q, s, x, y=None, ws=None, dev_status=None, stream=None):
     need = q8_workspace_size(N, K, M)
     if ws is None and need:
         ws = _alloc(stream, lambda: workspace(need, q.device))
-    st = lib().q8_gemm_skinny(_p(q), _p(s), N, K, _p(x), d.ldx, M, _p(y), d.ldy, _p(ws),
-                              0 if ws is None else ws.numel(), _p(dev_status), _stream(stream))
+    st = lib().q8_gemm_skinny(_p(q), _p(s), N, K, _p(x), d.ldx, M, _p(y), d.ldy, *_work(ws), _status(dev_status), _stream(stream))
     _check(st, "q8_gemm_skinny")
     return y
 
@@ -308,7 +332,7 @@ def q8_gemm_skinny_noalloc(q, s, x, y=None, dev_status=None, stream=None):
         y = _alloc(stream, lambda: torch.empty((M, N), dtype=torch.float32, device=q.device))
     d, _ = _desc(q, s, x, y)
     st = lib().q8_gemm_skinny_noalloc(_p(q), _p(s), N, K, _p(x), d.ldx, M, _p(y), d.ldy,
-                                      _p(dev_status), _stream(stream))
+                                      _status(dev_status), _stream(stream))
     _check(st, "q8_gemm_skinny_noalloc")
     return y
 
@@ -340,13 +364,12 @@ def q8_linear_batch(mats=None, ws=None, variant=Q8_VARIANT_AUTO, dev_status=None
     need = int(lib().q8_linear_batch_workspace_size_ex(descs, len(descs), M, variant))
     if ws is None and need:
         ws = _alloc(stream, lambda: workspace(need))
-    nbytes = 0 if ws is None else ws.numel()
     if chained:
         if variant != Q8_VARIANT_AUTO:
             raise ValueError("a chained call uses the automatic variant")
-        st = lib().q8_linear_batch_chained(descs, len(descs), M, _p(ws), nbytes, _p(dev_status), _stream(stream))
+        st = lib().q8_linear_batch_chained(descs, len(descs), M, *_work(ws), _status(dev_status), _stream(stream))
     else:
-        st = lib().q8_linear_batch_ex(descs, len(descs), M, variant, _p(ws), nbytes, _p(dev_status),
+        st = lib().q8_linear_batch_ex(descs, len(descs), M, variant, *_work(ws), _status(dev_status),
                                       _stream(stream))
     _check(st, "q8_linear_batch")
 
@@ -376,8 +399,7 @@ def q8_linear_chain(steps, M, ws=None, dev_status=None, stream=None):
     need = q8_linear_chain_workspace_size(steps, M)
     if ws is None and need:
         ws = _alloc(stream, lambda: workspace(need))
-    nbytes = 0 if ws is None else ws.numel()
-    st = lib().q8_linear_chain(steps, len(steps), M, _p(ws), nbytes, _p(dev_status), _stream(stream))
+    st = lib().q8_linear_chain(steps, len(steps), M, *_work(ws), _status(dev_status), _stream(stream))
     _check(st, "q8_linear_chain")
 
 
@@ -385,16 +407,19 @@ def q8_gemm_w8a8(q, s, x, y=None, ws=None, dev_status=None, stream=None):
     """y[M, N] (fp32) = the W8A8 product of x[M, K] (bf16, rows quantized to
     Q8_0) and dequant(q, s)^T, any M (q8_gemm_w8a8)."""
     _cuda(q, "q", (torch.int8,), 2)
+    _cuda(s, "s", _B16)
     _cuda(x, "x", _B16, 2)
     N, K = q.shape
     M = x.shape[0]
     if y is None:
         y = _alloc(stream, lambda: torch.empty((M, N), dtype=torch.float32, device=q.device))
+    else:
+        _cuda(y, "y", (torch.float32,), 2)
     need = int(lib().q8_gemm_w8a8_workspace_size(N, K, M))
     if ws is None and need:
         ws = _alloc(stream, lambda: workspace(need, q.device))
-    st = lib().q8_gemm_w8a8(_p(q), _p(s), N, K, _p(x), x.stride(0), M, _p(y), y.stride(0), _p(ws),
-                            0 if ws is None else ws.numel(), _p(dev_status), _stream(stream))
+    st = lib().q8_gemm_w8a8(_p(q), _p(s), N, K, _p(x), x.stride(0), M, _p(y), y.stride(0), *_work(ws),
+                            _status(dev_status), _stream(stream))
     _check(st, "q8_gemm_w8a8")
     return y
 
@@ -404,13 +429,16 @@ def q8_gemm(q, s, x, y=None, dev_status=None, stream=None, tile=0, splits=0):
     `tile` is one of the Q8_GEMM_TILE_* shapes and `splits` the number of
     CTAs sharing a tile's K range (0: automatic for either)."""
     _cuda(q, "q", (torch.int8,), 2)
+    _cuda(s, "s", _B16)
     _cuda(x, "x", _B16, 2)
     N, K = q.shape
     M = x.shape[0]
     if y is None:
         y = _alloc(stream, lambda: torch.empty((M, N), dtype=torch.bfloat16, device=q.device))
+    else:
+        _cuda(y, "y", _B16, 2)
     st = lib().q8_gemm_ex(_p(q), _p(s), N, K, _p(x), x.stride(0), M, _p(y), y.stride(0), int(tile), int(splits),
-                          _p(dev_status), _stream(stream))
+                          _status(dev_status), _stream(stream))
     _check(st, "q8_gemm")
     return y
 
@@ -499,7 +527,7 @@ def q8_kv_append(cache, k, v, slots, dev_status=None, stream=None):
     n, t = _slots(slots), k.dtype
     ldk, ldv = _kv_rows(cache, k, "k", n, t), _kv_rows(cache, v, "v", n, t)
     st = lib().q8_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[t], slots.data_ptr(), n,
-                            None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+                            _status(dev_status), _stream(stream))
     if st:
         _check(st, "q8_kv_append")
 
@@ -524,7 +552,7 @@ def q8_kv_read(cache, slots, k=None, v=None, dtype=torch.float32, dev_status=Non
         v, ldv = torch.empty((n, h, d), dtype=dtype, device=cache.device) if stream is None else _new(
             stream, lambda: torch.empty((n, h, d), dtype=dtype, device=cache.device)), row
     st = lib().q8_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[dtype],
-                          None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+                          _status(dev_status), _stream(stream))
     if st:
         _check(st, "q8_kv_read")
     return k, v
@@ -570,8 +598,7 @@ def q8_attn_decode(q, cache, table, lens, scale=None, softcap=0.0, window=0, out
     st = lib().q8_attn_decode(cache._ref, q.data_ptr(), sq[0] if B > 1 else H * D, H, table.data_ptr(), width, lens.data_ptr(), B,
                               D ** -0.5 if scale is None else scale, softcap, window if window < 2 ** 31 else 2 ** 31 - 1,
                               out.data_ptr(), lse.data_ptr(),
-                              *((None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())),
-                              None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+                              *_work(ws), _status(dev_status), _stream(stream))
     if st:
         _check(st, "q8_attn_decode")
     return out, lse
@@ -629,8 +656,7 @@ def q8_moe(x, logits, q13, s13, q2, s2, top_k, renorm=True, y=None, ids=None, we
     one = T <= 1
     st = lib().q8_moe(x.data_ptr(), H if one else sx[0], logits.data_ptr(), E if one else sl[0], T, E, top_k, 1 if renorm else 0,
                       q13.data_ptr(), s13.data_ptr(), q2.data_ptr(), s2.data_ptr(), H, F, y.data_ptr(), ldy, ids.data_ptr(),
-                      weights.data_ptr(), *((None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())),
-                      None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+                      weights.data_ptr(), *_work(ws), _status(dev_status), _stream(stream))
     if st:
         _check(st, "q8_moe")
     return y, ids, weights
@@ -671,7 +697,7 @@ def q8_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
                          _per_row(temperature, "temperature", n, _F32), _per_row(top_k, "top_k", n, _I32),
                          _per_row(top_p, "top_p", n, _F32), _per_row(min_p, "min_p", n, _F32), _per_row(u, "u", n, _F32),
                          _per_row(token, "token", n, _I32), _per_row(logprob, "logprob", n, _F32), _per_row(kept, "kept", n, _I32),
-                         None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+                         _status(dev_status), _stream(stream))
     if st:
         _check(st, "q8_sample")
     return token, logprob, kept
