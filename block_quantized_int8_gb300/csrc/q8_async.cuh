@@ -1,5 +1,5 @@
-// q8_async.cuh -- 16-byte asynchronous copies into shared memory and the
-// shared-memory reads of the decode-step kernels.
+// q8_async.cuh -- 16-byte asynchronous copies into shared memory, the
+// shared-memory accesses and the warp MMA of the decode-step kernels.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -39,6 +39,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// D = A * B, binary16 operands.
+__device__ __forceinline__ void mma_f16_16816_new(float &d0, float &d1, float &d2, float &d3, uint32_t a0, uint32_t a1,
+                                                  uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d0), "=f"(d1), "=f"(d2), "=f"(d3)
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 }  // namespace q8
