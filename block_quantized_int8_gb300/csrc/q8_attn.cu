@@ -13,7 +13,7 @@
 //
 // Scores: keys' codes are exact in binary16, and each query head is scaled by
 // a power of two so that its largest value lies in [2^14, 2^15): the bf16
-// query is then exact in binary16 down to 2^-31 of that value.  A warp MMA
+// query is then exact in binary16 down to 2^-31 of that value, and off by at most 2^-39 of it below.  A warp MMA
 // (m16n8k16) multiplies 16 tokens x 32 codes by 8 query heads; the block's
 // scale multiplies its fp32 result, as in the matmuls.
 // Weighted sum: O^T = V^T P, 16 dimensions x 16 tokens by 8 heads, sums in fp32.
@@ -26,11 +26,11 @@
 // of their own, with s 2^-9 and O 2^-9, both exact.
 //
 // Bound: bytes of the cache, 2.125 per dimension and token, each read once
-// for up to 16 query heads; beyond 8 query heads to a key head by the
-// instructions around the MMAs.  Measured: 262,144 tokens of 8 key heads (128
-// dimensions, 64 query heads) 96 us, 5.9 TB/s; 48 sequences of 0 to 6000 tokens,
-// 32 / 8 heads, 64 us, 5.4 TB/s; the loads alone take 93 and 61.  One sequence of
-// 200 tokens: 7.5 us, the list, one tile's latency and the join.
+// for up to 16 query heads; beyond 8 query heads to a key head by latency: 2 CTAs an
+// SM find room in shared memory, whose 8 warps issue in 42 % of the slots.  Measured: 262,144
+// tokens of 8 key heads (128 dimensions, 64 query heads) 96.5 us, 5.9 TB/s; 48 sequences of 0 to
+// 6000 tokens, 32 / 8 heads, 64.9 us, 5.35 TB/s; the loads alone take 93 and 61.  One sequence of
+// 200 tokens: 7.8 us, the list, one tile's latency and the join.
 //
 // Split: every warp is its own pipeline over 16-token tiles (a tile lies in
 // one page, so its codes and scales are four contiguous runs), filled by

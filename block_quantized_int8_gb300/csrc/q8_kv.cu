@@ -11,7 +11,7 @@
 // 2) bytes in and 1.0625 out for the write, the reverse for the read.  A lane
 // holds 16 bytes of a row (4 fp32 or 8 bf16 values), so a warp's accesses to
 // the rows are 512 contiguous bytes; 8 or 4 lanes own a block.  Each thread takes the same
-// place of the keys and of the values and is done (a grid of resident CTAs that loop was slower at
+// place of the keys and of the values (the write once it knows its slot) and is done (a grid of resident CTAs that loop was slower at
 // every size).  Where there are more such units than run at once, a thread reads two (8192 tokens x 1024
 // values in fp32: 16.7 us, 5.1 TB/s, with one 18.7; 1024 tokens 3.3 and 3.1; one token 1.9 and 1.7).  Writing
 // two was slower at every size (8192 tokens 13.1 us and 13.0, 3.9 TB/s, from bf16; one token 2.7 and 2.1).

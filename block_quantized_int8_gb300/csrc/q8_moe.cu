@@ -35,7 +35,8 @@
 // gate/up: a task is 8 hidden units of one expert: MMA rows 0..7 are
 // their gate rows, 8..15 their up rows, so a thread holds both factors of its
 // unit and SwiGLU needs no exchange.  x (bf16) is scaled by a power of two per
-// token to a largest value in [2^14, 2^15): exact in binary16 down to 2^-39 of it.
+// token to a largest value in [2^14, 2^15): exact in binary16 down to 2^-31 of it, and off by at
+// most 2^-39 of it below.
 // Hidden units go to the workspace in fp32.
 // down: a task is 16 output rows of one expert over a segment of its hidden
 // units.  The hidden units, scaled likewise per token and segment,

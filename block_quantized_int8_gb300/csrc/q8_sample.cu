@@ -45,8 +45,8 @@
 // latency for few rows (passes over shared memory with cluster barriers, about
 // 1000 cycles each, between them), by the passes' instructions for many.
 // Measured: one row of 262,144 words 12 us with top-k 50, 16 without a filter, 43
-// with top-p 0.95 alone (12,566 words kept); 64 rows of 131,071 words 30, 45 and 93 us,
-// 48 with mixed knobs.  A pass that weighs every word takes 70 instructions a word, the
+// with top-p 0.95 alone (13,823 words kept); 64 rows of 131,071 words 30, 45 and 113 us (9,032
+// kept), 52 with mixed knobs.  A pass that weighs every word takes 70 instructions a word, the
 // histogram of masses twice as many.
 #include <cooperative_groups.h>
 

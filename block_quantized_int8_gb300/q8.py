@@ -523,7 +523,7 @@ def _slots(slots):
 
 def q8_kv_append(cache, k, v, slots, dev_status=None, stream=None):
     """Quantize the rows k, v ([T, kv_heads, head_dim] or [T, kv_heads * head_dim], fp32 or
-    bf16) into the cache's slots (int64 [T]; negative: skipped)."""
+    bf16) into the cache's slots (int64 [T], each at most once; negative: skipped)."""
     n, t = _slots(slots), k.dtype
     ldk, ldv = _kv_rows(cache, k, "k", n, t), _kv_rows(cache, v, "v", n, t)
     st = lib().q8_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[t], slots.data_ptr(), n,

@@ -488,8 +488,8 @@ typedef struct q8_kv_cache {
  *           (bf16), so a row may be a part of a wider matmul's output.
  *   slots : int64 [T] (8-byte aligned).  A negative slot skips its token
  *           (padding); one past the cache is skipped and sets
- *           Q8_DEV_BAD_INDEX.  Slots that occur twice get one of the rows,
- *           undefined which.
+ *           Q8_DEV_BAD_INDEX.  What a slot that occurs twice holds afterwards
+ *           is undefined: codes and scales may be of different rows.
  * Codes and scales are those of q8_quantize_rows (Q8_QUANT_EXACT) on the
  * values, bit for bit, with the same flags.  T == 0 is a no-op.
  */
