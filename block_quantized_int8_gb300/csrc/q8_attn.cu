@@ -3,13 +3,13 @@
 //
 // Mathematics.  With s_t = scale * q . k_t and any m, out = (sum_t 2^(s'_t - m)
 // v_t) / (sum_t 2^(s'_t - m)), s' = s log2(e).  A warp walks tokens keeping
-// (m, l, O) = (reference maximum, sum, weighted sum); two such triples join
+// (m, l, O) = (reference, sum, weighted sum); two such triples join
 // into (max m, l1 2^(m1 - m) + l2 2^(m2 - m), ...), which is how the warps of
 // a CTA and the CTAs of a sequence are put together, in a fixed order.  The
-// reference is moved only when a score passes it by 4 (a vote, no shuffles
-// otherwise): any m gives the same quotient.  A warp weighs by 2^(s' - m + 11),
-// so that weights, below 2^15, use binary16's range downwards; the factor 2^11 of
-// l and O goes out in the quotient.
+// reference is set 11 below the largest score, so that weights use binary16's range
+// downwards, and is moved only when a score passes it by 15 (a vote, no shuffles
+// otherwise): any m gives the same quotient.  (From 2^23 on, where scores are 1 apart
+// and more, it is the largest score itself: rounded, 15 could become 16.)
 //
 // Scores: keys' codes are exact in binary16, and each query head is scaled by
 // a power of two so that its largest value lies in [2^14, 2^15): the bf16
@@ -30,7 +30,7 @@
 // SM find room in shared memory, whose 8 warps issue in 42 % of the slots.  Measured: 262,144
 // tokens of 8 key heads (128 dimensions, 64 query heads) 96.5 us, 5.9 TB/s; 48 sequences of 0 to
 // 6000 tokens, 32 / 8 heads, 64.9 us, 5.35 TB/s; the loads alone take 93 and 61.  One sequence of
-// 200 tokens: 7.8 us, the list, one tile's latency and the join.
+// 200 tokens: 7.9 us, the list, one tile's latency and the join.
 //
 // Split: every warp is its own pipeline over 16-token tiles (a tile lies in
 // one page, so its codes and scales are four contiguous runs), filled by
@@ -62,8 +62,9 @@ constexpr int kMaxGrid = 1024;    // CTAs a launch may have (sizes the workspace
 constexpr size_t kTicketBytes = Q8_ATTN_ZEROED_BYTES;
 static_assert(kTicketBytes == size_t{4} * kMaxGrid * 4, "the tickets");
 constexpr int kMinUnits = 2;      // units a CTA takes at least; 3 and 4 gain in one short case what they lose in another
-constexpr float kGrow = 4.0f;     // log2 growth of a score that moves the reference
-constexpr float kLift = 11.0f;    // log2 of a weight at the reference: 2^(kLift + kGrow) is within binary16
+constexpr float kLift = 11.0f;    // log2 of the largest weight when the reference is set
+constexpr float kTop = 15.0f;     // and of the largest that leaves it: 2^15 (2^15.5, rounded) is within binary16
+constexpr float kLiftEnd = 0x1p23f;  // magnitude of a score from which on there is neither
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
             fac[n][1] = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
         }
         float m[NT][2], l[NT][2], o[NT][D / 16][4];
-        float ref[NT][2], top[NT][2];  // m - kLift, or 0 where nothing was seen; the score that moves it
+        float ref[NT][2], top[NT][2];  // m, or 0 where nothing was seen; the score that moves it
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n][0] = m[n][1] = top[n][0] = top[n][1] = -INFINITY;
@@ -516,11 +517,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
                             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
                             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-                            y = fmaxf(y, m[n][j]);
+                            y = fmaxf(y - (fabsf(y) < kLiftEnd ? kLift : 0.f), m[n][j]);
                             const float f = m[n][j] == -INFINITY ? 0.f : ex2(m[n][j] - y);
                             m[n][j] = y;
-                            ref[n][j] = y == -INFINITY ? 0.f : y - kLift;
-                            top[n][j] = y + kGrow;
+                            ref[n][j] = y == -INFINITY ? 0.f : y;
+                            top[n][j] = y + (fabsf(y) < kLiftEnd ? kTop : 0.f);
                             l[n][j] *= f;
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) o[n][i][j] *= f, o[n][i][2 + j] *= f;
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn_kernel(const
             const int64_t row = static_cast<int64_t>(wk.b) * p.q_heads + head0 + h;
             *reinterpret_cast<uint2 *>(p.out + row * D + d) =
                 make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-            if (p.lse && d == 0) p.lse[row] = ll == 0.f ? -INFINITY : fmaf(mm, 0.69314718055994531f, logf(ll * 0x1p-11f));
+            if (p.lse && d == 0) p.lse[row] = ll == 0.f ? -INFINITY : fmaf(mm + kLift, 0.69314718055994531f, logf(ll * 0x1p-11f));
         };
         const int quads = nheads * (D / 4);
         auto own = [&](int h, int d) { return *reinterpret_cast<const float4 *>(s_o + h * C::kOPitch + d); };

@@ -91,3 +91,49 @@ def test_weights_far_below_the_largest(D, heads, log2):
     vs = np.full((32, 1, 16, D // 32), 0.01)
     table = list(range(32)) + ([-1] * (10016 * 64 // 16) if heads > 8 else [])
     check(*planes_to_cache(kq, ks, vq, vs), q.repeat(1, heads, 1), table, n)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("log2", [20, 23, 24, 24.7, 25, 25.6, 26, 26.4, 26.9, 27, 27.3, 27.8, 28, 28.5, 29, 31, 60])
+def test_scores_whose_neighbours_are_further_apart_than_the_weights_range(D, log2):
+    # equal scores of 2^log2 (and, in some tiles, others that are lower by 2^(log2 - 10) and do not count):
+    # the mean of the values that do
+    from block_quantized_int8_gb300 import q8
+    r = np.random.default_rng(D)
+    n, pages = 700, 48
+    kq = np.full((pages, 1, 16, D), 64, dtype=np.int8)
+    ks = np.full((pages, 1, 16, D // 32), 0.5)
+    low = np.zeros(pages * 16, dtype=bool)
+    low[100:260] = True
+    low[400::3] = True
+    ks[low.reshape(pages, 1, 16)] *= 1 - 2.0 ** -10
+    vq = r.integers(-127, 128, (pages, 1, 16, D), dtype=np.int8)
+    cache, kv, vv = planes_to_cache(kq, ks, vq, np.full((pages, 1, 16, D // 32), 0.01))
+    q = torch.ones((1, 4, D), dtype=torch.bfloat16, device="cuda")
+    scale = float(np.float32(2.0 ** log2 * np.log(2.0) / (32.0 * D)))
+    out, lse = q8.q8_attn_decode(q, cache, torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages),
+                                 torch.tensor([n], dtype=torch.int32, device="cuda"), scale=scale)
+    v = vv[:, 0].reshape(-1, D)[:n][~low[:n]]
+    mean, size = v.mean(0), np.abs(v).mean(0)
+    lo, hi = (torch.from_numpy(x).to(torch.bfloat16).double().numpy() for x in (mean - 2.0 ** -10 * size, mean + 2.0 ** -10 * size))
+    got = attn.f64(out)[0]
+    assert np.all((got >= lo) & (got <= hi)), (got[0][:4], mean[:4])
+    want = scale * 32.0 * D + np.log(v.shape[0])
+    assert np.all(np.abs(attn.f64(lse) - want) <= 2.0 ** -21 * want)
+
+
+@pytest.mark.parametrize("base", [0.0, 1e-3, 40.0, 3e4, 2.0 ** 22])
+def test_references_that_move_by_less_than_their_own_rounding(base):
+    # scores base + 0 .. 20 in any order, large ones late in some warps and early in others
+    r = np.random.default_rng(1)
+    D, pages = 64, 40
+    kq = np.zeros((pages, 1, 16, D), dtype=np.int8)
+    kq[..., 0] = 1
+    kq[..., 32] = r.integers(0, 21, (pages, 1, 16))
+    ks = np.ones((pages, 1, 16, 2))
+    vq = r.integers(64, 128, (pages, 1, 16, D), dtype=np.int8)
+    cache, kv, vv = planes_to_cache(kq, ks, vq, np.full((pages, 1, 16, 2), 0.01))
+    q = torch.zeros((1, 2, D), device="cuda")
+    q[..., 0], q[..., 32] = base, 1.0
+    q = q.to(torch.bfloat16)
+    check(cache, kv, vv, q, r.permutation(pages).tolist(), 633)
