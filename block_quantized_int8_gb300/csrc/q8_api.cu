@@ -533,4 +533,143 @@ q8_status q8_sample(const void *logits, int32_t dtype, int64_t ld, int32_t rows,
     return launch_sample(a, dev_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// ---- prompt step ---------------------------------------------------------------
+static bool dtype_ok(int32_t d) { return d == Q8_DTYPE_F32 || d == Q8_DTYPE_BF16; }
+// elements that a row's stride is a multiple of
+static int64_t row_step(int32_t d) { return d == Q8_DTYPE_F32 ? 4 : 8; }
+
+q8_status q8_rms_norm(const void *x, int64_t ldx, int32_t x_dtype, const void *residual, int64_t ldr, int32_t residual_dtype,
+                      void *residual_out, int64_t ldo, const float *weight, float offset, float eps, int64_t T, int64_t W,
+                      uint16_t *y, int64_t ldy, int8_t *q, uint16_t *s, uint32_t *dev_status, q8_stream_t stream) {
+    if (!dtype_ok(x_dtype) || !dtype_ok(residual_dtype)) return Q8_ERR_ARG;
+    if (T < 0 || T > INT32_MAX || W < 32 || W % 32 != 0 || W > Q8_NORM_MAX_WIDTH) return Q8_ERR_SHAPE;
+    if (!(eps >= 0.0f) || eps - eps != 0.0f || offset - offset != 0.0f) return Q8_ERR_ARG;
+    if ((q == nullptr) != (s == nullptr) || (residual_out && !residual)) return Q8_ERR_ARG;
+    if (ldx < W || (residual && ldr < W) || (residual_out && ldo < W) || (y && ldy < W)) return Q8_ERR_SHAPE;
+    if (T == 0) return Q8_OK;
+    if (!x || (!y && !q && !residual_out)) return Q8_ERR_ARG;
+    const int64_t xs = row_step(x_dtype), rs = row_step(residual_dtype);
+    if (!aligned(x, 16) || ldx % xs != 0 || !aligned(residual, 16) || (residual && ldr % rs != 0) || !aligned(residual_out, 16) ||
+        (residual_out && ldo % rs != 0) || !aligned(weight, 16) || !aligned(y, 16) || (y && ldy % 8 != 0) || !aligned(q, 16) ||
+        !aligned(s, 16) || !aligned(dev_status, 4))
+        return Q8_ERR_ALIGN;
+    const DeviceInfo *di;
+    const q8_status st = check_arch(&di);
+    if (st != Q8_OK) return st;
+    const NormArgs a = {x, residual, residual_out, weight, y, q, s, ldx, ldr, ldo, ldy, T, static_cast<int32_t>(W), x_dtype,
+                        residual_dtype, offset, eps};
+    return launch_norm(a, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q8_status q8_rope_turns(const double *inv_freq, int32_t n, uint64_t *turns) {
+    if (n < 0) return Q8_ERR_SHAPE;
+    if (n > 0 && (!inv_freq || !turns)) return Q8_ERR_ARG;
+    for (int32_t i = 0; i < n; ++i)
+        if (!(inv_freq[i] >= -Q8_ROPE_MAX_FREQ && inv_freq[i] <= Q8_ROPE_MAX_FREQ)) return Q8_ERR_ARG;
+    rope_turns(inv_freq, n, turns);
+    return Q8_OK;
+}
+
+static q8_status check_rope(int32_t dtype, int32_t heads, int32_t head_dim, int32_t rot, int32_t layout, float factor,
+                            const uint64_t *turns, const int32_t *positions, int64_t T, const uint32_t *dev_status) {
+    if (!dtype_ok(dtype) || (layout != Q8_ROPE_HALF && layout != Q8_ROPE_INTERLEAVED) || factor - factor != 0.0f) return Q8_ERR_ARG;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return Q8_ERR_SHAPE;
+    if (T < 0 || T > INT32_MAX || heads < 1 || heads > 65536 || rot < 16 || rot % 16 != 0 || rot > head_dim) return Q8_ERR_SHAPE;
+    if (T > 0 && (!turns || !positions)) return Q8_ERR_ARG;
+    if (!aligned(turns, 8) || !aligned(positions, 4) || !aligned(dev_status, 4)) return Q8_ERR_ALIGN;
+    return Q8_OK;
+}
+
+q8_status q8_rope(const void *x, int64_t ldx, int32_t dtype, uint16_t *y, int64_t ldy, int32_t heads, int32_t head_dim, int32_t rot,
+                  int32_t layout, float factor, const uint64_t *turns, const int32_t *positions, int64_t T, q8_stream_t stream) {
+    q8_status st = check_rope(dtype, heads, head_dim, rot, layout, factor, turns, positions, T, nullptr);
+    if (st != Q8_OK) return st;
+    const int64_t row = static_cast<int64_t>(heads) * head_dim;
+    if (ldx < row || ldy < row) return Q8_ERR_SHAPE;
+    if (T == 0) return Q8_OK;
+    if (!x || !y) return Q8_ERR_ARG;
+    if (!aligned(x, 16) || ldx % row_step(dtype) != 0 || !aligned(y, 16) || ldy % 8 != 0) return Q8_ERR_ALIGN;
+    const DeviceInfo *di;
+    st = check_arch(&di);
+    if (st != Q8_OK) return st;
+    RopeArgs a = {};
+    a.x = x, a.y = y, a.turns = turns, a.positions = positions, a.ldx = ldx, a.ldy = ldy, a.T = T;
+    a.heads = heads, a.head_dim = head_dim, a.rot = rot, a.layout = layout, a.dtype = dtype, a.factor = factor;
+    return launch_rope(a, nullptr, nullptr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q8_status q8_rope_append(const q8_kv_cache *cache, const void *q, int64_t ldq, int32_t q_heads, const void *k, const void *v,
+                         int64_t ldk, int64_t ldv, int32_t dtype, int32_t rot, int32_t layout, float factor, const uint64_t *turns,
+                         const int32_t *positions, const int64_t *slots, int64_t T, uint16_t *y, int64_t ldy, uint32_t *dev_status,
+                         q8_stream_t stream) {
+    q8_status st = check_kv_rows(cache, k, v, ldk, ldv, dtype, slots, T, dev_status);
+    if (st != Q8_OK) return st;
+    st = check_rope(dtype, q_heads, cache->head_dim, rot, layout, factor, turns, positions, T, dev_status);
+    if (st != Q8_OK) return st;
+    const int64_t row = static_cast<int64_t>(q_heads) * cache->head_dim;
+    if (ldq < row || ldy < row) return Q8_ERR_SHAPE;
+    if (T == 0) return Q8_OK;
+    if (!q || !y) return Q8_ERR_ARG;
+    if (!aligned(q, 16) || ldq % row_step(dtype) != 0 || !aligned(y, 16) || ldy % 8 != 0) return Q8_ERR_ALIGN;
+    const DeviceInfo *di;
+    st = check_arch(&di);
+    if (st != Q8_OK) return st;
+    const RopeArgs a = {q, k, v, y, turns, positions, slots, ldq, ldk, ldv, ldy, T, q_heads, cache->head_dim, rot, layout, dtype, factor};
+    return launch_rope(a, cache, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q8_status q8_kv_plan(int32_t *table, int32_t table_width, int32_t pages, int32_t page_size, const int32_t *lens,
+                     const int32_t *new_tokens, int32_t batch, const int32_t *free_pages, int32_t free_capacity,
+                     const int32_t *free_count, int32_t *free_left, int64_t T, int32_t *starts, int64_t *slots, int32_t *positions,
+                     int32_t *lens_out, uint32_t *dev_status, q8_stream_t stream) {
+    if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0 || pages < 1) return Q8_ERR_SHAPE;
+    if (table_width < 0 || static_cast<int64_t>(table_width) * page_size > INT32_MAX - 4096) return Q8_ERR_SHAPE;
+    if (batch < 0 || batch > Q8_PLAN_MAX_BATCH || T < 0 || T > INT32_MAX || free_capacity < 0) return Q8_ERR_SHAPE;
+    if (!starts || (batch > 0 && (!lens || !new_tokens || !lens_out || (table_width > 0 && !table)))) return Q8_ERR_ARG;
+    if ((T > 0 && (!slots || !positions)) || (free_pages && (!free_count || !free_left))) return Q8_ERR_ARG;
+    if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(new_tokens, 4) || !aligned(free_pages, 4) || !aligned(free_count, 4) ||
+        !aligned(free_left, 4) || !aligned(starts, 4) || !aligned(slots, 8) || !aligned(positions, 4) || !aligned(lens_out, 4) ||
+        !aligned(dev_status, 4))
+        return Q8_ERR_ALIGN;
+    const DeviceInfo *di;
+    const q8_status st = check_arch(&di);
+    if (st != Q8_OK) return st;
+    const PlanArgs a = {table, lens, new_tokens, free_pages, free_count, starts, positions, lens_out, free_left, slots, T, batch,
+                        table_width, page_size, pages, free_capacity};
+    return launch_plan(a, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t q8_attn_chunk_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+    if (check_heads(1, q_heads, kv_heads) != Q8_OK) return 0;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+    return chunk_workspace(q_heads, kv_heads, head_dim);
+}
+
+q8_status q8_attn_chunk(const q8_kv_cache *cache, const uint16_t *q, int64_t ldq, int32_t q_heads, int64_t T, const int32_t *table,
+                        int32_t table_width, const int32_t *lens, const int32_t *starts, int32_t batch, float scale, float softcap,
+                        int32_t window, uint16_t *out, float *lse, void *ws, size_t ws_bytes, uint32_t *dev_status,
+                        q8_stream_t stream) {
+    q8_status st = check_cache(cache);
+    if (st != Q8_OK) return st;
+    st = check_heads(batch, q_heads, cache->kv_heads);
+    if (st != Q8_OK) return st;
+    if (table_width < 0 || static_cast<int64_t>(table_width) * cache->page_size > INT32_MAX - 4096) return Q8_ERR_SHAPE;
+    if (T < 0 || T * (q_heads / cache->kv_heads) > INT32_MAX - 4096 || T > INT32_MAX) return Q8_ERR_SHAPE;
+    if (window < 0 || !(softcap >= 0.0f) || !(scale - scale == 0.0f) || softcap - softcap != 0.0f) return Q8_ERR_ARG;
+    if (ldq < static_cast<int64_t>(q_heads) * cache->head_dim) return Q8_ERR_SHAPE;
+    if (batch == 0 || T == 0) return Q8_OK;
+    if (!q || !lens || !starts || !out || (table_width > 0 && !table)) return Q8_ERR_ARG;
+    if (!aligned(q, 16) || ldq % 8 != 0 || !aligned(out, 16) || !aligned(lens, 4) || !aligned(starts, 4) || !aligned(table, 4) ||
+        !aligned(lse, 4) || !aligned(dev_status, 4))
+        return Q8_ERR_ALIGN;
+    const size_t need = chunk_workspace(q_heads, cache->kv_heads, cache->head_dim);
+    if (need > 0 && (!ws || ws_bytes < need)) return Q8_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return Q8_ERR_ALIGN;
+    const DeviceInfo *di;
+    st = check_arch(&di);
+    if (st != Q8_OK) return st;
+    const ChunkArgs a = {q, table, lens, starts, out, lse, ldq, T, q_heads, table_width, batch, window, scale, softcap};
+    return launch_chunk(*cache, a, ws, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

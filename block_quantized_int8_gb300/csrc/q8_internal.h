@@ -215,4 +215,53 @@ struct SampleArgs {
 };
 q8_status launch_sample(const SampleArgs &a, uint32_t *dev_status, cudaStream_t stream);
 
+// ---- prompt step: norm, rotary positions, pages and slots, attention of new tokens -----
+struct NormArgs {
+    const void *x, *residual;
+    void *residual_out;
+    const float *weight;
+    uint16_t *y;
+    int8_t *q;
+    uint16_t *s;
+    int64_t ldx, ldr, ldo, ldy, rows;
+    int32_t width, x_dtype, r_dtype;
+    float offset, eps;
+};
+q8_status launch_norm(const NormArgs &a, uint32_t *dev_status, cudaStream_t stream);
+
+struct RopeArgs {
+    const void *x, *k, *v;  // x: all heads, or the query heads where keys and values go to a cache
+    uint16_t *y;
+    const uint64_t *turns;
+    const int32_t *positions;
+    const int64_t *slots;
+    int64_t ldx, ldk, ldv, ldy, T;
+    int32_t heads, head_dim, rot, layout, dtype;
+    float factor;
+};
+q8_status launch_rope(const RopeArgs &a, const q8_kv_cache *c, uint32_t *dev_status, cudaStream_t stream);
+void rope_turns(const double *inv_freq, int32_t n, uint64_t *turns);  // host
+
+struct PlanArgs {
+    int32_t *table;
+    const int32_t *lens, *new_tokens, *free_pages, *free_count;
+    int32_t *starts, *positions, *lens_out, *free_left;
+    int64_t *slots;
+    int64_t T;
+    int32_t batch, table_width, page_size, pages, free_capacity;
+};
+q8_status launch_plan(const PlanArgs &a, uint32_t *dev_status, cudaStream_t stream);
+
+struct ChunkArgs {
+    const uint16_t *q;
+    const int32_t *table, *lens, *starts;
+    uint16_t *out;
+    float *lse;
+    int64_t ldq, T;
+    int32_t q_heads, table_width, batch, window;
+    float scale, softcap;
+};
+size_t chunk_workspace(int q_heads, int kv_heads, int head_dim);
+q8_status launch_chunk(const q8_kv_cache &c, const ChunkArgs &a, void *ws, uint32_t *dev_status, cudaStream_t stream);
+
 }  // namespace q8

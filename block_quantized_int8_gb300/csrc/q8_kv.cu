@@ -108,39 +108,6 @@ struct Unit<__nv_bfloat16> {
     }
 };
 
-// The codes of W values by the scale sf, four to a word: |x| / sf rounded half away from zero.
-// t = x * (1 / sf) is within 2^-16 of the quotient (at most 127.5), and adding 1.5 2^23 leaves its
-// nearest integer in the low byte.
-// bf16: x has 8 significant bits and sf 11, so a quotient that is no tie is at least 2^-12 from one
-// (both are multiples of a power of two that small against sf); 2^-14 away from zero puts ties on the
-// far side and nothing else across.  fp32: where t is within 2^-12 of a tie, the exact rule decides
-// (one value in 2048).
-template <typename T, int W>
-__device__ __forceinline__ void codes_of(const float (&x)[W], float sf, uint32_t (&packed)[W / 4]) {
-    constexpr float kMagic = 12582912.0f;
-    const float rcp = __frcp_rn(sf);
-    uint32_t c[W];
-    bool close = false;
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-        if constexpr (sizeof(T) == 2) {
-            const float away = __uint_as_float(0x38800000u | (__float_as_uint(x[j]) & 0x80000000u));  // +- 2^-14
-            c[j] = __float_as_uint(fminf(fmaxf(fmaf(x[j], rcp, away), -127.0f), 127.0f) + kMagic);
-        } else {
-            const float t = fminf(fmaxf(x[j] * rcp, -127.0f), 127.0f), z = t + kMagic;
-            c[j] = __float_as_uint(z);
-            close = close || fabsf(t - (z - kMagic)) > 0.5f - 0x1p-12f;
-        }
-    }
-    if (sizeof(T) == 4 && close) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) c[j] = static_cast<uint32_t>(code_of(x[j], sf, rcp));
-    }
-#pragma unroll
-    for (int j = 0; j < W; j += 4)
-        packed[j / 4] = __byte_perm(__byte_perm(c[j], c[j + 1], 0x0040), __byte_perm(c[j + 2], c[j + 3], 0x0040), 0x5410);
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvParams p) {
     constexpr int W = Unit<T>::W, kLanes = 32 / W;  // lanes of a block
@@ -162,9 +129,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
         uint32_t top = Unit<T>::largest(raw[i]);
 #pragma unroll
         for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const __half h = __float2half_rn(__fdiv_rn(__uint_as_float(top), 127.0f));
-        const float sf = __half2float(h);
-        const uint32_t flags = top >= 0x7F800000u ? Q8_DEV_NONFINITE : (isinf(sf) ? Q8_DEV_SCALE_OVF : 0u);
+        __half h;
+        float sf;
+        const uint32_t flags = block_scale(top, h, sf);
         uint32_t packed[W / 4] = {};
         if (!flags && sf != 0.0f) codes_of<T, W>(x, sf, packed);
         if (live) {

@@ -15,6 +15,7 @@ Tensor conventions (raw bits are accepted in any 16-bit dtype):
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -28,14 +29,19 @@ Q8_DEV_NONFINITE = 0x1
 Q8_DEV_SCALE_OVF = 0x2
 Q8_DEV_TIMEOUT = 0x4
 Q8_DEV_BAD_INDEX = 0x8
+Q8_DEV_NO_PAGE = 0x10
 Q8_DTYPE_F32, Q8_DTYPE_BF16 = 0, 1
 Q8_SKINNY_MAX_M = 32
 Q8_MAX_BATCH = 64
 Q8_VARIANT_AUTO, Q8_VARIANT_SIMT, Q8_VARIANT_MMA, Q8_VARIANT_BATCH_INVARIANT, Q8_VARIANT_W8A8 = 0, 1, 2, 3, 4
 Q8_GEMM_TILE_AUTO, Q8_GEMM_TILE_256x128, Q8_GEMM_TILE_128x128, Q8_GEMM_TILE_64x128 = 0, 1, 2, 3
 Q8_GEMM_MAX_SPLITS = 8
-Q8_ATTN_ZEROED_BYTES, Q8_MOE_ZEROED_BYTES = 16384, 256
+Q8_ATTN_ZEROED_BYTES, Q8_MOE_ZEROED_BYTES, Q8_CHUNK_ZEROED_BYTES = 16384, 256, 4096
 Q8_QUANT_EXACT, Q8_QUANT_FL32 = 0, 1
+Q8_NORM_MAX_WIDTH = 32768
+Q8_ROPE_HALF, Q8_ROPE_INTERLEAVED = 0, 1
+Q8_ROPE_MAX_FREQ = 65536.0
+Q8_PLAN_MAX_BATCH = 1 << 20
 
 EXPORTS = ("q8_quantize_rows", "q8_gemv", "q8_gemm_skinny", "q8_linear_batch", "q8_linear_batch_ex",
            "q8_linear_batch_chained", "q8_workspace_size", "q8_linear_batch_workspace_size", "q8_linear_batch_workspace_size_ex", "q8_gemm", "q8_status_str",
@@ -44,7 +50,8 @@ EXPORTS = ("q8_quantize_rows", "q8_gemv", "q8_gemm_skinny", "q8_linear_batch", "
            "q8_stream_read", "q8_stream_read_out_words", "q8_linear_chain", "q8_linear_chain_workspace_size",
            "q8_gemm_w8a8", "q8_gemm_w8a8_workspace_size", "q8_kv_append", "q8_kv_read", "q8_attn_decode",
            "q8_attn_decode_workspace_size", "q8_moe", "q8_moe_workspace_size",
-           "q8_sample", "q8_workspace_zero")
+           "q8_sample", "q8_workspace_zero", "q8_rms_norm", "q8_rope_turns", "q8_rope", "q8_rope_append", "q8_kv_plan",
+           "q8_attn_chunk", "q8_attn_chunk_workspace_size")
 Q8_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -129,6 +136,15 @@ def lib():
         L.q8_moe_workspace_size.restype = SZ
         L.q8_sample.argtypes = [P, I32, I64, I32, I64, P, P, P, P, P, P, P, P, P, P]
         L.q8_workspace_zero.argtypes = [P, SZ, P]
+        F32 = ctypes.c_float
+        L.q8_rms_norm.argtypes = [P, I64, I32, P, I64, I32, P, I64, P, F32, F32, I64, I64, P, I64, P, P, P, P]
+        L.q8_rope_turns.argtypes = [P, I32, P]
+        L.q8_rope.argtypes = [P, I64, I32, P, I64, I32, I32, I32, I32, F32, P, P, I64, P]
+        L.q8_rope_append.argtypes = [P, P, I64, I32, P, P, I64, I64, I32, I32, I32, F32, P, P, P, I64, P, I64, P, P]
+        L.q8_kv_plan.argtypes = [P, I32, I32, I32, P, P, I32, P, I32, P, P, I64, P, P, P, P, P, P]
+        L.q8_attn_chunk.argtypes = [P, P, I64, I32, I64, P, I32, P, P, I32, F32, F32, I32, P, P, P, SZ, P, P]
+        L.q8_attn_chunk_workspace_size.argtypes = [I32, I32, I32]
+        L.q8_attn_chunk_workspace_size.restype = SZ
         L.q8_status_str.argtypes = [ctypes.c_int]
         L.q8_status_str.restype = ctypes.c_char_p
         L.q8_abi_version.restype = I32
@@ -136,7 +152,8 @@ def lib():
                      "q8_linear_batch_ex", "q8_linear_batch_chained", "q8_gguf_to_planar",
                      "q8_planar_to_gguf", "q8_gemm", "q8_gemm_ex", "q8_gemm_skinny_noalloc", "q8_linear_chain", "q8_gemm_w8a8",
                      "q8_kv_append", "q8_kv_read", "q8_attn_decode", "q8_moe",
-                     "q8_sample", "q8_workspace_zero"):
+                     "q8_sample", "q8_workspace_zero", "q8_rms_norm", "q8_rope_turns", "q8_rope", "q8_rope_append", "q8_kv_plan",
+                     "q8_attn_chunk"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -701,3 +718,267 @@ def q8_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     if st:
         _check(st, "q8_sample")
     return token, logprob, kept
+
+
+# ---------------------------------------------------------------------------
+# a prompt step
+# ---------------------------------------------------------------------------
+def _here(first, *others):
+    """All of a call's tensors are on one device, the current one."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError("the tensors of a call must be on one device")
+    if dev.index is not None and _get_device is not None and dev.index != _get_device():
+        raise ValueError("the tensors of a call must be on the current device")
+
+
+def _rows(t, name, n, width):
+    """The stride of n rows of `width` values (one or more inner dimensions, contiguous)."""
+    sh, sd = t.shape, t.stride()
+    want = 1
+    ok = len(sh) >= 2 and sh[0] == n
+    for i in range(len(sh) - 1, 0, -1):
+        ok = ok and (sd[i] == want or sh[i] == 1)
+        want *= sh[i]
+    if not ok or want != width:
+        raise ValueError(f"{name} must hold {n} rows of {width} values, each row contiguous")
+    return sd[0] if n > 1 else width
+
+
+def _out(stream, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if stream is None else _new(
+        stream, lambda: torch.empty(shape, dtype=dtype, device=device))
+
+
+def q8_rms_norm(x, weight=None, offset=0.0, eps=1e-6, residual=None, residual_out=None, y=None, q=None, s=None, bf16=True,
+                quantized=False, dev_status=None, stream=None):
+    """h = x + residual and its root-mean-square norm times (weight + offset): x [T, W] fp32 or
+    bf16, residual [T, W] fp32 or bf16 (updated in place, or to `residual_out`), weight fp32 [W].
+    Returns (y bf16 [T, W], q int8 [T, W], s float16 [T, W / 32]): y unless bf16=False, the
+    Q8_0 rows if `quantized` (or q and s are given), None in the place of what is not asked for."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _ROW_DTYPES and x.dim() == 2):
+        _cuda(x, "x", tuple(_ROW_DTYPES), 2)
+    T, W = x.shape
+    ldx = _rows(x, "x", T, W)
+    kind, ldr, ldo = x.dtype, W, W
+    if residual is not None:
+        kind = _cuda(residual, "residual", tuple(_ROW_DTYPES), 2).dtype
+        ldr = _rows(residual, "residual", T, W)
+        if residual_out is None:
+            residual_out = residual
+        ldo = _rows(_cuda(residual_out, "residual_out", (kind,), 2), "residual_out", T, W)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if weight is not None and (_cuda(weight, "weight", (_F32,), 1).shape[0] != W or (W > 1 and weight.stride(0) != 1)):
+        raise ValueError("weight must hold W values, contiguous")
+    ldy = W
+    if y is not None:
+        ldy = _rows(_cuda(y, "y", (_BF16,), 2), "y", T, W)
+    elif bf16:
+        y = _out(stream, (T, W), _BF16, x.device)
+    if quantized or q is not None or s is not None:
+        if q is None:
+            q = _out(stream, (T, W), _I8, x.device)
+        if s is None:
+            s = _out(stream, (T, W // 32), torch.float16, x.device)
+        if _cuda(q, "q", (_I8,), 2).shape != (T, W) or not q.is_contiguous():
+            raise ValueError("q must be contiguous, [T, W]")
+        if _cuda(s, "s", _B16, 2).shape != (T, W // 32) or not s.is_contiguous():
+            raise ValueError("s must be contiguous, [T, W / 32]")
+    _here(x, weight, residual, residual_out, y, q, s)
+    st = lib().q8_rms_norm(x.data_ptr(), ldx, _ROW_DTYPES[x.dtype], _a(residual), ldr, _ROW_DTYPES[kind], _a(residual_out), ldo,
+                           _a(weight), offset, eps, T, W, _a(y), ldy, _a(q), _a(s), _status(dev_status), _stream(stream))
+    if st:
+        _check(st, "q8_rms_norm")
+    return y, q, s
+
+
+def _a(t):
+    return None if t is None else t.data_ptr()
+
+
+def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, trained=4096, fast=32.0, slow=1.0):
+    """(radians a token for each of rot / 2 pairs, the factor on cosines and sines), in 64 bits.
+    base ** (-2 i / rot) for pair i, and for contexts `factor` times the `trained` length:
+      "linear": all frequencies divided by `factor`;
+      "ntk":    the base raised so that the slowest pair is;
+      "yarn":   pairs that turn less than `slow` times in `trained` tokens divided, those that turn
+                more than `fast` times kept, a ramp between, and 1 + 0.1 log(factor) on the result."""
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError("scaling is None, 'linear', 'ntk' or 'yarn'")
+    if rot < 4 or rot % 2 or not factor >= 1.0:
+        raise ValueError("rot is even, 4 at least, and factor 1 at least")
+    if scaling == "ntk":
+        base = base * factor ** (rot / (rot - 2))
+    f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    if scaling == "linear":
+        return [x / factor for x in f], 1.0
+    if scaling != "yarn":
+        return f, 1.0
+
+    def pair(turns):  # the (fractional) pair that turns so many times in the trained length
+        return rot * math.log(trained / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+    lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot - 1)
+    ramp = [min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(rot // 2)]
+    return [x / factor * r + x * (1.0 - r) for x, r in zip(f, ramp)], 0.1 * math.log(factor) + 1.0
+
+
+def rope_turns(inv_freq, device=None):
+    """The table of q8_rope from frequencies in radians a token (a list, or a tensor of any
+    device): int64 [pairs] on `device` (the tensor's, else the current one).  Made once."""
+    if isinstance(inv_freq, torch.Tensor):
+        device = device or (inv_freq.device if inv_freq.is_cuda else None)
+        inv_freq = inv_freq.detach().to("cpu", torch.float64)
+    f = torch.as_tensor(inv_freq, dtype=torch.float64).contiguous()
+    if f.dim() != 1:
+        raise ValueError("inv_freq has one value per pair")
+    turns = torch.empty(f.shape, dtype=_I64)
+    _check(lib().q8_rope_turns(f.data_ptr(), f.shape[0], turns.data_ptr()), "q8_rope_turns")
+    return turns.to(device or "cuda")
+
+
+def _rope_args(turns, positions, n, d):
+    if not (turns.is_cuda and positions.is_cuda and turns.dtype is _I64 and positions.dtype is _I32):
+        _cuda(turns, "turns", (_I64,))
+        _cuda(positions, "positions", (_I32,))
+    if turns.dim() != 1 or not turns.is_contiguous() or 2 * turns.shape[0] > d:
+        raise ValueError("turns holds a contiguous value per pair, of head_dim / 2 pairs at most")
+    if positions.shape != (n,) or not positions.is_contiguous():
+        raise ValueError("positions must hold one value per token, contiguous")
+    return 2 * turns.shape[0]
+
+
+def q8_rope(x, positions, turns, interleaved=False, factor=1.0, y=None, stream=None):
+    """Rotary positions of x [T, heads, head_dim] (fp32 or bf16) at positions int32 [T], with the
+    table of rope_turns: the first 2 * len(turns) dimensions of each head turn.  Returns y
+    bf16 [T, heads, head_dim] (y may be x itself)."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _ROW_DTYPES and x.dim() == 3):
+        _cuda(x, "x", tuple(_ROW_DTYPES), 3)
+    n, h, d = x.shape
+    rot = _rope_args(turns, positions, n, d)
+    ldx = _rows(x, "x", n, h * d)
+    if y is None:
+        y = _out(stream, (n, h, d), _BF16, x.device)
+    elif _cuda(y, "y", (_BF16,), 3).shape != x.shape:
+        raise ValueError("y has x's shape")
+    _here(x, positions, turns, y)
+    st = lib().q8_rope(x.data_ptr(), ldx, _ROW_DTYPES[x.dtype], y.data_ptr(), _rows(y, "y", n, h * d), h, d, rot,
+                       1 if interleaved else 0, factor, turns.data_ptr(), positions.data_ptr(), n, _stream(stream))
+    if st:
+        _check(st, "q8_rope")
+    return y
+
+
+def q8_rope_append(q, k, v, cache, positions, slots, turns, interleaved=False, factor=1.0, y=None, dev_status=None, stream=None):
+    """q8_rope of the query heads q [T, q_heads, head_dim], and of the key heads k on their way
+    into the cache's slots with the values v ([T, kv_heads, head_dim] or [T, kv_heads * head_dim]),
+    all fp32 or all bf16.  Returns the turned queries, bf16 [T, q_heads, head_dim]."""
+    n, t = _slots(slots), k.dtype
+    ldk, ldv = _kv_rows(cache, k, "k", n, t), _kv_rows(cache, v, "v", n, t)
+    _cuda(q, "q", (t,), 3)
+    h, d = q.shape[1], cache.head_dim
+    if q.shape[0] != n or q.shape[2] != d:
+        raise ValueError("q is [T, q_heads, head_dim] with a slot per token and the cache's head_dim")
+    rot = _rope_args(turns, positions, n, d)
+    ldq = _rows(q, "q", n, h * d)
+    if y is None:
+        y = _out(stream, (n, h, d), _BF16, q.device)
+    elif _cuda(y, "y", (_BF16,), 3).shape != q.shape:
+        raise ValueError("y has q's shape")
+    _here(q, k, v, cache, positions, slots, turns, y)
+    st = lib().q8_rope_append(cache._ref, q.data_ptr(), ldq, h, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[t], rot,
+                              1 if interleaved else 0, factor, turns.data_ptr(), positions.data_ptr(), slots.data_ptr(), n,
+                              y.data_ptr(), _rows(y, "y", n, h * d), _status(dev_status), _stream(stream))
+    if st:
+        _check(st, "q8_rope_append")
+    return y
+
+
+def _ints(t, name, shape, dtype=_I32):
+    if not (t.is_cuda and t.dtype is dtype):
+        _cuda(t, name, (dtype,))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def q8_kv_plan(table, lens, new_tokens, page_size, pages, T, free_pages=None, free_count=None, free_left=None, starts=None,
+               slots=None, positions=None, lens_out=None, dev_status=None, stream=None):
+    """Where each new token goes: table int32 [B, width] (updated), lens int32 [B] tokens in the
+    cache, new_tokens int32 [B], T rows.  Pages are taken from the end of the first free_count
+    (int32 [1]) of free_pages (int32); without free_pages the table is complete.  Returns (starts int32
+    [B + 1], slots int64 [T], positions int32 [T], lens_out int32 [B], free_left int32 [1] or None)."""
+    _cuda(table, "table", (_I32,), 2)
+    B, width = table.shape
+    if not table.is_contiguous():
+        raise ValueError("table must be contiguous")
+    dev = table.device
+    args = [_ints(lens, "lens", (B,)), _ints(new_tokens, "new_tokens", (B,)), B]
+    if free_pages is None:
+        if free_count is not None or free_left is not None:
+            raise ValueError("free_count and free_left belong to free_pages")
+        args += [None, 0, None, None]
+    else:
+        if free_count is None:
+            raise ValueError("free_pages needs free_count")
+        if free_left is None:
+            free_left = _out(stream, (1,), _I32, dev)
+        n = _cuda(free_pages, "free_pages", (_I32,), 1).shape[0]
+        # an empty list is a list all the same
+        at = _ints(free_pages, "free_pages", (n,)) or table.data_ptr()
+        args += [at, n, _ints(free_count, "free_count", (1,)), _ints(free_left, "free_left", (1,))]
+    starts = _out(stream, (B + 1,), _I32, dev) if starts is None else starts
+    slots = _out(stream, (T,), _I64, dev) if slots is None else slots
+    positions = _out(stream, (T,), _I32, dev) if positions is None else positions
+    lens_out = _out(stream, (B,), _I32, dev) if lens_out is None else lens_out
+    _here(table, lens, new_tokens, free_pages, free_count, free_left, starts, slots, positions, lens_out)
+    st = lib().q8_kv_plan(table.data_ptr(), width, pages, page_size, *args, T, _ints(starts, "starts", (B + 1,)),
+                          _ints(slots, "slots", (T,), _I64), _ints(positions, "positions", (T,)), _ints(lens_out, "lens_out", (B,)),
+                          _status(dev_status), _stream(stream))
+    if st:
+        _check(st, "q8_kv_plan")
+    return starts, slots, positions, lens_out, free_left
+
+
+def q8_attn_chunk_workspace_size(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().q8_attn_chunk_workspace_size(q_heads, kv_heads, head_dim))
+
+
+def q8_attn_chunk(q, cache, table, lens, starts, scale=None, softcap=0.0, window=0, out=None, lse=None, return_lse=False, ws=None,
+                  dev_status=None, stream=None):
+    """Causal attention of each sequence's newest tokens over the cache: q bf16 [T, q_heads,
+    head_dim], the rows starts[b] .. starts[b + 1] - 1 (int32 [B + 1]) being the last of the lens[b]
+    (int32 [B]) tokens of sequence b, table int32 [B, pages of a sequence].  Returns (out
+    bf16 [T, q_heads, head_dim], lse fp32 [T, q_heads] if asked for or given, else None).  Rows of no
+    sequence are left as they are.  scale defaults to 1 / sqrt(head_dim); softcap 0: none; window 0: all."""
+    if not (q.is_cuda and table.is_cuda and q.dtype is _BF16 and table.dtype is _I32 and q.dim() == 3 and table.dim() == 2):
+        _cuda(q, "q", (_BF16,), 3)
+        _cuda(table, "table", (_I32,), 2)
+    T, H, D = q.shape
+    B, width = table.shape
+    if D != cache.head_dim:
+        raise ValueError("q has the cache's head_dim")
+    if not table.is_contiguous():
+        raise ValueError("table must be contiguous")
+    ldq = _rows(q, "q", T, H * D)
+    n_at, s_at = _ints(lens, "lens", (B,)), _ints(starts, "starts", (B + 1,))
+    if out is None:
+        out = _out(stream, (T, H, D), _BF16, cache.device)
+    elif _cuda(out, "out", (_BF16,), 3).shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape")
+    if lse is None:
+        if return_lse:
+            lse = _out(stream, (T, H), _F32, cache.device)
+    elif _cuda(lse, "lse", (_F32,), 2).shape != (T, H) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous, [T, q_heads]")
+    if ws is None:
+        nbytes = q8_attn_chunk_workspace_size(H, cache.kv_heads, D)
+        ws = _alloc(stream, lambda: _counting_workspace(nbytes, Q8_CHUNK_ZEROED_BYTES, cache.device))
+    _here(q, cache, table, lens, starts, out, lse, ws)
+    st = lib().q8_attn_chunk(cache._ref, q.data_ptr(), ldq, H, T, table.data_ptr(), width, n_at, s_at, B,
+                             D ** -0.5 if scale is None else scale, softcap, window if window < 2 ** 31 else 2 ** 31 - 1,
+                             out.data_ptr(), _a(lse), *_work(ws), _status(dev_status), _stream(stream))
+    if st:
+        _check(st, "q8_attn_chunk")
+    return out, lse

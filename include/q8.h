@@ -62,6 +62,7 @@ typedef enum q8_status {
 #define Q8_DEV_SCALE_OVF 0x2u /* quantizer: amax/127 overflowed binary16; block stored as zeros */
 #define Q8_DEV_TIMEOUT   0x4u /* a bounded wait gave up; outputs of that call are not valid */
 #define Q8_DEV_BAD_INDEX 0x8u /* a slot, page number or length outside the cache; what it named was left out */
+#define Q8_DEV_NO_PAGE   0x10u /* q8_kv_plan: the free list ran out; the tokens without a page have slot -1 */
 
 #define Q8_BLOCK 32          /* weights per block along K */
 #define Q8_SKINNY_MAX_M 32   /* largest M for q8_gemv / q8_gemm_skinny / q8_linear_batch */
@@ -609,6 +610,140 @@ size_t q8_moe_workspace_size(int32_t T, int32_t E, int64_t H, int64_t F, int32_t
 q8_status q8_sample(const void *logits, int32_t dtype, int64_t ld, int32_t rows, int64_t V, const float *temperature,
                     const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
                     float *logprob, int32_t *kept, uint32_t *dev_status, q8_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A prompt, a chunk of one, or draft tokens through a layer: what stands around
+ * the matmuls where a sequence gets several new tokens at once.  ("Frigg"
+ * README: the model card's RMSNorm and rotary positions, the int8 KV cache
+ * flag; "MODEL-BASELINE-RESULTS" (fak), ACT 4: a batched prefill.  The pages
+ * give no code for them.)
+ * ------------------------------------------------------------------------- */
+
+/*
+ * q8_rms_norm -- root-mean-square norm of T rows of W values, after the residual's
+ * addition, to bf16 rows, Q8_0 rows, or both:
+ *   h = x + residual (x alone where it is NULL), written to residual_out if given
+ *   y = h / sqrt(mean of h^2 + eps) * (weight + offset)
+ *   x            : x_dtype [T][ldx], 16-byte aligned rows (ldx a multiple of 4 in
+ *                  fp32, 8 in bf16)
+ *   residual     : residual_dtype [T][ldr], may be NULL; residual_out of the same
+ *                  type [T][ldo], may be NULL, may be residual itself, or x itself
+ *                  with the same type and ld
+ *   weight       : float [W], 16-byte aligned; NULL: no gains (and no offset).
+ *                  offset: 1 for gains stored less one, else 0
+ *   y            : bf16 [T][ldy], 16-byte aligned, ldy a multiple of 8; may be
+ *                  NULL, may be x itself (bf16, the same ld)
+ *   q, s         : codes int8 [T][W] and scales binary16 [T][W / 32] of y's values
+ *                  before their rounding to bf16, by the rule of q8_quantize_rows,
+ *                  with its flags; both NULL for none.  16-byte aligned
+ * h, the sum of squares and y are binary32; h is normalised as it is before its
+ * rounding to a bf16 residual.  Rows whose squares leave binary32's range are
+ * summed scaled, so that any finite row has its norm.  A row of zeros gives zeros;
+ * one with an infinity NaN there and 0 elsewhere; one with NaN gives NaN.  32 <= W <=
+ * Q8_NORM_MAX_WIDTH, a multiple of 32; eps >= 0.  T == 0 is a no-op.
+ */
+#define Q8_NORM_MAX_WIDTH 32768
+q8_status q8_rms_norm(const void *x, int64_t ldx, int32_t x_dtype, const void *residual, int64_t ldr, int32_t residual_dtype,
+                      void *residual_out, int64_t ldo, const float *weight, float offset, float eps, int64_t T, int64_t W,
+                      uint16_t *y, int64_t ldy, int8_t *q, uint16_t *s, uint32_t *dev_status, q8_stream_t stream);
+
+/* Which dimensions of a head make pair i: i and i + rot / 2, or 2 i and 2 i + 1. */
+#define Q8_ROPE_HALF 0
+#define Q8_ROPE_INTERLEAVED 1
+
+/*
+ * q8_rope_turns -- the table of q8_rope and q8_rope_append, made once for a model, from its
+ * frequencies: inv_freq[i] radians a token for pair i (any scaling for long contexts is
+ * in them), |inv_freq[i]| <= Q8_ROPE_MAX_FREQ.  turns[i] is inv_freq[i] / (2 pi) modulo
+ * one turn, in units of 2^-64 turns.  Both are HOST arrays of n; nothing is enqueued.
+ */
+#define Q8_ROPE_MAX_FREQ 65536.0
+q8_status q8_rope_turns(const double *inv_freq, int32_t n, uint64_t *turns);
+
+/*
+ * q8_rope -- rotary positions of `heads` heads a token (query and key heads side by
+ * side, for instance):
+ *   (y1, y2) = factor * (x1 cos a - x2 sin a, x2 cos a + x1 sin a)   a = position * inv_freq[i]
+ * for the pairs of the first `rot` dimensions of each head; the others pass as they are.
+ *   x         : dtype [T][ldx], heads * head_dim values a row, 16-byte aligned rows
+ *   y         : bf16 [T][ldy], 16-byte aligned, ldy a multiple of 8; may be x itself
+ *               (bf16, the same ld)
+ *   turns     : DEVICE copy of q8_rope_turns' table for rot / 2 pairs, 8-byte aligned
+ *   positions : int32 [T], any value
+ * head_dim 64, 128 or 256; rot a multiple of 16, 16 .. head_dim.  The angle is exact to
+ * 2^-25 half turns at any position; cosines, sines and sums are binary32, y is rounded once.
+ */
+q8_status q8_rope(const void *x, int64_t ldx, int32_t dtype, uint16_t *y, int64_t ldy, int32_t heads, int32_t head_dim, int32_t rot,
+                  int32_t layout, float factor, const uint64_t *turns, const int32_t *positions, int64_t T, q8_stream_t stream);
+
+/*
+ * q8_rope_append -- q8_rope of the query heads to bf16 rows y, and of the key heads on
+ * their way into the cache (in binary32, quantized without a rounding between), with
+ * the values as they are: q8_rope and q8_kv_append in one.  q, k and v of one dtype;
+ * slots, flags and k, v rows as q8_kv_append; q rows and y as q8_rope (y may be q itself).
+ * A token without a slot still gets its row of y.
+ */
+q8_status q8_rope_append(const q8_kv_cache *cache, const void *q, int64_t ldq, int32_t q_heads, const void *k, const void *v,
+                         int64_t ldk, int64_t ldv, int32_t dtype, int32_t rot, int32_t layout, float factor, const uint64_t *turns,
+                         const int32_t *positions, const int64_t *slots, int64_t T, uint16_t *y, int64_t ldy, uint32_t *dev_status,
+                         q8_stream_t stream);
+
+/*
+ * q8_kv_plan -- a step's bookkeeping on the device: where each new token of each sequence goes.
+ *   table      : int32 [batch][table_width], the pages of each sequence (updated)
+ *   lens       : int32 [batch], tokens in the cache before the step
+ *   new_tokens : int32 [batch], tokens that the step adds
+ *   free_pages : int32 [free_capacity], a stack of unused pages of which the first
+ *                *free_count count.  A sequence that outgrows its pages takes one after
+ *                another from its end (the k-th page taken in the step, in order of the
+ *                sequences, is free_pages[*free_count - 1 - k]); the table gets them.
+ *                NULL: the table is complete, and nothing is taken
+ *   free_left  : int32, what is left of *free_count; may be free_count itself
+ *   T          : rows of the step.  Written are
+ *     starts    int32 [batch + 1]: the first row of each sequence, and the end
+ *     slots     int64 [T]: each row's slot in the cache (as q8_kv_append takes it)
+ *     positions int32 [T]: its position in its sequence
+ *     lens_out  int32 [batch]: tokens in the cache after the step; may be lens itself
+ *   Rows behind the last sequence get slot -1 and position 0.
+ * A length outside 0 .. table_width * page_size, new tokens below 0 or past the table's or
+ * the rows' end, and a page outside the cache set Q8_DEV_BAD_INDEX: they are clamped, rows
+ * without a page get slot -1.  Where the free list runs out (Q8_DEV_NO_PAGE) the
+ * table gets -1, and the rows slot -1.
+ * batch <= Q8_PLAN_MAX_BATCH.  One launch; no workspace.
+ */
+#define Q8_PLAN_MAX_BATCH (1 << 20)
+q8_status q8_kv_plan(int32_t *table, int32_t table_width, int32_t pages, int32_t page_size, const int32_t *lens,
+                     const int32_t *new_tokens, int32_t batch, const int32_t *free_pages, int32_t free_capacity,
+                     const int32_t *free_count, int32_t *free_left, int64_t T, int32_t *starts, int64_t *slots, int32_t *positions,
+                     int32_t *lens_out, uint32_t *dev_status, q8_stream_t stream);
+
+/*
+ * q8_attn_chunk -- attention of each sequence's newest tokens over its cache, causally:
+ * the rows starts[b] .. starts[b + 1] - 1 of q are the last of the lens[b] tokens of sequence
+ * b, whose keys and values are in the cache already.  A row at position p sees the tokens
+ * max(0, p + 1 - window) .. p (window 0: all up to p); scores, softcap, heads, table and
+ * cache as q8_attn_decode.
+ *   q      : bf16 [T][ldq], q_heads * head_dim values a row, 16-byte aligned, ldq a multiple of 8
+ *   starts : int32 [batch + 1], not decreasing, within 0 .. T (else clamped, Q8_DEV_BAD_INDEX)
+ *   lens   : int32 [batch], the new tokens included; clamped as in q8_attn_decode.  Where it is
+ *            less than the sequence's rows, the first rows have no position (Q8_DEV_BAD_INDEX)
+ *            and see nothing
+ *   out    : bf16 [T][q_heads][head_dim], 16-byte aligned; rows of no sequence are left as they are
+ *   lse    : float [T][q_heads], log(sum_t exp(s_t)); may be NULL
+ * A row that sees nothing gives out = 0 and lse = -inf.
+ *   ws     : q8_attn_chunk_workspace_size() bytes, 256-byte aligned, the first
+ *            Q8_CHUNK_ZEROED_BYTES zeroed once (the kernel counts there and leaves
+ *            them zero; the rest may hold anything).  Not for two calls that may run at the
+ *            same time; may be shared with other calls (see q8_linear_batch)
+ * The work is split as the device reads starts and lens, so a captured graph may be
+ * replayed with others.
+ */
+#define Q8_CHUNK_ZEROED_BYTES 4096
+q8_status q8_attn_chunk(const q8_kv_cache *cache, const uint16_t *q, int64_t ldq, int32_t q_heads, int64_t T, const int32_t *table,
+                        int32_t table_width, const int32_t *lens, const int32_t *starts, int32_t batch, float scale, float softcap,
+                        int32_t window, uint16_t *out, float *lse, void *ws, size_t ws_bytes, uint32_t *dev_status,
+                        q8_stream_t stream);
+size_t q8_attn_chunk_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim);
 
 /*
  * q8_workspace_zero -- zero the first `bytes` of a workspace, in the stream:

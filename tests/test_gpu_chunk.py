@@ -1,0 +1,436 @@
+"""q8_attn_chunk against the binary64 definition.
+
+Tolerances, from the arithmetic: a key s * code is rounded to binary16 (2^-11 of it at most) and
+scores are fp32 sums (below 2^-17 of sum|q k| over 256 terms), so a score is off by
+fine = (2^-11 + 2^-17) max_t sum|q k_t| * scale + 2^-18; that moves the lse by as much and a
+quotient of weights by twice as much.  A value s * code and a weight are rounded to binary16 (2^-11
+each, and 2^-25 of the largest weight around it below the normal range); the result to bf16 (2^-8).
+Over many outputs roundings do not add up like that: the 2-norm of all that a call is off
+stays below 2^-8 of the result's (bf16's own rounding gives 2^-9.2 at most).
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_attn import bf16_of, f64, filled_cache
+
+pytestmark = pytest.mark.gpu
+
+BAD = 0x8
+
+
+def definition(q, k, v, pos, keep, scale, softcap=0.0, window=0):
+    """Rows q[n, D] at positions pos[n] over tokens k, v [t, D] (keep [t]: those that exist): (out, lse, sum p|v|, sum|q k|)."""
+    t = np.arange(k.shape[0])
+    s = q @ k.T * scale
+    if softcap > 0:
+        s = softcap * np.tanh(s / softcap)
+    seen = (t[None] <= pos[:, None]) & keep[None]
+    if window:
+        seen &= t[None] > pos[:, None] - window
+    s = np.where(seen, s, -np.inf)
+    m = s.max(-1, initial=-np.inf, keepdims=True)
+    none = m[:, 0] == -np.inf
+    with np.errstate(invalid="ignore", divide="ignore"):
+        e = np.where(seen, np.exp(s - np.where(none[:, None], 0, m)), 0.0)
+        z = e.sum(-1, keepdims=True)
+        p = np.where(z > 0, e / z, 0.0)
+        lse = np.where(none, -np.inf, m[:, 0] + np.log(z[:, 0]))
+    big = np.where(seen, np.abs(q) @ np.abs(k).T * abs(scale), 0.0).max(-1, initial=0.0)
+    top = np.where(seen.any(-1)[:, None], np.abs(v).max(0, initial=0.0)[None], 0.0)
+    return p @ v, lse, p @ np.abs(v), big, top, seen.sum(-1)
+
+
+def check(cache, kv, vv, q, table, lens, starts, scale=None, softcap=0.0, window=0, status=0, stream=None, want_lse=True, ws=None, tight=2.0 ** -8):
+    """q bf16 [T, H, D] on the GPU; table, lens, starts as arrays.  Returns (out, lse)."""
+    from block_quantized_int8_gb300 import q8
+    T, H, D = q.shape
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    tab, ln, sd = dev(table), dev(lens), dev(starts)
+    mark = torch.full((T, H, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), 5.0, device="cuda") if want_lse else None
+    torch.cuda.synchronize()
+    out, lse = q8.q8_attn_chunk(q, cache, tab, ln, sd, scale=scale, softcap=softcap, window=window, out=mark, lse=lse, dev_status=st,
+                                stream=stream, ws=ws)
+    torch.cuda.synchronize()
+    assert int(st.item()) == status
+    compare(out, lse, cache, kv, vv, q, table, lens, starts, scale, softcap, window, tight)
+    return out, lse
+
+
+def compare(out, lse, cache, kv, vv, q, table, lens, starts, scale=None, softcap=0.0, window=0, tight=2.0 ** -8):
+    T, H, D = q.shape
+    ps, pages = cache.page_size, cache.pages
+    table = np.asarray(table)
+    sc = D ** -0.5 if scale is None else scale
+    group = H // cache.kv_heads
+    o, qn = f64(out), f64(q)
+    l = None if lse is None else f64(lse)
+    used = np.zeros(T, dtype=bool)
+    off2 = ref2 = 0.0
+    for b in range(len(lens)):
+        s0 = min(max(int(starts[b]), 0), T)
+        s1 = min(max(int(starts[b + 1]), s0), T)
+        if s1 == s0:
+            continue
+        used[s0:s1] = True
+        n = min(max(int(lens[b]), 0), table.shape[1] * ps)
+        pos = n - (s1 - s0) + np.arange(s1 - s0)
+        t = np.arange(n)
+        pg = table[b][t // ps] if n else np.zeros(0, dtype=int)
+        keep = (pg >= 0) & (pg < pages)
+        pg = np.where(keep, pg, 0)
+        for h in range(H):
+            # what no row sees is not looked at
+            lo = max(0, int(pos[0]) + 1 - window) if window else 0
+            k, v = kv[pg[lo:], h // group, t[lo:] % ps], vv[pg[lo:], h // group, t[lo:] % ps]
+            ref, e, pv, big, top, count = definition(qn[s0:s1, h], k, v, pos - lo, keep[lo:], sc, softcap, window)
+            fine = (2.0 ** -11 + 2.0 ** -17) * big + 2.0 ** -18
+            got = o[s0:s1, h]
+            if l is not None:
+                some = e > -np.inf
+                assert np.all(l[s0:s1, h][~some] == -np.inf)
+                bad = ~(np.abs(l[s0:s1, h][some] - e[some]) <= (fine + 2.0 ** -22 * np.abs(e))[some])
+                assert not bad.any(), (b, h, l[s0:s1, h][some][bad][:4], e[some][bad][:4])
+            tol = 2.0 ** -8 * np.abs(ref) * 1.01 + (2.0 ** -10 + 2.2 * fine)[:, None] * pv + (count * 2.0 ** -25)[:, None] * top + 1e-30
+            bad = ~(np.abs(got - ref) <= tol)
+            assert not bad.any(), (b, h, n, np.argwhere(bad)[:4].tolist(), got[bad][:4], ref[bad][:4])
+            assert np.all(got[count == 0] == 0)
+            off2 += ((got - ref) ** 2).sum()
+            ref2 += (ref ** 2).sum()
+    assert off2 <= tight ** 2 * ref2 + 1e-60, (off2 / ref2) ** 0.5
+    assert np.all(o[~used] == 5.0)
+    if l is not None:
+        assert np.all(l[~used] == 5.0)
+
+
+def run_case(D, kv_heads, group, ps, new, lens, window=0, softcap=0.0, seed=0, pad=0, q_scale=1.5, spread=1.0, **kw):
+    B = len(new)
+    width = max(1, -(-max(max(lens), 1) // ps))
+    r = np.random.default_rng(seed)
+    cache, kv, vv = filled_cache(B * width, ps, kv_heads, D, seed, spread)
+    table = r.permutation(B * width).reshape(B, width)
+    starts = np.concatenate([[0], np.cumsum(new)])
+    T = int(starts[-1]) + pad
+    q = bf16_of(r.standard_normal((T, kv_heads * group, D)) * q_scale).cuda()
+    return check(cache, kv, vv, q, table, lens, starts, window=window, softcap=softcap, **kw)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,lens", [([1], [1]), ([1], [200]), ([2], [2]), ([5], [300]), ([16], [16]), ([17], [33]), ([128], [128]),
+                                      ([129], [129]), ([200], [777]), ([1, 2, 3, 4, 5], [1, 64, 65, 300, 5]), ([257], [300])])
+def test_lengths(D, new, lens):
+    run_case(D, 2, 2, 16, new, lens, seed=D + len(new) + sum(new))
+
+
+@pytest.mark.parametrize("D,group", [(64, 1), (64, 3), (64, 16), (128, 1), (128, 5), (128, 7), (128, 8), (128, 32), (256, 1), (256, 3), (256, 12)])
+def test_heads_that_share_keys(D, group):
+    run_case(D, 2, group, 16, [37, 3, 90], [150, 3, 411], seed=group)
+
+
+@pytest.mark.parametrize("ps", [16, 32, 64, 128, 256, 1024])
+def test_page_sizes(ps):
+    run_case(128, 3, 2, ps, [70, 1, 130], [300, 129, 1100], seed=ps)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 100, 128, 129, 1000, 2 ** 31 - 1])
+def test_windows(D, window):
+    run_case(D, 1, 3, 16, [150, 40, 1], [400, 40, 333], window=window, seed=window % 97)
+
+
+@pytest.mark.parametrize("D,softcap,scale", [(64, 30.0, None), (128, 1.0, None), (256, 30.0, 0.2), (128, 0.0, -0.05), (128, 0.0, 0.0)])
+def test_caps_and_scales(D, softcap, scale):
+    run_case(D, 2, 2, 16, [50, 90], [200, 90], softcap=softcap, scale=scale, seed=3)
+
+
+def test_sequences_that_take_no_part_and_rows_behind_the_last():
+    run_case(128, 2, 4, 16, [0, 5, 0, 0, 33, 0], [100, 5, 0, 7, 290, 40], pad=19, seed=4)
+    run_case(64, 2, 1, 16, [0, 0], [100, 5], pad=3, seed=5)
+
+
+def test_many_short_sequences():
+    r = np.random.default_rng(6)
+    new = r.integers(0, 6, 100)
+    run_case(128, 1, 4, 16, new.tolist(), (new + r.integers(0, 200, 100)).tolist(), seed=6)
+
+
+@pytest.mark.parametrize("D,group,new,lens", [(128, 4, [3], [9000]), (64, 8, [20, 1], [6000, 8000]), (256, 2, [5], [5000]),
+                                              (128, 1, [300], [3000]), (128, 4, [64, 64, 64], [4000, 10, 2000])])
+def test_long_caches_are_split_and_joined(D, group, new, lens):
+    lens = [max(a, b) for a, b in zip(new, lens)]
+    run_case(D, 2, group, 64, new, lens, seed=D)
+
+
+def test_large_scores_and_a_growing_maximum():
+    """Keys that grow along the sequence, so that the running maximum moves in every tile."""
+    from block_quantized_int8_gb300 import q8
+    r = np.random.default_rng(7)
+    D, n = 128, 700
+    cache, kv, vv = filled_cache(44, 16, 1, D, 7)
+    ramp = np.float16(0.01) * (1 + np.arange(44 * 16).reshape(44, 1, 16, 1) / 60)
+    s = np.broadcast_to(ramp, (44, 1, 16, D // 32)).astype(np.float16)
+    cache.ks.copy_(torch.from_numpy(np.ascontiguousarray(s)).view(cache.ks.dtype))
+    kv = cache.kq.cpu().numpy().astype(np.float64) * np.repeat(s.astype(np.float64), 32, -1)
+    q = bf16_of(r.standard_normal((300, 2, D)) * 2).cuda()
+    check(cache, kv, vv, q, np.arange(44).reshape(1, 44), [n], [0, 300])
+    assert q8
+
+
+def test_equal_scores_are_a_mean():
+    cache, kv, vv = filled_cache(8, 16, 1, 64, 8)
+    q = torch.zeros((128, 2, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = check(cache, kv, vv, q, np.arange(8).reshape(1, 8), [128], [0, 128])
+    assert np.allclose(f64(lse)[:, 0], np.log(np.arange(1, 129)), atol=2.0 ** -20)
+    assert np.allclose(f64(out)[0, 0], vv[0, 0, 0], rtol=2.0 ** -8)
+
+
+def test_what_lies_past_a_length_does_not_enter():
+    D, ps = 128, 16
+    for lens, new in (([37, 130], [20, 7]), ([1, 16], [1, 16])):
+        width = 9
+        cache, kv, vv = filled_cache(2 * width, ps, 2, D, 9)
+        table = np.arange(2 * width).reshape(2, width)
+        q = bf16_of(np.random.default_rng(9).standard_normal((sum(new), 4, D))).cuda()
+        starts = np.concatenate([[0], np.cumsum(new)])
+        a, al = check(cache, kv, vv, q, table, lens, starts)
+        for b, n in enumerate(lens):
+            for t in range(n, width * ps):
+                pg, off = table[b][t // ps], t % ps
+                cache.kq[pg, :, off], cache.vq[pg, :, off] = -128, 127
+                cache.ks[pg, :, off], cache.vs[pg, :, off] = float("nan"), float("inf")
+        b_, bl = check(cache, kv, vv, q, table, lens, starts)
+        assert torch.equal(a, b_) and torch.equal(al, bl)
+
+
+def test_scales_that_are_not_finite_count_as_zero():
+    D, ps = 128, 16
+    cache, kv, vv = filled_cache(8, ps, 1, D, 10)
+    cache.ks[2, 0, 3, 1], cache.vs[3, 0, 5, 2] = float("nan"), float("-inf")
+    kv[2, 0, 3, 32:64], vv[3, 0, 5, 64:96] = 0.0, 0.0
+    q = bf16_of(np.random.default_rng(10).standard_normal((90, 2, D))).cuda()
+    check(cache, kv, vv, q, np.arange(8).reshape(1, 8), [128], [0, 90], status=0x1)
+
+
+def test_pages_outside_the_cache_are_left_out():
+    D, ps = 64, 16
+    cache, kv, vv = filled_cache(20, ps, 2, D, 11)
+    table = np.arange(20).reshape(2, 10)
+    q = bf16_of(np.random.default_rng(11).standard_normal((60, 4, D))).cuda()
+    table[0, 3], table[0, 9], table[1, 0] = -1, 20, 2 ** 31 - 1
+    check(cache, kv, vv, q, table, [160, 40], [0, 40, 60], status=BAD)
+    # nothing but such pages: rows that see nothing
+    table[1, :] = -1
+    check(cache, kv, vv, q, table, [160, 40], [0, 40, 60], status=BAD)
+
+
+def test_bad_lengths_and_starts():
+    D, ps = 128, 16
+    cache, kv, vv = filled_cache(10, ps, 1, D, 12)
+    table = np.arange(10).reshape(2, 5)
+    q = bf16_of(np.random.default_rng(12).standard_normal((50, 2, D))).cuda()
+    for lens, starts in (([10, 80], [0, 30, 50]), ([0, 80], [0, 30, 50]), ([-3, 80], [0, 30, 50]), ([81, 60], [0, 30, 50]),
+                         ([2 ** 31 - 1, 60], [0, 30, 50]), ([60, 60], [0, 30, 51]), ([60, 60], [-4, 30, 50]), ([60, 60], [20, 10, 30]),
+                         ([60, 60], [0, 2 ** 31 - 1, 50]), ([60, 60], [-2 ** 31, 10, 20])):
+        check(cache, kv, vv, q, table, lens, starts, status=BAD)
+
+
+def test_strided_queries_and_no_lse():
+    cache, kv, vv = filled_cache(20, 16, 2, 128, 13)
+    big = bf16_of(np.random.default_rng(13).standard_normal((70, 9, 128))).cuda()
+    q = big[:, 3:7]
+    check(cache, kv, vv, q, np.arange(20).reshape(1, 20), [300], [0, 70], want_lse=False)
+
+
+def test_infinities_and_nan_stay_in_their_rows():
+    from block_quantized_int8_gb300 import q8
+    cache, kv, vv = filled_cache(20, 16, 2, 128, 14)
+    q = bf16_of(np.random.default_rng(14).standard_normal((70, 4, 128))).cuda()
+    tab = torch.arange(20, dtype=torch.int32, device="cuda").view(1, 20)
+    ln, st = torch.tensor([300], dtype=torch.int32, device="cuda"), torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+    a, _ = q8.q8_attn_chunk(q, cache, tab, ln, st)
+    q[3, 1, 7], q[40, 2, 9] = float("inf"), float("nan")
+    b, _ = q8.q8_attn_chunk(q, cache, tab, ln, st)
+    same = (a == b).all(-1)
+    assert not torch.isfinite(b[40, 2]).any()
+    same[3, 1] = same[40, 2] = True
+    assert bool(same.all())
+
+
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_at_the_end_of_their_range(D, which):
+    """Scales of 512 and more: s * code passes binary16's end.  Tiles that hold one keep values to 2^-16 (and weights
+    to 2^-16 of the largest): what is held against them says so."""
+    r = np.random.default_rng(15)
+    cache, kv, vv = filled_cache(20, 16, 1, D, 15)
+    for name, plane in (("k", cache.ks), ("v", cache.vs)):
+        if which in (name, "both"):
+            s = plane.cpu().numpy().view(np.float16).copy()
+            s[7:9] = r.uniform(400, 60000, s[7:9].shape).astype(np.float16)
+            plane.copy_(torch.from_numpy(s).view(plane.dtype))
+    kv, vv = (q.cpu().numpy().astype(np.float64) * np.repeat(s.cpu().numpy().view(np.float16).astype(np.float64), 32, -1)
+              for q, s in ((cache.kq, cache.ks), (cache.vq, cache.vs)))
+    q = bf16_of(r.standard_normal((60, 2, D)) * (1e-6 if which != "v" else 1.0)).cuda()
+    check(cache, kv, vv, q, np.arange(20).reshape(1, 20), [300], [0, 60])
+
+
+@pytest.mark.parametrize("q_scale", [1e-30, 1e-10, 1e10, 1e30])
+def test_queries_of_any_size(q_scale):
+    run_case(128, 1, 2, 16, [40], [200], q_scale=q_scale, scale=0.09 / q_scale, seed=16)
+
+
+def test_small_scales_are_exact():
+    """Subnormal scales: products with codes are whole numbers of 2^-24, which binary16 holds."""
+    run_case(128, 1, 2, 16, [40], [200], spread=1e-5, q_scale=1e4, seed=17)
+
+
+def test_a_call_repeats_bit_for_bit_and_rows_do_not_depend_on_their_neighbours():
+    from block_quantized_int8_gb300 import q8
+    cache, kv, vv = filled_cache(130, 64, 2, 128, 18)
+    q = bf16_of(np.random.default_rng(18).standard_normal((200, 8, 128))).cuda()
+    tab = torch.arange(130, dtype=torch.int32, device="cuda").view(1, 130)
+    ln, st = torch.tensor([8000], dtype=torch.int32, device="cuda"), torch.tensor([0, 200], dtype=torch.int32, device="cuda")
+    a, al = q8.q8_attn_chunk(q, cache, tab, ln, st, return_lse=True)
+    for _ in range(5):
+        b, bl = q8.q8_attn_chunk(q, cache, tab, ln, st, return_lse=True)
+        assert torch.equal(a, b) and torch.equal(al, bl)
+
+
+def test_a_chunk_in_one_or_in_pieces():
+    """Rows of one call against the same rows in two calls (the cache holds all tokens): within the tolerances of both."""
+    from block_quantized_int8_gb300 import q8
+    cache, kv, vv = filled_cache(40, 16, 2, 128, 19)
+    q = bf16_of(np.random.default_rng(19).standard_normal((300, 4, 128))).cuda()
+    tab = torch.arange(40, dtype=torch.int32, device="cuda").view(1, 40)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    whole, _ = q8.q8_attn_chunk(q, cache, tab, i32(600), i32(0, 300))
+    first, _ = q8.q8_attn_chunk(q[:111], cache, tab, i32(411), i32(0, 111))
+    second, _ = q8.q8_attn_chunk(q[111:], cache, tab, i32(600), i32(0, 189))
+    both = torch.cat((first, second)).float()
+    assert float((whole.float() - both).norm()) <= 2.0 ** -7 * float(both.norm())
+
+
+def test_one_new_token_is_the_decode_call():
+    from block_quantized_int8_gb300 import q8
+    for D in (64, 128, 256):
+        cache, kv, vv = filled_cache(40, 16, 2, D, 20)
+        q = bf16_of(np.random.default_rng(20).standard_normal((4, 6, D))).cuda()
+        tab = torch.arange(40, dtype=torch.int32, device="cuda").view(4, 10)
+        ln = torch.tensor([1, 160, 77, 0], dtype=torch.int32, device="cuda")
+        a, al = q8.q8_attn_decode(q, cache, tab, ln, window=90)
+        st = torch.tensor([0, 1, 2, 3, 3], dtype=torch.int32, device="cuda")
+        b, bl = q8.q8_attn_chunk(q[:3], cache, tab, ln, st, window=90, return_lse=True)
+        assert float((a[:3].float() - b.float()).norm()) <= 2.0 ** -7 * float(b.float().norm())
+        assert torch.allclose(al[:3], bl, atol=2e-2)
+
+
+def test_graph_replay_with_other_lengths():
+    from block_quantized_int8_gb300 import q8
+    D, H = 128, 4
+    cache, kv, vv = filled_cache(3 * 20, 16, 1, D, 21)
+    r = np.random.default_rng(21)
+    tables = np.arange(60).reshape(3, 20)
+    tab = torch.from_numpy(tables.astype(np.int32)).cuda()
+    ln, st = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    q = bf16_of(r.standard_normal((200, H, D))).cuda()
+    out, lse = torch.empty((200, H, D), dtype=torch.bfloat16, device="cuda"), torch.empty((200, H), device="cuda")
+    ws = q8.workspace(q8.q8_attn_chunk_workspace_size(H, 1, D))
+    q8.q8_attn_chunk(q, cache, tab, ln, st, out=out, lse=lse, ws=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q8.q8_attn_chunk(q, cache, tab, ln, st, out=out, lse=lse, ws=ws)
+    for lens, starts in (([300, 7, 100], [0, 100, 107, 200]), ([0, 0, 0], [0, 0, 0, 0]), ([1, 1, 1], [0, 1, 2, 3]), ([320, 320, 320], [0, 1, 1, 199]),
+                         ([199, 0, 0], [0, 199, 199, 199])):
+        ln.copy_(torch.tensor(lens, dtype=torch.int32))
+        st.copy_(torch.tensor(starts, dtype=torch.int32))
+        out.fill_(5.0)
+        lse.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(out, lse, cache, kv, vv, q, tables, lens, starts)
+
+
+def test_streams():
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        run_case(128, 2, 2, 16, [50, 9], [300, 90], seed=22)
+    run_case(128, 2, 2, 16, [50, 9], [300, 90], seed=22, stream=s)
+
+
+def test_two_calls_at_once():
+    """Two streams, each with a workspace of its own, many times over."""
+    from block_quantized_int8_gb300 import q8
+    cache, kv, vv = filled_cache(130, 64, 2, 128, 23)
+    tab = torch.arange(130, dtype=torch.int32, device="cuda").view(1, 130)
+    r = np.random.default_rng(23)
+    jobs = []
+    for n, t in ((64, 8000), (300, 3000)):
+        q = bf16_of(r.standard_normal((t and n, 8, 128))).cuda()
+        a = (q, cache, tab, torch.tensor([t], dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+        jobs.append((a, q8.q8_attn_chunk(*a)[0], torch.cuda.Stream(), q8.workspace(q8.q8_attn_chunk_workspace_size(8, 2, 128))))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for a, _, s, ws in jobs:
+            with torch.cuda.stream(s):
+                got.append(q8.q8_attn_chunk(*a, ws=ws)[0])
+    torch.cuda.synchronize()
+    for i, x in enumerate(got):
+        assert torch.equal(x, jobs[i % 2][1])
+
+
+def test_one_workspace_for_all_calls():
+    """The chunk's, the decode's and a matmul's workspace may be one, in stream order."""
+    from block_quantized_int8_gb300 import q8
+    cache, kv, vv = filled_cache(130, 64, 2, 128, 24)
+    r = np.random.default_rng(24)
+    tab = torch.arange(130, dtype=torch.int32, device="cuda").view(1, 130)
+    q = bf16_of(r.standard_normal((30, 8, 128))).cuda()
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = (q, cache, tab, i32(8000), i32(0, 30))
+    want, _ = q8.q8_attn_chunk(*args)
+    dec = (q[:1], cache, tab, i32(8000))
+    dwant, _ = q8.q8_attn_decode(*dec)
+    w = torch.randn(4096, 1536, device="cuda")
+    wq, wsc = q8.q8_quantize_rows(w)
+    x = torch.randn(16, 1536, device="cuda").to(torch.bfloat16)
+    ywant = q8.q8_gemm_skinny(wq, wsc, x)
+    ws = torch.full((max(q8.q8_attn_chunk_workspace_size(8, 2, 128), q8.q8_attn_decode_workspace_size(1, 8, 2, 128), 1 << 24),), 0,
+                    dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(q8.q8_attn_chunk(*args, ws=ws)[0], want)
+        assert torch.equal(q8.q8_gemm_skinny(wq, wsc, x, ws=ws), ywant)
+        assert torch.equal(q8.q8_attn_decode(*dec, ws=ws)[0], dwant)
+
+
+def test_offsets_past_32_bits():
+    """A cache whose codes pass 2^32 bytes: pages at both ends."""
+    D, kv_heads, ps = 128, 8, 1024
+    pages = 2 ** 32 // (D * kv_heads * ps) + 5
+    from block_quantized_int8_gb300 import q8
+    cache = q8.KvCache.empty(pages, ps, kv_heads, D)
+    small, kv, vv = filled_cache(2, ps, kv_heads, D, 25)
+    table = np.array([[pages - 1, 0]])
+    for i, pg in enumerate(table[0]):
+        for n in ("kq", "ks", "vq", "vs"):
+            getattr(cache, n)[pg] = getattr(small, n)[i]
+
+    class Far:  # kv[page, ...] for the two pages that exist
+        def __init__(self, a):
+            self.a = a
+
+        def __getitem__(self, i):
+            return self.a[(np.where(i[0] == 0, 1, 0),) + tuple(i[1:])]
+    q = bf16_of(np.random.default_rng(25).standard_normal((20, 8, D))).cuda()
+    check(cache, Far(kv), Far(vv), q, table, [1500], [0, 20])
+
+
+def test_no_rows():
+    from block_quantized_int8_gb300 import q8
+    cache, _, _ = filled_cache(2, 16, 1, 64, 26)
+    out, lse = q8.q8_attn_chunk(torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda"), cache,
+                                torch.zeros((1, 2), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert out.shape == (0, 2, 64) and lse is None
