@@ -89,44 +89,106 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lead) {
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
+// These are executed by a whole warp, one of whose threads is elected for the instruction: the operands are
+// then made in the warp's uniform registers.  (Behind a branch on the lane an MMA took 97 clocks to issue,
+// for 40 of the tensor cores'.)
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 r;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync r|q, 0xFFFFFFFF;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                  :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc));
 }
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 r;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync r|q, 0xFFFFFFFF;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
                  :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc));
 }
 __device__ __forceinline__ void umma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_addr(bar)) : "memory");
+    asm volatile("{\n\t.reg .pred q;\n\t.reg .b32 r;\n\telect.sync r|q, 0xFFFFFFFF;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" :: "r"(smem_addr(bar)) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t (&r)[32]) {
+// n columns of the warp's lanes; the wait stands in the same statement, so that nothing can use (or
+// spill) the registers before it
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(t));
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t) : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[32]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
-        :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-           "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-           "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-           "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(t)
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t) : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(t), "r"(t + 32) : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[128]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%129];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%130];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%131];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(t), "r"(t + 32), "r"(t + 64), "r"(t + 96) : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
+                 :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(t)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
@@ -134,7 +196,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
            "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---- small things -----------------------------------------------------------------
@@ -169,6 +230,16 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float lo2(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v)); }
 __device__ __forceinline__ float hi2(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t *p, uint32_t v) {
@@ -177,13 +248,6 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t *p, uint32_t v) 
     return old;
 }
 __device__ __forceinline__ void named_bar(int id, int threads) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory"); }
-__device__ __forceinline__ bool named_bar_or(int id, int threads, bool v) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-                 "barrier.cta.red.or.aligned.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r) : "r"(v ? 1u : 0u), "r"(id), "r"(threads) : "memory");
-    return r != 0;
-}
 
 // ---- shapes -------------------------------------------------------------------------
 template <int D_, int MT_>
@@ -191,9 +255,13 @@ struct Cfg {
     static constexpr int D = D_, MT = MT_;
     static constexpr int BN = D == 256 ? 64 : 128;          // tokens of a tile
     static constexpr int RT = 128 * MT;                     // rows of an item
-    static constexpr int CW = MT == 2 ? 6 : 8;              // converter warps (16 warps at most: 128 registers a thread)
     static constexpr int kSoftmax = 4 * MT;                 // softmax warps
+    static constexpr int CW = 14 - kSoftmax;                // converter warps: what is left of 16
+    // A softmax thread has a row's scores in registers: the other roles leave it what they do without of the
+    // 128 that each thread begins with (8 x 184 + 8 x 72, or 4 x 200 + 12 x 104)
+    static constexpr int kRegs = MT == 2 ? 184 : 200, kRegsLess = MT == 2 ? 72 : 104;
     static constexpr int kWarps = kSoftmax + 2 + CW;
+    static_assert(kWarps == 16 && kSoftmax * kRegs + (16 - kSoftmax) * kRegsLess <= 16 * 128, "registers");
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kQ = 256 * D;                      // bytes of a query tile
     static constexpr int kTile = BN * D * 2;                // bytes of a binary16 tile
@@ -215,8 +283,9 @@ struct Control {
     uint64_t raw_full[8], raw_empty[8];
     uint64_t t_full[4], t_empty[4];
     uint64_t s_full[2], p_full[2], q_full[2], pv_done[2];
-    uint32_t runs[8];       // of a raw tile: which runs of 16 tokens were loaded
-    uint32_t info[4];       // of the last tiles: bits 0-7 runs that must not be seen, 8 keys times 2^-9, 9 values
+    uint32_t meta[8];       // of a raw tile: bits 0-7 the runs of 16 tokens that were loaded, 8-15 tokens
+    uint32_t unseen[8];     // of the last tiles: runs that were not loaded
+    uint4 big[2][8];        // and tokens whose keys (values) are times 2^-9, a bit each
     uint32_t tmem, last[2];
     int32_t abort_flag;
     int32_t start;          // the sequence that this CTA begins in, and what the list holds before it
@@ -284,16 +353,36 @@ struct Walk {
     }
 };
 
-template <class C>
-__device__ __forceinline__ bool wait_for(Control &sm, const ChunkParams &p, uint64_t *bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
+// c tanh(x / cap) in units of log 2 (c = cap log2(e)), y being x / cap times 2 log2(e): c - 2 c / (1 + 2^y) is
+// off by 2^-22 c, which is 2^-13 at most for caps up to kCapEnd.  Above, where |x / cap| < 1/4, the series
+// of tanh to its ninth power (2^-26 of it off), and elsewhere the same form, 2^-20 of the score off.
+constexpr float kCapEnd = 256.f;
+__device__ __forceinline__ float capped(const ChunkParams &p, float y) {
+    const float c = p.softcap * kLog2e;
+    const float far = fmaf(-2.f * c, rcp(1.f + ex2(y)), c);
+    if (p.softcap <= kCapEnd) return far;
+    const float x = y * (0.5f / kLog2e), z = x * x;
+    const float series = fmaf(z, fmaf(z, fmaf(z, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f);
+    return fabsf(x) < 0.25f ? c * fmaf(x * z, series, x) : far;
+}
+
+// One try that sleeps in the barrier for up to 20 us (a loop of short tries took half of all issue slots).
+__device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_more(Control &sm, uint32_t *status, uint64_t *bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
     while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (try_wait_long(bar, parity)) return true;
         if (*reinterpret_cast<volatile int32_t *>(&sm.abort_flag)) return false;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
             atomicExch(&sm.abort_flag, 1);
-            if (p.status) atomicOr(p.status, Q8_DEV_TIMEOUT);
+            if (status) atomicOr(status, Q8_DEV_TIMEOUT);
             return false;
         }
     }
@@ -321,6 +410,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
             mbar_init(&sm.s_full[i], 1), mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.q_full[i], 4), mbar_init(&sm.pv_done[i], 1);
         }
+        for (int i = 0; i < 8; ++i) sm.big[0][i] = sm.big[1][i] = make_uint4(0, 0, 0, 0);
         sm.abort_flag = 0;
         sm.start = 0;
         fence_mbar_init();
@@ -460,11 +550,13 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
     const uint32_t q_at = smem_addr(base), tile_at = q_at + MT * C::kQ, raw_at = q_at + C::kRawAt;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, wait_for<C>(sm, p, bar, parity & 1u));
+        if (ok && __any_sync(0xffffffffu, !try_wait_long(bar, parity & 1u)))
+            ok = __all_sync(0xffffffffu, wait_more(sm, p.status, bar, parity & 1u));
     };
 
     if (warp == C::kSoftmax) {
         // ------------------------------------------------------------------ MMA
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kRegsLess));
         uint32_t c = 0, items = 0;  // tiles, items so far
         const auto bar_of = [&](uint32_t pos) { return pos % NR; };
         while (left > 0) {
@@ -472,7 +564,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
             auto qk = [&](int m, uint32_t tile) {  // scores of row tile m, tile `tile`
                 const uint32_t pos = 2 * tile, slot = bar_of(pos);
                 const uint32_t buf = MT == 2 ? m : (tile & 1);
-                if (ok && lane == 0) {
+                if (ok) {
                     const uint64_t a = sw128_desc(q_at + m * C::kQ, 16), b = sw128_desc(tile_at + slot * C::kTile, 16);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
@@ -501,11 +593,11 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                     const uint32_t buf = MT == 2 ? m : (c & 1);
                     wait(&sm.p_full[buf], MT == 2 ? c : c >> 1);
                     tc_fence_after();
-                    if (ok && lane == 0) {
+                    if (ok) {
                         const uint64_t b = sw128_desc(tile_at + vslot * C::kTile, C::kChunk);
 #pragma unroll
                         for (int k = 0; k < BN / 16; ++k)
-                            umma_ts(tmem + C::kColO + m * D, tmem + buf * BN + 8 * k, b + 2048 * k / 16, idesc(D, true), j > 0 || k > 0);
+                            umma_ts(tmem + C::kColO + m * D, tmem + buf * BN + BN / 2 + 8 * k, b + 2048 * k / 16, idesc(D, true), j > 0 || k > 0);
                         umma_commit(&sm.pv_done[m]);
                         if (m == MT - 1) umma_commit(&sm.t_empty[vslot]);
                     }
@@ -525,6 +617,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
         }
     } else if (warp == C::kSoftmax + 1) {
         // --------------------------------------------------------------- loader
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kRegsLess));
         uint32_t pos = 0;
         const int page_mask = (1 << p.page_shift) - 1;
         while (left > 0) {
@@ -549,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                     if (pos >= NW) wait(&sm.raw_empty[slot], pos / NW - 1);
                     if (!ok) continue;
                     if (lane == 0) {
-                        sm.runs[slot] = runs;
+                        sm.meta[slot] = runs | static_cast<uint32_t>(min(BN, wk.end - (wk.base + (wk.unit + j) * BN))) << 8;
                         mbar_arrive_expect_tx(&sm.raw_full[slot], __popc(runs) * 17 * D);
                     }
                     __syncwarp();
@@ -565,71 +658,84 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
         }
     } else if (warp > C::kSoftmax) {
         // ----------------------------------------------------------- converters
-        constexpr int kCT = C::CW * 32;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kRegsLess));
+        constexpr int kCT = C::CW * 32, kPer = D / 16, kUnits = BN * kPer;  // units of 16 codes, of a token and a tile
+        constexpr int kMine = (kUnits + kCT - 1) / kCT;
         const int ct = tid - (C::kSoftmax + 2) * 32;
+        // This thread's units are ct, ct + kCT, ...: unit x0 of tokens t0, t0 + kStep, ..., in the order of the raw tile.
+        // Which half of a unit's 16 codes comes first is chosen so that a warp's loads and its stores each hit all
+        // banks once
+        constexpr int kStep = kCT / kPer;
+        static_assert(kStep % 4 == 0, "the same place in the swizzle");
+        const int t0 = ct / kPer, x0 = ct % kPer;
+        const int half = D == 64 ? (t0 >> 1) & 1 : (D == 128 ? ((x0 >> 2) ^ t0) & 1 : ((x0 >> 2) ^ (x0 >> 3)) & 1);
+        const uint32_t from = ct * 16 + 8 * half, scale_at = (t0 * (D / 32) + (x0 >> 1)) * 2;
+        const uint32_t place = (x0 >> 2) * C::kChunk + t0 * 128;
+        const uint32_t piece0 = place + (((2 * (x0 & 3) + half) ^ (t0 & 7)) << 4), piece1 = place + (((2 * (x0 & 3) + (half ^ 1)) ^ (t0 & 7)) << 4);
         uint32_t pos = 0;
         while (left > 0) {
-            const int seg = static_cast<int>(min(left, static_cast<long long>(wk.units - wk.unit)));
-            for (int jj = 0; jj < 2 * seg; ++jj, ++pos) {
-                const int j = jj >> 1;
-                const bool is_v = jj & 1;
-                const int tok0 = wk.base + (wk.unit + j) * BN;
+            const int n = static_cast<int>(min(left, static_cast<long long>(wk.units - wk.unit)));
+            for (int jj = 0; jj < 2 * n; ++jj, ++pos) {
                 const uint32_t slot = pos % NW, to = pos % NR;
-                const uint32_t raw = raw_at + slot * C::kRaw, scales = raw + C::kCodes;
+                const uint32_t raw = raw_at + slot * C::kRaw;
                 wait(&sm.raw_full[slot], pos / NW);
-                // scales: of tokens that are not there 0, of what is not finite 0; are there any of 512 and more?
-                const uint32_t runs = ok ? sm.runs[slot] : 0u;
-                const int here = min(BN, wk.end - tok0);  // tokens of this tile
-                const bool whole = runs == (1u << (BN / 16)) - 1u && here == BN;
-                constexpr int kWords = BN * D / 64;       // pairs of scales
-                uint32_t odd = 0u;
-                for (int i = ct; i < kWords; i += kCT) odd |= __vcmpgeu2(lds32(scales + 4 * i) & 0x7FFF7FFFu, 0x60006000u);
-                bool big = named_bar_or(1, kCT, odd != 0u);
-                if (big || !whole) {
-                    bool over = false;
-                    for (int i = ct; i < kWords; i += kCT) {
-                        uint32_t w = lds32(scales + 4 * i);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int t = (2 * i + h) / (D / 32);
-                            const uint32_t mag = (w >> (16 * h)) & 0x7FFFu;
-                            const bool there = t < here && ((runs >> (t >> 4)) & 1u);
-                            if (there && mag >= 0x7C00u && p.status) atomicOr(p.status, Q8_DEV_NONFINITE);
-                            if (!there || mag >= 0x7C00u) w &= h ? 0x0000FFFFu : 0xFFFF0000u;
-                            else over = over || mag >= 0x6000u;
-                        }
-                        asm volatile("st.shared.u32 [%0], %1;" :: "r"(scales + 4 * i), "r"(w) : "memory");
-                    }
-                    big = named_bar_or(1, kCT, over);
-                }
                 if (pos >= NR) wait(&sm.t_empty[to], pos / NR - 1);
-                if (ct == 0) {
-                    uint32_t &info = sm.info[(pos >> 1) & 3];
-                    if (is_v) info |= big ? 0x200u : 0u;
-                    else info = (~runs & ((1u << (BN / 16)) - 1u)) | (big ? 0x100u : 0u);
-                }
                 if (ok) {
-                    const uint32_t down = big ? 0x18001800u : 0x3C003C00u;  // 2^-9, or 1
-                    const uint32_t tile = tile_at + to * C::kTile;
-                    constexpr int kPer = D / 16;  // units of 16 codes a token
+                    const uint32_t meta = sm.meta[slot];
+                    const bool is_v = pos & 1u;
+                    const int here = (meta >> 8) & 0xFF, ring = (pos >> 1) & 7;
+                    if (ct == 0 && !is_v) {
+                        sm.unseen[ring] = ~meta & ((1u << (BN / 16)) - 1u);
+                        // for a tile to come (the last that had the place is long done)
+                        sm.big[0][ring ^ 4] = sm.big[1][ring ^ 4] = make_uint4(0, 0, 0, 0);
+                    }
+                    uint2 w0[kMine], w1[kMine];
+                    uint32_t sc[kMine];
 #pragma unroll
-                    for (int n = 0; n < (BN * kPer + kCT - 1) / kCT; ++n) {
-                        const int u = ct + n * kCT, t = u / kPer, x = u % kPer;
-                        if (BN * kPer % kCT != 0 && u >= BN * kPer) break;
-                        // which half of the 16 codes first: both the loads and the stores of a warp then hit all banks once
-                        const int h = D == 64 ? (t >> 1) & 1 : (D == 128 ? ((x >> 2) ^ t) & 1 : ((x >> 2) ^ (x >> 3)) & 1);
-                        const uint32_t from = raw + t * D + x * 16;
-                        const uint2 c0 = lds64(from + 8 * h), c1 = lds64(from + 8 * (h ^ 1));
-                        uint32_t s2 = lds16(scales + (t * (D / 32) + (x >> 1)) * 2);
-                        s2 = hmul2(s2 | s2 << 16, down);
-                        const uint32_t row = tile + (x >> 2) * C::kChunk + t * 128;
+                    for (int i = 0; i < kMine; ++i) {
+                        if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
+                        w0[i] = lds64(raw + from + i * (kCT * 16));
+                        w1[i] = lds64(raw + (from ^ 8) + i * (kCT * 16));
+                        sc[i] = lds16(raw + C::kCodes + scale_at + i * (kStep * (D / 32) * 2));
+                    }
+                    // tokens that are not there and scales that are not finite count as 0, tokens with a scale of 512 or
+                    // more are taken times 2^-9 (a token's units are neighbouring lanes)
+                    uint32_t top = 0u, down = 0u;  // bit i: unit i is taken times 2^-9
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
+                        top = max(top, sc[i] & 0x7FFFu);
+                    }
+                    if (__any_sync(0xffffffffu, top >= 0x6000u) || here < BN || (meta & 0xFFu) != (1u << (BN / 16)) - 1u) {
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i) {
+                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;  // (whole warps)
+                            const int t = t0 + i * kStep;
+                            const bool there = t < here && ((meta >> (t >> 4)) & 1u), finite = (sc[i] & 0x7C00u) != 0x7C00u;
+                            if (there && !finite && p.status) atomicOr(p.status, Q8_DEV_NONFINITE);
+                            if (!there || !finite) sc[i] = 0u;
+                            const uint32_t mine = __ballot_sync(0xffffffffu, (sc[i] & 0x7FFFu) >= 0x6000u);
+                            if ((mine >> (lane & ~(kPer - 1))) & ((1u << kPer) - 1u)) {
+                                down |= 1u << i;
+                                if ((lane & (kPer - 1)) == 0) atomicOr(reinterpret_cast<uint32_t *>(&sm.big[is_v][ring]) + (t >> 5), 1u << (t & 31));
+                            }
+                        }
+                    }
+                    const uint32_t row = tile_at + to * C::kTile;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
+                        uint32_t s2 = sc[i] | sc[i] << 16;
+                        if (down) s2 = hmul2(s2, (down >> i) & 1u ? 0x18001800u : 0x3C003C00u);
+                        // (12 tokens on, of 256 dimensions, the swizzle's third bit is the other one)
+                        const uint32_t flip = kStep % 8 == 0 ? 0u : (i & 1) * 64u, on = i * (kStep * 128);
                         uint32_t a, b, c, d;
-                        codes4_to_f16x2(c0.x, a, b);
-                        codes4_to_f16x2(c0.y, c, d);
-                        sts128(row + (((2 * (x & 3) + h) ^ (t & 7)) << 4), make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
-                        codes4_to_f16x2(c1.x, a, b);
-                        codes4_to_f16x2(c1.y, c, d);
-                        sts128(row + (((2 * (x & 3) + (h ^ 1)) ^ (t & 7)) << 4), make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
+                        codes4_to_f16x2(w0[i].x, a, b);
+                        codes4_to_f16x2(w0[i].y, c, d);
+                        sts128(row + (piece0 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
+                        codes4_to_f16x2(w1[i].x, a, b);
+                        codes4_to_f16x2(w1[i].y, c, d);
+                        sts128(row + (piece1 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
                     }
                     fence_proxy_async_smem();
                 }
@@ -639,11 +745,13 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                     mbar_arrive(&sm.raw_empty[slot]);
                 }
             }
-            left -= seg + kEndUnits;
+            left -= n + kEndUnits;
             if (left > 0) wk.next(p);
         }
     } else {
         // -------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(C::kRegs));
+        constexpr int kLanes = D / 8;            // lanes of a query or answer row, 16 bytes each
         const int m = warp >> 2, r = tid & 127;  // row tile, row
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t o_at = tmem + lanes + C::kColO + m * D;
@@ -660,32 +768,34 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
             const int hi = live ? p1 : INT32_MAX, lo = live && p.window > 0 && from > 0 ? static_cast<int>(from) : 0;
 
             // ---- the query row: scaled to a largest magnitude in [2^14, 2^15), binary16, into the tile
+            // (kLanes lanes have a row: a warp loads whole rows, and each thread learns its own row's exponent)
             float fac;
             {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + qrow * p.ldq + static_cast<int64_t>(head) * D);
-                uint32_t top = 0u;  // of bf16 magnitudes, in either half
-                if (live) {
+                const uint64_t src = reinterpret_cast<uint64_t>(p.q + qrow * p.ldq + static_cast<int64_t>(head) * D);
+                int ex = 30;
 #pragma unroll 8
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 v = __ldg(src + i);
-                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-                    }
-                }
-                const int ex = min(max(static_cast<int>(max(top >> 16, top & 0xFFFFu) >> 7), 30), 254);
-                const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - ex) << 23) * (p.scale < 0.f ? -1.f : 1.f);
-                fac = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
-                fac = p.softcap > 0.f ? fac / p.softcap : fac * kLog2e;
-                fac = fminf(fac, FLT_MAX);  // a score of zero stays one
-                const uint32_t to = q_at + m * C::kQ + r * 128;
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < kLanes; ++i) {
+                    const int x = i * (32 / kLanes) + lane / kLanes;  // row of the warp
+                    const uint64_t from = __shfl_sync(0xffffffffu, src, x);
+                    const bool there = __shfl_sync(0xffffffffu, live, x);
+                    const uint4 v = there ? __ldg(reinterpret_cast<const uint4 *>(from) + lane % kLanes) : make_uint4(0, 0, 0, 0);
+                    uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+#pragma unroll
+                    for (int o = 1; o < kLanes; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int e = min(max(static_cast<int>(max(top >> 16, top & 0xFFFFu) >> 7), 30), 254);
+                    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - e) << 23) * (p.scale < 0.f ? -1.f : 1.f);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     uint32_t h[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) h[k] = f32x2_to_f16x2(bf16lo_f32(w[k]) * up, bf16hi_f32(w[k]) * up);
-                    sts128(to + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+                    const int c8 = lane % kLanes, row = 32 * (warp & 3) + x;
+                    sts128(q_at + m * C::kQ + (c8 >> 3) * 16384 + row * 128 + (((c8 & 7) ^ (row & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+                    const int of_mine = __shfl_sync(0xffffffffu, e, lane % (32 / kLanes) * kLanes);
+                    if (i == lane / (32 / kLanes)) ex = of_mine;
                 }
+                fac = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+                fac = p.softcap > 0.f ? fac / p.softcap * (2.f * kLog2e) : fac * kLog2e;
+                fac = fminf(fac, FLT_MAX);  // a score of zero stays one
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.q_full[m]);
@@ -698,42 +808,53 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                 const uint32_t s_at = tmem + lanes + buf * BN;
                 const uint32_t vpos = 2 * c + 1;
                 wait(&sm.s_full[buf], MT == 2 ? c : c >> 1);
-                wait(&sm.t_full[vpos % NR], vpos / NR);
                 tc_fence_after();
                 if (ok) {
-                    const uint32_t info = *reinterpret_cast<volatile uint32_t *>(&sm.info[c & 3]);
-                    const float f = info & 0x100u ? fminf(fac * 512.f, FLT_MAX) : fac;
-                    const float lift = info & 0x200u ? 9.f : 0.f;
+                    const uint32_t unseen = *reinterpret_cast<volatile uint32_t *>(&sm.unseen[c & 7]);
+                    const uint4 bk = *const_cast<const uint4 *>(&sm.big[0][c & 7]);
+                    const float f = fac;
+                    const bool cap = p.softcap > 0.f;
                     // bits of the tokens of 32 that the row sees
                     auto seen = [&](int c0) -> uint32_t {
                         const int a = lo - tok0 - c0, b = hi - tok0 - c0;  // [a, b)
                         uint32_t bits = b >= 32 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << b) - 1u);
                         if (a > 0) bits &= a >= 32 ? 0u : ~((1u << a) - 1u);
-                        if ((info >> (c0 >> 4)) & 1u) bits &= 0xFFFF0000u;
-                        if ((info >> ((c0 >> 4) + 1)) & 1u) bits &= 0x0000FFFFu;
+                        if ((unseen >> (c0 >> 4)) & 1u) bits &= 0xFFFF0000u;
+                        if ((unseen >> ((c0 >> 4) + 1)) & 1u) bits &= 0x0000FFFFu;
                         return bits;
                     };
-                    const bool masked = __any_sync(0xffffffffu, lo > tok0 || hi < tok0 + BN) || (info & 0xFFu);
-                    float y = -INFINITY;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < BN; c0 += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(s_at + c0, v);
-                        tmem_ld_wait();
-                        if (masked) {
-                            const uint32_t bits = seen(c0);
+                    const bool masked = __any_sync(0xffffffffu, lo > tok0 || hi < tok0 + BN) || unseen;
+                    uint32_t v[BN];  // the row's scores
+                    tmem_ld(s_at, v);
+                    if (masked) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) y = fmaxf(y, (bits >> i) & 1u ? __uint_as_float(v[i]) : -INFINITY);
-                        } else {
-                            float y1 = -INFINITY;
+                        for (int k = 0; k < BN; k += 32) {
+                            const uint32_t bits = seen(k);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) y = fmaxf(y, __uint_as_float(v[i])), y1 = fmaxf(y1, __uint_as_float(v[i + 1]));
-                            y = fmaxf(y, y1);
+                            for (int i = 0; i < 32; ++i) v[k + i] = (bits >> i) & 1u ? v[k + i] : 0xFF800000u;
                         }
                     }
-                    // (fac >= 0: the sign of scale is in the query)
+                    const bool shrunk = __any_sync(0xffffffffu, (bk.x | bk.y | bk.z | bk.w) != 0u);
+                    if (shrunk) {  // keys that are times 2^-9
+                        const uint32_t w[4] = {bk.x, bk.y, bk.z, bk.w};
+#pragma unroll
+                        for (int i = 0; i < BN; ++i)
+                            if ((w[i >> 5] >> (i & 31)) & 1u) v[i] = __float_as_uint(__uint_as_float(v[i]) * 512.f);
+                    }
+                    float y4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < BN; i += 8)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) y4[n] = max3(y4[n], __uint_as_float(v[i + n]), __uint_as_float(v[i + 4 + n]));
+                    float y = fmaxf(max3(y4[0], y4[1], y4[2]), y4[3]);
+                    // (f >= 0: the sign of scale is in the query)
                     y = y == -INFINITY ? y : y * f;
-                    if (p.softcap > 0.f && y != -INFINITY) y = p.softcap * kLog2e * tanhf(y);
+                    if (cap && y != -INFINITY) y = capped(p, y);
+                    wait(&sm.t_full[vpos % NR], vpos / NR);
+                    const uint4 bv = *const_cast<const uint4 *>(&sm.big[1][c & 7]);
+                    // values that are times 2^-9: their weights are raised by 2^9
+                    const bool raised = __any_sync(0xffffffffu, (bv.x | bv.y | bv.z | bv.w) != 0u);
+                    const float lift = raised ? 9.f : 0.f;
                     const float z = y + lift;
                     const bool grows = z > top;
                     if (__any_sync(0xffffffffu, grows)) {
@@ -751,55 +872,84 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                             tc_fence_after();
                             if (ok) {
 #pragma unroll 1
-                                for (int d = 0; d < D; d += 32) {
-                                    uint32_t v[32];
-                                    tmem_ld32(o_at + d, v);
-                                    tmem_ld_wait();
+                                for (int d = 0; d < D; d += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld(o_at + d, o);
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * g);
-                                    tmem_st32(o_at + d, v);
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * g);
+                                    tmem_st(o_at + d, o);
                                 }
                             }
                         }
                     }
-                    const float shift = ref - lift;  // weights are 2^(s - shift)
-                    const bool slow = masked || p.softcap > 0.f || __any_sync(0xffffffffu, !(fabsf(y) < kPlain));
-                    unsigned long long sum = 0ull;
+                    const float shift = ref;  // weights are 2^(s - shift)
+                    unsigned long long sum[2] = {0ull, 0ull};
+                    if (raised || p.softcap > kCapEnd || __any_sync(0xffffffffu, !(f > 0.f) || (y > -INFINITY && !(fabsf(y) < kPlain)))) {
+                        // raised weights, wide caps, and large scores, whose product's rounding would show in the weight (product
+                        // and difference one after the other): few at a time, read again.  From the last to the first,
+                        // as the weights go where scores lay that have been read
+                        const uint32_t wk4[4] = {bk.x, bk.y, bk.z, bk.w}, wv4[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll 1
-                    for (int c0 = 0; c0 < BN; c0 += 32) {
-                        uint32_t v[32], h[16];
-                        tmem_ld32(s_at + c0, v);
-                        tmem_ld_wait();
-                        if (slow) {
-                            const uint32_t bits = masked ? seen(c0) : 0xFFFFFFFFu;
+                        for (int k = BN - 16; k >= 0; k -= 16) {
+                            uint32_t x[16], h[8];
+                            tmem_ld(s_at + k, x);
+                            const uint32_t bits = masked ? seen(k & ~31) >> (k & 16) : 0xFFFFu;
+                            uint32_t bigk = 0u, bigv = 0u;
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float x[2];
+                            for (int n = 0; n < 4; ++n)
+                                if ((k >> 5) == n) bigk = wk4[n] >> (k & 16), bigv = wv4[n] >> (k & 16);
 #pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    x[k] = __fmul_rn(__uint_as_float(v[i + k]), f);
-                                    if (p.softcap > 0.f) x[k] = p.softcap * kLog2e * tanhf(x[k]);
-                                    x[k] = (bits >> (i + k)) & 1u ? ex2(__fadd_rn(x[k], -shift)) : 0.f;
+                            for (int i = 0; i < 16; i += 2) {
+                                float w[2], u[2];
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) {
+                                    w[n] = __uint_as_float(x[i + n]);
+                                    if ((bigk >> (i + n)) & 1u) w[n] *= 512.f;
+                                    w[n] = __fmul_rn(w[n], f);
+                                    if (cap) w[n] = capped(p, w[n]);
+                                    w[n] = (bits >> (i + n)) & 1u ? ex2(__fadd_rn(w[n], -shift)) : 0.f;
+                                    u[n] = (bigv >> (i + n)) & 1u ? w[n] * 512.f : w[n];
                                 }
-                                h[i / 2] = f32x2_to_f16x2(x[0], x[1]);
-                                sum = add2(sum, pack2(x[0], x[1]));
+                                h[i / 2] = f32x2_to_f16x2(u[0], u[1]);
+                                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(w[0], w[1]));
+                            }
+                            tmem_st(s_at + BN / 2 + k / 2, h);
+                        }
+                    } else {
+                        if (cap) {
+                            const float c1 = p.softcap * kLog2e, c2 = -2.f * c1, c3 = c1 - shift;
+#pragma unroll
+                            for (int i = 0; i < BN; ++i) {
+                                const float e = fmaf(c2, rcp(1.f + ex2(__uint_as_float(v[i]) * f)), c3);
+                                v[i] = masked && v[i] == 0xFF800000u ? v[i] : __float_as_uint(e);
                             }
                         } else {
                             const unsigned long long f2 = pack2(f, f), n2 = pack2(-shift, -shift);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const unsigned long long x = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f2, n2);
-                                const float x0 = ex2(lo2(x)), x1 = ex2(hi2(x));
-                                h[i / 2] = f32x2_to_f16x2(x0, x1);
-                                sum = add2(sum, pack2(x0, x1));
+                            for (int i = 0; i < BN; i += 2) {
+                                const unsigned long long e = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f2, n2);
+                                v[i] = static_cast<uint32_t>(e), v[i + 1] = static_cast<uint32_t>(e >> 32);
                             }
                         }
-                        tmem_st16(s_at + c0 / 2, h);
+#pragma unroll
+                        for (int k = 0; k < BN; k += 32) {
+                            uint32_t h[16];
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float w0 = ex2(__uint_as_float(v[k + i])), w1 = ex2(__uint_as_float(v[k + i + 1]));
+                                h[i / 2] = f32x2_to_f16x2(w0, w1);
+                                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(w0, w1));
+                            }
+                            tmem_st(s_at + BN / 2 + k / 2, h);
+                        }
                     }
-                    const float part = lo2(sum) + hi2(sum);
-                    l += lift > 0.f ? part * 0x1p-9f : part;
+                    const float part = (lo2(sum[0]) + hi2(sum[0])) + (lo2(sum[1]) + hi2(sum[1]));
+                    l += part;
                     tmem_st_wait();
                 }
+                // Every phase of pv_done is waited for in its turn: a wait on a later one alone could take the phase before
+                // it, unfinished, for its own.  (Where two row tiles take turns, these scores came after that product.)
+                if (MT == 1 && j > 0) wait(&sm.pv_done[m], c - 1);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_full[buf]);
@@ -809,7 +959,28 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
 
             // ---- the answer, or a part of it
             const int64_t at = qrow * p.q_heads + head;
-            auto store = [&](int d, const float (&v)[8]) { store8(reinterpret_cast<__nv_bfloat16 *>(p.out) + at * D + d, v); };
+            // An answer row lies in the query tile's place (same size, same swizzle) before it goes out, whole rows at a time
+            auto stage = [&](int d, const float (&x)[8]) {
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                    h[i] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+                sts128(q_at + m * C::kQ + (d >> 6) * 16384 + r * 128 + ((((d >> 3) & 7) ^ (r & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+            };
+            auto send = [&]() {
+                __syncwarp();
+#pragma unroll 4
+                for (int i = 0; i < kLanes; ++i) {
+                    const int x = i * (32 / kLanes) + lane / kLanes, row = 32 * (warp & 3) + x, c8 = lane % kLanes;
+                    const int64_t to = __shfl_sync(0xffffffffu, at, x);
+                    const bool there = __shfl_sync(0xffffffffu, live, x);
+                    const uint4 v = lds128(q_at + m * C::kQ + (c8 >> 3) * 16384 + row * 128 + (((c8 & 7) ^ (row & 7)) << 4));
+                    if (there) *reinterpret_cast<uint4 *>(p.out + to * D + 8 * c8) = v;
+                }
+                __syncwarp();
+            };
             auto give_lse = [&](float mx, float ls) {
                 if (p.lse) p.lse[at] = ls == 0.f ? -INFINITY : fmaf(mx + kLift, 0.69314718055994531f, logf(ls * 0x1p-11f));
             };
@@ -818,18 +989,16 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
 #pragma unroll 1
                 for (int d = 0; d < D && ok; d += 32) {
                     uint32_t v[32];
-                    tmem_ld32(o_at + d, v);
-                    tmem_ld_wait();
-                    if (live) {
+                    tmem_ld(o_at + d, v);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            float x[8];
+                    for (int i = 0; i < 32; i += 8) {
+                        float x[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) x[k] = l == 0.f ? 0.f : __uint_as_float(v[i + k]) * inv;
-                            store(d + i, x);
-                        }
+                        for (int k = 0; k < 8; ++k) x[k] = l == 0.f ? 0.f : __uint_as_float(v[i + k]) * inv;
+                        stage(d + i, x);
                     }
                 }
+                if (ok) send();
                 if (live && ok) give_lse(mm, l);
             } else {
                 const int c0 = static_cast<int>(item0 / per), c1 = static_cast<int>((item0 + wk.units - 1) / per);
@@ -839,8 +1008,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
 #pragma unroll 1
                 for (int d = 0; d < D && ok; d += 32) {
                     uint32_t v[32];
-                    tmem_ld32(o_at + d, v);
-                    tmem_ld_wait();
+                    tmem_ld(o_at + d, v);
                     if (live) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
@@ -855,9 +1023,9 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                     if (sm.last[m]) *ticket = 0u;
                 }
                 named_bar(2 + m, 128);
-                if (sm.last[m] && live) {
+                if (sm.last[m]) {
                     float mx = -INFINITY, ls = 0.f;
-                    auto ml = [&](int k) { return __ldcg(reinterpret_cast<const float2 *>(part(k) + D * 128) + r); };
+                    auto ml = [&](int k) { return live ? __ldcg(reinterpret_cast<const float2 *>(part(k) + D * 128) + r) : make_float2(0.f, 1.f); };
                     for (int k = c0; k <= c1; ++k) mx = fmaxf(mx, ml(k).x);
                     auto weight = [&](float m1) { return m1 == -INFINITY ? (mx == -INFINITY ? 1.f : 0.f) : ex2(m1 - mx); };
                     for (int k = c0; k <= c1; ++k) {
@@ -876,7 +1044,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                             const float4 *src = reinterpret_cast<const float4 *>(part(k)) + d / 4 * 128 + r;
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float4 v = __ldcg(src + i * 128);
+                                const float4 v = live ? __ldcg(src + i * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
                                 x[4 * i] = fmaf(v.x, w, x[4 * i]), x[4 * i + 1] = fmaf(v.y, w, x[4 * i + 1]);
                                 x[4 * i + 2] = fmaf(v.z, w, x[4 * i + 2]), x[4 * i + 3] = fmaf(v.w, w, x[4 * i + 3]);
                             }
@@ -886,10 +1054,11 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                             float o[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k) o[k] = ls == 0.f ? 0.f : x[i + k] * inv;
-                            store(d + i, o);
+                            stage(d + i, o);
                         }
                     }
-                    give_lse(mx, ls);
+                    send();
+                    if (live) give_lse(mx, ls);
                 }
                 named_bar(2 + m, 128);  // the flag has been read
             }
