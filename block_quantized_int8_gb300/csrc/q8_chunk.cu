@@ -54,6 +54,7 @@ namespace {
 constexpr int kMaxGrid = 160;   // CTAs a launch may have (sizes the workspace)
 constexpr int kEndUnits = 3;    // what beginning and ending an item takes, in units' time
 constexpr int kMinUnits = 2;    // units a CTA takes at least
+constexpr int kWhole = 4;       // items of up to so many are not divided (a join takes longer than three tiles)
 constexpr int kScan = 512;      // sequences looked at together
 constexpr float kLift = 11.0f;  // log2 of the largest weight when the reference is set
 constexpr float kTop = 15.0f;   // and of the largest that leaves it
@@ -333,6 +334,11 @@ struct Walk {
         nq = seq_tiles<C>(p, s);
         units = tile_units<C>(p, s, qt, base, end);
     }
+    // the units of this item that a CTA takes with `left` of its stretch of the list left: short items are not
+    // divided, but belong to the CTA that they begin in
+    __device__ __forceinline__ int stretch(long long left) const {
+        return units <= kWhole ? units : static_cast<int>(min(left, static_cast<long long>(units - unit)));
+    }
     // the next item (the caller knows that there is one)
     __device__ __forceinline__ void next(const ChunkParams &p) {
         unit = 0;
@@ -531,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
         wk.kvh = static_cast<int>(in / cost);
         wk.unit = static_cast<int>(in - static_cast<long long>(wk.kvh) * cost);
         item0 = u0 - wk.unit;
-        if (wk.unit >= wk.units) {  // at the end of an item that others work on: begin with the next
+        if (wk.unit >= wk.units || (wk.unit > 0 && wk.units <= kWhole)) {  // in an item that others end: begin with the next
             left -= cost - wk.unit;
             item0 += cost;
             if (left > 0) wk.next(p);
@@ -560,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
         uint32_t c = 0, items = 0;  // tiles, items so far
         const auto bar_of = [&](uint32_t pos) { return pos % NR; };
         while (left > 0) {
-            const int seg = static_cast<int>(min(left, static_cast<long long>(wk.units - wk.unit)));
+            const int seg = wk.stretch(left);
             auto qk = [&](int m, uint32_t tile) {  // scores of row tile m, tile `tile`
                 const uint32_t pos = 2 * tile, slot = bar_of(pos);
                 const uint32_t buf = MT == 2 ? m : (tile & 1);
@@ -621,7 +627,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
         uint32_t pos = 0;
         const int page_mask = (1 << p.page_shift) - 1;
         while (left > 0) {
-            const int seg = static_cast<int>(min(left, static_cast<long long>(wk.units - wk.unit)));
+            const int seg = wk.stretch(left);
             const int32_t *row = p.table + static_cast<int64_t>(wk.b) * p.table_width;
             auto page_of = [&](int j) {
                 const int tok = wk.base + (wk.unit + j) * BN + 16 * lane;
@@ -674,7 +680,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
         const uint32_t piece0 = place + (((2 * (x0 & 3) + half) ^ (t0 & 7)) << 4), piece1 = place + (((2 * (x0 & 3) + (half ^ 1)) ^ (t0 & 7)) << 4);
         uint32_t pos = 0;
         while (left > 0) {
-            const int n = static_cast<int>(min(left, static_cast<long long>(wk.units - wk.unit)));
+            const int n = wk.stretch(left);
             for (int jj = 0; jj < 2 * n; ++jj, ++pos) {
                 const uint32_t slot = pos % NW, to = pos % NR;
                 const uint32_t raw = raw_at + slot * C::kRaw;
@@ -757,7 +763,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
         const uint32_t o_at = tmem + lanes + C::kColO + m * D;
         uint32_t c = 0;
         while (left > 0) {
-            const int seg = static_cast<int>(min(left, static_cast<long long>(wk.units - wk.unit)));
+            const int seg = wk.stretch(left);
             const int rr = wk.qt * C::RT + m * 128 + r;  // row of the sequence
             const bool live = rr < wk.s.n * p.group;
             const int tok = live ? rr / p.group : 0, head = wk.kvh * p.group + (live ? rr - tok * p.group : 0);
