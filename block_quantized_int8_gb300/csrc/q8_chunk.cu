@@ -779,12 +779,20 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
             {
                 const uint64_t src = reinterpret_cast<uint64_t>(p.q + qrow * p.ldq + static_cast<int64_t>(head) * D);
                 int ex = 30;
-#pragma unroll 8
-                for (int i = 0; i < kLanes; ++i) {
-                    const int x = i * (32 / kLanes) + lane / kLanes;  // row of the warp
+                uint4 raw[8];  // eight loads under way at a time
+#pragma unroll 1
+                for (int i0 = 0; i0 < kLanes; i0 += 8) {
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    const int x = (i0 + b) * (32 / kLanes) + lane / kLanes;  // row of the warp
                     const uint64_t from = __shfl_sync(0xffffffffu, src, x);
                     const bool there = __shfl_sync(0xffffffffu, live, x);
-                    const uint4 v = there ? __ldg(reinterpret_cast<const uint4 *>(from) + lane % kLanes) : make_uint4(0, 0, 0, 0);
+                    raw[b] = there ? __ldg(reinterpret_cast<const uint4 *>(from) + lane % kLanes) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    const int i = i0 + b, x = i * (32 / kLanes) + lane / kLanes;
+                    const uint4 v = raw[b];
                     uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
 #pragma unroll
                     for (int o = 1; o < kLanes; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -798,6 +806,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                     sts128(q_at + m * C::kQ + (c8 >> 3) * 16384 + row * 128 + (((c8 & 7) ^ (row & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
                     const int of_mine = __shfl_sync(0xffffffffu, e, lane % (32 / kLanes) * kLanes);
                     if (i == lane / (32 / kLanes)) ex = of_mine;
+                }
                 }
                 fac = fabsf(p.scale) * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
                 fac = p.softcap > 0.f ? fac / p.softcap * (2.f * kLog2e) : fac * kLog2e;
@@ -1040,23 +1049,25 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                     }
                     const float inv = ls == 0.f ? 0.f : 1.f / ls;
 #pragma unroll 1
-                    for (int d = 0; d < D; d += 32) {
-                        float x[32];
+                    for (int d = 0; d < D; d += 64) {
+                        float x[64];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                        for (int i = 0; i < 64; ++i) x[i] = 0.f;
 #pragma unroll 1
                         for (int k = c0; k <= c1; ++k) {
-                            const float w = weight(ml(k).x);
                             const float4 *src = reinterpret_cast<const float4 *>(part(k)) + d / 4 * 128 + r;
+                            float4 v[16];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 v = live ? __ldcg(src + i * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
-                                x[4 * i] = fmaf(v.x, w, x[4 * i]), x[4 * i + 1] = fmaf(v.y, w, x[4 * i + 1]);
-                                x[4 * i + 2] = fmaf(v.z, w, x[4 * i + 2]), x[4 * i + 3] = fmaf(v.w, w, x[4 * i + 3]);
+                            for (int i = 0; i < 16; ++i) v[i] = live ? __ldcg(src + i * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            const float w = weight(ml(k).x);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                x[4 * i] = fmaf(v[i].x, w, x[4 * i]), x[4 * i + 1] = fmaf(v[i].y, w, x[4 * i + 1]);
+                                x[4 * i + 2] = fmaf(v[i].z, w, x[4 * i + 2]), x[4 * i + 3] = fmaf(v[i].w, w, x[4 * i + 3]);
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
+                        for (int i = 0; i < 64; i += 8) {
                             float o[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k) o[k] = ls == 0.f ? 0.f : x[i + k] * inv;
