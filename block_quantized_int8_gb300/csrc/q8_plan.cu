@@ -20,6 +20,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 constexpr int64_t kFewTokens = 4096;
+constexpr int kBatch = 4;  // rows that a thread has under way
 
 struct PlanParams {
     int32_t *table;
@@ -108,33 +109,44 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         // their rows
         const int64_t first = s_start[0], last = min(rows, p.T);
         const int held = min(kThreads, p.batch - b0);
-        for (int64_t t = first + rank * kThreads + tid; t < last; t += kCtas * kThreads) {
-            int lo = 0, hi = held;  // the last sequence that begins at or before t
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s_start[mid] <= t) lo = mid;
-                else hi = mid;
-            }
-            const int32_t pos = s_old[lo] + static_cast<int32_t>(t - s_start[lo]);
-            const int32_t entry = pos >> p.page_shift;
-            const int32_t seq_had = (s_old[lo] + page - 1) >> p.page_shift;
-            int32_t *at = p.table + static_cast<int64_t>(b0 + lo) * p.table_width + entry;
-            int32_t pg;
-            if (entry < seq_had || !p.free_pages) {
-                pg = *at;
-                if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) pg = -1, flags |= Q8_DEV_BAD_INDEX;
-            } else {
-                const int64_t k = s_taken[lo] + entry;  // rank among the new pages
-                if (k < count) {
-                    pg = p.free_pages[count - 1 - k];
-                    if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) pg = -1, flags |= Q8_DEV_BAD_INDEX;
-                } else {
-                    pg = -1, flags |= Q8_DEV_NO_PAGE;
+        // (kBatch rows of a thread at a time, so that their loads of pages are under way together)
+        constexpr int64_t kRows = kCtas * kThreads;
+        for (int64_t tb = first + rank * kThreads + tid; tb < last; tb += kBatch * kRows) {
+            int32_t pos[kBatch], pg[kBatch], *at[kBatch];
+            bool taken_now[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t t = tb + i * kRows;
+                if (t >= last) break;
+                int lo = 0, hi = held;  // the last sequence that begins at or before t
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_start[mid] <= t) lo = mid;
+                    else hi = mid;
                 }
-                if ((pos & (page - 1)) == 0) *at = pg;
+                pos[i] = s_old[lo] + static_cast<int32_t>(t - s_start[lo]);
+                const int32_t entry = pos[i] >> p.page_shift;
+                const int32_t seq_had = (s_old[lo] + page - 1) >> p.page_shift;
+                at[i] = p.table + static_cast<int64_t>(b0 + lo) * p.table_width + entry;
+                taken_now[i] = entry >= seq_had && p.free_pages;
+                const int64_t k = s_taken[lo] + entry;  // rank among the new pages
+                if (!taken_now[i]) pg[i] = *at[i];
+                else if (k < count) pg[i] = p.free_pages[count - 1 - k];
+                else flags |= Q8_DEV_NO_PAGE, pg[i] = INT32_MIN;
             }
-            p.slots[t] = pg < 0 ? -1 : (static_cast<int64_t>(pg) << p.page_shift) + (pos & (page - 1));
-            p.positions[t] = pos;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t t = tb + i * kRows;
+                if (t >= last) break;
+                if (static_cast<uint32_t>(pg[i]) >= static_cast<uint32_t>(p.pages)) {
+                    if (pg[i] != INT32_MIN || !taken_now[i]) flags |= Q8_DEV_BAD_INDEX;
+                    pg[i] = -1;
+                }
+                const int32_t off = pos[i] & (page - 1);
+                if (taken_now[i] && off == 0) *at[i] = pg[i];
+                p.slots[t] = pg[i] < 0 ? -1 : (static_cast<int64_t>(pg[i]) << p.page_shift) + off;
+                p.positions[t] = pos[i];
+            }
         }
         __syncthreads();  // the sequences in hand give way to the next
     }

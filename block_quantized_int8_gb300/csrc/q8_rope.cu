@@ -28,7 +28,7 @@ namespace q8 {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kRopeThreads = 128, kAppendThreads = 128;
 constexpr int kMaxPairs = 128;  // head_dim 256
 
 struct RopeParams {
@@ -51,6 +51,7 @@ __device__ __forceinline__ float turn1(float x1, float x2, float c, float s) { r
 __device__ __forceinline__ float turn2(float x1, float x2, float c, float s) { return fmaf(x2, c, __fmul_rn(x1, s)); }
 
 // The token's cosines and sines, times factor.
+template <int kThreads>
 __device__ __forceinline__ void make_angles(const RopeParams &p, int64_t token, float *s_cos, float *s_sin) {
     const int64_t pos = p.positions[token];
     for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) {
@@ -72,129 +73,160 @@ __device__ __forceinline__ void lds8(const float *s, float (&v)[8]) {
 // Sixteen values of a head (item i of D / 16), turned, to bf16: dimensions 8 i and rot / 2 + 8 i on of
 // the half layout, 16 i on of the interleaved and of what passes.
 template <typename T, bool kInter>
-__device__ __forceinline__ void turn_item(const RopeParams &p, const T *x, __nv_bfloat16 *y, int i, const float *s_cos,
-                                          const float *s_sin) {
-    float a[8], b[8], c[8], s[8];
+struct Item {
     Raw8<T> ra, rb;
-    if (16 * i >= p.rot || kInter) {
-        ra.load(x + 16 * i), rb.load(x + 16 * i + 8);
+    __device__ __forceinline__ void load(const RopeParams &p, const T *x, int i) {
+        const bool half = !kInter && 16 * i < p.rot;
+        ra.load(x + (half ? 8 * i : 16 * i));
+        rb.load(x + (half ? p.rot / 2 + 8 * i : 16 * i + 8));
+    }
+    __device__ __forceinline__ void finish(const RopeParams &p, __nv_bfloat16 *y, int i, const float *s_cos, const float *s_sin) const {
+        float a[8], b[8], c[8], s[8];
         ra.widen(a), rb.widen(b);
-        if (16 * i < p.rot) {
+        const bool turns = 16 * i < p.rot;
+        if (turns) {
             lds8(s_cos + 8 * i, c), lds8(s_sin + 8 * i, s);
+            if constexpr (kInter) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float x1 = a[2 * j], x2 = a[2 * j + 1], z1 = b[2 * j], z2 = b[2 * j + 1];
-                a[2 * j] = turn1(x1, x2, c[j], s[j]), a[2 * j + 1] = turn2(x1, x2, c[j], s[j]);
-                b[2 * j] = turn1(z1, z2, c[4 + j], s[4 + j]), b[2 * j + 1] = turn2(z1, z2, c[4 + j], s[4 + j]);
+                for (int j = 0; j < 4; ++j) {
+                    const float x1 = a[2 * j], x2 = a[2 * j + 1], z1 = b[2 * j], z2 = b[2 * j + 1];
+                    a[2 * j] = turn1(x1, x2, c[j], s[j]), a[2 * j + 1] = turn2(x1, x2, c[j], s[j]);
+                    b[2 * j] = turn1(z1, z2, c[4 + j], s[4 + j]), b[2 * j + 1] = turn2(z1, z2, c[4 + j], s[4 + j]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float x1 = a[j], x2 = b[j];
+                    a[j] = turn1(x1, x2, c[j], s[j]), b[j] = turn2(x1, x2, c[j], s[j]);
+                }
             }
         }
-        store8(y + 16 * i, a), store8(y + 16 * i + 8, b);
-    } else {
-        const int half = p.rot / 2;
-        ra.load(x + 8 * i), rb.load(x + half + 8 * i);
-        ra.widen(a), rb.widen(b);
-        lds8(s_cos + 8 * i, c), lds8(s_sin + 8 * i, s);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float x1 = a[j], x2 = b[j];
-            a[j] = turn1(x1, x2, c[j], s[j]), b[j] = turn2(x1, x2, c[j], s[j]);
-        }
-        store8(y + 8 * i, a), store8(y + half + 8 * i, b);
+        const bool half = !kInter && turns;
+        store8(y + (half ? 8 * i : 16 * i), a), store8(y + (half ? p.rot / 2 + 8 * i : 16 * i + 8), b);
     }
-}
+};
+
+// All heads of a row, each thread's next item on its way while it turns one; the first (begin()) while the
+// angles are made.
+template <typename T, bool kInter, int kThreads>
+struct Heads {
+    Item<T, kInter> item;
+    int u, n, shift;
+    const T *x;
+    __device__ __forceinline__ int64_t head_of(const RopeParams &p, int v) const { return static_cast<int64_t>(v >> shift) << p.d_shift; }
+    __device__ __forceinline__ void begin(const RopeParams &p, const T *row) {
+        x = row, shift = p.d_shift - 4, n = p.heads << shift, u = threadIdx.x;
+        if (u < n) item.load(p, x + head_of(p, u), u & ((1 << shift) - 1));
+    }
+    __device__ __forceinline__ void run(const RopeParams &p, __nv_bfloat16 *y, const float *s_cos, const float *s_sin) {
+        while (u < n) {
+            const Item<T, kInter> now = item;
+            const int v = u;
+            u += kThreads;
+            // (y may be x: another item's values are read before this one's are written, and no two share any)
+            if (u < n) item.load(p, x + head_of(p, u), u & ((1 << shift) - 1));
+            now.finish(p, y + head_of(p, v), v & ((1 << shift) - 1), s_cos, s_sin);
+        }
+    }
+};
 
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
     const int64_t token = blockIdx.x;
-    make_angles(p, token, s_cos, s_sin);
+    Heads<T, kInter, kRopeThreads> heads;
+    heads.begin(p, static_cast<const T *>(p.x) + token * p.ldx);
+    make_angles<kRopeThreads>(p, token, s_cos, s_sin);
     __syncthreads();
-    const T *x = static_cast<const T *>(p.x) + token * p.ldx;
-    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + token * p.ldy;
-    const int per = 1 << (p.d_shift - 4);  // items a head
-    for (int u = threadIdx.x; u < p.heads * per; u += kThreads) {
-        const int64_t head = static_cast<int64_t>(u >> (p.d_shift - 4)) << p.d_shift;
-        turn_item<T, kInter>(p, x + head, y + head, u & (per - 1), s_cos, s_sin);
-    }
+    heads.run(p, static_cast<__nv_bfloat16 *>(p.y) + token * p.ldy, s_cos, s_sin);
 }
 
-// Eight neighbouring dimensions d .. d + 7 of a key head, turned.  In the half layout the other
-// halves of their pairs are loaded too (from L1 for one of the two lanes that want them).
+// Eight neighbouring dimensions d .. d + 7 of a key or value head.  A key's turn; in the half layout
+// the other halves of their pairs are loaded too (from L1 for one of the two lanes that want them).
 template <typename T, bool kInter>
-__device__ __forceinline__ void turned8(const RopeParams &p, const T *x, int d, float (&v)[8], const float *s_cos,
-                                        const float *s_sin) {
-    Raw8<T> r;
-    r.load(x + d);
-    r.widen(v);
-    if (d >= p.rot) return;
-    float c[8], s[8];
-    if constexpr (kInter) {
-        const float4 c4 = *reinterpret_cast<const float4 *>(s_cos + d / 2), s4 = *reinterpret_cast<const float4 *>(s_sin + d / 2);
-        c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
-        s[0] = s4.x, s[1] = s4.y, s[2] = s4.z, s[3] = s4.w;
+struct Unit8 {
+    Raw8<T> own, other;
+    __device__ __forceinline__ void load(const RopeParams &p, const T *x, int d, bool turns) {
+        own.load(x + d);
+        if (!kInter && turns && d < p.rot) other.load(x + (d >= p.rot / 2 ? d - p.rot / 2 : d + p.rot / 2));
+    }
+    __device__ __forceinline__ void values(const RopeParams &p, int d, bool turns, float (&v)[8], const float *s_cos, const float *s_sin) const {
+        own.widen(v);
+        if (!turns || d >= p.rot) return;
+        float c[8], s[8];
+        if constexpr (kInter) {
+            const float4 c4 = *reinterpret_cast<const float4 *>(s_cos + d / 2), s4 = *reinterpret_cast<const float4 *>(s_sin + d / 2);
+            c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
+            s[0] = s4.x, s[1] = s4.y, s[2] = s4.z, s[3] = s4.w;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x1 = v[2 * j], x2 = v[2 * j + 1];
-            v[2 * j] = turn1(x1, x2, c[j], s[j]), v[2 * j + 1] = turn2(x1, x2, c[j], s[j]);
+            for (int j = 0; j < 4; ++j) {
+                const float x1 = v[2 * j], x2 = v[2 * j + 1];
+                v[2 * j] = turn1(x1, x2, c[j], s[j]), v[2 * j + 1] = turn2(x1, x2, c[j], s[j]);
+            }
+        } else {
+            const bool second = d >= p.rot / 2;
+            const int i = second ? d - p.rot / 2 : d;
+            float o[8];
+            other.widen(o);
+            lds8(s_cos + i, c), lds8(s_sin + i, s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = second ? turn2(o[j], v[j], c[j], s[j]) : turn1(v[j], o[j], c[j], s[j]);
         }
-    } else {
-        const int half = p.rot / 2;
-        const bool second = d >= half;
-        const int i = second ? d - half : d;
-        float o[8];
-        r.load(x + (second ? i : i + half));
-        r.widen(o);
-        lds8(s_cos + i, c), lds8(s_sin + i, s);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = second ? turn2(o[j], v[j], c[j], s[j]) : turn1(v[j], o[j], c[j], s[j]);
     }
-}
+};
 
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
     const int64_t token = blockIdx.x;
-    make_angles(p, token, s_cos, s_sin);
     const int64_t slot = p.slots[token];
+    Heads<T, kInter, kAppendThreads> heads;
+    heads.begin(p, static_cast<const T *>(p.x) + token * p.ldx);
+    // keys, then values, eight to a lane; four lanes own a block (a head has a multiple of four).  A thread's next
+    // unit is on its way while it works on one
+    const int units = p.kv_heads << (p.d_shift - 3);
+    const T *k = static_cast<const T *>(p.k) + token * p.ldk, *v = static_cast<const T *>(p.v) + token * p.ldv;
+    Unit8<T, kInter> unit;
+    auto fetch = [&](int u) {
+        if (u >= 2 * units) return;
+        const bool is_v = u >= units;
+        const int at = (is_v ? u - units : u) * 8, d = at & ((1 << p.d_shift) - 1);
+        unit.load(p, (is_v ? v : k) + (at - d), d, !is_v);
+    };
+    const bool held = slot >= 0 && slot < p.capacity;
+    if (held) fetch(threadIdx.x);
+    make_angles<kAppendThreads>(p, token, s_cos, s_sin);
     __syncthreads();
-    const T *x = static_cast<const T *>(p.x) + token * p.ldx;
-    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + token * p.ldy;
-    const int per = 1 << (p.d_shift - 4);
-    for (int u = threadIdx.x; u < p.heads * per; u += kThreads) {
-        const int64_t head = static_cast<int64_t>(u >> (p.d_shift - 4)) << p.d_shift;
-        turn_item<T, kInter>(p, x + head, y + head, u & (per - 1), s_cos, s_sin);
-    }
-    if (slot < 0 || slot >= p.capacity) {
+    // (y may be q, so the keys' and values' rows, which may lie behind it, are never written)
+    heads.run(p, static_cast<__nv_bfloat16 *>(p.y) + token * p.ldy, s_cos, s_sin);
+    if (!held) {
         if (slot >= 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, Q8_DEV_BAD_INDEX);
         return;
     }
-    // keys, then values, eight to a lane; four lanes own a block (a head has a multiple of four)
     const int64_t page = slot >> p.page_shift, off = slot & ((1 << p.page_shift) - 1);
-    const int units = p.kv_heads << (p.d_shift - 3);
-    for (int u0 = 0; u0 < 2 * units; u0 += kThreads) {
+    for (int u0 = 0; u0 < 2 * units; u0 += kAppendThreads) {
         const int u = u0 + threadIdx.x;
-        const bool live = u < 2 * units;
-        const bool is_v = u >= units;
+        const bool live = u < 2 * units, is_v = u >= units;
         const int at = (live ? (is_v ? u - units : u) : 0) * 8;
         const int h = at >> p.d_shift, d = at & ((1 << p.d_shift) - 1);
-        float v[8];
-        if (is_v) {
-            Raw8<T> r;
-            r.load(static_cast<const T *>(p.v) + token * p.ldv + at);
-            r.widen(v);
+        float x[8];
+        if (live) {
+            unit.values(p, d, !is_v, x, s_cos, s_sin);
         } else {
-            turned8<T, kInter>(p, static_cast<const T *>(p.k) + token * p.ldk + (static_cast<int64_t>(h) << p.d_shift), d, v, s_cos, s_sin);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = 0.f;
         }
+        fetch(u + kAppendThreads);
         uint32_t top = 0u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         __half hs;
         float sf;
         const uint32_t flags = block_scale(top, hs, sf);
         uint32_t packed[2] = {0u, 0u};
-        if (!flags && sf != 0.f) codes_of<float, 8>(v, sf, packed);
+        if (!flags && sf != 0.f) codes_of<float, 8>(x, sf, packed);
         if (live) {
             const int64_t code = ((((page * p.kv_heads + h) << p.page_shift) + off) << p.d_shift) + d;
             *reinterpret_cast<uint2 *>(p.codes[is_v] + code) = make_uint2(packed[0], packed[1]);
@@ -216,9 +248,9 @@ template <typename T>
 void launch(const RopeParams &p, int64_t T_, bool inter, bool append, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>(T_);
     if (append)
-        (inter ? rope_append_kernel<T, true> : rope_append_kernel<T, false>)<<<grid, kThreads, 0, stream>>>(p);
+        (inter ? rope_append_kernel<T, true> : rope_append_kernel<T, false>)<<<grid, kAppendThreads, 0, stream>>>(p);
     else
-        (inter ? rope_kernel<T, true> : rope_kernel<T, false>)<<<grid, kThreads, 0, stream>>>(p);
+        (inter ? rope_kernel<T, true> : rope_kernel<T, false>)<<<grid, kRopeThreads, 0, stream>>>(p);
 }
 
 }  // namespace

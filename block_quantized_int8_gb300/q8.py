@@ -500,6 +500,7 @@ class KvCache:
         self.kq, self.ks, self.vq, self.vs = kq, ks, vq, vs
         self.pages, self.kv_heads, self.page_size, self.head_dim = shape
         self.device = kq.device
+        self.get_device = kq.get_device
         self._c = _CKvCache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1], shape[3])
         self._ref = ctypes.byref(self._c)
 
@@ -725,17 +726,20 @@ def q8_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
 # ---------------------------------------------------------------------------
 def _here(first, *others):
     """All of a call's tensors are on one device, the current one."""
-    dev = first.device
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("the tensors of a call must be on one device")
-    if dev.index is not None and _get_device is not None and dev.index != _get_device():
+    if dev >= 0 and _get_device is not None and dev != _get_device():
         raise ValueError("the tensors of a call must be on the current device")
 
 
 def _rows(t, name, n, width):
     """The stride of n rows of `width` values (one or more inner dimensions, contiguous)."""
-    sh, sd = t.shape, t.stride()
+    sh = t.shape
+    if t.is_contiguous() and len(sh) >= 2 and sh[0] == n and t.numel() == n * width and n > 0:
+        return width
+    sd = t.stride()
     want = 1
     ok = len(sh) >= 2 and sh[0] == n
     for i in range(len(sh) - 1, 0, -1):
@@ -757,37 +761,40 @@ def q8_rms_norm(x, weight=None, offset=0.0, eps=1e-6, residual=None, residual_ou
     bf16, residual [T, W] fp32 or bf16 (updated in place, or to `residual_out`), weight fp32 [W].
     Returns (y bf16 [T, W], q int8 [T, W], s float16 [T, W / 32]): y unless bf16=False, the
     Q8_0 rows if `quantized` (or q and s are given), None in the place of what is not asked for."""
-    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _ROW_DTYPES and x.dim() == 2):
+    xt, xd = x.dtype, x.shape
+    if not (x.is_cuda and xt in _ROW_DTYPES and len(xd) == 2):
         _cuda(x, "x", tuple(_ROW_DTYPES), 2)
-    T, W = x.shape
+    T, W = xd
     ldx = _rows(x, "x", T, W)
-    kind, ldr, ldo = x.dtype, W, W
+    kind, ldr, ldo, ldy = xt, W, W, W
     if residual is not None:
-        kind = _cuda(residual, "residual", tuple(_ROW_DTYPES), 2).dtype
-        ldr = _rows(residual, "residual", T, W)
+        kind = residual.dtype
         if residual_out is None:
             residual_out = residual
-        ldo = _rows(_cuda(residual_out, "residual_out", (kind,), 2), "residual_out", T, W)
+        if not (residual.is_cuda and residual_out.is_cuda and kind in _ROW_DTYPES and residual_out.dtype is kind):
+            _cuda(residual, "residual", tuple(_ROW_DTYPES), 2)
+            _cuda(residual_out, "residual_out", (kind,), 2)
+        ldr, ldo = _rows(residual, "residual", T, W), _rows(residual_out, "residual_out", T, W)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    if weight is not None and (_cuda(weight, "weight", (_F32,), 1).shape[0] != W or (W > 1 and weight.stride(0) != 1)):
+    if weight is not None and not (weight.is_cuda and weight.dtype is _F32 and weight.shape == (W,) and weight.is_contiguous()):
+        _cuda(weight, "weight", (_F32,), 1)
         raise ValueError("weight must hold W values, contiguous")
-    ldy = W
     if y is not None:
         ldy = _rows(_cuda(y, "y", (_BF16,), 2), "y", T, W)
     elif bf16:
-        y = _out(stream, (T, W), _BF16, x.device)
+        y = _out(stream, xd, _BF16, x.device)
     if quantized or q is not None or s is not None:
         if q is None:
-            q = _out(stream, (T, W), _I8, x.device)
+            q = _out(stream, xd, _I8, x.device)
         if s is None:
             s = _out(stream, (T, W // 32), torch.float16, x.device)
-        if _cuda(q, "q", (_I8,), 2).shape != (T, W) or not q.is_contiguous():
+        if _cuda(q, "q", (_I8,), 2).shape != xd or not q.is_contiguous():
             raise ValueError("q must be contiguous, [T, W]")
         if _cuda(s, "s", _B16, 2).shape != (T, W // 32) or not s.is_contiguous():
             raise ValueError("s must be contiguous, [T, W / 32]")
     _here(x, weight, residual, residual_out, y, q, s)
-    st = lib().q8_rms_norm(x.data_ptr(), ldx, _ROW_DTYPES[x.dtype], _a(residual), ldr, _ROW_DTYPES[kind], _a(residual_out), ldo,
+    st = lib().q8_rms_norm(x.data_ptr(), ldx, _ROW_DTYPES[xt], _a(residual), ldr, _ROW_DTYPES[kind], _a(residual_out), ldo,
                            _a(weight), offset, eps, T, W, _a(y), ldy, _a(q), _a(s), _status(dev_status), _stream(stream))
     if st:
         _check(st, "q8_rms_norm")
@@ -853,7 +860,7 @@ def q8_rope(x, positions, turns, interleaved=False, factor=1.0, y=None, stream=N
     """Rotary positions of x [T, heads, head_dim] (fp32 or bf16) at positions int32 [T], with the
     table of rope_turns: the first 2 * len(turns) dimensions of each head turn.  Returns y
     bf16 [T, heads, head_dim] (y may be x itself)."""
-    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _ROW_DTYPES and x.dim() == 3):
+    if not (x.is_cuda and x.dtype in _ROW_DTYPES and x.dim() == 3):
         _cuda(x, "x", tuple(_ROW_DTYPES), 3)
     n, h, d = x.shape
     rot = _rope_args(turns, positions, n, d)
@@ -914,24 +921,30 @@ def q8_kv_plan(table, lens, new_tokens, page_size, pages, T, free_pages=None, fr
     if not table.is_contiguous():
         raise ValueError("table must be contiguous")
     dev = table.device
+    if free_pages is None and (free_count is not None or free_left is not None):
+        raise ValueError("free_count and free_left belong to free_pages")
+    if free_pages is not None and free_count is None:
+        raise ValueError("free_pages needs free_count")
+    slots = _out(stream, (T,), _I64, dev) if slots is None else slots
+    if starts is None and positions is None and lens_out is None:
+        # one allocation for the whole numbers of 32 bits
+        starts, positions, lens_out, left = _out(stream, (2 * B + T + 2,), _I32, dev).split_with_sizes((B + 1, T, B, 1))
+        if free_pages is not None and free_left is None:
+            free_left = left
+    else:
+        starts = _out(stream, (B + 1,), _I32, dev) if starts is None else starts
+        positions = _out(stream, (T,), _I32, dev) if positions is None else positions
+        lens_out = _out(stream, (B,), _I32, dev) if lens_out is None else lens_out
+        if free_pages is not None and free_left is None:
+            free_left = _out(stream, (1,), _I32, dev)
     args = [_ints(lens, "lens", (B,)), _ints(new_tokens, "new_tokens", (B,)), B]
     if free_pages is None:
-        if free_count is not None or free_left is not None:
-            raise ValueError("free_count and free_left belong to free_pages")
         args += [None, 0, None, None]
     else:
-        if free_count is None:
-            raise ValueError("free_pages needs free_count")
-        if free_left is None:
-            free_left = _out(stream, (1,), _I32, dev)
         n = _cuda(free_pages, "free_pages", (_I32,), 1).shape[0]
         # an empty list is a list all the same
         at = _ints(free_pages, "free_pages", (n,)) or table.data_ptr()
         args += [at, n, _ints(free_count, "free_count", (1,)), _ints(free_left, "free_left", (1,))]
-    starts = _out(stream, (B + 1,), _I32, dev) if starts is None else starts
-    slots = _out(stream, (T,), _I64, dev) if slots is None else slots
-    positions = _out(stream, (T,), _I32, dev) if positions is None else positions
-    lens_out = _out(stream, (B,), _I32, dev) if lens_out is None else lens_out
     _here(table, lens, new_tokens, free_pages, free_count, free_left, starts, slots, positions, lens_out)
     st = lib().q8_kv_plan(table.data_ptr(), width, pages, page_size, *args, T, _ints(starts, "starts", (B + 1,)),
                           _ints(slots, "slots", (T,), _I64), _ints(positions, "positions", (T,)), _ints(lens_out, "lens_out", (B,)),
