@@ -925,18 +925,12 @@ def q8_kv_plan(table, lens, new_tokens, page_size, pages, T, free_pages=None, fr
         raise ValueError("free_count and free_left belong to free_pages")
     if free_pages is not None and free_count is None:
         raise ValueError("free_pages needs free_count")
+    starts = _out(stream, (B + 1,), _I32, dev) if starts is None else starts
     slots = _out(stream, (T,), _I64, dev) if slots is None else slots
-    if starts is None and positions is None and lens_out is None:
-        # one allocation for the whole numbers of 32 bits
-        starts, positions, lens_out, left = _out(stream, (2 * B + T + 2,), _I32, dev).split_with_sizes((B + 1, T, B, 1))
-        if free_pages is not None and free_left is None:
-            free_left = left
-    else:
-        starts = _out(stream, (B + 1,), _I32, dev) if starts is None else starts
-        positions = _out(stream, (T,), _I32, dev) if positions is None else positions
-        lens_out = _out(stream, (B,), _I32, dev) if lens_out is None else lens_out
-        if free_pages is not None and free_left is None:
-            free_left = _out(stream, (1,), _I32, dev)
+    positions = _out(stream, (T,), _I32, dev) if positions is None else positions
+    lens_out = _out(stream, (B,), _I32, dev) if lens_out is None else lens_out
+    if free_pages is not None and free_left is None:
+        free_left = _out(stream, (1,), _I32, dev)
     args = [_ints(lens, "lens", (B,)), _ints(new_tokens, "new_tokens", (B,)), B]
     if free_pages is None:
         args += [None, 0, None, None]
