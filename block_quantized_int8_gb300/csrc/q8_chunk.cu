@@ -22,14 +22,25 @@
 // back, the weights are raised by 2^9 instead (their reference moves up for it).
 //
 // Roles (one CTA per SM):
-//   softmax     4 warps per row tile, a thread per row: scores from tensor memory in two passes (the
-//               largest, then the weights); the query rows into shared memory before an item, the answer after it
-//   MMA         one warp, one thread of it issuing
+//   softmax     4 warps per row tile, a thread per row, its scores of a tile in registers; the query rows
+//               into shared memory before an item, the answer after it
+//   MMA         one warp, an elected thread of it issuing
 //   loader      one warp: bulk copies of codes and scales, 16 tokens (a page's smallest part) each,
 //               into a ring of raw tiles
 //   converters  CW warps: codes times scales into a ring of binary16 tiles, in the 128-byte
 //               swizzle that the tensor cores read: K-major for the keys, and the same bytes as
 //               MN-major for the values, so nothing is transposed
+//
+// Bound: a tile of 128 tokens and 256 rows needs 2048 clocks of the tensor cores, 1024 of exponentials and
+// about 2600 of shared memory (operands, raw tiles in and out); it takes 4500, the turn of a row tile: scores out of tensor
+// memory, weights (2700), product, next scores.  With 128 rows 3700, converters and softmax about
+// 3000 each.  Measured: 1024 new tokens over 65,536 (32 / 8 heads of 128) 1004 us, 1.09 PFLOP/s; 4096
+// tokens alone 189 us, 0.73; 16 sequences of 1 to 5 new tokens over up to 6000 58 us; 32 new tokens over
+// 262,144 232 us, 2.46 TB/s.  Tiles of 80 tokens with a place of their own for the weights, so that the
+// next scores need not wait for the product: 1225 us in place of 1004.
+//
+// Two row tiles where sequences have more than 128 rows on average (128 rows take 2.2 us a tile, 256 2.4, so
+// that below it half of the work would be nobody's); at 256 dimensions tensor memory has room for one.
 //
 // Split: units of one tile are counted out evenly over the CTAs from the device's lengths, as in
 // q8_attn.cu; an item that crosses CTAs is joined by the last of them to arrive.

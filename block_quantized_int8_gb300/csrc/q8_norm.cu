@@ -8,6 +8,11 @@
 // neighbouring lanes hold a block of 32, whose largest magnitude they find by two shuffles.
 // All sums are fp32, in an order that the width alone sets.
 //
+// Bound by bytes for many rows and by the launch for few.  Measured: 4099 rows of 4096 in bf16 onto a bf16
+// residual 27.3 us (4.9 TB/s), with Q8_0 rows besides 33.4 (4.55); one row of 1536 about 3.
+// One unit a thread up to 256 units, then two and, past 1024, four: fewer and wider would leave
+// narrow rows a few warps, more would give the widest rows more than 1024 threads.
+//
 // Squares overflow binary32 from |h| of 2^64 on and vanish below 2^-75, where the row's norm does
 // neither: rows whose sum of squares is not within [2^-80, 2^126] (below it, only where eps does
 // not cover it) are summed again, scaled by the power of two of their largest value.

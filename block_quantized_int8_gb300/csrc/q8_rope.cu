@@ -14,6 +14,9 @@
 //
 // Bound by bytes: each row in once, rotated rows (bf16) or codes and scales out once.  A CTA has
 // one token: its threads make the token's cosines and sines once, in shared memory, for all heads.
+// Measured: 8192 tokens of 40 heads of 128 in bf16 31.4 us (5.3 TB/s); with 256, 384 and 512 threads 31 to 35
+// and 33 and 35.  With the write to the cache, 4096 tokens of 32 / 8 heads 27.3 us (3.4 TB/s; 29, 35 and 46 with
+// more threads, 27 with 64), of which the angles' latency before the first store is most.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

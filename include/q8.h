@@ -730,10 +730,16 @@ q8_status q8_kv_plan(int32_t *table, int32_t table_width, int32_t pages, int32_t
  *            and see nothing
  *   out    : bf16 [T][q_heads][head_dim], 16-byte aligned; rows of no sequence are left as they are
  *   lse    : float [T][q_heads], log(sum_t exp(s_t)); may be NULL
- * A row that sees nothing gives out = 0 and lse = -inf.
+ * A row that sees nothing gives out = 0 and lse = -inf.  A scale of the cache that is not finite
+ * counts as 0 and sets Q8_DEV_NONFINITE; nothing past a length enters the result.
+ * Sums, the running maximum and lse are fp32.  Rounded to binary16 before their products are: a
+ * query row, scaled by a power of two (exact down to 2^-31 of its largest value); keys and values
+ * s * code (by 2^-11 of themselves at most; of a token with a scale of 512 or more by 2^-16 besides); a
+ * weight (by 2^-11 of itself down to 2^-25 of the largest around it, and 2^-36 of that below).
+ * So a score is off by 2^-11 of sum|q k| * scale at most.  T * (q_heads / kv_heads) < 2^31 - 4096.
  *   ws     : q8_attn_chunk_workspace_size() bytes, 256-byte aligned, the first
  *            Q8_CHUNK_ZEROED_BYTES zeroed once (the kernel counts there and leaves
- *            them zero; the rest may hold anything).  Not for two calls that may run at the
+ *            them zero, but after a Q8_DEV_TIMEOUT; the rest may hold anything).  Not for two calls that may run at the
  *            same time; may be shared with other calls (see q8_linear_batch)
  * The work is split as the device reads starts and lens, so a captured graph may be
  * replayed with others.

@@ -163,6 +163,42 @@ def test_long_caches_are_split_and_joined(D, group, new, lens):
     run_case(D, 2, group, 64, new, lens, seed=D)
 
 
+@pytest.mark.parametrize("D,group", [(64, 1), (128, 4), (256, 2)])
+@pytest.mark.parametrize("batch", [512, 513, 1300])
+def test_batches_past_what_is_looked_at_together(D, group, batch):
+    """The list of items is made 512 sequences at a time; some of them take no part."""
+    r = np.random.default_rng(batch)
+    new = np.where(r.random(batch) < 0.7, r.integers(1, 4, batch), 0)
+    lens = new + r.integers(0, 30, batch)
+    new[700 % batch], lens[700 % batch] = 140, 500
+    run_case(D, 1, group, 16, new.tolist(), lens.tolist(), seed=batch)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_drawn_batches(seed):
+    r = np.random.default_rng(100 + seed)
+    D, kv, group, ps = int(r.choice([64, 128, 256])), int(r.integers(1, 5)), int(r.integers(1, 9)), int(r.choice([16, 64, 256]))
+    batch = int(r.integers(1, 12))
+    new = r.integers(0, 400 // batch + 2, batch)
+    lens = new + r.integers(0, 2500, batch)
+    run_case(D, kv, group, ps, new.tolist(), lens.tolist(), seed=seed, window=int(r.choice([0, 0, 333])), softcap=float(r.choice([0.0, 0.0, 20.0])),
+             pad=int(r.integers(0, 9)))
+
+
+def test_a_call_repeated_often_gives_the_same():
+    """Two tiles of one row tile, again and again: the answer is read after the last product."""
+    from block_quantized_int8_gb300 import q8
+    cache, kv, vv = filled_cache(26, 16, 2, 128, 31)
+    tab = torch.arange(26, dtype=torch.int32, device="cuda").view(2, 13)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = bf16_of(np.random.default_rng(31).standard_normal((60, 4, 128))).cuda()
+    args = (q, cache, tab, i32(200, 140), i32(0, 40, 60))
+    ws = q8.workspace(q8.q8_attn_chunk_workspace_size(4, 2, 128))
+    want = check(cache, kv, vv, q, tab.cpu().numpy(), [200, 140], [0, 40, 60])[0]
+    for _ in range(300):
+        assert torch.equal(q8.q8_attn_chunk(*args, ws=ws)[0], want)
+
+
 def test_large_scores_and_a_growing_maximum():
     """Keys that grow along the sequence, so that the running maximum moves in every tile."""
     from block_quantized_int8_gb300 import q8
