@@ -14,9 +14,9 @@
 //
 // Bound by bytes: each row in once, rotated rows (bf16) or codes and scales out once.  A CTA has
 // one token: its threads make the token's cosines and sines once, in shared memory, for all heads.
-// Measured: 8192 tokens of 40 heads of 128 in bf16 31.4 us (5.3 TB/s); with 256, 384 and 512 threads 31 to 35
-// and 33 and 35.  With the write to the cache, 4096 tokens of 32 / 8 heads 27.3 us (3.4 TB/s; 29, 35 and 46 with
-// more threads, 27 with 64), of which the angles' latency before the first store is most.
+// Measured: 8192 tokens of 40 heads of 128 in bf16 32 us (5.2 TB/s; 256 threads 31 to 35, 512 35).  With the
+// write to the cache, 4096 tokens of 32 / 8 heads 27.7 us (3.35 TB/s; 29, 35 and 46 with 256, 384 and 512 threads, 27 with
+// 64), of which the angles' latency before the first store is most.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -32,6 +32,7 @@ namespace q8 {
 namespace {
 
 constexpr int kRopeThreads = 128, kAppendThreads = 128;
+constexpr int kCtas = 10;  // an SM's that registers must allow (8192 tokens 32.0 us, appending 4096 27.7; unasked 33.4 and 29.3, 16: 49.5 and 40.1)
 constexpr int kMaxPairs = 128;  // head_dim 256
 
 struct RopeParams {
@@ -134,7 +135,7 @@ struct Heads {
 };
 
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kCtas) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
     const int64_t token = blockIdx.x;
     Heads<T, kInter, kRopeThreads> heads;
@@ -179,7 +180,7 @@ struct Unit8 {
 };
 
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kAppendThreads, kCtas) rope_append_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
     const int64_t token = blockIdx.x;
     const int64_t slot = p.slots[token];
