@@ -17,9 +17,9 @@
 //
 // Operands are binary16: a query row is scaled by a power of two (its bf16 values are then exact
 // down to 2^-31 of its largest), keys and values are s * code rounded once (by 2^-11 of themselves;
-// exact where the scale is subnormal, as all are whole multiples of 2^-24).  Tiles with a scale of
+// exact where the scale is subnormal, as all are whole multiples of 2^-24).  Tokens with a scale of
 // 512 or more, whose products could overflow, are taken times 2^-9: the scores get the factor
-// back, the weights are raised by 2^9 instead (their reference moves up for it).
+// back, or the weights are raised by 2^9 (their reference moves up for it).
 //
 // Roles (one CTA per SM):
 //   softmax     4 warps per row tile, a thread per row, its scores of a tile in registers; the query rows
@@ -56,7 +56,6 @@
 #include "q8_async.cuh"
 #include "q8_dev.cuh"
 #include "q8_internal.h"
-#include "q8_rows.cuh"
 
 namespace q8 {
 
