@@ -728,7 +728,8 @@ q8_status q8_kv_plan(int32_t *table, int32_t table_width, int32_t pages, int32_t
  *   lens   : int32 [batch], the new tokens included; clamped as in q8_attn_decode.  Where it is
  *            less than the sequence's rows, the first rows have no position (Q8_DEV_BAD_INDEX)
  *            and see nothing
- *   out    : bf16 [T][q_heads][head_dim], 16-byte aligned; rows of no sequence are left as they are
+ *   out    : bf16 [T][q_heads][head_dim], 16-byte aligned; rows of no sequence are left as they are.
+ *            May be q itself (ldq = q_heads * head_dim)
  *   lse    : float [T][q_heads], log(sum_t exp(s_t)); may be NULL
  * A row that sees nothing gives out = 0 and lse = -inf.  A scale of the cache that is not finite
  * counts as 0 and sets Q8_DEV_NONFINITE; nothing past a length enters the result.

@@ -129,6 +129,34 @@ def test_heads_that_share_keys(D, group):
     run_case(D, 2, group, 16, [37, 3, 90], [150, 3, 411], seed=group)
 
 
+def test_groups_wider_than_a_row_tile():
+    run_case(64, 1, 300, 16, [7, 1], [40, 90], seed=40)
+    run_case(128, 2, 130, 16, [3], [300], seed=41)
+
+
+def test_a_table_without_pages():
+    """No page, so no length: every row sees nothing."""
+    from block_quantized_int8_gb300 import q8
+    cache, _, _ = filled_cache(2, 16, 1, 64, 42)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.ones((5, 2, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = q8.q8_attn_chunk(q, cache, torch.empty((2, 0), dtype=torch.int32, device="cuda"), i32(3, 2), i32(0, 3, 5), return_lse=True,
+                                dev_status=st)
+    assert torch.all(out == 0) and torch.all(lse == -float("inf")) and int(st.item()) == BAD
+
+
+def test_the_answer_may_take_the_queries_place():
+    from block_quantized_int8_gb300 import q8
+    cache, kv, vv = filled_cache(65, 64, 2, 128, 43)
+    tab = torch.arange(65, dtype=torch.int32, device="cuda").view(1, 65)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = bf16_of(np.random.default_rng(43).standard_normal((90, 8, 128))).cuda()
+    want, _ = q8.q8_attn_chunk(q, cache, tab, i32(4000), i32(0, 90))
+    got, _ = q8.q8_attn_chunk(q, cache, tab, i32(4000), i32(0, 90), out=q)
+    assert torch.equal(want, got)
+
+
 @pytest.mark.parametrize("ps", [16, 32, 64, 128, 256, 1024])
 def test_page_sizes(ps):
     run_case(128, 3, 2, ps, [70, 1, 130], [300, 129, 1100], seed=ps)

@@ -111,6 +111,15 @@ def test_outputs_one_at_a_time_are_the_same():
     assert torch.equal(x2, y)
 
 
+def test_a_row_onto_itself():
+    from block_quantized_int8_gb300 import q8
+    x = rows(5, 320, 20).cuda()
+    y, _, _ = q8.q8_rms_norm(x.clone(), residual=x.clone())
+    z = x.clone()
+    y2, _, _ = q8.q8_rms_norm(z, residual=z)
+    assert torch.equal(y, y2) and torch.equal(z, x + x)
+
+
 def test_the_residual_may_go_to_x():
     from block_quantized_int8_gb300 import q8
     x, r = rows(6, 640, 8).cuda(), rows(6, 640, 9).cuda()
