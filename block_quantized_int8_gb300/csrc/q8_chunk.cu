@@ -273,6 +273,7 @@ struct Cfg {
     static constexpr int kRegs = MT == 2 ? 184 : 200, kRegsLess = MT == 2 ? 72 : 104;
     static constexpr int kWarps = kSoftmax + 2 + CW;
     static_assert(kWarps == 16 && kSoftmax * kRegs + (16 - kSoftmax) * kRegsLess <= 16 * 128, "registers");
+    static_assert(kSoftmax % 4 == 0, "registers are moved between whole warpgroups");
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kQ = 256 * D;                      // bytes of a query tile
     static constexpr int kTile = BN * D * 2;                // bytes of a binary16 tile
@@ -412,7 +413,10 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
     __shared__ Control sm;
     static_assert(sizeof(Control) <= 1024, "static shared memory");
     uint8_t *const base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    // From lane 0, so that branches on it are the warp's: the MMA warp's operands are then made in uniform registers
+    // (1024 over 65,536 takes 998 us, 1293 without)
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
     // the list is looked at in the room of the binary16 tiles
     long long *const s_cost = reinterpret_cast<long long *>(base + MT * C::kQ);
@@ -570,199 +574,200 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
             ok = __all_sync(0xffffffffu, wait_more(sm, p.status, bar, parity & 1u));
     };
 
-    if (warp == C::kSoftmax) {
-        // ------------------------------------------------------------------ MMA
+    // One statement for all warps of a warpgroup: PTX asks that they execute the same setmaxnreg
+    if (warp >= C::kSoftmax) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kRegsLess));
-        uint32_t c = 0, items = 0;  // tiles, items so far
-        const auto bar_of = [&](uint32_t pos) { return pos % NR; };
-        while (left > 0) {
-            const int seg = wk.stretch(left);
-            auto qk = [&](int m, uint32_t tile) {  // scores of row tile m, tile `tile`
-                const uint32_t pos = 2 * tile, slot = bar_of(pos);
-                const uint32_t buf = MT == 2 ? m : (tile & 1);
-                if (ok) {
-                    const uint64_t a = sw128_desc(q_at + m * C::kQ, 16), b = sw128_desc(tile_at + slot * C::kTile, 16);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        umma_ss(tmem + buf * BN, a + ((k / 4) * 16384 + (k % 4) * 32) / 16, b + ((k / 4) * C::kChunk + (k % 4) * 32) / 16,
-                                idesc(BN, false), k > 0);
-                    umma_commit(&sm.s_full[buf]);
-                    if (m == MT - 1) umma_commit(&sm.t_empty[slot]);
-                }
-                __syncwarp();
-            };
-            for (int m = 0; m < MT; ++m) wait(&sm.q_full[m], items);
-            wait(&sm.t_full[bar_of(2 * c)], 2 * c / NR);
-            tc_fence_after();
-            for (int m = 0; m < MT; ++m) qk(m, c);
-            for (int j = 0; j < seg; ++j, ++c) {
-                const bool more = j + 1 < seg;
-                const uint32_t vpos = 2 * c + 1, vslot = bar_of(vpos);
-                if (MT == 1 && more) {
-                    wait(&sm.t_full[bar_of(2 * c + 2)], (2 * c + 2) / NR);
-                    tc_fence_after();
-                    qk(0, c + 1);
-                }
-                wait(&sm.t_full[vslot], vpos / NR);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const uint32_t buf = MT == 2 ? m : (c & 1);
-                    wait(&sm.p_full[buf], MT == 2 ? c : c >> 1);
-                    tc_fence_after();
+        if (warp == C::kSoftmax) {
+            // ------------------------------------------------------------------ MMA
+            uint32_t c = 0, items = 0;  // tiles, items so far
+            const auto bar_of = [&](uint32_t pos) { return pos % NR; };
+            while (left > 0) {
+                const int seg = wk.stretch(left);
+                auto qk = [&](int m, uint32_t tile) {  // scores of row tile m, tile `tile`
+                    const uint32_t pos = 2 * tile, slot = bar_of(pos);
+                    const uint32_t buf = MT == 2 ? m : (tile & 1);
                     if (ok) {
-                        const uint64_t b = sw128_desc(tile_at + vslot * C::kTile, C::kChunk);
-#pragma unroll
-                        for (int k = 0; k < BN / 16; ++k)
-                            umma_ts(tmem + C::kColO + m * D, tmem + buf * BN + BN / 2 + 8 * k, b + 2048 * k / 16, idesc(D, true), j > 0 || k > 0);
-                        umma_commit(&sm.pv_done[m]);
-                        if (m == MT - 1) umma_commit(&sm.t_empty[vslot]);
+                        const uint64_t a = sw128_desc(q_at + m * C::kQ, 16), b = sw128_desc(tile_at + slot * C::kTile, 16);
+    #pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            umma_ss(tmem + buf * BN, a + ((k / 4) * 16384 + (k % 4) * 32) / 16, b + ((k / 4) * C::kChunk + (k % 4) * 32) / 16,
+                                    idesc(BN, false), k > 0);
+                        umma_commit(&sm.s_full[buf]);
+                        if (m == MT - 1) umma_commit(&sm.t_empty[slot]);
                     }
                     __syncwarp();
-                    if (MT == 2 && more) {
-                        if (m == 0) {
-                            wait(&sm.t_full[bar_of(2 * c + 2)], (2 * c + 2) / NR);
-                            tc_fence_after();
+                };
+                for (int m = 0; m < MT; ++m) wait(&sm.q_full[m], items);
+                wait(&sm.t_full[bar_of(2 * c)], 2 * c / NR);
+                tc_fence_after();
+                for (int m = 0; m < MT; ++m) qk(m, c);
+                for (int j = 0; j < seg; ++j, ++c) {
+                    const bool more = j + 1 < seg;
+                    const uint32_t vpos = 2 * c + 1, vslot = bar_of(vpos);
+                    if (MT == 1 && more) {
+                        wait(&sm.t_full[bar_of(2 * c + 2)], (2 * c + 2) / NR);
+                        tc_fence_after();
+                        qk(0, c + 1);
+                    }
+                    wait(&sm.t_full[vslot], vpos / NR);
+    #pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const uint32_t buf = MT == 2 ? m : (c & 1);
+                        wait(&sm.p_full[buf], MT == 2 ? c : c >> 1);
+                        tc_fence_after();
+                        if (ok) {
+                            const uint64_t b = sw128_desc(tile_at + vslot * C::kTile, C::kChunk);
+    #pragma unroll
+                            for (int k = 0; k < BN / 16; ++k)
+                                umma_ts(tmem + C::kColO + m * D, tmem + buf * BN + BN / 2 + 8 * k, b + 2048 * k / 16, idesc(D, true), j > 0 || k > 0);
+                            umma_commit(&sm.pv_done[m]);
+                            if (m == MT - 1) umma_commit(&sm.t_empty[vslot]);
                         }
-                        qk(m, c + 1);
+                        __syncwarp();
+                        if (MT == 2 && more) {
+                            if (m == 0) {
+                                wait(&sm.t_full[bar_of(2 * c + 2)], (2 * c + 2) / NR);
+                                tc_fence_after();
+                            }
+                            qk(m, c + 1);
+                        }
                     }
                 }
+                ++items;
+                left -= seg + kEndUnits;
+                if (left > 0) wk.next(p);
             }
-            ++items;
-            left -= seg + kEndUnits;
-            if (left > 0) wk.next(p);
-        }
-    } else if (warp == C::kSoftmax + 1) {
-        // --------------------------------------------------------------- loader
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kRegsLess));
-        uint32_t pos = 0;
-        const int page_mask = (1 << p.page_shift) - 1;
-        while (left > 0) {
-            const int seg = wk.stretch(left);
-            const int32_t *row = p.table + static_cast<int64_t>(wk.b) * p.table_width;
-            auto page_of = [&](int j) {
-                const int tok = wk.base + (wk.unit + j) * BN + 16 * lane;
-                return j < seg && lane < BN / 16 && tok < wk.end ? row[tok >> p.page_shift] : -1;
-            };
-            int page = page_of(0);
-            for (int j = 0; j < seg; ++j) {
-                const int tok = wk.base + (wk.unit + j) * BN + 16 * lane;
-                const bool in = lane < BN / 16 && tok < wk.end;
-                const bool good = in && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
-                const uint32_t runs = __ballot_sync(0xffffffffu, good);
-                if (in && !good && p.status) atomicOr(p.status, Q8_DEV_BAD_INDEX);
-                const int64_t at = ((static_cast<int64_t>(good ? page : 0) * p.kv_heads + wk.kvh) << p.page_shift) + (tok & page_mask);
-                page = page_of(j + 1);
-#pragma unroll
-                for (int v = 0; v < 2; ++v, ++pos) {
-                    const uint32_t slot = pos % NW;
-                    if (pos >= NW) wait(&sm.raw_empty[slot], pos / NW - 1);
-                    if (!ok) continue;
-                    if (lane == 0) {
-                        sm.meta[slot] = runs | static_cast<uint32_t>(min(BN, wk.end - (wk.base + (wk.unit + j) * BN))) << 8;
-                        mbar_arrive_expect_tx(&sm.raw_full[slot], __popc(runs) * 17 * D);
-                    }
-                    __syncwarp();
-                    if (good) {
-                        uint8_t *to = base + C::kRawAt + slot * C::kRaw;
-                        bulk_g2s(to + lane * 16 * D, (v ? p.vq : p.kq) + at * D, 16 * D, &sm.raw_full[slot]);
-                        bulk_g2s(to + C::kCodes + lane * D, (v ? p.vs : p.ks) + at * (D / 32), D, &sm.raw_full[slot]);
+        } else if (warp == C::kSoftmax + 1) {
+            // --------------------------------------------------------------- loader
+            uint32_t pos = 0;
+            const int page_mask = (1 << p.page_shift) - 1;
+            while (left > 0) {
+                const int seg = wk.stretch(left);
+                const int32_t *row = p.table + static_cast<int64_t>(wk.b) * p.table_width;
+                auto page_of = [&](int j) {
+                    const int tok = wk.base + (wk.unit + j) * BN + 16 * lane;
+                    return j < seg && lane < BN / 16 && tok < wk.end ? row[tok >> p.page_shift] : -1;
+                };
+                int page = page_of(0);
+                for (int j = 0; j < seg; ++j) {
+                    const int tok = wk.base + (wk.unit + j) * BN + 16 * lane;
+                    const bool in = lane < BN / 16 && tok < wk.end;
+                    const bool good = in && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
+                    const uint32_t runs = __ballot_sync(0xffffffffu, good);
+                    if (in && !good && p.status) atomicOr(p.status, Q8_DEV_BAD_INDEX);
+                    const int64_t at = ((static_cast<int64_t>(good ? page : 0) * p.kv_heads + wk.kvh) << p.page_shift) + (tok & page_mask);
+                    page = page_of(j + 1);
+    #pragma unroll
+                    for (int v = 0; v < 2; ++v, ++pos) {
+                        const uint32_t slot = pos % NW;
+                        if (pos >= NW) wait(&sm.raw_empty[slot], pos / NW - 1);
+                        if (!ok) continue;
+                        if (lane == 0) {
+                            sm.meta[slot] = runs | static_cast<uint32_t>(min(BN, wk.end - (wk.base + (wk.unit + j) * BN))) << 8;
+                            mbar_arrive_expect_tx(&sm.raw_full[slot], __popc(runs) * 17 * D);
+                        }
+                        __syncwarp();
+                        if (good) {
+                            uint8_t *to = base + C::kRawAt + slot * C::kRaw;
+                            bulk_g2s(to + lane * 16 * D, (v ? p.vq : p.kq) + at * D, 16 * D, &sm.raw_full[slot]);
+                            bulk_g2s(to + C::kCodes + lane * D, (v ? p.vs : p.ks) + at * (D / 32), D, &sm.raw_full[slot]);
+                        }
                     }
                 }
+                left -= seg + kEndUnits;
+                if (left > 0) wk.next(p);
             }
-            left -= seg + kEndUnits;
-            if (left > 0) wk.next(p);
-        }
-    } else if (warp > C::kSoftmax) {
-        // ----------------------------------------------------------- converters
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kRegsLess));
-        constexpr int kCT = C::CW * 32, kPer = D / 16, kUnits = BN * kPer;  // units of 16 codes, of a token and a tile
-        constexpr int kMine = (kUnits + kCT - 1) / kCT;
-        const int ct = tid - (C::kSoftmax + 2) * 32;
-        // This thread's units are ct, ct + kCT, ...: unit x0 of tokens t0, t0 + kStep, ..., in the order of the raw tile.
-        // Which half of a unit's 16 codes comes first is chosen so that a warp's loads and its stores each hit all
-        // banks once
-        constexpr int kStep = kCT / kPer;
-        static_assert(kStep % 4 == 0, "the same place in the swizzle");
-        const int t0 = ct / kPer, x0 = ct % kPer;
-        const int half = D == 64 ? (t0 >> 1) & 1 : (D == 128 ? ((x0 >> 2) ^ t0) & 1 : ((x0 >> 2) ^ (x0 >> 3)) & 1);
-        const uint32_t from = ct * 16 + 8 * half, scale_at = (t0 * (D / 32) + (x0 >> 1)) * 2;
-        const uint32_t place = (x0 >> 2) * C::kChunk + t0 * 128;
-        const uint32_t piece0 = place + (((2 * (x0 & 3) + half) ^ (t0 & 7)) << 4), piece1 = place + (((2 * (x0 & 3) + (half ^ 1)) ^ (t0 & 7)) << 4);
-        uint32_t pos = 0;
-        while (left > 0) {
-            const int n = wk.stretch(left);
-            for (int jj = 0; jj < 2 * n; ++jj, ++pos) {
-                const uint32_t slot = pos % NW, to = pos % NR;
-                const uint32_t raw = raw_at + slot * C::kRaw;
-                wait(&sm.raw_full[slot], pos / NW);
-                if (pos >= NR) wait(&sm.t_empty[to], pos / NR - 1);
-                if (ok) {
-                    const uint32_t meta = sm.meta[slot];
-                    const bool is_v = pos & 1u;
-                    const int here = (meta >> 8) & 0xFF, ring = (pos >> 1) & 7;
-                    if (ct == 0 && !is_v) {
-                        sm.unseen[ring] = ~meta & ((1u << (BN / 16)) - 1u);
-                        // for a tile to come (the last that had the place is long done)
-                        sm.big[0][ring ^ 4] = sm.big[1][ring ^ 4] = make_uint4(0, 0, 0, 0);
-                    }
-                    uint2 w0[kMine], w1[kMine];
-                    uint32_t sc[kMine];
-#pragma unroll
-                    for (int i = 0; i < kMine; ++i) {
-                        if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
-                        w0[i] = lds64(raw + from + i * (kCT * 16));
-                        w1[i] = lds64(raw + (from ^ 8) + i * (kCT * 16));
-                        sc[i] = lds16(raw + C::kCodes + scale_at + i * (kStep * (D / 32) * 2));
-                    }
-                    // tokens that are not there and scales that are not finite count as 0, tokens with a scale of 512 or
-                    // more are taken times 2^-9 (a token's units are neighbouring lanes)
-                    uint32_t top = 0u, down = 0u;  // bit i: unit i is taken times 2^-9
-#pragma unroll
-                    for (int i = 0; i < kMine; ++i) {
-                        if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
-                        top = max(top, sc[i] & 0x7FFFu);
-                    }
-                    if (__any_sync(0xffffffffu, top >= 0x6000u) || here < BN || (meta & 0xFFu) != (1u << (BN / 16)) - 1u) {
-#pragma unroll
+        } else {
+            // ----------------------------------------------------------- converters
+            constexpr int kCT = C::CW * 32, kPer = D / 16, kUnits = BN * kPer;  // units of 16 codes, of a token and a tile
+            constexpr int kMine = (kUnits + kCT - 1) / kCT;
+            const int ct = tid - (C::kSoftmax + 2) * 32;
+            // This thread's units are ct, ct + kCT, ...: unit x0 of tokens t0, t0 + kStep, ..., in the order of the raw tile.
+            // Which half of a unit's 16 codes comes first is chosen so that a warp's loads and its stores each hit all
+            // banks once
+            constexpr int kStep = kCT / kPer;
+            static_assert(kStep % 4 == 0, "the same place in the swizzle");
+            const int t0 = ct / kPer, x0 = ct % kPer;
+            const int half = D == 64 ? (t0 >> 1) & 1 : (D == 128 ? ((x0 >> 2) ^ t0) & 1 : ((x0 >> 2) ^ (x0 >> 3)) & 1);
+            const uint32_t from = ct * 16 + 8 * half, scale_at = (t0 * (D / 32) + (x0 >> 1)) * 2;
+            const uint32_t place = (x0 >> 2) * C::kChunk + t0 * 128;
+            const uint32_t piece0 = place + (((2 * (x0 & 3) + half) ^ (t0 & 7)) << 4), piece1 = place + (((2 * (x0 & 3) + (half ^ 1)) ^ (t0 & 7)) << 4);
+            uint32_t pos = 0;
+            while (left > 0) {
+                const int n = wk.stretch(left);
+                for (int jj = 0; jj < 2 * n; ++jj, ++pos) {
+                    const uint32_t slot = pos % NW, to = pos % NR;
+                    const uint32_t raw = raw_at + slot * C::kRaw;
+                    wait(&sm.raw_full[slot], pos / NW);
+                    if (pos >= NR) wait(&sm.t_empty[to], pos / NR - 1);
+                    if (ok) {
+                        const uint32_t meta = sm.meta[slot];
+                        const bool is_v = pos & 1u;
+                        const int here = (meta >> 8) & 0xFF, ring = (pos >> 1) & 7;
+                        if (ct == 0 && !is_v) {
+                            sm.unseen[ring] = ~meta & ((1u << (BN / 16)) - 1u);
+                            // for a tile to come (the last that had the place is long done)
+                            sm.big[0][ring ^ 4] = sm.big[1][ring ^ 4] = make_uint4(0, 0, 0, 0);
+                        }
+                        uint2 w0[kMine], w1[kMine];
+                        uint32_t sc[kMine];
+    #pragma unroll
                         for (int i = 0; i < kMine; ++i) {
-                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;  // (whole warps)
-                            const int t = t0 + i * kStep;
-                            const bool there = t < here && ((meta >> (t >> 4)) & 1u), finite = (sc[i] & 0x7C00u) != 0x7C00u;
-                            if (there && !finite && p.status) atomicOr(p.status, Q8_DEV_NONFINITE);
-                            if (!there || !finite) sc[i] = 0u;
-                            const uint32_t mine = __ballot_sync(0xffffffffu, (sc[i] & 0x7FFFu) >= 0x6000u);
-                            if ((mine >> (lane & ~(kPer - 1))) & ((1u << kPer) - 1u)) {
-                                down |= 1u << i;
-                                if ((lane & (kPer - 1)) == 0) atomicOr(reinterpret_cast<uint32_t *>(&sm.big[is_v][ring]) + (t >> 5), 1u << (t & 31));
+                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
+                            w0[i] = lds64(raw + from + i * (kCT * 16));
+                            w1[i] = lds64(raw + (from ^ 8) + i * (kCT * 16));
+                            sc[i] = lds16(raw + C::kCodes + scale_at + i * (kStep * (D / 32) * 2));
+                        }
+                        // tokens that are not there and scales that are not finite count as 0, tokens with a scale of 512 or
+                        // more are taken times 2^-9 (a token's units are neighbouring lanes)
+                        uint32_t top = 0u, down = 0u;  // bit i: unit i is taken times 2^-9
+    #pragma unroll
+                        for (int i = 0; i < kMine; ++i) {
+                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
+                            top = max(top, sc[i] & 0x7FFFu);
+                        }
+                        if (__any_sync(0xffffffffu, top >= 0x6000u) || here < BN || (meta & 0xFFu) != (1u << (BN / 16)) - 1u) {
+    #pragma unroll
+                            for (int i = 0; i < kMine; ++i) {
+                                if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;  // (whole warps)
+                                const int t = t0 + i * kStep;
+                                const bool there = t < here && ((meta >> (t >> 4)) & 1u), finite = (sc[i] & 0x7C00u) != 0x7C00u;
+                                if (there && !finite && p.status) atomicOr(p.status, Q8_DEV_NONFINITE);
+                                if (!there || !finite) sc[i] = 0u;
+                                const uint32_t mine = __ballot_sync(0xffffffffu, (sc[i] & 0x7FFFu) >= 0x6000u);
+                                if ((mine >> (lane & ~(kPer - 1))) & ((1u << kPer) - 1u)) {
+                                    down |= 1u << i;
+                                    if ((lane & (kPer - 1)) == 0) atomicOr(reinterpret_cast<uint32_t *>(&sm.big[is_v][ring]) + (t >> 5), 1u << (t & 31));
+                                }
                             }
                         }
+                        const uint32_t row = tile_at + to * C::kTile;
+    #pragma unroll
+                        for (int i = 0; i < kMine; ++i) {
+                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
+                            uint32_t s2 = sc[i] | sc[i] << 16;
+                            if (down) s2 = hmul2(s2, (down >> i) & 1u ? 0x18001800u : 0x3C003C00u);
+                            // (12 tokens on, of 256 dimensions, the swizzle's third bit is the other one)
+                            const uint32_t flip = kStep % 8 == 0 ? 0u : (i & 1) * 64u, on = i * (kStep * 128);
+                            uint32_t a, b, c, d;
+                            codes4_to_f16x2(w0[i].x, a, b);
+                            codes4_to_f16x2(w0[i].y, c, d);
+                            sts128(row + (piece0 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
+                            codes4_to_f16x2(w1[i].x, a, b);
+                            codes4_to_f16x2(w1[i].y, c, d);
+                            sts128(row + (piece1 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
+                        }
+                        fence_proxy_async_smem();
                     }
-                    const uint32_t row = tile_at + to * C::kTile;
-#pragma unroll
-                    for (int i = 0; i < kMine; ++i) {
-                        if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
-                        uint32_t s2 = sc[i] | sc[i] << 16;
-                        if (down) s2 = hmul2(s2, (down >> i) & 1u ? 0x18001800u : 0x3C003C00u);
-                        // (12 tokens on, of 256 dimensions, the swizzle's third bit is the other one)
-                        const uint32_t flip = kStep % 8 == 0 ? 0u : (i & 1) * 64u, on = i * (kStep * 128);
-                        uint32_t a, b, c, d;
-                        codes4_to_f16x2(w0[i].x, a, b);
-                        codes4_to_f16x2(w0[i].y, c, d);
-                        sts128(row + (piece0 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
-                        codes4_to_f16x2(w1[i].x, a, b);
-                        codes4_to_f16x2(w1[i].y, c, d);
-                        sts128(row + (piece1 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.t_full[to]);
+                        mbar_arrive(&sm.raw_empty[slot]);
                     }
-                    fence_proxy_async_smem();
                 }
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.t_full[to]);
-                    mbar_arrive(&sm.raw_empty[slot]);
-                }
+                left -= n + kEndUnits;
+                if (left > 0) wk.next(p);
             }
-            left -= n + kEndUnits;
-            if (left > 0) wk.next(p);
         }
     } else {
         // -------------------------------------------------------------- softmax
