@@ -802,7 +802,8 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                     const int x = (i0 + b) * (32 / kLanes) + lane / kLanes;  // row of the warp
                     const uint64_t from = __shfl_sync(0xffffffffu, src, x);
                     const bool there = __shfl_sync(0xffffffffu, live, x);
-                    raw[b] = there ? __ldg(reinterpret_cast<const uint4 *>(from) + lane % kLanes) : make_uint4(0, 0, 0, 0);
+                    // (out may be q: not by the loads that ask for memory that the kernel leaves alone)
+                    raw[b] = there ? __ldcg(reinterpret_cast<const uint4 *>(from) + lane % kLanes) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
                 for (int b = 0; b < 8; ++b) {

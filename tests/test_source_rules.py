@@ -24,3 +24,11 @@ def test_the_warps_of_a_warpgroup_execute_the_same_setmaxnreg(name):
         # the branch between the two is between whole warpgroups
         assert re.search(r"if \(warp >= C::kSoftmax\) \{\s*asm volatile\(\"setmaxnreg\.dec", text)
         assert "static_assert(kSoftmax % 4 == 0" in text
+
+
+@pytest.mark.parametrize("name,others", [("q8_chunk.cu", 0), ("q8_norm.cu", 2), ("q8_rope.cu", 0), ("q8_plan.cu", 0), ("q8_rows.cuh", 0)])
+def test_what_may_be_written_in_place_is_read_by_ordinary_loads(name, others):
+    """The non-coherent loads are for memory that nobody writes while the kernel runs: of these files' operands the norm's gains alone."""
+    loads = re.findall(r"__ldg\(([^;]*);", source(name))
+    assert len(loads) == others and all("p.weight" in x for x in loads)
+    assert not re.search(r"\.nc\.|__restrict__", source(name))
