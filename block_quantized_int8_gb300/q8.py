@@ -725,7 +725,7 @@ def q8_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
 # a prompt step
 # ---------------------------------------------------------------------------
 def _here(first, *others):
-    """All of a call's tensors are on one device, the current one."""
+    """All of a call's tensors (the status word among them) are on one device, the current one."""
     dev = first.get_device()
     for t in others:
         if t is not None and t.get_device() != dev:
@@ -793,9 +793,10 @@ def q8_rms_norm(x, weight=None, offset=0.0, eps=1e-6, residual=None, residual_ou
             raise ValueError("q must be contiguous, [T, W]")
         if _cuda(s, "s", _B16, 2).shape != (T, W // 32) or not s.is_contiguous():
             raise ValueError("s must be contiguous, [T, W / 32]")
-    _here(x, weight, residual, residual_out, y, q, s)
+    status = _status(dev_status)
+    _here(x, weight, residual, residual_out, y, q, s, dev_status)
     st = lib().q8_rms_norm(x.data_ptr(), ldx, _ROW_DTYPES[xt], _a(residual), ldr, _ROW_DTYPES[kind], _a(residual_out), ldo,
-                           _a(weight), offset, eps, T, W, _a(y), ldy, _a(q), _a(s), _status(dev_status), _stream(stream))
+                           _a(weight), offset, eps, T, W, _a(y), ldy, _a(q), _a(s), status, _stream(stream))
     if st:
         _check(st, "q8_rms_norm")
     return y, q, s
@@ -893,10 +894,11 @@ def q8_rope_append(q, k, v, cache, positions, slots, turns, interleaved=False, f
         y = _out(stream, (n, h, d), _BF16, q.device)
     elif _cuda(y, "y", (_BF16,), 3).shape != q.shape:
         raise ValueError("y has q's shape")
-    _here(q, k, v, cache, positions, slots, turns, y)
+    status = _status(dev_status)
+    _here(q, k, v, cache, positions, slots, turns, y, dev_status)
     st = lib().q8_rope_append(cache._ref, q.data_ptr(), ldq, h, k.data_ptr(), v.data_ptr(), ldk, ldv, _ROW_DTYPES[t], rot,
                               1 if interleaved else 0, factor, turns.data_ptr(), positions.data_ptr(), slots.data_ptr(), n,
-                              y.data_ptr(), _rows(y, "y", n, h * d), _status(dev_status), _stream(stream))
+                              y.data_ptr(), _rows(y, "y", n, h * d), status, _stream(stream))
     if st:
         _check(st, "q8_rope_append")
     return y
@@ -939,10 +941,11 @@ def q8_kv_plan(table, lens, new_tokens, page_size, pages, T, free_pages=None, fr
         # an empty list is a list all the same
         at = _ints(free_pages, "free_pages", (n,)) or table.data_ptr()
         args += [at, n, _ints(free_count, "free_count", (1,)), _ints(free_left, "free_left", (1,))]
-    _here(table, lens, new_tokens, free_pages, free_count, free_left, starts, slots, positions, lens_out)
+    status = _status(dev_status)
+    _here(table, lens, new_tokens, free_pages, free_count, free_left, starts, slots, positions, lens_out, dev_status)
     st = lib().q8_kv_plan(table.data_ptr(), width, pages, page_size, *args, T, _ints(starts, "starts", (B + 1,)),
                           _ints(slots, "slots", (T,), _I64), _ints(positions, "positions", (T,)), _ints(lens_out, "lens_out", (B,)),
-                          _status(dev_status), _stream(stream))
+                          status, _stream(stream))
     if st:
         _check(st, "q8_kv_plan")
     return starts, slots, positions, lens_out, free_left
@@ -979,13 +982,14 @@ def q8_attn_chunk(q, cache, table, lens, starts, scale=None, softcap=0.0, window
             lse = _out(stream, (T, H), _F32, cache.device)
     elif _cuda(lse, "lse", (_F32,), 2).shape != (T, H) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous, [T, q_heads]")
+    status = _status(dev_status)
+    _here(q, cache, table, lens, starts, out, lse, ws, dev_status)
     if ws is None:
         nbytes = q8_attn_chunk_workspace_size(H, cache.kv_heads, D)
         ws = _alloc(stream, lambda: _counting_workspace(nbytes, Q8_CHUNK_ZEROED_BYTES, cache.device))
-    _here(q, cache, table, lens, starts, out, lse, ws)
     st = lib().q8_attn_chunk(cache._ref, q.data_ptr(), ldq, H, T, table.data_ptr(), width, n_at, s_at, B,
                              D ** -0.5 if scale is None else scale, softcap, window if window < 2 ** 31 else 2 ** 31 - 1,
-                             out.data_ptr(), _a(lse), *_work(ws), _status(dev_status), _stream(stream))
+                             out.data_ptr(), _a(lse), *_work(ws), status, _stream(stream))
     if st:
         _check(st, "q8_attn_chunk")
     return out, lse

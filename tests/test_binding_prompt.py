@@ -92,3 +92,13 @@ def test_arguments_that_belong_together(q8):  # noqa: F811
         call(q8, "plan", free_pages=None)
     with pytest.raises(ValueError):
         call(q8, "plan", free_count=None)
+
+
+def test_a_status_word_of_another_device_is_refused(q8):  # noqa: F811
+    """Kernels write to it."""
+    class Other(type(ints(1))):
+        def get_device(self):
+            return 1
+    for name in ("norm", "append", "plan", "chunk"):
+        with pytest.raises(ValueError, match="device"):
+            call(q8, name, dev_status=ints(1).as_subclass(Other))
