@@ -938,8 +938,8 @@ def q8_kv_plan(table, lens, new_tokens, page_size, pages, T, free_pages=None, fr
         args += [None, 0, None, None]
     else:
         n = _cuda(free_pages, "free_pages", (_I32,), 1).shape[0]
-        # an empty list is a list all the same
-        at = _ints(free_pages, "free_pages", (n,)) or table.data_ptr()
+        # an empty list is a list all the same (its address, and an empty table's, are NULL; nothing is read there)
+        at = _ints(free_pages, "free_pages", (n,)) or starts.data_ptr()
         args += [at, n, _ints(free_count, "free_count", (1,)), _ints(free_left, "free_left", (1,))]
     status = _status(dev_status)
     _here(table, lens, new_tokens, free_pages, free_count, free_left, starts, slots, positions, lens_out, dev_status)

@@ -102,3 +102,16 @@ def test_a_status_word_of_another_device_is_refused(q8):  # noqa: F811
     for name in ("norm", "append", "plan", "chunk"):
         with pytest.raises(ValueError, match="device"):
             call(q8, name, dev_status=ints(1).as_subclass(Other))
+
+
+@pytest.mark.parametrize("B,width", [(0, 4), (2, 0), (2, 4)])
+def test_an_empty_free_list_is_a_list(q8, monkeypatch, B, width):  # noqa: F811
+    """Its tensor has no address, nor has an empty table: the library gets another, as NULL is no list (free_left is then not written)."""
+    class Empty(type(ints(1))):
+        def data_ptr(self):
+            return 0 if self.numel() == 0 else 1 << 20
+    given = []
+    monkeypatch.setattr(q8.lib(), "q8_kv_plan", lambda *a: given.append(a) or 0, raising=False)
+    call(q8, "plan", table=ints(B, width).as_subclass(Empty), lens=ints(B), new_tokens=ints(B), starts=ints(B + 1), lens_out=ints(B),
+         free_pages=ints(0).as_subclass(Empty))
+    assert given[0][7] and given[0][8] == 0

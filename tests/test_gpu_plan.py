@@ -196,3 +196,16 @@ def test_on_another_stream():
     with torch.cuda.stream(s):
         run(table, lens, new, 16, pages, int(new.sum()), free, len(free))
     run(table, lens, new, 16, pages, int(new.sum()), free, len(free), stream=s)
+
+
+@pytest.mark.parametrize("B,width,count", [(0, 4, 0), (3, 0, 0), (0, 4, 2), (3, 0, -1)])
+def test_an_empty_free_list_beside_an_empty_table(B, width, count):
+    """An empty list is a list all the same: what is left of it is given."""
+    from block_quantized_int8_gb300 import q8
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    zeros = torch.zeros(B, dtype=torch.int32, device="cuda")
+    st, left = i32(0), i32(77)
+    starts, slots, pos, out, got = q8.q8_kv_plan(torch.empty((B, width), dtype=torch.int32, device="cuda"), zeros, zeros, 16, 4, 3,
+                                                 free_pages=i32(), free_count=i32(count), free_left=left, dev_status=st)
+    assert starts.tolist() == [0] * (B + 1) and slots.tolist() == [-1] * 3 and pos.tolist() == [0] * 3 and out.tolist() == [0] * B
+    assert got is left and left.tolist() == [0] and int(st.item()) == (BAD if count else 0)
