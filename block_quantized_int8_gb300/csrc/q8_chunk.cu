@@ -719,8 +719,9 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                             sc[i] = lds16(raw + C::kCodes + scale_at + i * (kStep * (D / 32) * 2));
                         }
                         // tokens that are not there and scales that are not finite count as 0, tokens with a scale of 512 or
-                        // more are taken times 2^-9 (a token's units are neighbouring lanes)
-                        uint32_t top = 0u, down = 0u;  // bit i: unit i is taken times 2^-9
+                        // more are taken times 2^-9 (a token's units are neighbouring lanes): such a scale before the product,
+                        // which would overflow; the token's others after it, as a small scale would lose its digits
+                        uint32_t top = 0u, after = 0u;  // bit i: unit i's products are still to be taken times 2^-9
     #pragma unroll
                         for (int i = 0; i < kMine; ++i) {
                             if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
@@ -736,7 +737,8 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                                 if (!there || !finite) sc[i] = 0u;
                                 const uint32_t mine = __ballot_sync(0xffffffffu, (sc[i] & 0x7FFFu) >= 0x6000u);
                                 if ((mine >> (lane & ~(kPer - 1))) & ((1u << kPer) - 1u)) {
-                                    down |= 1u << i;
+                                    if ((sc[i] & 0x7FFFu) >= 0x6000u) sc[i] = hmul2(sc[i], 0x1800u);
+                                    else after |= 1u << i;
                                     if ((lane & (kPer - 1)) == 0) atomicOr(reinterpret_cast<uint32_t *>(&sm.big[is_v][ring]) + (t >> 5), 1u << (t & 31));
                                 }
                             }
@@ -745,8 +747,7 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
     #pragma unroll
                         for (int i = 0; i < kMine; ++i) {
                             if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
-                            uint32_t s2 = sc[i] | sc[i] << 16;
-                            if (down) s2 = hmul2(s2, (down >> i) & 1u ? 0x18001800u : 0x3C003C00u);
+                            const uint32_t s2 = sc[i] | sc[i] << 16;
                             // (12 tokens on, of 256 dimensions, the swizzle's third bit is the other one)
                             const uint32_t flip = kStep % 8 == 0 ? 0u : (i & 1) * 64u, on = i * (kStep * 128);
                             uint32_t a, b, c, d;
@@ -756,6 +757,15 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                             codes4_to_f16x2(w1[i].x, a, b);
                             codes4_to_f16x2(w1[i].y, c, d);
                             sts128(row + (piece1 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
+                        }
+#pragma unroll 1
+                        for (; after; after &= after - 1u) {
+                            const int i = __ffs(after) - 1;
+                            const uint32_t flip = kStep % 8 == 0 ? 0u : (i & 1) * 64u, on = i * (kStep * 128);
+                            for (const uint32_t at : {row + (piece0 ^ flip) + on, row + (piece1 ^ flip) + on}) {
+                                const uint4 v = lds128(at);
+                                sts128(at, make_uint4(hmul2(v.x, 0x18001800u), hmul2(v.y, 0x18001800u), hmul2(v.z, 0x18001800u), hmul2(v.w, 0x18001800u)));
+                            }
                         }
                         fence_proxy_async_smem();
                     }

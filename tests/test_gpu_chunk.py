@@ -498,3 +498,37 @@ def test_no_rows():
                                 torch.zeros((1, 2), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"),
                                 torch.zeros(2, dtype=torch.int32, device="cuda"))
     assert out.shape == (0, 2, 64) and lse is None
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_small_blocks_beside_a_scale_of_512(D):
+    """A token's blocks have scales of their own.  Where one is 512 or more the token is taken times 2^-9, and what its
+    other blocks hold is kept to 2^-11 of itself and 2^-16 besides: the product s * code is rounded to binary16, and
+    times 2^-9 to whole multiples of 2^-24 (half of one, times 2^9).  With a window of 1 a row is its own token: out is the
+    value, by one weight (2^-11) and bf16 (2^-8), and the lse is the score."""
+    r = np.random.default_rng(50)
+    n, ps, large = 200, 16, [3, 17, 130]
+    cache, _, _ = filled_cache(13, ps, 1, D, 50)
+    for plane in (cache.ks, cache.vs):
+        s = (2.0 ** r.uniform(-15, -5, (13 * ps, D // 32))).astype(np.float16)
+        s[17, 1:] = s[130, 1:] = 2.5 * 2.0 ** -15
+        s[large, 0] = [600, 512, 40000]
+        plane.copy_(torch.from_numpy(s.reshape(13, 1, ps, D // 32)).view(plane.dtype))
+    k, v = (c.cpu().numpy().astype(np.float64).reshape(-1, D)[:n] * np.repeat(f64(s).reshape(-1, D // 32)[:n], 32, -1)
+            for c, s in ((cache.kq, cache.ks), (cache.vq, cache.vs)))
+    q = bf16_of(r.standard_normal((n, 2, D)))
+    q[..., :32] = 0  # sees none of the large blocks
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    from block_quantized_int8_gb300 import q8
+    out, lse = q8.q8_attn_chunk(q.cuda(), cache, torch.arange(13, dtype=torch.int32, device="cuda").view(1, 13), i32(n), i32(0, n), window=1,
+                                return_lse=True)
+    out, lse, qn = f64(out), f64(lse), f64(q)
+    more = np.zeros((n, 1))
+    more[large] = 2.0 ** -16
+    for h in range(2):
+        bad = ~(np.abs(out[:, h] - v) <= (2.0 ** -8 + 2.0 ** -10) * 1.01 * np.abs(v) + more)
+        assert not bad.any(), (np.argwhere(bad)[:4].tolist(), out[:, h][bad][:4], v[bad][:4])
+        score, big = (qn[:, h] * k).sum(-1) * D ** -0.5, (np.abs(qn[:, h]) * np.abs(k)).sum(-1) * D ** -0.5
+        tol = (2.0 ** -11 + 2.0 ** -17) * big + 2.0 ** -18 + more[:, 0] * np.abs(qn[:, h]).sum(-1) * D ** -0.5
+        bad = ~(np.abs(lse[:, h] - score) <= tol)
+        assert not bad.any(), (np.argwhere(bad)[:4].tolist(), lse[:, h][bad][:4], score[bad][:4])
