@@ -574,212 +574,9 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
             ok = __all_sync(0xffffffffu, wait_more(sm, p.status, bar, parity & 1u));
     };
 
-    // One statement for all warps of a warpgroup: PTX asks that they execute the same setmaxnreg
-    if (warp >= C::kSoftmax) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kRegsLess));
-        if (warp == C::kSoftmax) {
-            // ------------------------------------------------------------------ MMA
-            uint32_t c = 0, items = 0;  // tiles, items so far
-            const auto bar_of = [&](uint32_t pos) { return pos % NR; };
-            while (left > 0) {
-                const int seg = wk.stretch(left);
-                auto qk = [&](int m, uint32_t tile) {  // scores of row tile m, tile `tile`
-                    const uint32_t pos = 2 * tile, slot = bar_of(pos);
-                    const uint32_t buf = MT == 2 ? m : (tile & 1);
-                    if (ok) {
-                        const uint64_t a = sw128_desc(q_at + m * C::kQ, 16), b = sw128_desc(tile_at + slot * C::kTile, 16);
-    #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            umma_ss(tmem + buf * BN, a + ((k / 4) * 16384 + (k % 4) * 32) / 16, b + ((k / 4) * C::kChunk + (k % 4) * 32) / 16,
-                                    idesc(BN, false), k > 0);
-                        umma_commit(&sm.s_full[buf]);
-                        if (m == MT - 1) umma_commit(&sm.t_empty[slot]);
-                    }
-                    __syncwarp();
-                };
-                for (int m = 0; m < MT; ++m) wait(&sm.q_full[m], items);
-                wait(&sm.t_full[bar_of(2 * c)], 2 * c / NR);
-                tc_fence_after();
-                for (int m = 0; m < MT; ++m) qk(m, c);
-                for (int j = 0; j < seg; ++j, ++c) {
-                    const bool more = j + 1 < seg;
-                    const uint32_t vpos = 2 * c + 1, vslot = bar_of(vpos);
-                    if (MT == 1 && more) {
-                        wait(&sm.t_full[bar_of(2 * c + 2)], (2 * c + 2) / NR);
-                        tc_fence_after();
-                        qk(0, c + 1);
-                    }
-                    wait(&sm.t_full[vslot], vpos / NR);
-    #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const uint32_t buf = MT == 2 ? m : (c & 1);
-                        wait(&sm.p_full[buf], MT == 2 ? c : c >> 1);
-                        tc_fence_after();
-                        if (ok) {
-                            const uint64_t b = sw128_desc(tile_at + vslot * C::kTile, C::kChunk);
-    #pragma unroll
-                            for (int k = 0; k < BN / 16; ++k)
-                                umma_ts(tmem + C::kColO + m * D, tmem + buf * BN + BN / 2 + 8 * k, b + 2048 * k / 16, idesc(D, true), j > 0 || k > 0);
-                            umma_commit(&sm.pv_done[m]);
-                            if (m == MT - 1) umma_commit(&sm.t_empty[vslot]);
-                        }
-                        __syncwarp();
-                        if (MT == 2 && more) {
-                            if (m == 0) {
-                                wait(&sm.t_full[bar_of(2 * c + 2)], (2 * c + 2) / NR);
-                                tc_fence_after();
-                            }
-                            qk(m, c + 1);
-                        }
-                    }
-                }
-                ++items;
-                left -= seg + kEndUnits;
-                if (left > 0) wk.next(p);
-            }
-        } else if (warp == C::kSoftmax + 1) {
-            // --------------------------------------------------------------- loader
-            uint32_t pos = 0;
-            const int page_mask = (1 << p.page_shift) - 1;
-            while (left > 0) {
-                const int seg = wk.stretch(left);
-                const int32_t *row = p.table + static_cast<int64_t>(wk.b) * p.table_width;
-                auto page_of = [&](int j) {
-                    const int tok = wk.base + (wk.unit + j) * BN + 16 * lane;
-                    return j < seg && lane < BN / 16 && tok < wk.end ? row[tok >> p.page_shift] : -1;
-                };
-                int page = page_of(0);
-                for (int j = 0; j < seg; ++j) {
-                    const int tok = wk.base + (wk.unit + j) * BN + 16 * lane;
-                    const bool in = lane < BN / 16 && tok < wk.end;
-                    const bool good = in && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
-                    const uint32_t runs = __ballot_sync(0xffffffffu, good);
-                    if (in && !good && p.status) atomicOr(p.status, Q8_DEV_BAD_INDEX);
-                    const int64_t at = ((static_cast<int64_t>(good ? page : 0) * p.kv_heads + wk.kvh) << p.page_shift) + (tok & page_mask);
-                    page = page_of(j + 1);
-    #pragma unroll
-                    for (int v = 0; v < 2; ++v, ++pos) {
-                        const uint32_t slot = pos % NW;
-                        if (pos >= NW) wait(&sm.raw_empty[slot], pos / NW - 1);
-                        if (!ok) continue;
-                        if (lane == 0) {
-                            sm.meta[slot] = runs | static_cast<uint32_t>(min(BN, wk.end - (wk.base + (wk.unit + j) * BN))) << 8;
-                            mbar_arrive_expect_tx(&sm.raw_full[slot], __popc(runs) * 17 * D);
-                        }
-                        __syncwarp();
-                        if (good) {
-                            uint8_t *to = base + C::kRawAt + slot * C::kRaw;
-                            bulk_g2s(to + lane * 16 * D, (v ? p.vq : p.kq) + at * D, 16 * D, &sm.raw_full[slot]);
-                            bulk_g2s(to + C::kCodes + lane * D, (v ? p.vs : p.ks) + at * (D / 32), D, &sm.raw_full[slot]);
-                        }
-                    }
-                }
-                left -= seg + kEndUnits;
-                if (left > 0) wk.next(p);
-            }
-        } else {
-            // ----------------------------------------------------------- converters
-            constexpr int kCT = C::CW * 32, kPer = D / 16, kUnits = BN * kPer;  // units of 16 codes, of a token and a tile
-            constexpr int kMine = (kUnits + kCT - 1) / kCT;
-            const int ct = tid - (C::kSoftmax + 2) * 32;
-            // This thread's units are ct, ct + kCT, ...: unit x0 of tokens t0, t0 + kStep, ..., in the order of the raw tile.
-            // Which half of a unit's 16 codes comes first is chosen so that a warp's loads and its stores each hit all
-            // banks once
-            constexpr int kStep = kCT / kPer;
-            static_assert(kStep % 4 == 0, "the same place in the swizzle");
-            const int t0 = ct / kPer, x0 = ct % kPer;
-            const int half = D == 64 ? (t0 >> 1) & 1 : (D == 128 ? ((x0 >> 2) ^ t0) & 1 : ((x0 >> 2) ^ (x0 >> 3)) & 1);
-            const uint32_t from = ct * 16 + 8 * half, scale_at = (t0 * (D / 32) + (x0 >> 1)) * 2;
-            const uint32_t place = (x0 >> 2) * C::kChunk + t0 * 128;
-            const uint32_t piece0 = place + (((2 * (x0 & 3) + half) ^ (t0 & 7)) << 4), piece1 = place + (((2 * (x0 & 3) + (half ^ 1)) ^ (t0 & 7)) << 4);
-            uint32_t pos = 0;
-            while (left > 0) {
-                const int n = wk.stretch(left);
-                for (int jj = 0; jj < 2 * n; ++jj, ++pos) {
-                    const uint32_t slot = pos % NW, to = pos % NR;
-                    const uint32_t raw = raw_at + slot * C::kRaw;
-                    wait(&sm.raw_full[slot], pos / NW);
-                    if (pos >= NR) wait(&sm.t_empty[to], pos / NR - 1);
-                    if (ok) {
-                        const uint32_t meta = sm.meta[slot];
-                        const bool is_v = pos & 1u;
-                        const int here = (meta >> 8) & 0xFF, ring = (pos >> 1) & 7;
-                        if (ct == 0 && !is_v) {
-                            sm.unseen[ring] = ~meta & ((1u << (BN / 16)) - 1u);
-                            // for a tile to come (the last that had the place is long done)
-                            sm.big[0][ring ^ 4] = sm.big[1][ring ^ 4] = make_uint4(0, 0, 0, 0);
-                        }
-                        uint2 w0[kMine], w1[kMine];
-                        uint32_t sc[kMine];
-    #pragma unroll
-                        for (int i = 0; i < kMine; ++i) {
-                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
-                            w0[i] = lds64(raw + from + i * (kCT * 16));
-                            w1[i] = lds64(raw + (from ^ 8) + i * (kCT * 16));
-                            sc[i] = lds16(raw + C::kCodes + scale_at + i * (kStep * (D / 32) * 2));
-                        }
-                        // tokens that are not there and scales that are not finite count as 0, tokens with a scale of 512 or
-                        // more are taken times 2^-9 (a token's units are neighbouring lanes): such a scale before the product,
-                        // which would overflow; the token's others after it, as a small scale would lose its digits
-                        uint32_t top = 0u, after = 0u;  // bit i: unit i's products are still to be taken times 2^-9
-    #pragma unroll
-                        for (int i = 0; i < kMine; ++i) {
-                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
-                            top = max(top, sc[i] & 0x7FFFu);
-                        }
-                        if (__any_sync(0xffffffffu, top >= 0x6000u) || here < BN || (meta & 0xFFu) != (1u << (BN / 16)) - 1u) {
-    #pragma unroll
-                            for (int i = 0; i < kMine; ++i) {
-                                if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;  // (whole warps)
-                                const int t = t0 + i * kStep;
-                                const bool there = t < here && ((meta >> (t >> 4)) & 1u), finite = (sc[i] & 0x7C00u) != 0x7C00u;
-                                if (there && !finite && p.status) atomicOr(p.status, Q8_DEV_NONFINITE);
-                                if (!there || !finite) sc[i] = 0u;
-                                const uint32_t mine = __ballot_sync(0xffffffffu, (sc[i] & 0x7FFFu) >= 0x6000u);
-                                if ((mine >> (lane & ~(kPer - 1))) & ((1u << kPer) - 1u)) {
-                                    if ((sc[i] & 0x7FFFu) >= 0x6000u) sc[i] = hmul2(sc[i], 0x1800u);
-                                    else after |= 1u << i;
-                                    if ((lane & (kPer - 1)) == 0) atomicOr(reinterpret_cast<uint32_t *>(&sm.big[is_v][ring]) + (t >> 5), 1u << (t & 31));
-                                }
-                            }
-                        }
-                        const uint32_t row = tile_at + to * C::kTile;
-    #pragma unroll
-                        for (int i = 0; i < kMine; ++i) {
-                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
-                            const uint32_t s2 = sc[i] | sc[i] << 16;
-                            // (12 tokens on, of 256 dimensions, the swizzle's third bit is the other one)
-                            const uint32_t flip = kStep % 8 == 0 ? 0u : (i & 1) * 64u, on = i * (kStep * 128);
-                            uint32_t a, b, c, d;
-                            codes4_to_f16x2(w0[i].x, a, b);
-                            codes4_to_f16x2(w0[i].y, c, d);
-                            sts128(row + (piece0 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
-                            codes4_to_f16x2(w1[i].x, a, b);
-                            codes4_to_f16x2(w1[i].y, c, d);
-                            sts128(row + (piece1 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
-                        }
-#pragma unroll 1
-                        for (; after; after &= after - 1u) {
-                            const int i = __ffs(after) - 1;
-                            const uint32_t flip = kStep % 8 == 0 ? 0u : (i & 1) * 64u, on = i * (kStep * 128);
-                            for (const uint32_t at : {row + (piece0 ^ flip) + on, row + (piece1 ^ flip) + on}) {
-                                const uint4 v = lds128(at);
-                                sts128(at, make_uint4(hmul2(v.x, 0x18001800u), hmul2(v.y, 0x18001800u), hmul2(v.z, 0x18001800u), hmul2(v.w, 0x18001800u)));
-                            }
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sm.t_full[to]);
-                        mbar_arrive(&sm.raw_empty[slot]);
-                    }
-                }
-                left -= n + kEndUnits;
-                if (left > 0) wk.next(p);
-            }
-        }
-    } else {
+    // One setmaxnreg for all warps of a warpgroup: PTX asks that they execute the same one.  (The softmax first: with the other
+    // roles before it more instruction fetches missed, 1.28 in place of 0.8 stalls an instruction, 1105 us in place of 915)
+    if (warp < C::kSoftmax) {
         // -------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(C::kRegs));
         constexpr int kLanes = D / 8;            // lanes of a query or answer row, 16 bytes each
@@ -925,36 +722,45 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                     }
                     const float shift = ref;  // weights are 2^(s - shift)
                     unsigned long long sum[2] = {0ull, 0ull};
-                    if (raised || p.softcap > kCapEnd || __any_sync(0xffffffffu, !(f > 0.f) || (y > -INFINITY && !(fabsf(y) < kPlain)))) {
-                        // raised weights, wide caps, and large scores, whose product's rounding would show in the weight (product
-                        // and difference one after the other): few at a time, read again.  From the last to the first,
-                        // as the weights go where scores lay that have been read
+                    // large scores, whose product's rounding would show in the weight: product and difference one after the other
+                    const bool apart = !(f > 0.f) || (y > -INFINITY && !(fabsf(y) < kPlain));
+                    if (raised || p.softcap > kCapEnd || __any_sync(0xffffffffu, apart)) {
+                        // raised weights, wide caps, and warps with a row of large scores: few at a time, read again, from the last
+                        // to the first, as the weights go where scores lay that have been read.  The other rows of such a warp get
+                        // what the other branch would give them, bit for bit: their sums are taken in its order, in a pass before
+                        const bool late = raised || p.softcap > kCapEnd || apart;  // the row's sum is taken in the last pass
+                        const float c1 = p.softcap * kLog2e, c2 = -2.f * c1, c3 = c1 - shift;
                         const uint32_t wk4[4] = {bk.x, bk.y, bk.z, bk.w}, wv4[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll 1
-                        for (int k = BN - 16; k >= 0; k -= 16) {
-                            uint32_t x[16], h[8];
-                            tmem_ld(s_at + k, x);
-                            const uint32_t bits = masked ? seen(k & ~31) >> (k & 16) : 0xFFFFu;
-                            uint32_t bigk = 0u, bigv = 0u;
+                        for (int pass = __all_sync(0xffffffffu, late) ? 1 : 0; pass < 2; ++pass) {
+#pragma unroll 1
+                            for (int b = 0; b < BN; b += 16) {
+                                const int k = pass ? BN - 16 - b : b;
+                                uint32_t x[16], h[8];
+                                tmem_ld(s_at + k, x);
+                                const uint32_t bits = masked ? seen(k & ~31) >> (k & 16) : 0xFFFFu;
+                                uint32_t bigk = 0u, bigv = 0u;
 #pragma unroll
-                            for (int n = 0; n < 4; ++n)
-                                if ((k >> 5) == n) bigk = wk4[n] >> (k & 16), bigv = wv4[n] >> (k & 16);
+                                for (int n = 0; n < 4; ++n)
+                                    if ((k >> 5) == n) bigk = wk4[n] >> (k & 16), bigv = wv4[n] >> (k & 16);
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                float w[2], u[2];
+                                for (int i = 0; i < 16; i += 2) {
+                                    float w[2], u[2];
 #pragma unroll
-                                for (int n = 0; n < 2; ++n) {
-                                    w[n] = __uint_as_float(x[i + n]);
-                                    if ((bigk >> (i + n)) & 1u) w[n] *= 512.f;
-                                    w[n] = __fmul_rn(w[n], f);
-                                    if (cap) w[n] = capped(p, w[n]);
-                                    w[n] = (bits >> (i + n)) & 1u ? ex2(__fadd_rn(w[n], -shift)) : 0.f;
-                                    u[n] = (bigv >> (i + n)) & 1u ? w[n] * 512.f : w[n];
+                                    for (int n = 0; n < 2; ++n) {
+                                        w[n] = __uint_as_float(x[i + n]);
+                                        if ((bigk >> (i + n)) & 1u) w[n] *= 512.f;
+                                        const float s = __fmul_rn(w[n], f);
+                                        float e = apart ? __fadd_rn(s, -shift) : fmaf(w[n], f, -shift);
+                                        if (cap) e = p.softcap > kCapEnd ? __fadd_rn(capped(p, s), -shift) : fmaf(c2, rcp(1.f + ex2(s)), c3);
+                                        w[n] = (bits >> (i + n)) & 1u ? ex2(e) : 0.f;
+                                        u[n] = (bigv >> (i + n)) & 1u ? w[n] * 512.f : w[n];
+                                    }
+                                    h[i / 2] = f32x2_to_f16x2(u[0], u[1]);
+                                    if ((pass != 0) == late) sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(w[0], w[1]));
                                 }
-                                h[i / 2] = f32x2_to_f16x2(u[0], u[1]);
-                                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(w[0], w[1]));
+                                if (pass) tmem_st(s_at + BN / 2 + k / 2, h);
                             }
-                            tmem_st(s_at + BN / 2 + k / 2, h);
                         }
                     } else {
                         if (cap) {
@@ -1108,6 +914,210 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
             left -= seg + kEndUnits;
             item0 += wk.units + kEndUnits;
             if (left > 0) wk.next(p);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kRegsLess));
+        if (warp == C::kSoftmax) {
+            // ------------------------------------------------------------------ MMA
+            uint32_t c = 0, items = 0;  // tiles, items so far
+            const auto bar_of = [&](uint32_t pos) { return pos % NR; };
+            while (left > 0) {
+                const int seg = wk.stretch(left);
+                auto qk = [&](int m, uint32_t tile) {  // scores of row tile m, tile `tile`
+                    const uint32_t pos = 2 * tile, slot = bar_of(pos);
+                    const uint32_t buf = MT == 2 ? m : (tile & 1);
+                    if (ok) {
+                        const uint64_t a = sw128_desc(q_at + m * C::kQ, 16), b = sw128_desc(tile_at + slot * C::kTile, 16);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            umma_ss(tmem + buf * BN, a + ((k / 4) * 16384 + (k % 4) * 32) / 16, b + ((k / 4) * C::kChunk + (k % 4) * 32) / 16,
+                                    idesc(BN, false), k > 0);
+                        umma_commit(&sm.s_full[buf]);
+                        if (m == MT - 1) umma_commit(&sm.t_empty[slot]);
+                    }
+                    __syncwarp();
+                };
+                for (int m = 0; m < MT; ++m) wait(&sm.q_full[m], items);
+                wait(&sm.t_full[bar_of(2 * c)], 2 * c / NR);
+                tc_fence_after();
+                for (int m = 0; m < MT; ++m) qk(m, c);
+                for (int j = 0; j < seg; ++j, ++c) {
+                    const bool more = j + 1 < seg;
+                    const uint32_t vpos = 2 * c + 1, vslot = bar_of(vpos);
+                    if (MT == 1 && more) {
+                        wait(&sm.t_full[bar_of(2 * c + 2)], (2 * c + 2) / NR);
+                        tc_fence_after();
+                        qk(0, c + 1);
+                    }
+                    wait(&sm.t_full[vslot], vpos / NR);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const uint32_t buf = MT == 2 ? m : (c & 1);
+                        wait(&sm.p_full[buf], MT == 2 ? c : c >> 1);
+                        tc_fence_after();
+                        if (ok) {
+                            const uint64_t b = sw128_desc(tile_at + vslot * C::kTile, C::kChunk);
+#pragma unroll
+                            for (int k = 0; k < BN / 16; ++k)
+                                umma_ts(tmem + C::kColO + m * D, tmem + buf * BN + BN / 2 + 8 * k, b + 2048 * k / 16, idesc(D, true), j > 0 || k > 0);
+                            umma_commit(&sm.pv_done[m]);
+                            if (m == MT - 1) umma_commit(&sm.t_empty[vslot]);
+                        }
+                        __syncwarp();
+                        if (MT == 2 && more) {
+                            if (m == 0) {
+                                wait(&sm.t_full[bar_of(2 * c + 2)], (2 * c + 2) / NR);
+                                tc_fence_after();
+                            }
+                            qk(m, c + 1);
+                        }
+                    }
+                }
+                ++items;
+                left -= seg + kEndUnits;
+                if (left > 0) wk.next(p);
+            }
+        } else if (warp == C::kSoftmax + 1) {
+            // --------------------------------------------------------------- loader
+            uint32_t pos = 0;
+            const int page_mask = (1 << p.page_shift) - 1;
+            while (left > 0) {
+                const int seg = wk.stretch(left);
+                const int32_t *row = p.table + static_cast<int64_t>(wk.b) * p.table_width;
+                auto page_of = [&](int j) {
+                    const int tok = wk.base + (wk.unit + j) * BN + 16 * lane;
+                    return j < seg && lane < BN / 16 && tok < wk.end ? row[tok >> p.page_shift] : -1;
+                };
+                int page = page_of(0);
+                for (int j = 0; j < seg; ++j) {
+                    const int tok = wk.base + (wk.unit + j) * BN + 16 * lane;
+                    const bool in = lane < BN / 16 && tok < wk.end;
+                    const bool good = in && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
+                    const uint32_t runs = __ballot_sync(0xffffffffu, good);
+                    if (in && !good && p.status) atomicOr(p.status, Q8_DEV_BAD_INDEX);
+                    const int64_t at = ((static_cast<int64_t>(good ? page : 0) * p.kv_heads + wk.kvh) << p.page_shift) + (tok & page_mask);
+                    page = page_of(j + 1);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v, ++pos) {
+                        const uint32_t slot = pos % NW;
+                        if (pos >= NW) wait(&sm.raw_empty[slot], pos / NW - 1);
+                        if (!ok) continue;
+                        if (lane == 0) {
+                            sm.meta[slot] = runs | static_cast<uint32_t>(min(BN, wk.end - (wk.base + (wk.unit + j) * BN))) << 8;
+                            mbar_arrive_expect_tx(&sm.raw_full[slot], __popc(runs) * 17 * D);
+                        }
+                        __syncwarp();
+                        if (good) {
+                            uint8_t *to = base + C::kRawAt + slot * C::kRaw;
+                            bulk_g2s(to + lane * 16 * D, (v ? p.vq : p.kq) + at * D, 16 * D, &sm.raw_full[slot]);
+                            bulk_g2s(to + C::kCodes + lane * D, (v ? p.vs : p.ks) + at * (D / 32), D, &sm.raw_full[slot]);
+                        }
+                    }
+                }
+                left -= seg + kEndUnits;
+                if (left > 0) wk.next(p);
+            }
+        } else {
+            // ----------------------------------------------------------- converters
+            constexpr int kCT = C::CW * 32, kPer = D / 16, kUnits = BN * kPer;  // units of 16 codes, of a token and a tile
+            constexpr int kMine = (kUnits + kCT - 1) / kCT;
+            const int ct = tid - (C::kSoftmax + 2) * 32;
+            // This thread's units are ct, ct + kCT, ...: unit x0 of tokens t0, t0 + kStep, ..., in the order of the raw tile.
+            // Which half of a unit's 16 codes comes first is chosen so that a warp's loads and its stores each hit all
+            // banks once
+            constexpr int kStep = kCT / kPer;
+            static_assert(kStep % 4 == 0, "the same place in the swizzle");
+            const int t0 = ct / kPer, x0 = ct % kPer;
+            const int half = D == 64 ? (t0 >> 1) & 1 : (D == 128 ? ((x0 >> 2) ^ t0) & 1 : ((x0 >> 2) ^ (x0 >> 3)) & 1);
+            const uint32_t from = ct * 16 + 8 * half, scale_at = (t0 * (D / 32) + (x0 >> 1)) * 2;
+            const uint32_t place = (x0 >> 2) * C::kChunk + t0 * 128;
+            const uint32_t piece0 = place + (((2 * (x0 & 3) + half) ^ (t0 & 7)) << 4), piece1 = place + (((2 * (x0 & 3) + (half ^ 1)) ^ (t0 & 7)) << 4);
+            uint32_t pos = 0;
+            while (left > 0) {
+                const int n = wk.stretch(left);
+                for (int jj = 0; jj < 2 * n; ++jj, ++pos) {
+                    const uint32_t slot = pos % NW, to = pos % NR;
+                    const uint32_t raw = raw_at + slot * C::kRaw;
+                    wait(&sm.raw_full[slot], pos / NW);
+                    if (pos >= NR) wait(&sm.t_empty[to], pos / NR - 1);
+                    if (ok) {
+                        const uint32_t meta = sm.meta[slot];
+                        const bool is_v = pos & 1u;
+                        const int here = (meta >> 8) & 0xFF, ring = (pos >> 1) & 7;
+                        if (ct == 0 && !is_v) {
+                            sm.unseen[ring] = ~meta & ((1u << (BN / 16)) - 1u);
+                            // for a tile to come (the last that had the place is long done)
+                            sm.big[0][ring ^ 4] = sm.big[1][ring ^ 4] = make_uint4(0, 0, 0, 0);
+                        }
+                        uint2 w0[kMine], w1[kMine];
+                        uint32_t sc[kMine];
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i) {
+                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
+                            w0[i] = lds64(raw + from + i * (kCT * 16));
+                            w1[i] = lds64(raw + (from ^ 8) + i * (kCT * 16));
+                            sc[i] = lds16(raw + C::kCodes + scale_at + i * (kStep * (D / 32) * 2));
+                        }
+                        // tokens that are not there and scales that are not finite count as 0, tokens with a scale of 512 or
+                        // more are taken times 2^-9 (a token's units are neighbouring lanes): such a scale before the product,
+                        // which would overflow; the token's others after it, as a small scale would lose its digits
+                        uint32_t top = 0u, after = 0u;  // bit i: unit i's products are still to be taken times 2^-9
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i) {
+                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
+                            top = max(top, sc[i] & 0x7FFFu);
+                        }
+                        if (__any_sync(0xffffffffu, top >= 0x6000u) || here < BN || (meta & 0xFFu) != (1u << (BN / 16)) - 1u) {
+#pragma unroll
+                            for (int i = 0; i < kMine; ++i) {
+                                if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;  // (whole warps)
+                                const int t = t0 + i * kStep;
+                                const bool there = t < here && ((meta >> (t >> 4)) & 1u), finite = (sc[i] & 0x7C00u) != 0x7C00u;
+                                if (there && !finite && p.status) atomicOr(p.status, Q8_DEV_NONFINITE);
+                                if (!there || !finite) sc[i] = 0u;
+                                const uint32_t mine = __ballot_sync(0xffffffffu, (sc[i] & 0x7FFFu) >= 0x6000u);
+                                if ((mine >> (lane & ~(kPer - 1))) & ((1u << kPer) - 1u)) {
+                                    if ((sc[i] & 0x7FFFu) >= 0x6000u) sc[i] = hmul2(sc[i], 0x1800u);
+                                    else after |= 1u << i;
+                                    if ((lane & (kPer - 1)) == 0) atomicOr(reinterpret_cast<uint32_t *>(&sm.big[is_v][ring]) + (t >> 5), 1u << (t & 31));
+                                }
+                            }
+                        }
+                        const uint32_t row = tile_at + to * C::kTile;
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i) {
+                            if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
+                            const uint32_t s2 = sc[i] | sc[i] << 16;
+                            // (12 tokens on, of 256 dimensions, the swizzle's third bit is the other one)
+                            const uint32_t flip = kStep % 8 == 0 ? 0u : (i & 1) * 64u, on = i * (kStep * 128);
+                            uint32_t a, b, c, d;
+                            codes4_to_f16x2(w0[i].x, a, b);
+                            codes4_to_f16x2(w0[i].y, c, d);
+                            sts128(row + (piece0 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
+                            codes4_to_f16x2(w1[i].x, a, b);
+                            codes4_to_f16x2(w1[i].y, c, d);
+                            sts128(row + (piece1 ^ flip) + on, make_uint4(hmul2(a, s2), hmul2(b, s2), hmul2(c, s2), hmul2(d, s2)));
+                        }
+#pragma unroll 1
+                        for (; after; after &= after - 1u) {
+                            const int i = __ffs(after) - 1;
+                            const uint32_t flip = kStep % 8 == 0 ? 0u : (i & 1) * 64u, on = i * (kStep * 128);
+                            for (const uint32_t at : {row + (piece0 ^ flip) + on, row + (piece1 ^ flip) + on}) {
+                                const uint4 v = lds128(at);
+                                sts128(at, make_uint4(hmul2(v.x, 0x18001800u), hmul2(v.y, 0x18001800u), hmul2(v.z, 0x18001800u), hmul2(v.w, 0x18001800u)));
+                            }
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.t_full[to]);
+                        mbar_arrive(&sm.raw_empty[slot]);
+                    }
+                }
+                left -= n + kEndUnits;
+                if (left > 0) wk.next(p);
+            }
         }
     }
 

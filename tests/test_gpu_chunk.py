@@ -532,3 +532,21 @@ def test_small_blocks_beside_a_scale_of_512(D):
         tol = (2.0 ** -11 + 2.0 ** -17) * big + 2.0 ** -18 + more[:, 0] * np.abs(qn[:, h]).sum(-1) * D ** -0.5
         bad = ~(np.abs(lse[:, h] - score) <= tol)
         assert not bad.any(), (np.argwhere(bad)[:4].tolist(), lse[:, h][bad][:4], score[bad][:4])
+
+
+@pytest.mark.parametrize("D,n,lens,group", [(64, 64, 64, 1), (128, 200, 700, 1), (128, 20, 9000, 4), (256, 100, 300, 2)])
+@pytest.mark.parametrize("factor", [1e9, float("nan"), float("inf"), 0.0])
+def test_what_other_rows_hold_does_not_change_a_row(D, n, lens, group, factor):
+    """Bit for bit, lse included, where starts and lengths are the same: every second row of the tile is made so large that
+    its scores pass 2^20, or is not finite, or zero."""
+    from block_quantized_int8_gb300 import q8
+    pages = -(-lens // 64)
+    cache, _, _ = filled_cache(pages, 64, 1, D, 51)
+    q = bf16_of(np.random.default_rng(51).standard_normal((n, group, D)) * 3).cuda()
+    tab = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    a, al = q8.q8_attn_chunk(q, cache, tab, i32(lens), i32(0, n), return_lse=True)
+    other = q.clone()
+    other[1::2] *= factor
+    b, bl = q8.q8_attn_chunk(other, cache, tab, i32(lens), i32(0, n), return_lse=True)
+    assert torch.equal(a[::2], b[::2]) and torch.equal(al[::2], bl[::2])

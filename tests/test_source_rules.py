@@ -22,7 +22,7 @@ def test_the_warps_of_a_warpgroup_execute_the_same_setmaxnreg(name):
         assert len(re.findall(r"setmaxnreg\." + kind, text)) <= 1
     if "setmaxnreg" in text:
         # the branch between the two is between whole warpgroups
-        assert re.search(r"if \(warp >= C::kSoftmax\) \{\s*asm volatile\(\"setmaxnreg\.dec", text)
+        assert re.search(r"if \(warp (<|>=) C::kSoftmax\) \{\s*asm volatile\(\"setmaxnreg\.", text)
         assert "static_assert(kSoftmax % 4 == 0" in text
 
 
