@@ -735,9 +735,14 @@ q8_status q8_kv_plan(int32_t *table, int32_t table_width, int32_t pages, int32_t
  * counts as 0 and sets Q8_DEV_NONFINITE; nothing past a length enters the result.
  * Sums, the running maximum and lse are fp32.  Rounded to binary16 before their products are: a
  * query row, scaled by a power of two (exact down to 2^-31 of its largest value); keys and values
- * s * code (by 2^-11 of themselves at most; of a token with a scale of 512 or more by 2^-16 besides); a
- * weight (by 2^-11 of itself down to 2^-25 of the largest around it, and 2^-36 of that below).
- * So a score is off by 2^-11 of sum|q k| * scale at most.  T * (q_heads / kv_heads) < 2^31 - 4096.
+ * s * code (by 2^-11 of themselves at most; of a token with a scale of 512 or more by an absolute 2^-16
+ * besides), where q8_attn_decode takes key codes exactly; a weight (by 2^-11 of itself down to 2^-25 of
+ * the largest around it, and 2^-36 of that below; of a row that has come to a value scale of 512 or more down to
+ * 2^-16, and 2^-27 below).  So a score is off by 2^-11 of sum|q k| * scale at most, and of a token with a
+ * scale of 512 or more by 2^-16 of sum|q| * scale besides; a softcap adds 2^-21 of the cap (above 256: 2^-18 of the
+ * capped score; from 2^40 on there is none).  A call repeats bit for bit; a row does not depend on what
+ * other rows hold, but on starts and lens in its last bits, as the work is split by them.
+ * T * (q_heads / kv_heads) < 2^31 - 4096.
  *   ws     : q8_attn_chunk_workspace_size() bytes, 256-byte aligned, the first
  *            Q8_CHUNK_ZEROED_BYTES zeroed once (the kernel counts there and leaves
  *            them zero, but after a Q8_DEV_TIMEOUT; the rest may hold anything).  Not for two calls that may run at the

@@ -550,3 +550,106 @@ def test_what_other_rows_hold_does_not_change_a_row(D, n, lens, group, factor):
     other[1::2] *= factor
     b, bl = q8.q8_attn_chunk(other, cache, tab, i32(lens), i32(0, n), return_lse=True)
     assert torch.equal(a[::2], b[::2]) and torch.equal(al[::2], bl[::2])
+
+
+@pytest.mark.parametrize("cap", [1.0, 30.0, 255.0, 256.0, 257.0, 1000.0, 1e5, 2.0 ** 30, 2.0 ** 39, 2.0 ** 40, 3e38])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_caps_of_any_width(D, cap):
+    """With a window of 1 the lse is the capped score.  Scales are powers of two and a query has one value, so that the products
+    are exact and what is left is the cap's own error: 2^-21 of it where c - 2 c / (1 + 2^y) is used (exponential 2^-22,
+    reciprocal 2^-23, sums 2^-24 each: 1.8 * 2^-22 of c at most), and roundings of the score (the factor's three, the product,
+    and the lse: below 2^-20 of it).  The reference lies 11 below a small score: their difference, near 11, is rounded by 2^-21,
+    and the weight by the exponential's 2^-22, together below 2^-20 besides.  Scores on both sides of a quarter of the cap,
+    where wide caps change form."""
+    r = np.random.default_rng(52)
+    n, ps = 400, 16
+    cache, _, _ = filled_cache(25, ps, 1, D, 52)
+    cache.ks.fill_(2.0 ** -6)
+    k = cache.kq.cpu().numpy().astype(np.float64).reshape(-1, D)[:n, 5] * 2.0 ** -6
+    k[k == 0] = 1.0
+    x = np.concatenate([r.uniform(-3, 3, 100), r.uniform(0.2, 0.3, 100) * r.choice([-1, 1], 100), 2.0 ** r.uniform(-20, 0, 200) * r.choice([-1, 1], 200)])
+    want = x * min(cap, 2.0 ** 27)  # (a cap of 2^40 or more is none: it would move larger scores by more than 2^-20 of them)
+    q = torch.zeros((n, 2, D), dtype=torch.bfloat16)
+    q[:, :, 5] = bf16_of(want / k * D ** 0.5)[:, None]
+    k = cache.kq.cpu().numpy().astype(np.float64).reshape(-1, D)[:n, 5] * 2.0 ** -6
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    from block_quantized_int8_gb300 import q8
+    tab = torch.arange(25, dtype=torch.int32, device="cuda").view(1, 25)
+    out, lse = q8.q8_attn_chunk(q.cuda(), cache, tab, i32(n), i32(0, n), softcap=cap, window=1, return_lse=True)
+    score = f64(q)[:, :, 5] * k[:, None] * D ** -0.5
+    ref = cap * np.tanh(score / cap)
+    formed = (cap <= 256) | (np.abs(score / cap) > 0.249)
+    tol = 2.0 ** -20 * np.abs(score) + np.where(formed, 2.0 ** -21 * cap, 0.0) + 2.0 ** -20
+    bad = ~(np.abs(f64(lse) - ref) <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:4].tolist(), f64(lse)[bad][:4], ref[bad][:4], score[bad][:4])
+    v = cache.vq.cpu().numpy().astype(np.float64).reshape(-1, D)[:n] * np.repeat(f64(cache.vs).reshape(-1, D // 32)[:n], 32, -1)
+    assert np.all(np.abs(f64(out) - v[:, None]) <= (2.0 ** -8 + 2.0 ** -10) * 1.01 * np.abs(v)[:, None])
+
+
+@pytest.mark.parametrize("D,q_scale", [(64, 3.0), (128, 40.0), (256, 400.0)])
+@pytest.mark.parametrize("softcap", [256.0, 257.0, 1000.0, 2.0 ** 40])
+def test_wide_caps_of_masked_tiles(D, q_scale, softcap):
+    """(Scores in the hundreds are off by more than the 2-norm's bound foresees; each output's own bound says so.)"""
+    run_case(D, 2, 2, 16, [150, 3, 40], [333, 3, 401], softcap=softcap, q_scale=q_scale, seed=53, tight=1.0)
+    run_case(D, 1, 3, 16, [150, 40], [400, 90], softcap=softcap, q_scale=q_scale, window=70, seed=54, tight=1.0)
+
+
+@pytest.mark.parametrize("softcap", [30.0, 1000.0])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_caps_and_scales_at_the_end_of_their_range(D, softcap):
+    r = np.random.default_rng(55)
+    cache, kv, vv = filled_cache(20, 16, 1, D, 55)
+    for plane in (cache.ks, cache.vs):
+        s = f64(plane).astype(np.float16)
+        s[7:9] = r.uniform(400, 60000, s[7:9].shape).astype(np.float16)
+        plane.copy_(torch.from_numpy(s).view(plane.dtype))
+    kv, vv = (c.cpu().numpy().astype(np.float64) * np.repeat(f64(s), 32, -1) for c, s in ((cache.kq, cache.ks), (cache.vq, cache.vs)))
+    q = bf16_of(r.standard_normal((60, 2, D)) * 1e-5).cuda()
+    check(cache, kv, vv, q, np.arange(20).reshape(1, 20), [300], [0, 60], softcap=softcap)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("at", [5, 250])
+def test_ordinary_values_beside_a_scale_of_512(D, at):
+    """From a tile with a value scale of 512 or more on, a weight is good to 2^-11 of itself down to 2^-16 of the largest and to
+    2^-27 of that below.  Held against the dimensions whose own scales are ordinary, with their own largest value."""
+    r = np.random.default_rng(56)
+    n, new = 900, 100
+    cache, _, _ = filled_cache(57, 16, 1, D, 56)
+    s = f64(cache.vs).astype(np.float16).reshape(57 * 16, D // 32)
+    s[at, 0] = 600
+    cache.vs.copy_(torch.from_numpy(s.reshape(57, 1, 16, D // 32)).view(cache.vs.dtype))
+    k, v = (c.cpu().numpy().astype(np.float64).reshape(-1, D)[:n] * np.repeat(f64(s).reshape(-1, D // 32)[:n], 32, -1)
+            for c, s in ((cache.kq, cache.ks), (cache.vq, cache.vs)))
+    q = bf16_of(r.standard_normal((new, 2, D)) * 4)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    from block_quantized_int8_gb300 import q8
+    tab = torch.arange(57, dtype=torch.int32, device="cuda").view(1, 57)
+    out, _ = q8.q8_attn_chunk(q.cuda(), cache, tab, i32(n), i32(0, new))
+    for h in range(2):
+        ref, _, pv, big, top, count = definition(f64(q)[:, h], k, v[:, 32:], n - new + np.arange(new), np.ones(n, dtype=bool), D ** -0.5)
+        fine = (2.0 ** -11 + 2.0 ** -17) * big + 2.0 ** -18
+        tol = 2.0 ** -8 * 1.01 * np.abs(ref) + (2.0 ** -10 + 2.2 * fine)[:, None] * pv + (count * 2.0 ** -27)[:, None] * top + 2.0 ** -16
+        bad = ~(np.abs(f64(out)[:, h, 32:] - ref) <= tol)
+        assert not bad.any(), (np.argwhere(bad)[:4].tolist(), f64(out)[:, h, 32:][bad][:4], ref[bad][:4])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 90])
+def test_the_lse_of_one_new_token_is_the_decode_calls(D, window):
+    """There key codes enter exactly, here a key is rounded to binary16 (2^-11 of sum|q k|); fp32 sums are 2^-17 of it in each."""
+    from block_quantized_int8_gb300 import q8
+    cache, kv, vv = filled_cache(40, 16, 2, D, 57)
+    q = bf16_of(np.random.default_rng(57).standard_normal((3, 6, D)) * 2)
+    tables, lens = np.arange(40).reshape(4, 10)[:3], [1, 160, 77]
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    tab = torch.from_numpy(tables.astype(np.int32)).cuda()
+    _, al = q8.q8_attn_decode(q.cuda(), cache, tab, i32(*lens), window=window)
+    _, bl = q8.q8_attn_chunk(q.cuda(), cache, tab, i32(*lens), i32(0, 1, 2, 3), window=window, return_lse=True)
+    for b, n in enumerate(lens):
+        t = np.arange(n)
+        for h in range(6):
+            k, v = (a[tables[b][t // 16], h // 3, t % 16] for a in (kv, vv))
+            _, e, _, big, _, _ = definition(f64(q)[b:b + 1, h], k, v, np.array([n - 1]), np.ones(n, dtype=bool), D ** -0.5, 0.0, window)
+            off = abs(float(al[b, h]) - float(bl[b, h]))
+            assert off <= (2.0 ** -11 + 2.0 ** -16) * big[0] + 2.0 ** -17 + 2.0 ** -21 * abs(e[0]), (b, h, off, big)
