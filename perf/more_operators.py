@@ -361,6 +361,22 @@ def _plain_attn(st):
 # ---------------------------------------------------------------------------------------------
 # one pass
 # ---------------------------------------------------------------------------------------------
+def _cache(q8, st):
+    """The handle that a program makes once for its cache, of the tensors that the state has now."""
+    k = st.get("cache")
+    if k is None or k.kq is not st["kq"] or k.ks is not st["ks"] or k.vq is not st["vq"] or k.vs is not st["vs"]:
+        k = st["cache"] = q8.KvCache(st["kq"], st["ks"], st["vq"], st["vs"])
+    return k
+
+
+def _turns(q8, st):
+    """The table that a program makes once for its model, of the frequencies that the state has now."""
+    f, made = st["inv_freq"], st.get("turns")
+    if made is None or made[0] is not f or made[1] != f._version:
+        made = st["turns"] = (f, f._version, q8.rope_turns(f))
+    return made[2]
+
+
 def _own(st):
     from block_quantized_int8_gb300 import q8
     c = st["case"]
@@ -370,25 +386,23 @@ def _own(st):
         out = [st["residual_out"]] if c["res"] != "none" else []
         return out + ([y, _coded_values(q, s)] if c["q8"] else [y])
     if c["op"] in ("rope", "rope_append"):
-        if "turns" not in st:  # the table that a program makes once for its model
-            st["turns"] = q8.rope_turns(st["inv_freq"])
+        turns = _turns(q8, st)
         if c["op"] == "rope":
-            return [q8.q8_rope(st["x"], st["positions"], st["turns"], interleaved=c["interleaved"], factor=st["factor"])]
-        if "cache" not in st:  # the handle that a program makes once for its cache
-            st["cache"] = q8.KvCache(st["kq"], st["ks"], st["vq"], st["vs"])
+            return [q8.q8_rope(st["x"], st["positions"], turns, interleaved=c["interleaved"], factor=st["factor"])]
+        cache = _cache(q8, st)
         h, kv = c["q_heads"], c["kv_heads"]
         x = st["qkv"]
-        q = q8.q8_rope_append(x[:, :h], x[:, h:h + kv], x[:, h + kv:], st["cache"], st["positions"], st["slots"], st["turns"],
+        q = q8.q8_rope_append(x[:, :h], x[:, h:h + kv], x[:, h + kv:], cache, st["positions"], st["slots"], turns,
                               interleaved=c["interleaved"], factor=st["factor"])
-        return [q, *q8.q8_kv_read(st["cache"], st["slots"], dtype=torch.bfloat16)]
+        return [q, *q8.q8_kv_read(cache, st["slots"], dtype=torch.bfloat16)]
     if c["op"] == "plan":
         starts, slots, positions, lens, left = q8.q8_kv_plan(st["table"], st["lens"], st["new"], c["page"], st["pages"], st["tokens"],
                                                              free_pages=st["free"], free_count=st["free_count"])
         return [st["table"], starts, slots, positions, lens, left]
-    if "cache" not in st:
-        st["cache"] = q8.KvCache(st["kq"], st["ks"], st["vq"], st["vs"])
+    cache = _cache(q8, st)
+    if "ws" not in st:
         st["ws"] = q8.workspace(q8.q8_attn_chunk_workspace_size(c["q_heads"], c["kv_heads"], c["head_dim"]))
-    out, _ = q8.q8_attn_chunk(st["q"], st["cache"], st["table"], st["lens"], st["starts"], scale=st["scale"], softcap=c["softcap"],
+    out, _ = q8.q8_attn_chunk(st["q"], cache, st["table"], st["lens"], st["starts"], scale=st["scale"], softcap=c["softcap"],
                               window=c["window"], out=st["out"], ws=st["ws"])
     return [out]
 
