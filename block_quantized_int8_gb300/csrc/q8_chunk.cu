@@ -18,8 +18,11 @@
 // Operands are binary16: a query row is scaled by a power of two (its bf16 values are then exact
 // down to 2^-31 of its largest), keys and values are s * code rounded once (by 2^-11 of themselves;
 // exact where the scale is subnormal, as all are whole multiples of 2^-24).  Tokens with a scale of
-// 512 or more, whose products could overflow, are taken times 2^-9: the scores get the factor
-// back, or the weights are raised by 2^9 (their reference moves up for it).
+// 512 or more, whose products could overflow, are taken times 2^-9 (what their small blocks hold to
+// 2^-16): the scores get the factor back, or the weights are raised by 2^9 (their reference moves up for
+// it, and stays, so that the row's other weights are good down to 2^-16 of the largest from then on).
+//
+// A row's arithmetic does not depend on what other rows hold, whichever branch its warp takes.
 //
 // Roles (one CTA per SM):
 //   softmax     4 warps per row tile, a thread per row, its scores of a tile in registers; the query rows
@@ -32,14 +35,16 @@
 //               MN-major for the values, so nothing is transposed
 //
 // Bound: a tile of 128 tokens and 256 rows needs 2048 clocks of the tensor cores, 1024 of exponentials and
-// about 2600 of shared memory (operands, raw tiles in and out); it takes 4500, the turn of a row tile: scores out of tensor
-// memory, weights (2700), product, next scores.  With 128 rows 3700, converters and softmax about
-// 3000 each.  Measured: 1024 new tokens over 65,536 (32 / 8 heads of 128) 1004 us, 1.09 PFLOP/s; 4096
-// tokens alone 189 us, 0.73; 16 sequences of 1 to 5 new tokens over up to 6000 58 us; 32 new tokens over
-// 262,144 232 us, 2.46 TB/s.  Tiles of 80 tokens with a place of their own for the weights, so that the
-// next scores need not wait for the product: 1225 us in place of 1004.
+// about 2600 of shared memory (operands, raw tiles in and out); it takes 4100, the turn of a row tile: scores out of tensor
+// memory, weights, product, next scores.  With 128 rows it is as much, converters and softmax about
+// 3000 each.  Measured on the device (events around one call, L2 flushed before it): 1024 new tokens over 65,536 (32 / 8
+// heads of 128) 916 us, 1.19 PFLOP/s; 4096 tokens alone 176 to 187 us, 0.75; 16 sequences of 1 to 5 new tokens
+// over up to 6000 60 us; 32 new tokens over 262,144 229 us, 2.49 TB/s; 1024 over 65,536 with 12 / 4 heads of 256
+// 1103 us, 0.74 PFLOP/s.  (Calls one after the other hold the clock lower: the first takes 990 us then.)  Tiles of 80
+// tokens with a place of their own for the weights, so that the next scores need not wait for the product: 1225 us where
+// this form took 1004.
 //
-// Two row tiles where sequences have more than 128 rows on average (128 rows take 2.2 us a tile, 256 2.4, so
+// Two row tiles where sequences have more than 128 rows on average (a tile takes 2.1 us with 128 rows and with 256, so
 // that below it half of the work would be nobody's); at 256 dimensions tensor memory has room for one.
 //
 // Split: units of one tile are counted out evenly over the CTAs from the device's lengths, as in
@@ -1088,7 +1093,8 @@ __global__ void __launch_bounds__(Cfg<D_, MT_>::kThreads, 1) chunk_kernel(const 
                         for (int i = 0; i < kMine; ++i) {
                             if (kUnits % kCT != 0 && ct + i * kCT >= kUnits) break;
                             const uint32_t s2 = sc[i] | sc[i] << 16;
-                            // (12 tokens on, of 256 dimensions, the swizzle's third bit is the other one)
+                            // (kStep tokens on, where that is an odd multiple of four as for 256 dimensions, the swizzle's
+                            // third bit is the other one)
                             const uint32_t flip = kStep % 8 == 0 ? 0u : (i & 1) * 64u, on = i * (kStep * 128);
                             uint32_t a, b, c, d;
                             codes4_to_f16x2(w0[i].x, a, b);

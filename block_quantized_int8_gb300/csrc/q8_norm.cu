@@ -8,8 +8,10 @@
 // neighbouring lanes hold a block of 32, whose largest magnitude they find by two shuffles.
 // All sums are fp32, in an order that the width alone sets.
 //
-// Bound by bytes for many rows and by the launch for few.  Measured: 4099 rows of 4096 in bf16 onto a bf16
-// residual 27.3 us (4.9 TB/s), with Q8_0 rows besides 33.4 (4.55); one row of 1536 about 3.
+// Bound by bytes for many wide rows, by the launch for few, and for many narrow ones by the CTAs: a row of 64
+// values keeps 8 lanes busy.  Measured on the device (events around one call, L2 flushed before it): 4099 rows of
+// 4096 in bf16 onto a bf16 residual 27.3 to 28.3 us (4.7 TB/s), with Q8_0 rows besides 33.4 to 35.5 (4.3); in bf16 alone
+// 81,920 rows of 512 48 us (3.5 TB/s), 163,840 of 256 89 (1.9), 655,360 of 64 336 (0.5, two CTAs a nanosecond).
 // One unit a thread up to 256 units, then two and, past 1024, four: fewer and wider would leave
 // narrow rows a few warps, more would give the widest rows more than 1024 threads.
 //

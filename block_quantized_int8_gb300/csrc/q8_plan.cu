@@ -6,8 +6,8 @@
 // a second one the pages before them; then each token finds its sequence by bisection of the first
 // rows, and its page from the table (a page that the sequence had) or from the free list (a new
 // one, whose rank among all new pages is known, so nothing waits for the table's update).  Bound by
-// latency: 12 bytes written a token (48 sequences of a token each 6 us; 300 of up to 400 tokens, 57,000 rows,
-// 19, and 21 with one row of a thread at a time).  One CTA serves up to kFewTokens rows; more are spread over a
+// latency: 12 bytes written a token (on the device, after a flush of L2: 48 sequences of a token each 6 to 9 us; 300 of
+// up to 400 tokens, 57,000 rows, 19, and 21 with one row of a thread at a time).  One CTA serves up to kFewTokens rows; more are spread over a
 // cluster, whose CTAs scan alike and share the rows; its barrier also keeps apart the reading of
 // the lengths and of the free count from their update in place.
 #include "q8_dev.cuh"

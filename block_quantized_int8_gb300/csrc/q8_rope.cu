@@ -7,14 +7,15 @@
 // dimensions from `rot` on pass.
 //
 // Angles: the table holds F_i = f_i / (2 pi) as a 64-bit fraction of a turn, so that t F_i modulo
-// 2^64 is the angle within its turn, exactly for the F_i given, at any distance: off by |t| 2^-65
-// turns at most.  Its upper 32 bits go to fp32 as half turns in [-1, 1) (2^-25 half turns of
-// rounding at most), whose sine and cosine are taken.  A product t f_i in fp32 would be off by
-// 0.008 at t = 200,000, two bf16 steps of the result.
+// 2^64 is the angle within its turn, exactly for the F_i given, at any distance: off by |t| times
+// the three units of 2^-64 turns that F_i may be off, below 2^-31 turns.  Its upper 32 bits go to fp32
+// as half turns in [-1, 1) (2^-25 half turns of rounding at most), whose sine and cosine are taken.  A
+// product t f_i in fp32 would be off by 0.008 at t = 200,000, two bf16 steps of the result.
 //
 // Bound by bytes: each row in once, rotated rows (bf16) or codes and scales out once.  A CTA has
 // one token: its threads make the token's cosines and sines once, in shared memory, for all heads.
-// Measured: 8192 tokens of 40 heads of 128 in bf16 32 us (5.2 TB/s; 256 threads 31 to 35, 512 35).  With the
+// Measured on the device (events around one call, L2 flushed before it; one after the other, as a part of the rows stays
+// in L2, 29.4): 8192 tokens of 40 heads of 128 in bf16 32 us (5.2 TB/s; 256 threads 31 to 35, 512 35).  With the
 // write to the cache, 4096 tokens of 32 / 8 heads 27.7 us (3.35 TB/s; 29, 35 and 46 with 256, 384 and 512 threads, 27 with
 // 64), of which the angles' latency before the first store is most.
 #include <cuda_bf16.h>

@@ -56,7 +56,8 @@ class PromptStep:
         self.starts, self.slots, self.positions = ints(batch + 1), ints(rows, -1, torch.int64), ints(rows)
         self.status = ints(1)
         self.ws = q8.workspace(q8.q8_attn_chunk_workspace_size(heads, kv_heads, head_dim))
-        self.attn = torch.zeros((rows, heads, head_dim), dtype=torch.bfloat16, device="cuda")  # rows of no sequence stay zero
+        self.attn = torch.zeros((rows, heads, head_dim), dtype=torch.bfloat16, device="cuda")
+        # (rows of no sequence keep what an earlier step wrote there; their hidden states are nobody's)
         self.queries = None
 
     def __call__(self):

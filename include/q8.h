@@ -671,7 +671,7 @@ q8_status q8_rope_turns(const double *inv_freq, int32_t n, uint64_t *turns);
  *   turns     : DEVICE copy of q8_rope_turns' table for rot / 2 pairs, 8-byte aligned
  *   positions : int32 [T], any value
  * head_dim 64, 128 or 256; rot a multiple of 16, 16 .. head_dim.  The angle is exact to
- * 2^-25 half turns at any position; cosines, sines and sums are binary32, y is rounded once.
+ * 2^-24 half turns at any position; cosines, sines and sums are binary32, y is rounded once.
  */
 q8_status q8_rope(const void *x, int64_t ldx, int32_t dtype, uint16_t *y, int64_t ldy, int32_t heads, int32_t head_dim, int32_t rot,
                   int32_t layout, float factor, const uint64_t *turns, const int32_t *positions, int64_t T, q8_stream_t stream);
